@@ -492,6 +492,168 @@ int kvarn_decode_attention_noalloc(const float* q, const uint8_t* tiles, int64_t
                                    const kvarn_layout_t* layout, float* out,
                                    unsigned launch_flags, kvarn_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The 8-bit cache. The pages have no counterpart: it is the same cache (128-token
+ * tiles per KV head, byte-offset tile tables, FP32 staging window, whole-tile
+ * promotion) with records that hold every K and V value in 8 bits, unrotated,
+ * with one fp32 scale for each block of tokens of a head. It is for the layers
+ * and models for which 2- to 4-bit values lose too much; window, tile tables and
+ * bookkeeping calls are shared with the packed cache above.
+ *
+ * A value is code * scale. Two code formats:
+ *   KVARN_CODE8_I8    integers -127..127, stored as unsigned bytes code + 128;
+ *                     code = x / scale rounded to the nearest integer, ties
+ *                     to even; scale = largest magnitude of the block / 127.
+ *   KVARN_CODE8_E4M3  8-bit floating point (sign, 4-bit exponent of bias 7,
+ *                     3-bit mantissa, largest 448); code = x / scale rounded
+ *                     to nearest, ties to even; scale = largest magnitude / 448.
+ * Both scales are at least 2^-100 (a block of zeros has that scale and zero
+ * codes); divisions are IEEE fp32. A block that holds a NaN or an infinity gets
+ * the scale NaN and zero codes: every attention row that sees it is NaN.
+ * A block is block_tokens (16, 32, 64 or 128) consecutive tokens of a tile over
+ * all head_dim channels of one head; K and V have scales of their own.
+ *
+ * Record of one (tile, KV head), D = head_dim, 256 D + 128 bytes:
+ *   off_k_codes  u8 [16][D/64][8][64]  token t, channel c: byte (t/8) 8 D +
+ *                                      (c/64) 512 + (t%8) 64 + c%64
+ *   off_v_codes  u8 [D/8][2][8][64]    token t, channel c: byte (c/8) 1024 +
+ *                                      (t/64) 512 + (c%8) 64 + t%64
+ *   off_k_scale  f32 [8]               scale of K tokens [16 i, 16 i + 16)
+ *   off_v_scale  f32 [8]               the same for V; then 64 zero bytes
+ * (a block of more than 16 tokens repeats its scale, so that a reader does not
+ * need block_tokens).
+ */
+#define KVARN_LAYOUT8_VERSION 1
+#define KVARN_CODE8_I8 0
+#define KVARN_CODE8_E4M3 1
+
+typedef struct kvarn_layout8 {
+  int32_t version;      /* KVARN_LAYOUT8_VERSION            */
+  int32_t head_dim;     /* D                                */
+  int32_t tile_tokens;  /* 128                              */
+  int32_t code_format;  /* KVARN_CODE8_*                    */
+  int32_t block_tokens; /* tokens that share a scale        */
+  int32_t reserved;     /* 0                                */
+  int64_t record_bytes; /* 256 D + 128                      */
+  int64_t off_k_codes, off_v_codes, off_k_scale, off_v_scale;
+} kvarn_layout8_t;
+
+/* Fills *out (host pointer). KVARN_ERR_UNSUPPORTED for head dims other than 64,
+ * 128 and 256, other formats, or block_tokens other than 16, 32, 64 and 128. */
+int kvarn_layout8(int head_dim, int code_format, int block_tokens, kvarn_layout8_t* out);
+
+/*
+ * Element type of the queries and the outputs of the 8-bit cache's attention
+ * calls. KVARN_IO_F32 keeps about 22 bits of every operand. With the 16-bit
+ * types the queries enter the products exactly (bf16: down to 2^-25 of the
+ * row's largest) and the output is rounded once.
+ */
+#define KVARN_IO_F32 0
+#define KVARN_IO_F16 1
+#define KVARN_IO_BF16 2
+
+/*
+ * Tile compression to 8 bits: unit u turns 128 consecutive raw K rows and the
+ * matching V rows into one record. Arguments, bounds and refusals as in
+ * kvarn_compress_tile (rows from src_row0[u], record at dst_record[u]).
+ */
+int kvarn_compress_tile8(const float* k_raw, const float* v_raw, int64_t row_stride,
+                         int64_t n_rows, const int64_t* src_row0, uint8_t* tiles,
+                         int64_t tiles_bytes, const int64_t* dst_record, int64_t n_units,
+                         const kvarn_layout8_t* layout, kvarn_stream_t stream);
+
+/*
+ * The inverse: unit u writes the 128 K and V rows (code * scale, fp32) of the
+ * record at src_record[u] to rows dst_row0[u] .. + 127 of k_out and v_out, for
+ * callers that hand tiles on in another form. Columns past D of a row and rows
+ * of no unit are left as they are. Units' rows must not overlap. A
+ * unit whose rows do not lie inside [0, n_rows) is skipped, one whose record is
+ * not inside the pool (or not 16-byte aligned) writes NaN rows; both set
+ * KVARN_DEVERR_RECORD.
+ */
+int kvarn_expand_tile8(const uint8_t* tiles, int64_t tiles_bytes, const int64_t* src_record,
+                       float* k_out, float* v_out, int64_t row_stride, int64_t n_rows,
+                       const int64_t* dst_row0, int64_t n_units, const kvarn_layout8_t* layout,
+                       kvarn_stream_t stream);
+
+/*
+ * Decode attention over the 8-bit cache: as kvarn_decode_attention, over records
+ * of a kvarn_layout8_t, with queries and outputs of type io_type
+ * ([B][Hq][D], 16-byte aligned), and with the attention weight of each tile on
+ * request:
+ *   mass_out : fp32 [B][Hkv][max_tiles] or NULL. mass_out[b][h][i] =
+ *              mass_in[b][h][i] + the softmax weights that the G query heads of
+ *              KV head h give to the 128 tokens of tile i, summed (the window's
+ *              tokens are weighed in the softmax but not recorded). Entries at
+ *              or past n_tiles[b] are copied from mass_in.
+ *   mass_in  : the same shape; may be mass_out itself (accumulate in place);
+ *              NULL counts as zeros. Must be NULL when mass_out is.
+ * tile_table entries are multiples of 16. An entry that is misaligned, negative or
+ * runs past tiles_bytes makes that head's output and masses NaN and sets
+ * KVARN_DEVERR_RECORD. A head with no tokens at all gets zeros. A NaN or an
+ * infinity in a cached row, or in a query, makes the rows that see it NaN.
+ * The grids depend only on the sizes, so the call can be captured in a CUDA graph;
+ * results are deterministic. launch_flags as in kvarn_decode_attention.
+ *   ws       : at least kvarn_decode8_workspace_bytes() bytes, 256-byte aligned,
+ *              no initialisation. Calls sharing ws must not overlap.
+ */
+int kvarn_decode8_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int max_tiles,
+                                  int win_capacity, size_t* bytes);
+int kvarn_decode_attention8(const void* q, int io_type, const uint8_t* tiles, int64_t tiles_bytes,
+                            const int64_t* tile_table, const int32_t* n_tiles, const float* win_k,
+                            const float* win_v, const int32_t* win_start, const int32_t* win_len,
+                            int win_capacity, int B, int Hq, int Hkv, int head_dim, int max_tiles,
+                            float softmax_scale, const kvarn_layout8_t* layout,
+                            const float* mass_in, float* mass_out, void* ws, size_t ws_bytes,
+                            void* out, unsigned launch_flags, kvarn_stream_t stream);
+
+/*
+ * Chunked-prefill attention over the 8-bit cache: the result that
+ * kvarn_prefill_attention defines (same positions, window and causal rule), over
+ * records of a kvarn_layout8_t, with queries and outputs [C][Hq][D] of type
+ * io_type. A row that sees a NaN or an infinity in a cached K or V row is NaN;
+ * rows before it are not touched by it. tile_table entries are multiples of 16; one
+ * outside the pool makes the rows that see it NaN and sets KVARN_DEVERR_RECORD.
+ *   ws       : at least kvarn_prefill8_workspace_bytes(C, n_tiles, win_len, Hq, Hkv,
+ *              head_dim) bytes, 256-byte aligned, no initialisation. Calls
+ *              sharing ws must not overlap.
+ * After tiles were evicted (kvarn_evict_tiles) positions count the cached tokens
+ * that are left: pos0 = 128 n_tiles + win_len - C for the newest C tokens.
+ */
+int kvarn_prefill8_workspace_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int head_dim,
+                                   size_t* bytes);
+int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t pos0,
+                             const uint8_t* tiles, int64_t tiles_bytes, const int64_t* tile_table,
+                             int table_stride, int n_tiles, const float* win_k, const float* win_v,
+                             int win_start, int win_len, int win_capacity, int Hq, int Hkv,
+                             int head_dim, float softmax_scale, const kvarn_layout8_t* layout,
+                             void* ws, size_t ws_bytes, void* out, kvarn_stream_t stream);
+
+/*
+ * Eviction of whole tiles by accumulated attention weight. For each KV head of each
+ * sequence with n_tiles[b] > keep, `keep` tiles stay: the first `sinks`, the last
+ * `recent`, and of those between the keep - sinks - recent with the largest
+ * weights (of equal weights the lower index; NaN counts as infinite, -0 as 0). Every
+ * KV head loses the same number of tiles, its own choice of them. Works on the
+ * tile tables of both caches; the records themselves are not touched.
+ *   tile_table : int64 [B][Hkv][max_tiles]; tile_mass: fp32, the same shape.
+ *   n_tiles    : int32 [B] (clamped to 0..max_tiles).
+ *   table_out, mass_out : the same shapes: the tiles that stay, in their old order,
+ *                then -1 (mass: 0). May be tile_table and tile_mass themselves.
+ *   n_tiles_out: int32 [B], min(n_tiles[b], keep). May be n_tiles itself.
+ *   evicted    : int64 [B][Hkv][max_tiles] or NULL: the offsets that left, in their
+ *                old order, then -1. Must not overlap the other arrays.
+ *   keep       : >= 1, sinks and recent >= 0, sinks + recent <= keep.
+ * One launch, deterministic, no workspace; can be captured. After it, tile i no longer
+ * holds positions [128 i, 128 i + 128): see kvarn_prefill_attention8.
+ * launch_flags: 0 or KVARN_LAUNCH_PDL.
+ */
+int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const int32_t* n_tiles,
+                      int64_t* table_out, float* mass_out, int32_t* n_tiles_out, int64_t* evicted,
+                      int B, int Hkv, int max_tiles, int keep, int sinks, int recent,
+                      unsigned launch_flags, kvarn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

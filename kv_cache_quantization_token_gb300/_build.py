@@ -20,9 +20,12 @@ UNITS = [("kvarn_abi.cu", "kvarn_abi.o", []), ("compress.cu", "compress.o", []),
          ("decode.cu", "decode_sb2_v4.o", ["-DKVARN_BUILD_SCALE_BYTES=2", "-DKVARN_BUILD_V_BITS=4"]),
          ("decode.cu", "decode_v3.o", ["-DKVARN_BUILD_V_BITS=3"]),
          ("decode.cu", "decode_sb2_v3.o", ["-DKVARN_BUILD_SCALE_BYTES=2", "-DKVARN_BUILD_V_BITS=3"]),
-         ("decode_noalloc.cu", "decode_noalloc.o", []), ("prefill.cu", "prefill.o", [])]
+         ("decode_noalloc.cu", "decode_noalloc.o", []), ("prefill.cu", "prefill.o", []),
+         ("kvarn8_abi.cu", "kvarn8_abi.o", []), ("compress8.cu", "compress8.o", []),
+         ("decode8.cu", "decode8.o", []), ("prefill8.cu", "prefill8.o", []), ("evict.cu", "evict.o", [])]
 SOURCES = sorted({u[0] for u in UNITS})
-HEADERS = [os.path.join(CSRC, "kvarn_common.cuh"), os.path.join(ROOT, "include", "kvarn.h")]
+HEADERS = [os.path.join(CSRC, h) for h in ("kvarn_common.cuh", "cache8.cuh", "tcgen05.cuh")] + [
+    os.path.join(ROOT, "include", "kvarn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

@@ -1,0 +1,545 @@
+// decode8.cu -- single-token attention over 8-bit tile records and the FP32 window.
+//
+//   split kernel   grid (item, KV head, sequence). A tile item owns `span` consecutive
+//                  tiles of one KV head; a window item owns a run of window rows. It
+//                  writes the item's softmax maximum m, sum l and value accumulator
+//                  (in units of 2^m) to the workspace.
+//   merge kernel   grid (query head | KV head and run of tiles, sequence): joins the
+//                  items of a head, sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i, and,
+//                  on request, adds each tile's weight over the heads of its group.
+//
+// All G <= 8 query heads of a KV head share one pass over its records. Both products
+// run on mma.sync m16n8k16 (fp16 in, fp32 out) with the codes as the B operand: a code
+// is exact in fp16, so only the other operand is split. The query rows, scaled by a
+// power of two each, and the weighted probabilities enter as pairs hi + lo (22 bits) in
+// the 16 rows of A: head g's hi part in row g and its lo part in row g + 8. The two
+// parts of a result then lie in registers of one lane and are added there, and the
+// accumulator layout of the scores is a permutation of the A layout of the second product.
+//   s_t = (q . code_t) * (kscale_t scale),   O += (2^(s_t - m) vscale_t) code_t
+// A scale is constant over 16 tokens, so it multiplies scores and probabilities, never codes.
+// The weighted probabilities have a reference exponent u of their own (their running
+// maximum), so that any ratio between the value scales keeps its 22 bits.
+//
+// Records arrive by bulk copies, kStages of them in flight per CTA. Their code order is
+// made for this kernel: a warp's 16-byte reads cover 512 consecutive bytes, and what a
+// lane reads is what it needs of the B fragments of four products, up to an order of the
+// summed index (channels, or tokens) that both operands share.
+//
+// A CTA's warps split a tile's tokens for the scores and its channels for the values,
+// with one exchange of row maxima and one of probabilities per tile through shared memory.
+#include "cache8.cuh"
+
+namespace kvarn {
+namespace {
+
+constexpr float kNone = -3.0e38f;  // reference exponent before the first tile
+constexpr int kStages = 3;
+constexpr int kPRow = 576;          // bytes per head of the probability buffer (4 bytes x 2 parts x 64 pairs + pad)
+constexpr float kHead = 14.f;       // weighted probabilities reach 2^14: lo parts stay normal fp16 numbers
+
+template <int D_>
+struct D8 {
+  static constexpr int D = D_;
+  static constexpr int NW = D == 256 ? 16 : 8;   // warps per CTA
+  static constexpr int NTHR = 32 * NW;
+  static constexpr int NT = 16 / NW;             // 8-token column tiles of the scores per warp
+  static constexpr int NC = D / 8 / NW;          // 8-channel column tiles of the values per warp
+  static constexpr int NJ = D / 64;              // 64-channel runs
+  static constexpr int SLOT = Rec8<D>::kBytes;
+  static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 2 : 1;  // resident per SM
+  static constexpr int WROWS = 8 * NW;           // window rows per window item
+  static constexpr int OFF_P = kStages * SLOT;
+  static constexpr int OFF_MX = OFF_P + 8 * kPRow;              // float2 [8][NW]: (max s, max s + log2 vscale)
+  static constexpr int OFF_L = OFF_MX + 8 * NW * 8;             // float [NW][8]
+  static constexpr int OFF_BAR = OFF_L + 8 * NW * 4;
+  static constexpr int OFF_FLG = OFF_BAR + 8 * kStages;         // int: a wait ran out or a record was refused
+  static constexpr int SMEM = (OFF_FLG + 8 + 127) / 128 * 128;
+  static_assert(SLOT % 128 == 0 && OFF_P % 128 == 0, "alignment");
+  static_assert(8 * (WROWS + 4) * 4 <= 8 * kPRow, "window probabilities fit");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo with hi a tf32 number; lo keeps the rest (tf32 reads its top 11 bits).
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, shfl_xor(v, 1));
+  return fmaxf(v, shfl_xor(v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += shfl_xor(v, 1);
+  return v + shfl_xor(v, 2);
+}
+
+// Sum over the CTA's warps of a quad-reduced row value l of head g (lanes with q == 0 hold it).
+template <int NW>
+__device__ __forceinline__ float cta_row_sum(float l, float* buf, int warp, int g, int q) {
+  __syncthreads();
+  if (q == 0) buf[warp * 8 + g] = l;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) s += buf[w * 8 + g];
+  return s;
+}
+
+struct Split8Args {
+  Decode8Args a;
+  float2* ml;      // [B][Hq][items]
+  float* acc;      // [B][Hq][items][D]
+  float2* tile_ml; // [B][Hkv][max_tiles][8], or NULL
+  int span, tile_items, items;
+};
+
+// A run of window rows: fp32 rows against fp32 queries and probabilities, every operand a
+// pair of tf32 numbers.
+template <int D>
+__device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* smem, int item, int kvh,
+                                            int b, int64_t part) {
+  using C = D8<D>;
+  const Decode8Args& a = s.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  float* P = reinterpret_cast<float*>(smem + C::OFF_P);
+  float2* mx = reinterpret_cast<float2*>(smem + C::OFF_MX);
+  constexpr int PS = C::WROWS + 4;
+  const int wlen = min(max(a.win_len[b], 0), a.win_cap);
+  const int r0 = C::WROWS * (item - s.tile_items);
+  const int n = min(C::WROWS, wlen - r0);
+  pdl_trigger();
+  if (n <= 0) {
+    if (tid < a.G) s.ml[part + (int64_t)tid * s.items] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  const int start = ((a.win_start[b] % a.win_cap) + a.win_cap) % a.win_cap;
+  const int64_t head = ((int64_t)b * a.Hkv + kvh) * a.win_cap;
+  auto row = [&](int t) { return (head + (start + r0 + t) % a.win_cap) * (int64_t)D; };
+  // the values this warp's channels need, under way while the scores are formed
+  float v[C::NW][C::NC][2];
+#pragma unroll
+  for (int k = 0; k < C::NW; ++k) {
+    const int t0 = 8 * k + q, t1 = t0 + 4;
+    const float* v0 = a.win_v + (t0 < n ? row(t0) : 0) + 8 * C::NC * warp + g;
+    const float* v1 = a.win_v + (t1 < n ? row(t1) : 0) + 8 * C::NC * warp + g;
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c) {
+      v[k][c][0] = t0 < n ? v0[8 * c] : 0.f;
+      v[k][c][1] = t1 < n ? v1[8 * c] : 0.f;
+    }
+  }
+  const bool have = 8 * warp + g < n;
+  const float* kr = a.win_k + (have ? row(8 * warp + g) : 0) + 4 * q;
+  const int64_t qrow = ((int64_t)b * a.Hq + (int64_t)kvh * a.G + min(g, a.G - 1)) * D + 4 * q;
+  float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int m = 0; m < D / 16; ++m) {
+    const float4 kx = have ? *reinterpret_cast<const float4*>(kr + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 qx = g < a.G ? io_ld4(a.q, a.io, qrow + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t qa[4], kh[2], kl[2];
+      split_tf32(h ? qx.z : qx.x, qa[0], qa[1]);
+      split_tf32(h ? qx.w : qx.y, qa[2], qa[3]);
+      split_tf32(h ? kx.z : kx.x, kh[0], kl[0]);
+      split_tf32(h ? kx.w : kx.y, kh[1], kl[1]);
+      mma_tf32(sc, qa, kh[0], kh[1]);
+      mma_tf32(sc, qa, kl[0], kl[1]);
+    }
+  }
+  const int t0 = 8 * warp + 2 * q;
+  const float s0 = t0 < n ? (sc[0] + sc[2]) * a.scale : -INFINITY;
+  const float s1 = t0 + 1 < n ? (sc[1] + sc[3]) * a.scale : -INFINITY;
+  const float mw = quad_max(fmaxf(s0, s1));
+  if (q == 0) mx[g * C::NW + warp].x = mw;
+  __syncthreads();
+  float M = kNone;
+#pragma unroll
+  for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mx[g * C::NW + w].x);
+  const float p0 = t0 < n ? fast_ex2(s0 - M) : 0.f, p1 = t0 + 1 < n ? fast_ex2(s1 - M) : 0.f;
+  *reinterpret_cast<float2*>(P + g * PS + t0) = make_float2(p0, p1);
+  const float l = cta_row_sum<C::NW>(quad_sum(p0 + p1), reinterpret_cast<float*>(smem + C::OFF_L), warp, g, q);
+  float o[C::NC][4] = {};
+#pragma unroll
+  for (int k = 0; k < C::NW; ++k) {
+    uint32_t pa[4];
+    split_tf32(P[g * PS + 8 * k + q], pa[0], pa[1]);
+    split_tf32(P[g * PS + 8 * k + q + 4], pa[2], pa[3]);
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c) {
+      uint32_t vh[2], vl[2];
+      split_tf32(v[k][c][0], vh[0], vl[0]);
+      split_tf32(v[k][c][1], vh[1], vl[1]);
+      mma_tf32(o[c], pa, vh[0], vh[1]);
+      mma_tf32(o[c], pa, vl[0], vl[1]);
+    }
+  }
+  if (g < a.G) {
+    float* dst = s.acc + (part + (int64_t)g * s.items) * D + 8 * C::NC * warp + 2 * q;
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c)
+      *reinterpret_cast<float2*>(dst + 8 * c) = make_float2(o[c][0] + o[c][2], o[c][1] + o[c][3]);
+    if (warp == 0 && q == 0) s.ml[part + (int64_t)g * s.items] = make_float2(M, l);
+  }
+}
+
+template <int D, int F>
+__global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const Split8Args s) {
+  using C = D8<D>;
+  using R = Rec8<D>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const Decode8Args& a = s.a;
+  const int item = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int64_t part = ((int64_t)b * a.Hq + (int64_t)kvh * a.G) * s.items + item;
+  if (item >= s.tile_items) {
+    pdl_wait();
+    window_item<D>(s, smem, item, kvh, b, part);
+    return;
+  }
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  volatile int* flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLG);
+  // with prefetch, the records (which, by the caller's guarantee, nothing still running
+  // writes) are requested before the previous kernel on the stream is waited for
+  const bool early = a.flags & KVARN_LAUNCH_PREFETCH;
+  if (!early) pdl_wait();
+  const int first = item * s.span;
+  const int nt = min(max(min(max(a.n_tiles[b], 0), a.max_tiles) - first, 0), s.span);
+  if (nt == 0) {
+    if (early) pdl_wait();
+    pdl_trigger();
+    if (tid < a.G) s.ml[part + (int64_t)tid * s.items] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  const int64_t* table = a.tile_table + ((int64_t)b * a.Hkv + kvh) * a.max_tiles + first;
+  auto request = [&](int i) {  // one thread: tile i of the item into its stage
+    uint64_t* br = bar + i % kStages;
+    const int64_t off = table[i];
+    if ((off & 15) || off < 0 || off > a.tiles_bytes - R::kBytes) {
+      report(a.err, KVARN_DEVERR_RECORD);
+      *flag = 1;
+      mbar_arrive1(br);
+      return;
+    }
+    mbar_arrive_tx(br, R::kBytes);
+    bulk_in(smem + (i % kStages) * C::SLOT, a.tiles + off, R::kBytes, br);
+  };
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init_n(bar + i, 1);
+    mbar_fence_init();
+    *flag = 0;
+    for (int i = 0; i < min(nt, kStages); ++i) request(i);
+  }
+  if (early) pdl_wait();
+  pdl_trigger();
+
+  // A fragments of the query: head g's row, channels 64 j + 16 q + 4 r + {0, 1} and {2, 3}
+  // of product (j, r); hi in the registers of row g, lo in those of row g + 8
+  uint32_t qa[4 * C::NJ][4];
+  float c1;
+  {
+    float x[C::NJ][16];
+    const int64_t qrow = ((int64_t)b * a.Hq + (int64_t)kvh * a.G + min(g, a.G - 1)) * D + 16 * q;
+    float mxq = 0.f;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 v = g < a.G ? io_ld4(a.q, a.io, qrow + 64 * j + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[j][4 * r] = v.x; x[j][4 * r + 1] = v.y; x[j][4 * r + 2] = v.z; x[j][4 * r + 3] = v.w;
+        mxq = fmaxf(fmaxf(mxq, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+      }
+    const float p2 = pow2_to(quad_max(mxq), 10);
+    c1 = a.scale * pow2_inverse(p2);
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        split_pair(x[j][4 * r] * p2, x[j][4 * r + 1] * p2, qa[4 * j + r][0], qa[4 * j + r][1]);
+        split_pair(x[j][4 * r + 2] * p2, x[j][4 * r + 3] * p2, qa[4 * j + r][2], qa[4 * j + r][3]);
+      }
+  }
+  float2* mx = reinterpret_cast<float2*>(smem + C::OFF_MX);
+  float* lbuf = reinterpret_cast<float*>(smem + C::OFF_L);
+  unsigned char* P = smem + C::OFF_P;
+  __syncthreads();  // barriers initialised
+
+  float M = kNone, U = kNone, l = 0.f;
+  float o[C::NC][4] = {};
+  float sc[C::NT][2];
+  float vs = 0.f;
+  bool ok = true;
+  const int grp = (warp * C::NT) >> 1;  // scale entry of this warp's tokens
+
+  auto scores = [&](int i) {  // scores of tile i's tokens 8 NT warp .., and their row maxima
+    ok &= mbar_wait_timed(bar + i % kStages, (uint32_t)(i / kStages) & 1u, a.err, KVARN_DEVERR_WAIT);
+    const unsigned char* rec = smem + (i % kStages) * C::SLOT;
+    const float kc = reinterpret_cast<const float*>(rec + R::kKScale)[grp] * c1;
+    vs = reinterpret_cast<const float*>(rec + R::kVScale)[grp];
+    float mw = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4*>(rec + R::kKCodes +
+                                                        ((warp * C::NT + t) * C::NJ + j) * 512 + lane * 16);
+        uint32_t b0, b1;
+        codes_to_half<F>(w.x, b0, b1); mma_f16(c, qa[4 * j], b0, b1);
+        codes_to_half<F>(w.y, b0, b1); mma_f16(c, qa[4 * j + 1], b0, b1);
+        codes_to_half<F>(w.z, b0, b1); mma_f16(c, qa[4 * j + 2], b0, b1);
+        codes_to_half<F>(w.w, b0, b1); mma_f16(c, qa[4 * j + 3], b0, b1);
+      }
+      sc[t][0] = (c[0] + c[2]) * kc;
+      sc[t][1] = (c[1] + c[3]) * kc;
+      mw = fmaxf(mw, fmaxf(sc[t][0], sc[t][1]));
+    }
+    mw = quad_max(mw);
+    if (q == 0) mx[g * C::NW + warp] = make_float2(mw, mw + fast_lg2(vs));
+  };
+
+  scores(0);
+  for (int i = 0; i < nt; ++i) {
+    __syncthreads();  // row maxima of tile i are in; tile i - 1 and its probabilities are used up
+    if (tid == 0 && i > 0 && i - 1 + kStages < nt) request(i - 1 + kStages);
+    float Mn = M, Un = U;
+#pragma unroll
+    for (int w = 0; w < C::NW; w += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(mx + g * C::NW + w);
+      Mn = fmaxf(Mn, fmaxf(v.x, v.z));
+      Un = fmaxf(Un, fmaxf(v.y, v.w));
+    }
+    const float al = fast_ex2(M - Mn), ao = fast_ex2(U - Un);
+    const bool moved = Un != U;
+    M = Mn;
+    U = Un;
+    // weight of a value code: probability * scale, in units of 2^(U - kHead); a factor past the
+    // range belongs to probabilities below 2^-100
+    float fw = vs * fast_ex2(fminf(M - U + kHead, 126.f));
+    if (fw > 1e30f) fw = 1e30f;
+    float lt = 0.f;
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t) {
+      const float p0 = fast_ex2(sc[t][0] - M), p1 = fast_ex2(sc[t][1] - M);
+      lt += p0 + p1;
+      uint32_t hi, lo;
+      split_pair(p0 * fw, p1 * fw, hi, lo);
+      // tokens 8 n + 2 q, + 1 in the order the second product's A fragments are read
+      const int n = warp * C::NT + t;
+      *reinterpret_cast<uint2*>(P + g * kPRow + (((n >> 3) * 4 + 2 * (n & 1) + (q >> 1)) * 4 + ((n & 7) >> 1)) * 16 +
+                                (q & 1) * 8) = make_uint2(hi, lo);
+    }
+    l = fmaf(l, al, lt);
+    if (s.tile_ml) {
+      lt = quad_sum(lt);
+      if (q == 0) lbuf[warp * 8 + g] = lt;
+    }
+    __syncthreads();  // probabilities of tile i are in
+    if (s.tile_ml && warp == 0 && q == 0) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) t += lbuf[w * 8 + g];
+      s.tile_ml[(((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + i) * 8 + g] = make_float2(M, t);
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[c][r] *= ao;
+    }
+    const unsigned char* V = smem + (i % kStages) * C::SLOT + R::kVCodes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 w[C::NC];
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c)
+        w[c] = *reinterpret_cast<const uint4*>(V + ((warp * C::NC + c) * 2 + h) * 512 + lane * 16);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint4 f = *reinterpret_cast<const uint4*>(P + g * kPRow + ((h * 4 + r) * 4 + q) * 16);
+        const uint32_t pa[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+          uint32_t b0, b1;
+          codes_to_half<F>((&w[c].x)[r], b0, b1);
+          mma_f16(o[c], pa, b0, b1);
+        }
+      }
+    }
+    if (i + 1 < nt) scores(i + 1);
+  }
+  if (!ok) *flag = 1;
+  l = cta_row_sum<C::NW>(quad_sum(l), lbuf, warp, g, q);  // its barriers also publish the flag
+  const bool bad = *flag != 0;
+  if (g < a.G) {
+    const float f = fast_ex2(U - kHead - M);
+    float* dst = s.acc + (part + (int64_t)g * s.items) * D + 8 * C::NC * warp + 2 * q;
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c)
+      *reinterpret_cast<float2*>(dst + 8 * c) = make_float2((o[c][0] + o[c][2]) * f, (o[c][1] + o[c][3]) * f);
+    if (warp == 0 && q == 0)
+      s.ml[part + (int64_t)g * s.items] = bad ? make_float2(0.f, NAN) : make_float2(M, l);
+  }
+}
+
+// Joins the items of query head blockIdx.x (blockIdx.x < Hq), or adds up the weights of 256 tiles
+// of a KV head.
+template <int D>
+__global__ void __launch_bounds__(256) merge8_kernel(const Split8Args s, int mass_blocks) {
+  const Decode8Args& a = s.a;
+  __shared__ __align__(16) float4 part_s[256];
+  __shared__ float red[2][8];
+  __shared__ float2 stat[8];
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  if ((int)blockIdx.x >= a.Hq) {
+    const int kvh = ((int)blockIdx.x - a.Hq) / mass_blocks, run = ((int)blockIdx.x - a.Hq) % mass_blocks;
+    if (warp < a.G) {  // (maximum, sum) of query head `warp` of the group
+      const float2* ml = s.ml + ((int64_t)b * a.Hq + kvh * a.G + warp) * s.items;
+      float M = -INFINITY, L = 0.f;
+      for (int i = lane; i < s.items; i += 32) M = fmaxf(M, ml[i].x);
+      for (int m = 16; m; m >>= 1) M = fmaxf(M, shfl_xor(M, m));
+      for (int i = lane; i < s.items; i += 32)
+        if (ml[i].y != 0.f) L += fast_ex2(ml[i].x - M) * ml[i].y;
+      for (int m = 16; m; m >>= 1) L += shfl_xor(L, m);
+      if (lane == 0) stat[warp] = make_float2(M, 1.f / L);
+    }
+    __syncthreads();
+    const int i = 256 * run + tid;
+    if (i < a.max_tiles) {
+      const int64_t at = ((int64_t)b * a.Hkv + kvh) * a.max_tiles + i;
+      float w = a.mass_in ? a.mass_in[at] : 0.f;
+      if (i < min(a.n_tiles[b], a.max_tiles)) {
+        float sum = 0.f;
+        for (int h = 0; h < a.G; ++h) {
+          const float2 t = s.tile_ml[at * 8 + h];
+          sum += fast_ex2(t.x - stat[h].x) * t.y * stat[h].y;
+        }
+        w += sum;
+      }
+      a.mass_out[at] = w;
+    }
+    return;
+  }
+  const int h = blockIdx.x;
+  const int64_t base = ((int64_t)b * a.Hq + h) * s.items;
+  const float2* ml = s.ml + base;
+  float M = -INFINITY;
+  for (int i = tid; i < s.items; i += 256) M = fmaxf(M, ml[i].x);
+  for (int m = 16; m; m >>= 1) M = fmaxf(M, shfl_xor(M, m));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, red[0][w]);
+  float L = 0.f;
+  for (int i = tid; i < s.items; i += 256) {
+    const float2 v = ml[i];
+    if (v.y != 0.f) L += fast_ex2(v.x - M) * v.y;
+  }
+  for (int m = 16; m; m >>= 1) L += shfl_xor(L, m);
+  if (lane == 0) red[1][warp] = L;
+  constexpr int COLS = D / 4, PARTS = 256 / COLS;
+  const int col = tid % COLS, pt = tid / COLS;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = pt; i < s.items; i += PARTS) {
+    const float2 v = ml[i];
+    if (v.y != 0.f) {  // an empty item wrote no accumulator
+      const float w = fast_ex2(v.x - M);
+      const float4 x = *reinterpret_cast<const float4*>(s.acc + (base + i) * D + 4 * col);
+      acc.x = fmaf(w, x.x, acc.x); acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z); acc.w = fmaf(w, x.w, acc.w);
+    }
+  }
+  part_s[tid] = acc;
+  __syncthreads();
+  if (tid < COLS) {
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) L += red[1][w];
+    for (int p = 1; p < PARTS; ++p) {
+      const float4 x = part_s[p * COLS + tid];
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    io_st4(a.out, a.io, ((int64_t)b * a.Hq + h) * D + 4 * tid,
+           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  }
+}
+
+template <int D, int F>
+cudaError_t launch_d8(const Decode8Plan& p, const Decode8Args& a, void* ws, cudaStream_t st) {
+  using C = D8<D>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    e = cudaFuncSetAttribute(split8_kernel<D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  Split8Args s;
+  s.a = a;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  s.ml = reinterpret_cast<float2*>(w);
+  s.acc = reinterpret_cast<float*>(w + p.off_acc);
+  s.tile_ml = a.mass_out ? reinterpret_cast<float2*>(w + p.off_tile) : nullptr;
+  s.span = p.span;
+  s.tile_items = p.tile_items;
+  s.items = p.items;
+  if (p.items > 0) {
+    LaunchCfg L(dim3(p.items, a.Hkv, a.B), dim3(C::NTHR), C::SMEM, st, a.flags);
+    e = cudaLaunchKernelEx(&L.cfg, split8_kernel<D, F>, s);
+    if (e != cudaSuccess) return e;
+  }
+  const int mass_blocks = a.mass_out ? (a.max_tiles + 255) / 256 : 0;
+  // the merge waits for the split kernel on the device, whatever the caller's flags
+  LaunchCfg L(dim3(a.Hq + a.Hkv * mass_blocks, a.B), dim3(256), 0, st, a.flags | KVARN_LAUNCH_PDL);
+  return cudaLaunchKernelEx(&L.cfg, merge8_kernel<D>, s, mass_blocks);
+}
+
+}  // namespace
+
+void decode8_plan(int B, int Hq, int Hkv, int D, int max_tiles, int win_capacity, Decode8Plan* p) {
+  const int ctas = D == 64 ? D8<64>::CTAS : D == 128 ? D8<128>::CTAS : D8<256>::CTAS;
+  const int64_t slots = (int64_t)sm_count() * ctas;
+  const int64_t work = (int64_t)B * Hkv * max_tiles;
+  int64_t span = (work + slots - 1) / slots;
+  p->span = (int)(span < 1 ? 1 : span > 16 ? 16 : span);
+  p->tile_items = (max_tiles + p->span - 1) / p->span;
+  p->win_rows = D == 256 ? D8<256>::WROWS : D8<128>::WROWS;
+  p->items = p->tile_items + (win_capacity + p->win_rows - 1) / p->win_rows;
+  const size_t rows = (size_t)B * Hq * p->items;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  p->off_acc = up(rows * sizeof(float2));
+  p->off_tile = p->off_acc + up(rows * D * sizeof(float));
+  p->ws_bytes = p->off_tile + up((size_t)B * Hkv * max_tiles * 8 * sizeof(float2));
+}
+
+cudaError_t launch_decode8(const Decode8Plan& p, const Decode8Args& a, void* ws, cudaStream_t st) {
+  const bool e = a.format == KVARN_CODE8_E4M3;
+  switch (a.D) {
+    case 64: return e ? launch_d8<64, 1>(p, a, ws, st) : launch_d8<64, 0>(p, a, ws, st);
+    case 128: return e ? launch_d8<128, 1>(p, a, ws, st) : launch_d8<128, 0>(p, a, ws, st);
+    case 256: return e ? launch_d8<256, 1>(p, a, ws, st) : launch_d8<256, 0>(p, a, ws, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace kvarn

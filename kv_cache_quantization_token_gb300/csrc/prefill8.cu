@@ -1,0 +1,671 @@
+// prefill8.cu -- causal attention of a chunk of query positions over 8-bit tile records and the
+// FP32 window, on tcgen05 tensor cores.
+//
+//   out[i][h] = sum_j softmax_j(scale q[i][h] . k_j) v_j over keys j with position(j) <= pos0 + i
+//
+//   image kernel      one CTA per (128-key block, KV head): codes, exact in fp16, or window rows as
+//                     fp16 pairs hi + lo scaled by a power of two per 16 rows, as operand images
+//                     K [key][channel] and V^T [channel][key] in the 128-byte-swizzled K-major layout
+//                     the tensor cores read, plus the scales of each 16-token group.
+//   attention kernel  one CTA per KV head, 128 score rows (the G heads of the group x 128 / G
+//                     positions) and, when there are few rows, a share of the keys. 8 softmax warps,
+//                     an MMA warp, and a copy warp for each of K and V.
+//   merge kernel      joins the key shares, when there are several.
+//
+// A scale is constant over 16 keys, so it multiplies scores and probabilities and the codes are used as
+// they are: S = Q K^T with the query rows scaled by a power of two, then per group of 16 keys
+//   p = 2^(S kscale c - m),  l += p,  w = p vscale 2^(m - u),  O += w V
+// with running references m (scores) and u (weighted scores), both moved only when exceeded by several
+// powers of two, so that O is rarely rescaled.
+// Precision: fp32 queries and their probabilities are pairs hi + lo of fp16 (22 bits), two products per
+// code operand. 16-bit queries are exact in one fp16 operand, and then w is rounded to fp16 once (2^-12
+// relative, a quarter or less of the rounding of the output): one product. Window rows are always pairs.
+// The query and w are read from tensor memory (the A operand), so shared memory feeds B operands only; at
+// head_dim 256 the lo part of the query lives in shared memory.
+//
+// A cached row with a NaN or an infinity gets a NaN key and a zero value in the images: a score row that
+// sees it becomes NaN, one that does not is untouched (0 x NaN never enters the value product).
+// Every wait is bounded; a CTA that gives up writes NaN rows, frees its TMEM and returns.
+#include <math.h>
+
+#include "cache8.cuh"
+#include "tcgen05.cuh"
+
+namespace kvarn {
+namespace {
+
+constexpr float kHead = 8.f;  // w is about 2^8: lo parts of fp16 pairs stay normal
+constexpr float kLag = 7.f;   // references move when exceeded by this power of two
+
+template <int D, int NP>
+struct PC8 {
+  static constexpr int KB = D == 256 ? 64 : 128;  // keys of a block
+  static constexpr int SUB = kTile / KB;          // blocks of a tile
+  static constexpr int IMG = KB * D * 2;          // bytes of an operand image
+  static constexpr int NGB = KB / kGrp;           // scale groups of a block
+  static constexpr bool QL_SMEM = D == 256 && NP == 2;
+  static constexpr int NK = D == 64 ? 4 : QL_SMEM ? 2 : 3;  // image slots of the K and of the V ring
+  static constexpr int NV = NK;
+  static constexpr int QL_BYTES = QL_SMEM ? 128 * D * 2 : 0;
+  static constexpr int OFF_K = QL_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * IMG;
+  static constexpr int OFF_BAR = OFF_V + NV * IMG;
+  static constexpr int OFF_X = OFF_BAR + 256;              // float2 [2][2][128] row-maximum exchange
+  static constexpr int OFF_XB = OFF_X + 2 * 2 * 128 * 8;   // int [2][8] stop flags
+  static constexpr int OFF_MISC = OFF_XB + 64;
+  static constexpr int SMEM = OFF_MISC + 64 + 1024;        // + slack to align the base to 1024
+  // tensor memory columns
+  static constexpr int T_QH = 0;
+  [[maybe_unused]] static constexpr int T_QL = D / 2;
+  static constexpr int T_S = D == 256 ? 128 : D / 2 * NP;
+  static constexpr int T_O = T_S + 2 * KB;
+  static constexpr int TMEM = 512;
+  static_assert(T_O + D <= TMEM && SMEM <= 227 * 1024, "TMEM and shared memory");
+};
+constexpr int kThreads = 352;  // 8 softmax warps, MMA, K copies, V copies
+
+// Workspace of a call: images [Hkv][blocks] of 2 (tiles) or 4 (window) operands, the groups'
+// scales, and the key shares' partial results.
+struct Plan8 {
+  int n_tsub, n_wsub;     // blocks of visible tiles and window rows
+  int row_blocks, shares;
+  int64_t head_imgs;      // operand images per KV head
+  size_t off_scale, off_ml, off_acc, bytes;
+};
+
+template <int KB>
+__host__ __device__ inline int64_t image_index(const Plan8& p, int sub) {
+  return sub < p.n_tsub ? 2LL * sub : 2LL * p.n_tsub + 4LL * (sub - p.n_tsub);
+}
+
+struct Att8Args {
+  Prefill8Args a;
+  Plan8 p;
+  float* scale;  // [Hkv][blocks][2][8]
+  float2* ml;    // [shares][C][Hq]
+  float* acc;    // [shares][C][Hq][D]
+};
+
+// ---------------------------------------------------------------------------
+// images of the 128-key block blockIdx.x (tiles, then window) of KV head blockIdx.y
+template <int D, int F>
+__global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
+  using P = PC8<D, 1>;
+  using R = Rec8<D>;
+  constexpr int KB = P::KB, SUB = P::SUB;
+  __shared__ unsigned amax_s[2][kGrps];
+  __shared__ int bad_row[kTile];
+  const Prefill8Args& a = s.a;
+  const int kvh = blockIdx.y, tid = threadIdx.x;
+  const int n_tblk = s.p.n_tsub / SUB;
+  const int j = blockIdx.x;
+  pdl_trigger();
+  const int n_sub = s.p.n_tsub + s.p.n_wsub;
+  uint8_t* head = a.ws + (int64_t)kvh * s.p.head_imgs * P::IMG;
+  float* sc = s.scale + ((int64_t)kvh * n_sub + (int64_t)j * SUB) * 16;
+  constexpr uint32_t kNaN2 = 0x7E007E00u;
+  if (j < n_tblk) {
+    const int64_t off = a.tile_table[(int64_t)kvh * a.table_stride + j];
+    const bool good = !(off & 15) && off >= 0 && off <= a.tiles_bytes - R::kBytes;
+    if (!good && tid == 0) report(a.err, KVARN_DEVERR_RECORD);
+    const unsigned char* rec = a.tiles + (good ? off : 0);
+    const float* ks = reinterpret_cast<const float*>(rec + R::kKScale);
+    const float* vs = reinterpret_cast<const float*>(rec + R::kVScale);
+    unsigned dead = 0;  // groups whose tokens poison what sees them
+    for (int g = 0; g < kGrps; ++g)
+      if (!good || !isfinite(ks[g]) || !isfinite(vs[g])) dead |= 1u << g;
+    if (tid < 16) {
+      const int g = tid & 7, sub = g / P::NGB;
+      sc[16 * sub + (tid >> 3) * 8 + g % P::NGB] = (dead >> g & 1) ? 1.f : (tid < 8 ? ks[g] : vs[g]);
+    }
+    // units of 16 codes: 8 D of K (16 channels of a token), then 8 D of V (16 tokens of a channel)
+    for (int u = tid; u < 16 * D; u += 256) {
+      const bool is_v = u >= 8 * D;
+      const int x = is_v ? u - 8 * D : u;
+      // unit x holds bytes 16 x ..: group of 8 rows, run of 64, row, piece of 16
+      const int piece = x & 3, r8 = (x >> 2) & 7, blk = x >> 5;
+      int row, k;  // image row, first element along the summed index
+      if (is_v) {
+        row = (blk >> 1) * 8 + r8;
+        k = (blk & 1) * 64 + piece * 16;
+      } else {
+        row = (blk / (D / 64)) * 8 + r8;
+        k = (blk % (D / 64)) * 64 + piece * 16;
+      }
+      const int tok = is_v ? k : row;
+      uint32_t h[8];
+      if (dead >> (tok / kGrp) & 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = is_v ? 0u : kNaN2;
+      } else {
+        const uint4 w = *reinterpret_cast<const uint4*>(rec + (is_v ? R::kVCodes : R::kKCodes) + 16 * x);
+        codes_to_half<F>(w.x, h[0], h[1]);
+        codes_to_half<F>(w.y, h[2], h[3]);
+        codes_to_half<F>(w.z, h[4], h[5]);
+        codes_to_half<F>(w.w, h[6], h[7]);
+      }
+      const int sub = j * SUB + tok / KB;
+      uint8_t* img = head + (image_index<KB>(s.p, sub) + (is_v ? 1 : 0)) * P::IMG;
+      const int rr = is_v ? row : row % KB, kk = is_v ? k % KB : k, rows = is_v ? D : KB;
+      *reinterpret_cast<uint4*>(img + sw_off(rr, kk, rows)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(img + sw_off(rr, kk + 8, rows)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    return;
+  }
+  // window rows 128 w ..: pairs hi + lo of row / 2^e, 2^e per group of 16 rows
+  const int w0 = 128 * (j - n_tblk);
+  const int n = min(kTile, a.win_len - w0);
+  auto src = [&](const float* base, int t) {
+    return base + ((int64_t)kvh * a.win_cap + (a.win_start + w0 + t) % a.win_cap) * D;
+  };
+  if (tid < 2 * kGrps) amax_s[tid >> 3][tid & 7] = 0u;
+  if (tid < kTile) bad_row[tid] = 0;
+  __syncthreads();
+  for (int u = tid; u < kTile * D / 2; u += 256) {  // float4 pieces of K, then of V
+    const int is_v = u >= kTile * D / 4, x = is_v ? u - kTile * D / 4 : u;
+    const int t = x / (D / 4), c = x % (D / 4);
+    if (t < n) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src(is_v ? a.win_v : a.win_k, t) + 4 * c);
+      const unsigned m = max(max(v.x & 0x7FFFFFFFu, v.y & 0x7FFFFFFFu), max(v.z & 0x7FFFFFFFu, v.w & 0x7FFFFFFFu));
+      if (m >= 0x7F800000u) bad_row[t] = 1;
+      else atomicMax(&amax_s[is_v][t / kGrp], m);
+    }
+  }
+  __syncthreads();
+  const int n_sub_here = min(SUB, n_sub - j * SUB);
+  if (tid < 16 && (tid & 7) / P::NGB < n_sub_here) {
+    const int g = tid & 7;
+    sc[16 * (g / P::NGB) + (tid >> 3) * 8 + g % P::NGB] =
+        pow2_inverse(pow2_to(__uint_as_float(amax_s[tid >> 3][g]), 8));
+  }
+  for (int u = tid; u < kTile * D / 4; u += 256) {  // 8 elements along the summed index
+    const bool is_v = u >= kTile * D / 8;
+    const int x = is_v ? u - kTile * D / 8 : u;
+    int row, k;
+    if (is_v) { row = x % D; k = (x / D) * 8; }  // neighbouring threads read neighbouring channels
+    else { row = x / (D / 8); k = (x % (D / 8)) * 8; }
+    const int tok = is_v ? k : row;
+    if (tok / KB >= n_sub_here) continue;
+    const float f = pow2_to(__uint_as_float(amax_s[is_v][tok / kGrp]), 8);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = is_v ? k + i : row;
+      v[i] = 0.f;
+      if (t < n) {
+        if (bad_row[t]) v[i] = is_v ? 0.f : NAN;
+        else v[i] = f * (is_v ? src(a.win_v, t)[row] : src(a.win_k, t)[k + i]);
+      }
+    }
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_pair(v[2 * i], v[2 * i + 1], h[i], l[i]);
+    uint8_t* img = head + (image_index<KB>(s.p, j * SUB + tok / KB) + (is_v ? 2 : 0)) * P::IMG;
+    const uint32_t o = sw_off(is_v ? row : row % KB, is_v ? k % KB : k, is_v ? D : KB);
+    *reinterpret_cast<uint4*>(img + o) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(img + P::IMG + o) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+template <int D, int NP>
+__global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) {
+  using P = PC8<D, NP>;
+  constexpr int KB = P::KB, HK = KB / 2, NK = P::NK, NV = P::NV, HG = P::NGB / 2;
+  const Prefill8Args& a = s.a;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                       ~uintptr_t(1023));
+  uint64_t* bar_kf = reinterpret_cast<uint64_t*>(sm + P::OFF_BAR);  // [NK] K image landed
+  uint64_t* bar_ke = bar_kf + NK;   // [NK] K slot read
+  uint64_t* bar_vf = bar_ke + NK;   // [NV]
+  uint64_t* bar_ve = bar_vf + NV;   // [NV]
+  uint64_t* bar_s = bar_ve + NV;    // [2] S of the block's parity complete
+  uint64_t* bar_p = bar_s + 2;      // [2] w in TMEM, O rescaled (one arrival per softmax warp)
+  uint64_t* bar_o = bar_p + 2;      // O of a block complete
+  float2* xm = reinterpret_cast<float2*>(sm + P::OFF_X);
+  int* xb = reinterpret_cast<int*>(sm + P::OFF_XB);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + P::OFF_MISC);
+  volatile int* fail = reinterpret_cast<volatile int*>(sm + P::OFF_MISC + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = tid & 127, half = (tid >> 7) & 1;
+  const int kvh = blockIdx.y, share = blockIdx.z;
+  const int ppc = 128 / a.G, i0 = blockIdx.x * ppc;
+  const int my_g = row / ppc, my_i = i0 + row % ppc;
+  const bool my_valid = my_i < a.C && my_g < a.G;
+  const int64_t my_pos = a.pos0 + my_i;
+  const int64_t pmin = a.pos0 + i0, pmax = a.pos0 + min(a.C, i0 + ppc) - 1;
+  const int hq = kvh * a.G + min(my_g, a.G - 1);
+  const int64_t win_pos0 = 128LL * a.n_tiles;
+  // blocks this CTA sees: tiles up to pmax, window blocks up to pmax; its share of them
+  const int n_sub = s.p.n_tsub + s.p.n_wsub;
+  int vis_t = (int)min((int64_t)s.p.n_tsub, pmax / KB + 1);
+  int vis_w = pmax >= win_pos0 ? (int)min((int64_t)s.p.n_wsub, (pmax - win_pos0) / KB + 1) : 0;
+  const int vis = vis_t + vis_w;
+  const int b0 = (int)((int64_t)vis * share / s.p.shares), b1 = (int)((int64_t)vis * (share + 1) / s.p.shares);
+  const int n_blk = b1 - b0;
+  auto sub_of = [&](int j) { const int v = b0 + j; return v < vis_t ? v : s.p.n_tsub + (v - vis_t); };
+  const uint8_t* head = a.ws + (int64_t)kvh * s.p.head_imgs * P::IMG;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2 * NK + 2 * NV + 2; ++i) mbar_init_n(bar_kf + i, 1);
+    mbar_init_n(bar_p, 8);
+    mbar_init_n(bar_p + 1, 8);
+    mbar_init_n(bar_o, 1);
+    mbar_fence_init();
+    *fail = 0;
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, P::TMEM);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_o = tmem + P::T_O;
+  const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
+
+  // query rows into TMEM: scaled by a power of two, fp16 (hi and lo); two threads per row
+  float qscale = 0.f;
+  if (tid < 256) {
+    const int64_t at = ((int64_t)my_i * a.Hq + hq) * D + half * (D / 2);
+    float m = 0.f;
+    if (my_valid)
+#pragma unroll 8
+      for (int c = 0; c < D / 2; c += 4) {
+        const float4 v = io_ld4(a.q, a.io, at + c);
+        m = fmaxf(fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+      }
+    xm[half * 128 + row].x = m;
+    asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+    const float up = pow2_to(fmaxf(m, xm[(half ^ 1) * 128 + row].x), 10);
+    qscale = fabsf(a.scale) * pow2_inverse(up);
+    const float p2 = copysignf(up, a.scale);  // maxima are taken before the (positive) scales
+#pragma unroll 1
+    for (int c0 = 0; c0 < D / 2; c0 += 32) {
+      uint32_t hw[16], lw[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 v = my_valid ? io_ld4(a.q, a.io, at + c0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        split_pair(v.x * p2, v.y * p2, hw[2 * e], lw[2 * e]);
+        split_pair(v.z * p2, v.w * p2, hw[2 * e + 1], lw[2 * e + 1]);
+      }
+      tmem_st16(tmem + lb + P::T_QH + half * (D / 4) + c0 / 2, hw);
+      if constexpr (NP == 2 && !P::QL_SMEM) tmem_st16(tmem + lb + P::T_QL + half * (D / 4) + c0 / 2, lw);
+      if constexpr (P::QL_SMEM) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(sm + sw_off(row, half * (D / 2) + c0 + 8 * e, 128)) =
+              make_uint4(lw[4 * e], lw[4 * e + 1], lw[4 * e + 2], lw[4 * e + 3]);
+      }
+    }
+    tmem_wait_st();
+    if constexpr (P::QL_SMEM) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  float m_ref = -INFINITY, u_ref = -INFINITY, l_part = 0.f;
+  if (warp >= 9) {
+    // ---------------- copies: K images (warp 9), V images (warp 10)
+    if (lane == 0 && n_blk > 0) {
+      const bool is_v = warp == 10;
+      uint64_t* full = is_v ? bar_vf : bar_kf;
+      uint64_t* empty = is_v ? bar_ve : bar_ke;
+      unsigned char* ring = sm + (is_v ? P::OFF_V : P::OFF_K);
+      const int slots = is_v ? NV : NK;
+      int n = 0;  // images requested
+      bool go = true;
+      pdl_wait();  // the images of this call are complete
+      for (int j = 0; go && j < n_blk; ++j) {
+        const int sub = sub_of(j), parts = sub < s.p.n_tsub ? 1 : 2;
+        const uint8_t* img = head + (image_index<KB>(s.p, sub) + (is_v ? parts : 0)) * P::IMG;
+        for (int p = 0; p < parts; ++p, ++n) {
+          const int sl = n % slots;
+          if (n >= slots && !mbar_wait_timed(empty + sl, (uint32_t)(n / slots - 1) & 1u, a.err, KVARN_DEVERR_WAIT, fail)) {
+            go = false;
+            break;
+          }
+          mbar_arrive_tx(full + sl, P::IMG);
+          bulk_in(ring + sl * P::IMG, img + (int64_t)p * P::IMG, P::IMG, full + sl);
+        }
+      }
+      // every copy has landed before the CTA can retire
+      for (int i = max(0, n - slots); i < n; ++i)
+        mbar_wait_timed(full + i % slots, (uint32_t)(i / slots) & 1u, a.err, KVARN_DEVERR_WAIT);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ---------------- products. The whole warp runs the loop and one elected lane issues.
+    if (n_blk > 0) {
+      const uint64_t dk = sdesc(smem_addr(sm + P::OFF_K)), dv = sdesc(smem_addr(sm + P::OFF_V));
+      const uint64_t dq = sdesc(smem_addr(sm));  // lo part of the query (head_dim 256)
+      int nk = 0, nv = 0;
+      uint64_t* last = nullptr;
+      uint32_t last_par = 0;
+      auto parts_of = [&](int j) { return b0 + j < vis_t ? 1 : 2; };
+      auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail));
+      };
+      auto issue_s = [&](int j) -> bool {
+        const uint32_t t_s = tmem + P::T_S + KB * (j & 1);
+        const int parts = parts_of(j);
+        for (int p = 0; p < parts; ++p, ++nk) {
+          const int sl = nk % NK;
+          if (!wait(bar_kf + sl, (uint32_t)(nk / NK) & 1u)) return false;
+          tc_fence_after();
+          const uint64_t kd = sdesc_add(dk, sl * P::IMG);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
+              if (kk == 0) mma_ts(t_s, tmem + P::T_QH, bd, idesc_f16<KB>(), p > 0);
+              else mma_ts_acc(t_s, tmem + P::T_QH + 8 * kk, bd, idesc_f16<KB>());
+              if (NP == 2 && p == 0) {  // lo x lo (2^-22) is dropped
+                if constexpr (P::QL_SMEM)
+                  mma_ss_acc(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>());
+                else
+                  mma_ts_acc(t_s, tmem + P::T_QL + 8 * kk, bd, idesc_f16<KB>());
+              }
+            }
+            mma_commit(bar_ke + sl);
+            if (p == parts - 1) mma_commit(bar_s + (j & 1));
+          }
+          __syncwarp();
+          last = bar_ke + sl;
+          last_par = (uint32_t)(nk / NK) & 1u;
+        }
+        return true;
+      };
+      bool ok = issue_s(0);
+      for (int j = 0; ok && j < n_blk; ++j) {
+        if (j + 1 < n_blk && !issue_s(j + 1)) break;
+        if (!wait(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u)) break;
+        const uint32_t t_p = tmem + P::T_S + KB * (j & 1);
+        const int parts = parts_of(j);
+        for (int p = 0; ok && p < parts; ++p, ++nv) {
+          const int sl = nv % NV;
+          if (!wait(bar_vf + sl, (uint32_t)(nv / NV) & 1u)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t vd = sdesc_add(dv, sl * P::IMG);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < KB / 16; ++kk) {  // 16 keys each; a thread half's P columns: hi, then lo
+              const uint32_t ph = t_p + (kk / (KB / 32)) * HK + 8 * (kk % (KB / 32));
+              const uint64_t bd = sdesc_add(vd, (kk >> 2) * D * 128 + (kk & 3) * 32);
+              if (kk == 0) mma_ts(t_o, ph, bd, idesc_f16<D>(), j > 0 || p > 0);
+              else mma_ts_acc(t_o, ph, bd, idesc_f16<D>());
+              if (NP == 2 && p == 0) mma_ts_acc(t_o, ph + HK / 2, bd, idesc_f16<D>());
+            }
+            mma_commit(bar_ve + sl);
+            if (p == parts - 1) mma_commit(bar_o);
+          }
+          __syncwarp();
+          last = bar_ve + sl;
+          last_par = (uint32_t)(nv / NV) & 1u;
+        }
+      }
+      // the tensor pipe completes in order: the last commit covers everything
+      if (last != nullptr && !__all_sync(0xffffffffu, mbar_wait_timed(last, last_par, a.err, KVARN_DEVERR_WAIT)))
+        *fail = 1;
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax (warps 0-7): two threads per row, HK keys each
+    for (int j = 0; j < n_blk; ++j) {
+      const int sub = sub_of(j);
+      const bool is_tile = sub < s.p.n_tsub;
+      const int64_t kpos0 = is_tile ? (int64_t)KB * sub : win_pos0 + (int64_t)KB * (sub - s.p.n_tsub);
+      const int nkeys = is_tile ? KB : min(KB, a.win_len - KB * (sub - s.p.n_tsub));
+      const bool full_vis = kpos0 + KB - 1 <= pmin && nkeys == KB;
+      if (j == 0) pdl_wait();  // the scales below belong to this call's images
+      const float* scp = s.scale + ((int64_t)kvh * n_sub + sub) * 16 + half * HG;
+      float ks[HG], vs[HG];
+#pragma unroll
+      for (int g = 0; g < HG; ++g) {
+        // (not zero, so that a hidden key's -inf stays; a factor that small makes every score 0 anyway)
+        ks[g] = fmaxf(scp[g] * qscale, 1e-37f);
+        vs[g] = scp[8 + g];
+      }
+      bool bad = !mbar_wait_timed(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u, a.err, KVARN_DEVERR_WAIT, fail);
+      bad = __any_sync(0xffffffffu, bad || *fail != 0);
+      const uint32_t t_s = tmem + P::T_S + KB * (j & 1) + lb + HK * half;
+      float sv[HK];
+      float mloc = -INFINITY, uloc = -INFINITY;
+      if (!bad) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < HK; c += 32) tmem_ld32(t_s + c, *reinterpret_cast<float(*)[32]>(sv + c));
+        if (!full_vis) {
+#pragma unroll
+          for (int u = 0; u < HK; ++u) {
+            const int t = HK * half + u;
+            if (!(my_valid && t < nkeys && kpos0 + t <= my_pos)) sv[u] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < HG; ++g) {
+          float m = sv[16 * g];
+#pragma unroll
+          for (int u = 1; u < 15; u += 2) m = fmax3(m, sv[16 * g + u], sv[16 * g + u + 1]);
+          m = fmaxf(m, sv[16 * g + 15]) * ks[g];
+          mloc = fmaxf(mloc, m);
+          uloc = fmaxf(uloc, m + fast_lg2(vs[g]));
+        }
+      }
+      // the pair of threads of a row (warps w and w + 4) agrees on the maxima and on going on; slots
+      // alternate with the block's parity
+      const int par = j & 1;
+      xm[(par * 2 + half) * 128 + row] = make_float2(mloc, uloc);
+      if (lane == 0) xb[par * 8 + warp] = bad ? 1 : 0;
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+      const float2 other = xm[(par * 2 + (half ^ 1)) * 128 + row];
+      if (bad || xb[par * 8 + (warp ^ 4)] != 0) break;
+      const float mblk = fmaxf(mloc, other.x), ublk = fmaxf(uloc, other.y);
+      const float m_new = mblk > m_ref + kLag ? mblk : m_ref;
+      const float alpha = m_ref != -INFINITY ? fast_ex2(m_ref - m_new) : 1.f;
+      const bool need = ublk > u_ref + kLag;
+      const float u_new = need ? ublk : u_ref;
+      const float alpha_o = u_ref != -INFINITY ? fast_ex2(u_ref - u_new) : 1.f;
+      m_ref = m_new;
+      u_ref = u_new;
+      // a row with no visible key yet subtracts +inf and gets 0
+      const bool none = m_ref == -INFINITY;
+      const float msub = none ? INFINITY : m_ref;
+      const float fu = none ? 0.f : fast_ex2(fminf(m_ref - u_ref + kHead, 126.f));
+      uint32_t hw[HK / 2], lw[HK / 2];
+      float ls = 0.f;
+#pragma unroll
+      for (int g = 0; g < HG; ++g) {
+        float f = vs[g] * fu;
+        if (f > 1e30f) f = 1e30f;  // belongs to probabilities below 2^-90
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float p0 = fast_ex2(fmaf(sv[16 * g + 2 * e], ks[g], -msub));
+          const float p1 = fast_ex2(fmaf(sv[16 * g + 2 * e + 1], ks[g], -msub));
+          ls += p0 + p1;
+          if constexpr (NP == 2) {
+            split_pair(p0 * f, p1 * f, hw[8 * g + e], lw[8 * g + e]);
+          } else {
+            const __half2 h = __floats2half2_rn(p0 * f, p1 * f);
+            hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+      }
+      l_part = fmaf(l_part, alpha, ls);
+      // w replaces this thread's scores: hi in the first half of its columns, lo in the second
+#pragma unroll
+      for (int c = 0; c < HK / 2; c += 16) {
+        tmem_st16(t_s + c, *reinterpret_cast<uint32_t(*)[16]>(hw + c));
+        if constexpr (NP == 2) tmem_st16(t_s + HK / 2 + c, *reinterpret_cast<uint32_t(*)[16]>(lw + c));
+      }
+      // O belongs to the previous block's product until that completes
+      if (j > 0 && __any_sync(0xffffffffu, need)) {
+        if (mbar_wait_timed(bar_o, (uint32_t)(j - 1) & 1u, a.err, KVARN_DEVERR_WAIT, fail)) {
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < D / 2; c0 += 32) {
+            float v[32];
+            tmem_ld32(t_o + lb + half * (D / 2) + c0, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= alpha_o;
+            tmem_st32(t_o + lb + half * (D / 2) + c0, v);
+          }
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(bar_p + (j & 1));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const bool ok = *fail == 0;
+  if (tid < 256) xm[half * 128 + row].x = l_part;
+  __syncthreads();
+  // ---- epilogue: this thread's half of the row's channels
+  if (tid < 256) {
+    const float l = xm[row].x + xm[128 + row].x;
+    const bool any = n_blk > 0 && m_ref != -INFINITY;
+    // O is in units of 2^(u - kHead), l in units of 2^m
+    float f = any ? fast_ex2(u_ref - kHead - m_ref) : 0.f;
+    if (s.p.shares == 1) f = l != 0.f ? f / l : 0.f;
+    if (!ok) f = NAN;
+    const int64_t orow = (int64_t)my_i * a.Hq + hq;
+    const int64_t prow = (int64_t)share * a.C * a.Hq + orow;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D / 2; c0 += 32) {
+      float v[32];
+      if (n_blk > 0 && ok) {
+        tmem_ld32(t_o + lb + half * (D / 2) + c0, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      }
+      if (my_valid) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 o = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
+          const int c = half * (D / 2) + c0 + i;
+          if (s.p.shares == 1) io_st4(a.out, a.io, orow * D + c, o);
+          else *reinterpret_cast<float4*>(s.acc + prow * D + c) = o;
+        }
+      }
+    }
+    if (s.p.shares > 1 && my_valid && half == 0)
+      s.ml[prow] = ok ? make_float2(any ? m_ref : -INFINITY, l) : make_float2(0.f, NAN);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, P::TMEM);
+}
+
+// ---------------------------------------------------------------------------
+// sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s for each (position, head); D / 4 threads per row
+template <int D>
+__global__ void __launch_bounds__(256) join8_kernel(const Att8Args s) {
+  pdl_wait();
+  const Prefill8Args& a = s.a;
+  const int64_t rows = (int64_t)a.C * a.Hq;
+  const int64_t r = (int64_t)blockIdx.x * (1024 / D) + threadIdx.x / (D / 4);
+  const int c = 4 * (threadIdx.x % (D / 4));
+  if (r >= rows) return;
+  float M = -INFINITY;
+  for (int i = 0; i < s.p.shares; ++i) M = fmaxf(M, s.ml[i * rows + r].x);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < s.p.shares; ++i) {
+    const float2 ml = s.ml[i * rows + r];
+    if (ml.y == 0.f) continue;
+    const float w = fast_ex2(ml.x - M);
+    const float4 v = *reinterpret_cast<const float4*>(s.acc + (i * rows + r) * D + c);
+    L = fmaf(w, ml.y, L);
+    o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y); o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  io_st4(a.out, a.io, r * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+}
+
+Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D) {
+  Plan8 p;
+  const int KB = D == 256 ? 64 : 128, G = Hq / Hkv, ppc = 128 / G;
+  p.n_tsub = n_tblk * (kTile / KB);
+  p.n_wsub = (win_vis + KB - 1) / KB;
+  p.head_imgs = 2LL * p.n_tsub + 4LL * p.n_wsub;
+  p.row_blocks = (C + ppc - 1) / ppc;
+  const int64_t ctas = (int64_t)p.row_blocks * Hkv;
+  int64_t shares = ctas > 0 ? sm_count() / ctas : 1;
+  const int64_t most = (p.n_tsub + p.n_wsub + 1) / 2;  // two blocks per share at least
+  if (shares > most) shares = most;
+  if (shares > 64) shares = 64;
+  p.shares = shares < 1 ? 1 : (int)shares;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  p.off_scale = up((size_t)Hkv * p.head_imgs * KB * D * 2);
+  p.off_ml = p.off_scale + up((size_t)Hkv * (p.n_tsub + p.n_wsub) * 64);
+  const size_t rows = p.shares > 1 ? (size_t)p.shares * C * Hq : 0;
+  p.off_acc = p.off_ml + up(rows * sizeof(float2));
+  p.bytes = p.off_acc + up(rows * D * sizeof(float));
+  return p;
+}
+
+template <int D, int F, int NP>
+cudaError_t launch_p8(const Att8Args& s, cudaStream_t st) {
+  using P = PC8<D, NP>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    e = cudaFuncSetAttribute(attend8_kernel<D, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  const int blocks = (s.p.n_tsub + s.p.n_wsub + P::SUB - 1) / P::SUB;
+  image8_kernel<D, F><<<dim3(blocks, s.a.Hkv), 256, 0, st>>>(s);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  LaunchCfg L(dim3(s.p.row_blocks, s.a.Hkv, s.p.shares), dim3(kThreads), P::SMEM, st, KVARN_LAUNCH_PDL);
+  e = cudaLaunchKernelEx(&L.cfg, attend8_kernel<D, NP>, s);
+  if (e != cudaSuccess || s.p.shares == 1) return e;
+  const int64_t rows = (int64_t)s.a.C * s.a.Hq;
+  LaunchCfg J(dim3((unsigned)((rows + 1024 / D - 1) / (1024 / D))), dim3(256), 0, st, KVARN_LAUNCH_PDL);
+  return cudaLaunchKernelEx(&J.cfg, join8_kernel<D>, s);
+}
+
+template <int D>
+cudaError_t launch_p8d(const Att8Args& s, cudaStream_t st) {
+  const bool e = s.a.format == KVARN_CODE8_E4M3;
+  if (s.a.io == KVARN_IO_F32) return e ? launch_p8<D, 1, 2>(s, st) : launch_p8<D, 0, 2>(s, st);
+  return e ? launch_p8<D, 1, 1>(s, st) : launch_p8<D, 0, 1>(s, st);
+}
+
+}  // namespace
+
+size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D) {
+  // shares (and with them the partial results) grow as the visible blocks do
+  return plan8(C, n_tiles, win_len, Hq, Hkv, D).bytes;
+}
+
+cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st) {
+  // blocks visible to the chunk's last position
+  const int64_t pmax = a.pos0 + a.C - 1;
+  const int n_tblk = (int)(pmax / kTile + 1 < a.n_tiles ? pmax / kTile + 1 : a.n_tiles);
+  const int64_t w = pmax - 128LL * a.n_tiles + 1;
+  const int win_vis = (int)(w < 0 ? 0 : w < a.win_len ? w : a.win_len);
+  Att8Args s;
+  s.a = a;
+  s.p = plan8(a.C, n_tblk, win_vis, a.Hq, a.Hkv, a.D);
+  s.scale = reinterpret_cast<float*>(a.ws + s.p.off_scale);
+  s.ml = reinterpret_cast<float2*>(a.ws + s.p.off_ml);
+  s.acc = reinterpret_cast<float*>(a.ws + s.p.off_acc);
+  switch (a.D) {
+    case 64: return launch_p8d<64>(s, st);
+    case 128: return launch_p8d<128>(s, st);
+    case 256: return launch_p8d<256>(s, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace kvarn

@@ -23,6 +23,9 @@ DEVERR_RECORD = 2    # KVARN_DEVERR_RECORD
 DEVERR_WINDOW = 4    # KVARN_DEVERR_WINDOW
 DEVERR_SELFTEST = 8  # KVARN_DEVERR_SELFTEST
 
+CODE8 = {"i8": 0, "e4m3": 1}  # KVARN_CODE8_*
+IO_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # KVARN_IO_*
+
 _lib = None
 
 
@@ -45,6 +48,16 @@ class Layout(ctypes.Structure):
                 ("off_k_s", ctypes.c_int64), ("off_k_r", ctypes.c_int64),
                 ("off_v_delta", ctypes.c_int64), ("off_v_lo", ctypes.c_int64),
                 ("off_v_r", ctypes.c_int64), ("off_v_s", ctypes.c_int64)]
+
+
+class Layout8(ctypes.Structure):
+    """Mirror of kvarn_layout8_t."""
+    _fields_ = [("version", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("tile_tokens", ctypes.c_int32), ("code_format", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("record_bytes", ctypes.c_int64),
+                ("off_k_codes", ctypes.c_int64), ("off_v_codes", ctypes.c_int64),
+                ("off_k_scale", ctypes.c_int64), ("off_v_scale", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -91,6 +104,27 @@ def _L():
                                                        vp, vp, c_int, c_int, c_int, c_int, c_int,
                                                        c_int, f32, lay, vp, sz, c_int, c_int, vp, vp]
         lib.kvarn_prefill_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, ctypes.POINTER(sz)]
+        lay8 = ctypes.POINTER(Layout8)
+        lib.kvarn_layout8.argtypes = [c_int, c_int, c_int, lay8]
+        lib.kvarn_compress_tile8.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, i64, lay8, vp]
+        lib.kvarn_expand_tile8.argtypes = [vp, i64, vp, vp, vp, i64, i64, vp, i64, lay8, vp]
+        lib.kvarn_decode8_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int,
+                                                      ctypes.POINTER(sz)]
+        lib.kvarn_decode_attention8.argtypes = [vp, c_int, vp, i64, vp, vp, vp, vp, vp, vp, c_int,
+                                                c_int, c_int, c_int, c_int, c_int, f32, lay8, vp, vp,
+                                                vp, sz, vp, u32, vp]
+        lib.kvarn_prefill8_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int,
+                                                       ctypes.POINTER(sz)]
+        lib.kvarn_prefill_attention8.argtypes = [vp, c_int, c_int, i64, vp, i64, vp, c_int, c_int, vp,
+                                                 vp, c_int, c_int, c_int, c_int, c_int, c_int, f32,
+                                                 lay8, vp, sz, vp, vp]
+        lib.kvarn_evict_tiles.argtypes = [vp, vp, vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int,
+                                          c_int, u32, vp]
+        for name in ("kvarn_layout8", "kvarn_compress_tile8", "kvarn_expand_tile8",
+                     "kvarn_decode8_workspace_bytes", "kvarn_decode_attention8",
+                     "kvarn_prefill8_workspace_bytes", "kvarn_prefill_attention8",
+                     "kvarn_evict_tiles"):
+            getattr(lib, name).restype = c_int
         for name in ("kvarn_layout", "kvarn_layout_scales", "kvarn_layout_ex", "kvarn_rotate_query",
                      "kvarn_compress_tile", "kvarn_get_device_error", "kvarn_selftest_bounded_wait",
                      "kvarn_append_window", "kvarn_decode_workspace_bytes",
@@ -382,3 +416,198 @@ def decode_attention_noalloc(q, tiles, tile_table, n_tiles, win_k, win_v, win_st
                _ptr(win_v), _ptr(win_start), _ptr(win_len), cap, B, Hq, Hkv, D, max_tiles,
                float(softmax_scale), ctypes.byref(lay), _ptr(out), int(flags), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache and eviction
+
+def layout8(head_dim: int, code: str = "i8", block_tokens: int = 64) -> Layout8:
+    """Layout of an 8-bit tile record: code "i8" (integers -127..127) or "e4m3"
+    (8-bit floating point), one fp32 scale for each block of block_tokens (16,
+    32, 64 or 128) tokens of a head's K and of its V."""
+    if code not in CODE8:
+        raise ValueError(f"code must be one of {sorted(CODE8)}, got {code!r}")
+    L = Layout8()
+    _check("kvarn_layout8", _L().kvarn_layout8(head_dim, CODE8[code], block_tokens, ctypes.byref(L)))
+    return L
+
+
+def _io(t, name, device=None):
+    """A contiguous CUDA tensor of a query/output type; returns its KVARN_IO_* code."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype not in IO_TYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    _dev(t, name, getattr(t, "dtype", None), device)
+    return IO_TYPES[t.dtype]
+
+
+def _on(device):
+    """The device of a call's tensors as the current one: its kernels, its error
+    word and its default stream are that device's."""
+    return torch.cuda.device(device)
+
+
+def _rows8(k, v, rows, tiles, records, names):
+    _dev(k, names[0], torch.float32)
+    _all_dev(k.device, **{names[1]: (v, torch.float32), names[2]: (rows, torch.int64),
+                          names[3]: (records, torch.int64), "tiles": (tiles, torch.uint8)})
+    if k.shape != v.shape or k.dim() < 1:
+        raise ValueError(f"{names[0]} and {names[1]} must have the same shape")
+    if rows.numel() != records.numel():
+        raise ValueError(f"{names[2]} and {names[3]} must have one entry per unit")
+    return k.shape[-1], (k.numel() // k.shape[-1] if k.shape[-1] else 0)
+
+
+def compress_tile8(k_raw, v_raw, src_row0, tiles, dst_record, lay: Layout8, stream=None):
+    """128 raw rows per unit into 8-bit records: arguments as compress_tile's
+    (k_raw, v_raw fp32 [n_rows][row_stride]; src_row0, dst_record int64 [n_units])."""
+    row_stride, n_rows = _rows8(k_raw, v_raw, src_row0, tiles, dst_record,
+                                ("k_raw", "v_raw", "src_row0", "dst_record"))
+    with _on(k_raw.device):
+        _check("kvarn_compress_tile8",
+               _L().kvarn_compress_tile8(_ptr(k_raw), _ptr(v_raw), row_stride, n_rows, _ptr(src_row0),
+                                         _ptr(tiles), tiles.numel(), _ptr(dst_record),
+                                         src_row0.numel(), ctypes.byref(lay), _stream(stream)))
+
+
+def expand_tile8(tiles, src_record, k_out, v_out, dst_row0, lay: Layout8, stream=None):
+    """The records at src_record (int64 [n_units]) as fp32 rows dst_row0[u] .. + 127
+    of k_out and v_out, fp32 [n_rows][row_stride]; other rows stay as they are."""
+    row_stride, n_rows = _rows8(k_out, v_out, dst_row0, tiles, src_record,
+                                ("k_out", "v_out", "dst_row0", "src_record"))
+    with _on(k_out.device):
+        _check("kvarn_expand_tile8",
+               _L().kvarn_expand_tile8(_ptr(tiles), tiles.numel(), _ptr(src_record), _ptr(k_out),
+                                       _ptr(v_out), row_stride, n_rows, _ptr(dst_row0),
+                                       dst_row0.numel(), ctypes.byref(lay), _stream(stream)))
+
+
+def decode8_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles, win_capacity) -> int:
+    n = ctypes.c_size_t()
+    _check("kvarn_decode8_workspace_bytes",
+           _L().kvarn_decode8_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles, win_capacity,
+                                              ctypes.byref(n)))
+    return n.value
+
+
+def decode_attention8(q, tiles, tile_table, n_tiles, win_k, win_v, win_start, win_len,
+                      lay: Layout8, softmax_scale=None, mass_in=None, mass_out=None, ws=None,
+                      out=None, stream=None, flags=0):
+    """decode_attention over 8-bit records: q and out fp32, fp16 or bf16 [B][Hq][D],
+    the other arguments as decode_attention's. With mass_out (fp32, tile_table's
+    shape) the softmax weight each tile received, summed over the query heads of
+    its KV head, is added to mass_in (None: zeros; may be mass_out itself)."""
+    io = _io(q, "q")
+    _all_dev(q.device, tiles=(tiles, torch.uint8), tile_table=(tile_table, torch.int64),
+             n_tiles=(n_tiles, torch.int32), win_k=(win_k, torch.float32),
+             win_v=(win_v, torch.float32), win_start=(win_start, torch.int32),
+             win_len=(win_len, torch.int32))
+    if q.dim() != 3 or tile_table.dim() != 3 or win_k.dim() != 4:
+        raise ValueError("decode_attention8: q [B][Hq][D], tile_table [B][Hkv][max_tiles], "
+                         "win_k [B][Hkv][cap][D] expected")
+    B, Hq, D = q.shape
+    Hkv, max_tiles = tile_table.shape[1], tile_table.shape[2]
+    cap = win_k.shape[2]
+    if (tile_table.shape[0] != B or n_tiles.numel() != B or win_start.numel() != B
+            or win_len.numel() != B or win_k.shape != win_v.shape
+            or tuple(win_k.shape[:2]) != (B, Hkv) or win_k.shape[3] != D):
+        raise ValueError("decode_attention8: inconsistent shapes")
+    for name, m in (("mass_in", mass_in), ("mass_out", mass_out)):
+        if m is not None:
+            _dev(m, name, torch.float32, q.device)
+            if m.shape != tile_table.shape:
+                raise ValueError(f"{name} must have tile_table's shape")
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    with _on(q.device):
+        if ws is None:
+            need = decode8_workspace_bytes(B, Hq, Hkv, D, max_tiles, cap)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        if out is None:
+            out = torch.empty_like(q)
+        _all_dev(q.device, ws=(ws, torch.uint8), out=(out, q.dtype))
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        _check("kvarn_decode_attention8",
+               _L().kvarn_decode_attention8(_ptr(q), io, _ptr(tiles), tiles.numel(), _ptr(tile_table),
+                                            _ptr(n_tiles), _ptr(win_k), _ptr(win_v), _ptr(win_start),
+                                            _ptr(win_len), cap, B, Hq, Hkv, D, max_tiles,
+                                            float(softmax_scale), ctypes.byref(lay), _ptr(mass_in),
+                                            _ptr(mass_out), _ptr(ws), ws.numel(), _ptr(out),
+                                            int(flags), _stream(stream)))
+    return out
+
+
+def prefill8_workspace_bytes(C, n_tiles, win_len, Hq, Hkv, head_dim) -> int:
+    n = ctypes.c_size_t()
+    _check("kvarn_prefill8_workspace_bytes",
+           _L().kvarn_prefill8_workspace_bytes(int(C), int(n_tiles), int(win_len), Hq, Hkv, head_dim,
+                                               ctypes.byref(n)))
+    return n.value
+
+
+def prefill_attention8(q_chunk, pos0, tiles, tile_table, n_tiles, win_k, win_v, win_start, win_len,
+                       lay: Layout8, softmax_scale=None, ws=None, out=None, stream=None):
+    """prefill_attention over 8-bit records: q_chunk and out fp32, fp16 or bf16
+    [C][Hq][D], the other arguments as prefill_attention's; ws a uint8 device
+    workspace of prefill8_workspace_bytes() (allocated here when None)."""
+    io = _io(q_chunk, "q_chunk")
+    _all_dev(q_chunk.device, tiles=(tiles, torch.uint8), tile_table=(tile_table, torch.int64),
+             win_k=(win_k, torch.float32), win_v=(win_v, torch.float32))
+    if q_chunk.dim() != 3 or tile_table.dim() != 2 or win_k.dim() != 3:
+        raise ValueError("prefill_attention8: q_chunk [C][Hq][D], tile_table [Hkv][stride], "
+                         "win_k [Hkv][cap][D] expected")
+    C, Hq, D = q_chunk.shape
+    Hkv, stride = tile_table.shape
+    cap = win_k.shape[1]
+    if win_k.shape != win_v.shape or win_k.shape[0] != Hkv or win_k.shape[2] != D:
+        raise ValueError("prefill_attention8: inconsistent shapes")
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    with _on(q_chunk.device):
+        if out is None:
+            out = torch.empty_like(q_chunk)
+        if ws is None:
+            need = prefill8_workspace_bytes(C, n_tiles, win_len, Hq, Hkv, D)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q_chunk.device)
+        _all_dev(q_chunk.device, ws=(ws, torch.uint8), out=(out, q_chunk.dtype))
+        if out.shape != q_chunk.shape:
+            raise ValueError("out must have q_chunk's shape")
+        _check("kvarn_prefill_attention8",
+               _L().kvarn_prefill_attention8(_ptr(q_chunk), io, C, int(pos0), _ptr(tiles),
+                                             tiles.numel(), _ptr(tile_table), stride, int(n_tiles),
+                                             _ptr(win_k), _ptr(win_v), int(win_start), int(win_len),
+                                             cap, Hq, Hkv, D, float(softmax_scale), ctypes.byref(lay),
+                                             _ptr(ws), ws.numel(), _ptr(out), _stream(stream)))
+    return out
+
+
+def evict_tiles(tile_table, tile_mass, n_tiles, keep, sinks=0, recent=0, table_out=None,
+                mass_out=None, n_tiles_out=None, evicted=None, stream=None, flags=0):
+    """Drops tiles by accumulated weight (kvarn_evict_tiles): per KV head, of more
+    than `keep` tiles stay the first `sinks`, the last `recent` and the heaviest
+    between. tile_table int64 and tile_mass fp32 [B][Hkv][max_tiles], n_tiles int32
+    [B]. Outputs default to the inputs (in place); evicted (int64, tile_table's
+    shape) receives the offsets that left. Returns (table, mass, n_tiles, evicted)."""
+    _dev(tile_table, "tile_table", torch.int64)
+    table_out = tile_table if table_out is None else table_out
+    mass_out = tile_mass if mass_out is None else mass_out
+    n_tiles_out = n_tiles if n_tiles_out is None else n_tiles_out
+    _all_dev(tile_table.device, tile_mass=(tile_mass, torch.float32), n_tiles=(n_tiles, torch.int32),
+             table_out=(table_out, torch.int64), mass_out=(mass_out, torch.float32),
+             n_tiles_out=(n_tiles_out, torch.int32))
+    if evicted is not None:
+        _dev(evicted, "evicted", torch.int64, tile_table.device)
+    if tile_table.dim() != 3:
+        raise ValueError("tile_table must be [B][Hkv][max_tiles]")
+    B, Hkv, max_tiles = tile_table.shape
+    if (tile_mass.shape != tile_table.shape or table_out.shape != tile_table.shape
+            or mass_out.shape != tile_table.shape or n_tiles.numel() != B or n_tiles_out.numel() != B
+            or (evicted is not None and evicted.shape != tile_table.shape)):
+        raise ValueError("evict_tiles: inconsistent shapes")
+    with _on(tile_table.device):
+        _check("kvarn_evict_tiles",
+               _L().kvarn_evict_tiles(_ptr(tile_table), _ptr(tile_mass), _ptr(n_tiles), _ptr(table_out),
+                                      _ptr(mass_out), _ptr(n_tiles_out), _ptr(evicted), B, Hkv,
+                                      max_tiles, int(keep), int(sinks), int(recent), int(flags),
+                                      _stream(stream)))
+    return table_out, mass_out, n_tiles_out, evicted
