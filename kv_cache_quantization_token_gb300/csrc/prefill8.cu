@@ -87,121 +87,115 @@ struct Att8Args {
 };
 
 // ---------------------------------------------------------------------------
-// images of the 128-key block blockIdx.x (tiles, then window) of KV head blockIdx.y
+// images: of tile blockIdx.x of KV head blockIdx.y, or (past the tiles) of 16 window rows of K or of V
 template <int D, int F>
 __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
   using P = PC8<D, 1>;
   using R = Rec8<D>;
   constexpr int KB = P::KB, SUB = P::SUB;
-  __shared__ unsigned amax_s[2][kGrps];
-  __shared__ int bad_row[kTile];
   const Prefill8Args& a = s.a;
   const int kvh = blockIdx.y, tid = threadIdx.x;
   const int n_tblk = s.p.n_tsub / SUB;
-  const int j = blockIdx.x;
   pdl_trigger();
   const int n_sub = s.p.n_tsub + s.p.n_wsub;
   uint8_t* head = a.ws + (int64_t)kvh * s.p.head_imgs * P::IMG;
-  float* sc = s.scale + ((int64_t)kvh * n_sub + (int64_t)j * SUB) * 16;
-  constexpr uint32_t kNaN2 = 0x7E007E00u;
-  if (j < n_tblk) {
+  if ((int)blockIdx.x < n_tblk) {
+    const int j = blockIdx.x;
     const int64_t off = a.tile_table[(int64_t)kvh * a.table_stride + j];
     const bool good = !(off & 15) && off >= 0 && off <= a.tiles_bytes - R::kBytes;
     if (!good && tid == 0) report(a.err, KVARN_DEVERR_RECORD);
     const unsigned char* rec = a.tiles + (good ? off : 0);
-    const float* ks = reinterpret_cast<const float*>(rec + R::kKScale);
-    const float* vs = reinterpret_cast<const float*>(rec + R::kVScale);
+    // 16 D units of 16 codes: K (16 channels of a token), then V (16 tokens of a channel)
+    constexpr int UNITS = 16 * D / 256;
+    uint4 w[UNITS];
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) w[i] = *reinterpret_cast<const uint4*>(rec + 16 * (tid + 256 * i));
+    const float4* sp = reinterpret_cast<const float4*>(rec + R::kKScale);
+    const float4 f[4] = {sp[0], sp[1], sp[2], sp[3]};
+    const float* fs = &f[0].x;
     unsigned dead = 0;  // groups whose tokens poison what sees them
+#pragma unroll
     for (int g = 0; g < kGrps; ++g)
-      if (!good || !isfinite(ks[g]) || !isfinite(vs[g])) dead |= 1u << g;
+      if (!good || !isfinite(fs[g]) || !isfinite(fs[8 + g])) dead |= 1u << g;
     if (tid < 16) {
-      const int g = tid & 7, sub = g / P::NGB;
-      sc[16 * sub + (tid >> 3) * 8 + g % P::NGB] = (dead >> g & 1) ? 1.f : (tid < 8 ? ks[g] : vs[g]);
+      const int g = tid & 7;
+      float* sc = s.scale + ((int64_t)kvh * n_sub + (int64_t)j * SUB + g / P::NGB) * 16;
+      sc[(tid >> 3) * 8 + g % P::NGB] =
+          (dead >> g & 1) ? 1.f : *reinterpret_cast<const float*>(rec + R::kKScale + 4 * tid);
     }
-    // units of 16 codes: 8 D of K (16 channels of a token), then 8 D of V (16 tokens of a channel)
-    for (int u = tid; u < 16 * D; u += 256) {
-      const bool is_v = u >= 8 * D;
-      const int x = is_v ? u - 8 * D : u;
-      // unit x holds bytes 16 x ..: group of 8 rows, run of 64, row, piece of 16
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      const bool is_v = i >= UNITS / 2;
+      const int x = tid + 256 * (is_v ? i - UNITS / 2 : i);
+      // unit x: group of 8 rows and run of 64 (blk), row of the group, piece of 16 of the run
       const int piece = x & 3, r8 = (x >> 2) & 7, blk = x >> 5;
-      int row, k;  // image row, first element along the summed index
-      if (is_v) {
-        row = (blk >> 1) * 8 + r8;
-        k = (blk & 1) * 64 + piece * 16;
-      } else {
-        row = (blk / (D / 64)) * 8 + r8;
-        k = (blk % (D / 64)) * 64 + piece * 16;
-      }
+      constexpr int RUNS_K = D / 64;
+      const int row = (is_v ? blk >> 1 : blk / RUNS_K) * 8 + r8;
+      const int k = (is_v ? blk & 1 : blk % RUNS_K) * 64 + piece * 16;
       const int tok = is_v ? k : row;
       uint32_t h[8];
+      codes_to_half<F>(w[i].x, h[0], h[1]);
+      codes_to_half<F>(w[i].y, h[2], h[3]);
+      codes_to_half<F>(w[i].z, h[4], h[5]);
+      codes_to_half<F>(w[i].w, h[6], h[7]);
       if (dead >> (tok / kGrp) & 1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = is_v ? 0u : kNaN2;
-      } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(rec + (is_v ? R::kVCodes : R::kKCodes) + 16 * x);
-        codes_to_half<F>(w.x, h[0], h[1]);
-        codes_to_half<F>(w.y, h[2], h[3]);
-        codes_to_half<F>(w.z, h[4], h[5]);
-        codes_to_half<F>(w.w, h[6], h[7]);
+        for (int e = 0; e < 8; ++e) h[e] = is_v ? 0u : 0x7E007E00u;  // 0, or NaN
       }
-      const int sub = j * SUB + tok / KB;
-      uint8_t* img = head + (image_index<KB>(s.p, sub) + (is_v ? 1 : 0)) * P::IMG;
+      uint8_t* img = head + (image_index<KB>(s.p, j * SUB + tok / KB) + (is_v ? 1 : 0)) * P::IMG;
       const int rr = is_v ? row : row % KB, kk = is_v ? k % KB : k, rows = is_v ? D : KB;
       *reinterpret_cast<uint4*>(img + sw_off(rr, kk, rows)) = make_uint4(h[0], h[1], h[2], h[3]);
       *reinterpret_cast<uint4*>(img + sw_off(rr, kk + 8, rows)) = make_uint4(h[4], h[5], h[6], h[7]);
     }
     return;
   }
-  // window rows 128 w ..: pairs hi + lo of row / 2^e, 2^e per group of 16 rows
-  const int w0 = 128 * (j - n_tblk);
-  const int n = min(kTile, a.win_len - w0);
-  auto src = [&](const float* base, int t) {
-    return base + ((int64_t)kvh * a.win_cap + (a.win_start + w0 + t) % a.win_cap) * D;
+  // 16 window rows: pairs hi + lo of row / 2^e, one e for the 16
+  __shared__ unsigned amax_s;
+  __shared__ unsigned bad_s;  // bit t: row t holds a NaN or an infinity
+  const int wx = blockIdx.x - n_tblk, g = wx >> 1;
+  const bool is_v = wx & 1;
+  const int t0 = kGrp * g;  // first window row
+  const int sub = s.p.n_tsub + t0 / KB, gb = (t0 % KB) / kGrp;
+  auto row_of = [&](const float* base, int t) {
+    return base + ((int64_t)kvh * a.win_cap + (a.win_start + t0 + t) % a.win_cap) * D;
   };
-  if (tid < 2 * kGrps) amax_s[tid >> 3][tid & 7] = 0u;
-  if (tid < kTile) bad_row[tid] = 0;
+  if (tid == 0) amax_s = bad_s = 0u;
   __syncthreads();
-  for (int u = tid; u < kTile * D / 2; u += 256) {  // float4 pieces of K, then of V
-    const int is_v = u >= kTile * D / 4, x = is_v ? u - kTile * D / 4 : u;
-    const int t = x / (D / 4), c = x % (D / 4);
-    if (t < n) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src(is_v ? a.win_v : a.win_k, t) + 4 * c);
-      const unsigned m = max(max(v.x & 0x7FFFFFFFu, v.y & 0x7FFFFFFFu), max(v.z & 0x7FFFFFFFu, v.w & 0x7FFFFFFFu));
-      if (m >= 0x7F800000u) bad_row[t] = 1;
-      else atomicMax(&amax_s[is_v][t / kGrp], m);
+  // one pass over the rows of this tensor for the largest magnitude, over both for bad rows
+  unsigned m = 0u;
+  for (int u = tid; u < 2 * kGrp * D / 4; u += 256) {
+    const bool v2 = u >= kGrp * D / 4;
+    const int x = v2 ? u - kGrp * D / 4 : u, t = x / (D / 4);
+    if (t0 + t < a.win_len) {
+      const uint4 y = *reinterpret_cast<const uint4*>(row_of(v2 ? a.win_v : a.win_k, t) + 4 * (x % (D / 4)));
+      const unsigned z = max(max(y.x & 0x7FFFFFFFu, y.y & 0x7FFFFFFFu), max(y.z & 0x7FFFFFFFu, y.w & 0x7FFFFFFFu));
+      if (z >= 0x7F800000u) atomicOr(&bad_s, 1u << t);
+      else if (v2 == is_v) m = max(m, z);
     }
   }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((tid & 31) == 0) atomicMax(&amax_s, m);
   __syncthreads();
-  const int n_sub_here = min(SUB, n_sub - j * SUB);
-  if (tid < 16 && (tid & 7) / P::NGB < n_sub_here) {
-    const int g = tid & 7;
-    sc[16 * (g / P::NGB) + (tid >> 3) * 8 + g % P::NGB] =
-        pow2_inverse(pow2_to(__uint_as_float(amax_s[tid >> 3][g]), 8));
-  }
-  for (int u = tid; u < kTile * D / 4; u += 256) {  // 8 elements along the summed index
-    const bool is_v = u >= kTile * D / 8;
-    const int x = is_v ? u - kTile * D / 8 : u;
-    int row, k;
-    if (is_v) { row = x % D; k = (x / D) * 8; }  // neighbouring threads read neighbouring channels
-    else { row = x / (D / 8); k = (x % (D / 8)) * 8; }
-    const int tok = is_v ? k : row;
-    if (tok / KB >= n_sub_here) continue;
-    const float f = pow2_to(__uint_as_float(amax_s[is_v][tok / kGrp]), 8);
+  const float f = pow2_to(__uint_as_float(amax_s), 8);
+  const unsigned bad = bad_s;
+  if (tid == 0) s.scale[((int64_t)kvh * n_sub + sub) * 16 + (is_v ? 8 : 0) + gb] = pow2_inverse(f);
+  uint8_t* img = head + (image_index<KB>(s.p, sub) + (is_v ? 2 : 0)) * P::IMG;
+  for (int u = tid; u < 2 * D; u += 256) {  // 8 elements along the summed index: channels of K, tokens of V
+    const int row = is_v ? u % D : u / (D / 8), k = is_v ? (u / D) * 8 : (u % (D / 8)) * 8;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = is_v ? k + i : row;
       v[i] = 0.f;
-      if (t < n) {
-        if (bad_row[t]) v[i] = is_v ? 0.f : NAN;
-        else v[i] = f * (is_v ? src(a.win_v, t)[row] : src(a.win_k, t)[k + i]);
+      if (t0 + t < a.win_len) {
+        const float x = is_v ? row_of(a.win_v, t)[row] : row_of(a.win_k, t)[k + i];
+        v[i] = (bad >> t & 1) ? (is_v ? 0.f : NAN) : f * x;
       }
     }
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_pair(v[2 * i], v[2 * i + 1], h[i], l[i]);
-    uint8_t* img = head + (image_index<KB>(s.p, j * SUB + tok / KB) + (is_v ? 2 : 0)) * P::IMG;
-    const uint32_t o = sw_off(is_v ? row : row % KB, is_v ? k % KB : k, is_v ? D : KB);
+    const uint32_t o = is_v ? sw_off(row, t0 % KB + k, D) : sw_off(t0 % KB + row, k, KB);
     *reinterpret_cast<uint4*>(img + o) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4*>(img + P::IMG + o) = make_uint4(l[0], l[1], l[2], l[3]);
   }
@@ -357,15 +351,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) 
           const uint64_t kd = sdesc_add(dk, sl * P::IMG);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
-              if (kk == 0) mma_ts(t_s, tmem + P::T_QH, bd, idesc_f16<KB>(), p > 0);
-              else mma_ts_acc(t_s, tmem + P::T_QH + 8 * kk, bd, idesc_f16<KB>());
-              if (NP == 2 && p == 0) {  // lo x lo (2^-22) is dropped
-                if constexpr (P::QL_SMEM)
-                  mma_ss_acc(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>());
+            for (int h = NP - 1; h >= 0; --h) {  // the query's lo part first: while the sums are small
+              if (h == 1 && p > 0) continue;     // lo x lo (2^-22) is dropped
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
+                const uint32_t acc = p > 0 || h < NP - 1 || kk > 0;
+                if (P::QL_SMEM && h == 1)
+                  mma_ss(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>(), acc);
                 else
-                  mma_ts_acc(t_s, tmem + P::T_QL + 8 * kk, bd, idesc_f16<KB>());
+                  mma_ts(t_s, tmem + (h == 1 ? P::T_QL : P::T_QH) + 8 * kk, bd, idesc_f16<KB>(), acc);
               }
             }
             mma_commit(bar_ke + sl);
@@ -435,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) 
       if (!bad) {
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < HK; c += 32) tmem_ld32(t_s + c, *reinterpret_cast<float(*)[32]>(sv + c));
+        for (int c = 0; c < HK; c += 32) tmem_ld32_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+        tmem_wait_ld(sv);
         if (!full_vis) {
 #pragma unroll
           for (int u = 0; u < HK; ++u) {
@@ -474,25 +470,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) 
       const float msub = none ? INFINITY : m_ref;
       const float fu = none ? 0.f : fast_ex2(fminf(m_ref - u_ref + kHead, 126.f));
       uint32_t hw[HK / 2], lw[HK / 2];
-      float ls = 0.f;
+      float2 ls2 = make_float2(0.f, 0.f);
+      const float2 nm2 = make_float2(-msub, -msub);
 #pragma unroll
       for (int g = 0; g < HG; ++g) {
         float f = vs[g] * fu;
         if (f > 1e30f) f = 1e30f;  // belongs to probabilities below 2^-90
+        const float2 k2 = make_float2(ks[g], ks[g]), f2 = make_float2(f, f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float p0 = fast_ex2(fmaf(sv[16 * g + 2 * e], ks[g], -msub));
-          const float p1 = fast_ex2(fmaf(sv[16 * g + 2 * e + 1], ks[g], -msub));
-          ls += p0 + p1;
+          const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, nm2);
+          const float2 p = make_float2(fast_ex2(x.x), fast_ex2(x.y));
+          ls2 = __fadd2_rn(ls2, p);
+          const float2 w = __fmul2_rn(p, f2);
           if constexpr (NP == 2) {
-            split_pair(p0 * f, p1 * f, hw[8 * g + e], lw[8 * g + e]);
+            split_pair(w.x, w.y, hw[8 * g + e], lw[8 * g + e]);
           } else {
-            const __half2 h = __floats2half2_rn(p0 * f, p1 * f);
+            const __half2 h = __floats2half2_rn(w.x, w.y);
             hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
       }
-      l_part = fmaf(l_part, alpha, ls);
+      l_part = fmaf(l_part, alpha, ls2.x + ls2.y);
       // w replaces this thread's scores: hi in the first half of its columns, lo in the second
 #pragma unroll
       for (int c = 0; c < HK / 2; c += 16) {
@@ -622,7 +621,7 @@ cudaError_t launch_p8(const Att8Args& s, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  const int blocks = (s.p.n_tsub + s.p.n_wsub + P::SUB - 1) / P::SUB;
+  const int blocks = s.p.n_tsub / P::SUB + 2 * s.p.n_wsub * P::NGB;
   image8_kernel<D, F><<<dim3(blocks, s.a.Hkv), 256, 0, st>>>(s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

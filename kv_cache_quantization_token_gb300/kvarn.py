@@ -432,53 +432,68 @@ def layout8(head_dim: int, code: str = "i8", block_tokens: int = 64) -> Layout8:
     return L
 
 
-def _io(t, name, device=None):
-    """A contiguous CUDA tensor of a query/output type; returns its KVARN_IO_* code."""
+def _fit(device, *checks):
+    """Each (name, tensor, dtype) is a contiguous tensor of dtype on the CUDA device of
+    index `device`. One pass over what a decode step calls often; the tensor that does
+    not fit is named by _dev."""
+    for name, t, dtype in checks:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+                and t.is_contiguous()):
+            _dev(t, name, dtype, torch.device("cuda", max(device, 0)))
+
+
+def _io(t, name):
+    """A contiguous CUDA tensor of a query/output type: its KVARN_IO_* code and device index."""
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype not in IO_TYPES:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    _dev(t, name, getattr(t, "dtype", None), device)
-    return IO_TYPES[t.dtype]
+    _dev(t, name, getattr(t, "dtype", None))
+    return IO_TYPES[t.dtype], t.get_device()
 
 
-def _on(device):
-    """The device of a call's tensors as the current one: its kernels, its error
-    word and its default stream are that device's."""
-    return torch.cuda.device(device)
+def _call(device, fn, stream, *args):
+    """fn(*args, stream) with the tensors' device current: the kernels, the error word and
+    the default stream are that device's."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _call(device, fn, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    rc = getattr(_lib or _L(), fn)(*args, stream.cuda_stream)
+    if rc != 0:
+        raise KvarnError(fn, rc)
 
 
 def _rows8(k, v, rows, tiles, records, names):
     _dev(k, names[0], torch.float32)
-    _all_dev(k.device, **{names[1]: (v, torch.float32), names[2]: (rows, torch.int64),
-                          names[3]: (records, torch.int64), "tiles": (tiles, torch.uint8)})
+    device = k.get_device()
+    _fit(device, (names[1], v, torch.float32), (names[2], rows, torch.int64),
+         (names[3], records, torch.int64), ("tiles", tiles, torch.uint8))
     if k.shape != v.shape or k.dim() < 1:
         raise ValueError(f"{names[0]} and {names[1]} must have the same shape")
     if rows.numel() != records.numel():
         raise ValueError(f"{names[2]} and {names[3]} must have one entry per unit")
-    return k.shape[-1], (k.numel() // k.shape[-1] if k.shape[-1] else 0)
+    stride = k.shape[-1]
+    return device, stride, (k.numel() // stride if stride else 0)
 
 
 def compress_tile8(k_raw, v_raw, src_row0, tiles, dst_record, lay: Layout8, stream=None):
     """128 raw rows per unit into 8-bit records: arguments as compress_tile's
     (k_raw, v_raw fp32 [n_rows][row_stride]; src_row0, dst_record int64 [n_units])."""
-    row_stride, n_rows = _rows8(k_raw, v_raw, src_row0, tiles, dst_record,
-                                ("k_raw", "v_raw", "src_row0", "dst_record"))
-    with _on(k_raw.device):
-        _check("kvarn_compress_tile8",
-               _L().kvarn_compress_tile8(_ptr(k_raw), _ptr(v_raw), row_stride, n_rows, _ptr(src_row0),
-                                         _ptr(tiles), tiles.numel(), _ptr(dst_record),
-                                         src_row0.numel(), ctypes.byref(lay), _stream(stream)))
+    device, stride, n_rows = _rows8(k_raw, v_raw, src_row0, tiles, dst_record,
+                                    ("k_raw", "v_raw", "src_row0", "dst_record"))
+    _call(device, "kvarn_compress_tile8", stream, k_raw.data_ptr(), v_raw.data_ptr(), stride, n_rows,
+          src_row0.data_ptr(), tiles.data_ptr(), tiles.numel(), dst_record.data_ptr(),
+          src_row0.numel(), ctypes.byref(lay))
 
 
 def expand_tile8(tiles, src_record, k_out, v_out, dst_row0, lay: Layout8, stream=None):
     """The records at src_record (int64 [n_units]) as fp32 rows dst_row0[u] .. + 127
     of k_out and v_out, fp32 [n_rows][row_stride]; other rows stay as they are."""
-    row_stride, n_rows = _rows8(k_out, v_out, dst_row0, tiles, src_record,
-                                ("k_out", "v_out", "dst_row0", "src_record"))
-    with _on(k_out.device):
-        _check("kvarn_expand_tile8",
-               _L().kvarn_expand_tile8(_ptr(tiles), tiles.numel(), _ptr(src_record), _ptr(k_out),
-                                       _ptr(v_out), row_stride, n_rows, _ptr(dst_row0),
-                                       dst_row0.numel(), ctypes.byref(lay), _stream(stream)))
+    device, stride, n_rows = _rows8(k_out, v_out, dst_row0, tiles, src_record,
+                                    ("k_out", "v_out", "dst_row0", "src_record"))
+    _call(device, "kvarn_expand_tile8", stream, tiles.data_ptr(), tiles.numel(), src_record.data_ptr(),
+          k_out.data_ptr(), v_out.data_ptr(), stride, n_rows, dst_row0.data_ptr(), dst_row0.numel(),
+          ctypes.byref(lay))
 
 
 def decode8_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles, win_capacity) -> int:
@@ -496,44 +511,41 @@ def decode_attention8(q, tiles, tile_table, n_tiles, win_k, win_v, win_start, wi
     the other arguments as decode_attention's. With mass_out (fp32, tile_table's
     shape) the softmax weight each tile received, summed over the query heads of
     its KV head, is added to mass_in (None: zeros; may be mass_out itself)."""
-    io = _io(q, "q")
-    _all_dev(q.device, tiles=(tiles, torch.uint8), tile_table=(tile_table, torch.int64),
-             n_tiles=(n_tiles, torch.int32), win_k=(win_k, torch.float32),
-             win_v=(win_v, torch.float32), win_start=(win_start, torch.int32),
-             win_len=(win_len, torch.int32))
+    io, device = _io(q, "q")
+    _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64),
+         ("n_tiles", n_tiles, torch.int32), ("win_k", win_k, torch.float32),
+         ("win_v", win_v, torch.float32), ("win_start", win_start, torch.int32),
+         ("win_len", win_len, torch.int32))
     if q.dim() != 3 or tile_table.dim() != 3 or win_k.dim() != 4:
         raise ValueError("decode_attention8: q [B][Hq][D], tile_table [B][Hkv][max_tiles], "
                          "win_k [B][Hkv][cap][D] expected")
     B, Hq, D = q.shape
-    Hkv, max_tiles = tile_table.shape[1], tile_table.shape[2]
-    cap = win_k.shape[2]
-    if (tile_table.shape[0] != B or n_tiles.numel() != B or win_start.numel() != B
-            or win_len.numel() != B or win_k.shape != win_v.shape
-            or tuple(win_k.shape[:2]) != (B, Hkv) or win_k.shape[3] != D):
+    Bt, Hkv, max_tiles = tile_table.shape
+    Bw, Hw, cap, Dw = win_k.shape
+    if (Bt != B or n_tiles.numel() != B or win_start.numel() != B or win_len.numel() != B
+            or win_k.shape != win_v.shape or (Bw, Hw, Dw) != (B, Hkv, D)):
         raise ValueError("decode_attention8: inconsistent shapes")
     for name, m in (("mass_in", mass_in), ("mass_out", mass_out)):
         if m is not None:
-            _dev(m, name, torch.float32, q.device)
+            _fit(device, (name, m, torch.float32))
             if m.shape != tile_table.shape:
                 raise ValueError(f"{name} must have tile_table's shape")
-    if softmax_scale is None:
-        softmax_scale = D ** -0.5
-    with _on(q.device):
-        if ws is None:
+    if ws is None:
+        with torch.cuda.device(device):  # the split of the work depends on the device
             need = decode8_workspace_bytes(B, Hq, Hkv, D, max_tiles, cap)
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        if out is None:
-            out = torch.empty_like(q)
-        _all_dev(q.device, ws=(ws, torch.uint8), out=(out, q.dtype))
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        _check("kvarn_decode_attention8",
-               _L().kvarn_decode_attention8(_ptr(q), io, _ptr(tiles), tiles.numel(), _ptr(tile_table),
-                                            _ptr(n_tiles), _ptr(win_k), _ptr(win_v), _ptr(win_start),
-                                            _ptr(win_len), cap, B, Hq, Hkv, D, max_tiles,
-                                            float(softmax_scale), ctypes.byref(lay), _ptr(mass_in),
-                                            _ptr(mass_out), _ptr(ws), ws.numel(), _ptr(out),
-                                            int(flags), _stream(stream)))
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    _fit(device, ("ws", ws, torch.uint8), ("out", out, q.dtype))
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _call(device, "kvarn_decode_attention8", stream, q.data_ptr(), io, tiles.data_ptr(), tiles.numel(),
+          tile_table.data_ptr(), n_tiles.data_ptr(), win_k.data_ptr(), win_v.data_ptr(),
+          win_start.data_ptr(), win_len.data_ptr(), cap, B, Hq, Hkv, D, max_tiles,
+          D ** -0.5 if softmax_scale is None else float(softmax_scale), ctypes.byref(lay),
+          None if mass_in is None else mass_in.data_ptr(),
+          None if mass_out is None else mass_out.data_ptr(), ws.data_ptr(), ws.numel(), out.data_ptr(),
+          int(flags))
     return out
 
 
@@ -550,34 +562,31 @@ def prefill_attention8(q_chunk, pos0, tiles, tile_table, n_tiles, win_k, win_v, 
     """prefill_attention over 8-bit records: q_chunk and out fp32, fp16 or bf16
     [C][Hq][D], the other arguments as prefill_attention's; ws a uint8 device
     workspace of prefill8_workspace_bytes() (allocated here when None)."""
-    io = _io(q_chunk, "q_chunk")
-    _all_dev(q_chunk.device, tiles=(tiles, torch.uint8), tile_table=(tile_table, torch.int64),
-             win_k=(win_k, torch.float32), win_v=(win_v, torch.float32))
+    io, device = _io(q_chunk, "q_chunk")
+    _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64),
+         ("win_k", win_k, torch.float32), ("win_v", win_v, torch.float32))
     if q_chunk.dim() != 3 or tile_table.dim() != 2 or win_k.dim() != 3:
         raise ValueError("prefill_attention8: q_chunk [C][Hq][D], tile_table [Hkv][stride], "
                          "win_k [Hkv][cap][D] expected")
     C, Hq, D = q_chunk.shape
     Hkv, stride = tile_table.shape
-    cap = win_k.shape[1]
-    if win_k.shape != win_v.shape or win_k.shape[0] != Hkv or win_k.shape[2] != D:
+    Hw, cap, Dw = win_k.shape
+    if win_k.shape != win_v.shape or (Hw, Dw) != (Hkv, D):
         raise ValueError("prefill_attention8: inconsistent shapes")
-    if softmax_scale is None:
-        softmax_scale = D ** -0.5
-    with _on(q_chunk.device):
-        if out is None:
-            out = torch.empty_like(q_chunk)
-        if ws is None:
+    if out is None:
+        out = torch.empty_like(q_chunk)
+    if ws is None:
+        with torch.cuda.device(device):
             need = prefill8_workspace_bytes(C, n_tiles, win_len, Hq, Hkv, D)
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q_chunk.device)
-        _all_dev(q_chunk.device, ws=(ws, torch.uint8), out=(out, q_chunk.dtype))
-        if out.shape != q_chunk.shape:
-            raise ValueError("out must have q_chunk's shape")
-        _check("kvarn_prefill_attention8",
-               _L().kvarn_prefill_attention8(_ptr(q_chunk), io, C, int(pos0), _ptr(tiles),
-                                             tiles.numel(), _ptr(tile_table), stride, int(n_tiles),
-                                             _ptr(win_k), _ptr(win_v), int(win_start), int(win_len),
-                                             cap, Hq, Hkv, D, float(softmax_scale), ctypes.byref(lay),
-                                             _ptr(ws), ws.numel(), _ptr(out), _stream(stream)))
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q_chunk.device)
+    _fit(device, ("ws", ws, torch.uint8), ("out", out, q_chunk.dtype))
+    if out.shape != q_chunk.shape:
+        raise ValueError("out must have q_chunk's shape")
+    _call(device, "kvarn_prefill_attention8", stream, q_chunk.data_ptr(), io, C, int(pos0),
+          tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(), stride, int(n_tiles),
+          win_k.data_ptr(), win_v.data_ptr(), int(win_start), int(win_len), cap, Hq, Hkv, D,
+          D ** -0.5 if softmax_scale is None else float(softmax_scale), ctypes.byref(lay),
+          ws.data_ptr(), ws.numel(), out.data_ptr())
     return out
 
 
@@ -589,25 +598,25 @@ def evict_tiles(tile_table, tile_mass, n_tiles, keep, sinks=0, recent=0, table_o
     [B]. Outputs default to the inputs (in place); evicted (int64, tile_table's
     shape) receives the offsets that left. Returns (table, mass, n_tiles, evicted)."""
     _dev(tile_table, "tile_table", torch.int64)
+    device = tile_table.get_device()
     table_out = tile_table if table_out is None else table_out
     mass_out = tile_mass if mass_out is None else mass_out
     n_tiles_out = n_tiles if n_tiles_out is None else n_tiles_out
-    _all_dev(tile_table.device, tile_mass=(tile_mass, torch.float32), n_tiles=(n_tiles, torch.int32),
-             table_out=(table_out, torch.int64), mass_out=(mass_out, torch.float32),
-             n_tiles_out=(n_tiles_out, torch.int32))
+    _fit(device, ("tile_mass", tile_mass, torch.float32), ("n_tiles", n_tiles, torch.int32),
+         ("table_out", table_out, torch.int64), ("mass_out", mass_out, torch.float32),
+         ("n_tiles_out", n_tiles_out, torch.int32))
     if evicted is not None:
-        _dev(evicted, "evicted", torch.int64, tile_table.device)
+        _fit(device, ("evicted", evicted, torch.int64))
     if tile_table.dim() != 3:
         raise ValueError("tile_table must be [B][Hkv][max_tiles]")
-    B, Hkv, max_tiles = tile_table.shape
-    if (tile_mass.shape != tile_table.shape or table_out.shape != tile_table.shape
-            or mass_out.shape != tile_table.shape or n_tiles.numel() != B or n_tiles_out.numel() != B
-            or (evicted is not None and evicted.shape != tile_table.shape)):
+    shape = tile_table.shape
+    B, Hkv, max_tiles = shape
+    if (tile_mass.shape != shape or table_out.shape != shape or mass_out.shape != shape
+            or n_tiles.numel() != B or n_tiles_out.numel() != B
+            or (evicted is not None and evicted.shape != shape)):
         raise ValueError("evict_tiles: inconsistent shapes")
-    with _on(tile_table.device):
-        _check("kvarn_evict_tiles",
-               _L().kvarn_evict_tiles(_ptr(tile_table), _ptr(tile_mass), _ptr(n_tiles), _ptr(table_out),
-                                      _ptr(mass_out), _ptr(n_tiles_out), _ptr(evicted), B, Hkv,
-                                      max_tiles, int(keep), int(sinks), int(recent), int(flags),
-                                      _stream(stream)))
+    _call(device, "kvarn_evict_tiles", stream, tile_table.data_ptr(), tile_mass.data_ptr(),
+          n_tiles.data_ptr(), table_out.data_ptr(), mass_out.data_ptr(), n_tiles_out.data_ptr(),
+          None if evicted is None else evicted.data_ptr(), B, Hkv, max_tiles, int(keep), int(sinks),
+          int(recent), int(flags))
     return table_out, mass_out, n_tiles_out, evicted
