@@ -9,7 +9,7 @@
 //                     the tensor cores read, plus the scales of each 16-token group.
 //   attention kernel  one CTA per KV head, 128 score rows (the G heads of the group x 128 / G
 //                     positions) and, when there are few rows, a share of the keys. 8 softmax warps,
-//                     an MMA warp, and a copy warp for each of K and V.
+//                     an MMA warp and a copy warp.
 //   merge kernel      joins the key shares, when there are several.
 //
 // A scale is constant over 16 keys, so it multiplies scores and probabilities and the codes are used as
@@ -39,30 +39,32 @@ constexpr float kLag = 7.f;   // references move when exceeded by this power of 
 
 template <int D, int NP>
 struct PC8 {
-  static constexpr int KB = D == 256 ? 64 : 128;  // keys of a block
+  static constexpr int KB = 64;                   // keys of a block
   static constexpr int SUB = kTile / KB;          // blocks of a tile
   static constexpr int IMG = KB * D * 2;          // bytes of an operand image
   static constexpr int NGB = KB / kGrp;           // scale groups of a block
+  static constexpr int NG = D == 256 ? 2 : 3;     // softmax groups (of 4 warps), a block's scores each
+  static constexpr int THREADS = 128 * NG + 64;   // and an MMA and a copy warp
   static constexpr bool QL_SMEM = D == 256 && NP == 2;
-  static constexpr int NK = D == 64 ? 4 : QL_SMEM ? 2 : 3;  // image slots of the K and of the V ring
+  static constexpr int NK = D == 64 ? 8 : D == 128 ? 6 : QL_SMEM ? 2 : 3;  // image slots of the K and of the V ring
   static constexpr int NV = NK;
   static constexpr int QL_BYTES = QL_SMEM ? 128 * D * 2 : 0;
   static constexpr int OFF_K = QL_BYTES;
   static constexpr int OFF_V = OFF_K + NK * IMG;
   static constexpr int OFF_BAR = OFF_V + NV * IMG;
-  static constexpr int OFF_X = OFF_BAR + 256;              // float2 [2][2][128] row-maximum exchange
-  static constexpr int OFF_XB = OFF_X + 2 * 2 * 128 * 8;   // int [2][8] stop flags
-  static constexpr int OFF_MISC = OFF_XB + 64;
+  static constexpr int OFF_X = OFF_BAR + 512;              // float2 [NG][128]: (m, l) of a row's threads
+  static constexpr int OFF_U = OFF_X + NG * 128 * 8;       // float [NG][128]: reference u after a group's block
+  static constexpr int OFF_MISC = OFF_U + NG * 128 * 4;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;        // + slack to align the base to 1024
   // tensor memory columns
   static constexpr int T_QH = 0;
   [[maybe_unused]] static constexpr int T_QL = D / 2;
   static constexpr int T_S = D == 256 ? 128 : D / 2 * NP;
-  static constexpr int T_O = T_S + 2 * KB;
+  static constexpr int T_O = T_S + NG * KB;
   static constexpr int TMEM = 512;
   static_assert(T_O + D <= TMEM && SMEM <= 227 * 1024, "TMEM and shared memory");
+  static_assert(8 * (2 * NK + 2 * NV + 2 * NG + 1 + 4 * NG) <= 512, "barriers");
 };
-constexpr int kThreads = 352;  // 8 softmax warps, MMA, K copies, V copies
 
 // Workspace of a call: images [Hkv][blocks] of 2 (tiles) or 4 (window) operands, the groups'
 // scales, and the key shares' partial results.
@@ -77,6 +79,19 @@ template <int KB>
 __host__ __device__ inline int64_t image_index(const Plan8& p, int sub) {
   return sub < p.n_tsub ? 2LL * sub : 2LL * p.n_tsub + 4LL * (sub - p.n_tsub);
 }
+
+// Slot of a ring of N and the parity of its current use.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 struct Att8Args {
   Prefill8Args a;
@@ -203,9 +218,9 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
 
 // ---------------------------------------------------------------------------
 template <int D, int NP>
-__global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) {
+__global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const Att8Args s) {
   using P = PC8<D, NP>;
-  constexpr int KB = P::KB, HK = KB / 2, NK = P::NK, NV = P::NV, HG = P::NGB / 2;
+  constexpr int KB = P::KB, NK = P::NK, NV = P::NV, NGB = P::NGB, NG = P::NG;
   const Prefill8Args& a = s.a;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -214,11 +229,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) 
   uint64_t* bar_ke = bar_kf + NK;   // [NK] K slot read
   uint64_t* bar_vf = bar_ke + NK;   // [NV]
   uint64_t* bar_ve = bar_vf + NV;   // [NV]
-  uint64_t* bar_s = bar_ve + NV;    // [2] S of the block's parity complete
-  uint64_t* bar_p = bar_s + 2;      // [2] w in TMEM, O rescaled (one arrival per softmax warp)
-  uint64_t* bar_o = bar_p + 2;      // O of a block complete
+  uint64_t* bar_s = bar_ve + NV;    // [NG] S of the group's block complete
+  uint64_t* bar_p = bar_s + NG;     // [NG] w in TMEM, O rescaled (one arrival per softmax warp)
+  uint64_t* bar_o = bar_p + NG;     // every product complete
+  uint64_t* bar_u = bar_o + 1;      // [NG][4] u after the group's block published by warp w % 4
   float2* xm = reinterpret_cast<float2*>(sm + P::OFF_X);
-  int* xb = reinterpret_cast<int*>(sm + P::OFF_XB);
+  float* su = reinterpret_cast<float*>(sm + P::OFF_U);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + P::OFF_MISC);
   volatile int* fail = reinterpret_cast<volatile int*>(sm + P::OFF_MISC + 4);
 
@@ -243,10 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) 
   const uint8_t* head = a.ws + (int64_t)kvh * s.p.head_imgs * P::IMG;
 
   if (tid == 0) {
-    for (int i = 0; i < 2 * NK + 2 * NV + 2; ++i) mbar_init_n(bar_kf + i, 1);
-    mbar_init_n(bar_p, 8);
-    mbar_init_n(bar_p + 1, 8);
-    mbar_init_n(bar_o, 1);
+    for (int i = 0; i < 2 * NK + 2 * NV + NG; ++i) mbar_init_n(bar_kf + i, 1);
+    for (int i = 0; i < NG; ++i) mbar_init_n(bar_p + i, 4);
+    for (int i = 0; i < 1 + 4 * NG; ++i) mbar_init_n(bar_o + i, 1);
     mbar_fence_init();
     *fail = 0;
   }
@@ -299,237 +314,320 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) 
   __syncthreads();
   tc_fence_after();
 
-  float m_ref = -INFINITY, u_ref = -INFINITY, l_part = 0.f;
-  if (warp >= 9) {
-    // ---------------- copies: K images (warp 9), V images (warp 10)
+  float m_ref = -INFINITY, l_part = 0.f;
+  if (warp == 4 * NG + 1) {
+    // ---------------- copies: one thread keeps both rings full
     if (lane == 0 && n_blk > 0) {
-      const bool is_v = warp == 10;
-      uint64_t* full = is_v ? bar_vf : bar_kf;
-      uint64_t* empty = is_v ? bar_ve : bar_ke;
-      unsigned char* ring = sm + (is_v ? P::OFF_V : P::OFF_K);
-      const int slots = is_v ? NV : NK;
-      int n = 0;  // images requested
-      bool go = true;
+      const int n_t = max(0, min(n_blk, vis_t - b0));  // tile blocks, one image each; window blocks two
+      const int total = n_t + 2 * (n_blk - n_t);
+      const int w0 = s.p.n_tsub + max(b0 - vis_t, 0);  // first window block
+      auto image = [&](int i, bool v) -> const uint8_t* {
+        const int64_t x = i < n_t ? 2LL * (b0 + i) + (v ? 1 : 0)
+                                  : image_index<KB>(s.p, w0 + ((i - n_t) >> 1)) + ((i - n_t) & 1) + (v ? 2 : 0);
+        return head + x * P::IMG;
+      };
+      int nk = 0, nv = 0;  // images requested
+      uint64_t t0 = 0;
       pdl_wait();  // the images of this call are complete
-      for (int j = 0; go && j < n_blk; ++j) {
-        const int sub = sub_of(j), parts = sub < s.p.n_tsub ? 1 : 2;
-        const uint8_t* img = head + (image_index<KB>(s.p, sub) + (is_v ? parts : 0)) * P::IMG;
-        for (int p = 0; p < parts; ++p, ++n) {
-          const int sl = n % slots;
-          if (n >= slots && !mbar_wait_timed(empty + sl, (uint32_t)(n / slots - 1) & 1u, a.err, KVARN_DEVERR_WAIT, fail)) {
-            go = false;
+      while (nk < total || nv < total) {
+        bool moved = false;
+        if (nk < total && (nk < NK || mbar_done(bar_ke + nk % NK, (uint32_t)(nk / NK - 1) & 1u))) {
+          mbar_arrive_tx(bar_kf + nk % NK, P::IMG);
+          bulk_in(sm + P::OFF_K + (nk % NK) * P::IMG, image(nk, false), P::IMG, bar_kf + nk % NK);
+          ++nk;
+          moved = true;
+        }
+        if (nv < total && (nv < NV || mbar_done(bar_ve + nv % NV, (uint32_t)(nv / NV - 1) & 1u))) {
+          mbar_arrive_tx(bar_vf + nv % NV, P::IMG);
+          bulk_in(sm + P::OFF_V + (nv % NV) * P::IMG, image(nv, true), P::IMG, bar_vf + nv % NV);
+          ++nv;
+          moved = true;
+        }
+        if (moved) {
+          t0 = 0;
+        } else {
+          if (*fail) break;
+          const uint64_t now = global_ns();
+          if (t0 == 0) t0 = now;
+          if (now - t0 > kWaitLimitNs) {
+            *fail = 1;
+            report(a.err, KVARN_DEVERR_WAIT);
             break;
           }
-          mbar_arrive_tx(full + sl, P::IMG);
-          bulk_in(ring + sl * P::IMG, img + (int64_t)p * P::IMG, P::IMG, full + sl);
         }
       }
       // every copy has landed before the CTA can retire
-      for (int i = max(0, n - slots); i < n; ++i)
-        mbar_wait_timed(full + i % slots, (uint32_t)(i / slots) & 1u, a.err, KVARN_DEVERR_WAIT);
+      for (int i = max(0, nk - NK); i < nk; ++i)
+        mbar_wait_timed(bar_kf + i % NK, (uint32_t)(i / NK) & 1u, a.err, KVARN_DEVERR_WAIT);
+      for (int i = max(0, nv - NV); i < nv; ++i)
+        mbar_wait_timed(bar_vf + i % NV, (uint32_t)(i / NV) & 1u, a.err, KVARN_DEVERR_WAIT);
     }
     __syncwarp();
-  } else if (warp == 8) {
-    // ---------------- products. The whole warp runs the loop and one elected lane issues.
+  } else if (warp == 4 * NG) {
+    // ---------------- products. The whole warp runs the loop, so that operand addresses stay uniform,
+    // and one elected lane issues. A step is PV(j) and then S(j + NG), into the columns P(j) leaves;
+    // its three barriers are tested at once and nothing else is done per step: time that this warp
+    // spends between products is time the tensor pipe stands still once its short queue is empty.
     if (n_blk > 0) {
       const uint64_t dk = sdesc(smem_addr(sm + P::OFF_K)), dv = sdesc(smem_addr(sm + P::OFF_V));
-      const uint64_t dq = sdesc(smem_addr(sm));  // lo part of the query (head_dim 256)
-      int nk = 0, nv = 0;
-      uint64_t* last = nullptr;
-      uint32_t last_par = 0;
-      auto parts_of = [&](int j) { return b0 + j < vis_t ? 1 : 2; };
-      auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail));
+      [[maybe_unused]] const uint64_t dq = sdesc(smem_addr(sm));  // lo part of the query (head_dim 256)
+      constexpr uint32_t kStep = P::IMG >> 4;
+      const int n_t = max(0, min(n_blk, vis_t - b0));  // tile blocks, one image each; window blocks two
+      Ring<NK> rk;
+      Ring<NV> rv;
+      Ring<NG> rs, rp;  // score columns: S to write, P to read
+      // S of a block from the image in slot rk, its first (hi) or second (lo) part
+      auto s_products = [&](bool lo_part) {
+        const uint64_t kd = dk + rk.slot * kStep;
+        const uint32_t t_s = tmem + P::T_S + KB * rs.slot;
+#pragma unroll
+        for (int h = NP - 1; h >= 0; --h) {  // the query's lo part first: while the sums are small
+          if (h == 1 && lo_part) continue;   // lo x lo (2^-22) is dropped
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
+            const uint32_t acc = lo_part || h < NP - 1 || kk > 0;
+            if (P::QL_SMEM && h == 1)
+              mma_ss(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>(), acc);
+            else
+              mma_ts(t_s, tmem + (h == 1 ? P::T_QL : P::T_QH) + 8 * kk, bd, idesc_f16<KB>(), acc);
+          }
+        }
+        mma_commit(bar_ke + rk.slot);
       };
+      auto o_products = [&](bool lo_part, bool first) {
+        const uint64_t vd = dv + rv.slot * kStep;
+        const uint32_t t_p = tmem + P::T_S + KB * rp.slot;  // 32 columns hi, then 32 lo
+#pragma unroll
+        for (int kk = 0; kk < KB / 16; ++kk) {
+          const uint64_t bd = sdesc_add(vd, kk * 32);
+          mma_ts(t_o, t_p + 8 * kk, bd, idesc_f16<D>(), !first || kk > 0);
+          if (NP == 2 && !lo_part) mma_ts(t_o, t_p + 32 + 8 * kk, bd, idesc_f16<D>(), 1);
+        }
+        mma_commit(bar_ve + rv.slot);
+      };
+      auto all_done = [&](bool a0) { return __all_sync(0xffffffffu, a0); };
+      auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
+        return all_done(mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail));
+      };
+      // S of block j whose barriers were not tested yet
       auto issue_s = [&](int j) -> bool {
-        const uint32_t t_s = tmem + P::T_S + KB * (j & 1);
-        const int parts = parts_of(j);
-        for (int p = 0; p < parts; ++p, ++nk) {
-          const int sl = nk % NK;
-          if (!wait(bar_kf + sl, (uint32_t)(nk / NK) & 1u)) return false;
+        for (int p = 0; p < (j < n_t ? 1 : 2); ++p) {
+          if (!wait(bar_kf + rk.slot, rk.phase)) return false;
           tc_fence_after();
-          const uint64_t kd = sdesc_add(dk, sl * P::IMG);
           if (elect_one()) {
-#pragma unroll
-            for (int h = NP - 1; h >= 0; --h) {  // the query's lo part first: while the sums are small
-              if (h == 1 && p > 0) continue;     // lo x lo (2^-22) is dropped
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
-                const uint32_t acc = p > 0 || h < NP - 1 || kk > 0;
-                if (P::QL_SMEM && h == 1)
-                  mma_ss(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>(), acc);
-                else
-                  mma_ts(t_s, tmem + (h == 1 ? P::T_QL : P::T_QH) + 8 * kk, bd, idesc_f16<KB>(), acc);
-              }
-            }
-            mma_commit(bar_ke + sl);
-            if (p == parts - 1) mma_commit(bar_s + (j & 1));
+            s_products(p == 1);
+            if (p == 1 || j < n_t) mma_commit(bar_s + rs.slot);
           }
           __syncwarp();
-          last = bar_ke + sl;
-          last_par = (uint32_t)(nk / NK) & 1u;
+          rk.next();
         }
+        rs.next();
         return true;
       };
-      bool ok = issue_s(0);
-      for (int j = 0; ok && j < n_blk; ++j) {
-        if (j + 1 < n_blk && !issue_s(j + 1)) break;
-        if (!wait(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u)) break;
-        const uint32_t t_p = tmem + P::T_S + KB * (j & 1);
-        const int parts = parts_of(j);
-        for (int p = 0; ok && p < parts; ++p, ++nv) {
-          const int sl = nv % NV;
-          if (!wait(bar_vf + sl, (uint32_t)(nv / NV) & 1u)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t vd = sdesc_add(dv, sl * P::IMG);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < KB / 16; ++kk) {  // 16 keys each; a thread half's P columns: hi, then lo
-              const uint32_t ph = t_p + (kk / (KB / 32)) * HK + 8 * (kk % (KB / 32));
-              const uint64_t bd = sdesc_add(vd, (kk >> 2) * D * 128 + (kk & 3) * 32);
-              if (kk == 0) mma_ts(t_o, ph, bd, idesc_f16<D>(), j > 0 || p > 0);
-              else mma_ts_acc(t_o, ph, bd, idesc_f16<D>());
-              if (NP == 2 && p == 0) mma_ts_acc(t_o, ph + HK / 2, bd, idesc_f16<D>());
-            }
-            mma_commit(bar_ve + sl);
-            if (p == parts - 1) mma_commit(bar_o);
-          }
-          __syncwarp();
-          last = bar_ve + sl;
-          last_par = (uint32_t)(nv / NV) & 1u;
+      bool ok = true;
+      for (int j = 0; ok && j < min(NG, n_blk); ++j) ok = issue_s(j);
+      int j = 0;
+      for (; ok && j + NG < n_t; ++j) {  // tile blocks whose successors are tile blocks
+        const bool r0 = mbar_test_parity(bar_p + rp.slot, rp.phase);
+        const bool r1 = mbar_test_parity(bar_vf + rv.slot, rv.phase);
+        const bool r2 = mbar_test_parity(bar_kf + rk.slot, rk.phase);
+        if (!all_done(r0 && r1 && r2) &&
+            !(wait(bar_p + rp.slot, rp.phase) && wait(bar_vf + rv.slot, rv.phase) && wait(bar_kf + rk.slot, rk.phase))) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+        if (elect_one()) {
+          o_products(false, j == 0);
+          s_products(false);
+          mma_commit(bar_s + rs.slot);
+        }
+        __syncwarp();
+        rp.next();
+        rv.next();
+        rk.next();
+        rs.next();
       }
-      // the tensor pipe completes in order: the last commit covers everything
-      if (last != nullptr && !__all_sync(0xffffffffu, mbar_wait_timed(last, last_par, a.err, KVARN_DEVERR_WAIT)))
-        *fail = 1;
+      for (; ok && j < n_blk; ++j) {  // and the rest
+        if (!wait(bar_p + rp.slot, rp.phase)) break;
+        for (int p = 0; ok && p < (j < n_t ? 1 : 2); ++p) {
+          if (!wait(bar_vf + rv.slot, rv.phase)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) o_products(p == 1, j == 0 && p == 0);
+          __syncwarp();
+          rv.next();
+        }
+        rp.next();
+        if (ok && j + NG < n_blk) ok = issue_s(j + NG);
+      }
+      // everything issued has completed before the CTA goes on: one commit behind it all
+      if (elect_one()) mma_commit(bar_o);
+      __syncwarp();
+      if (!all_done(mbar_wait_timed(bar_o, 0, a.err, KVARN_DEVERR_WAIT))) *fail = 1;
     }
     __syncwarp();
   } else {
-    // ---------------- softmax (warps 0-7): two threads per row, HK keys each
-    for (int j = 0; j < n_blk; ++j) {
+    // ---------------- softmax: one thread per row; the groups of four warps take the blocks in turn,
+    // so that the latencies of one are covered by the others' arithmetic. m and l are a thread's own;
+    // u, which scales O, is decided block after block and handed from group to group.
+    const int grp = warp >> 2, grp_before = (grp + NG - 1) % NG;
+    const uint32_t t_s = tmem + P::T_S + KB * grp + lb;
+    // a block's scales are read from L2 while the block before it is worked on
+    float ks_next[NGB] = {}, vs_next[NGB] = {};
+    auto fetch_scales = [&](int j) {
+      const float4* p = reinterpret_cast<const float4*>(s.scale + ((int64_t)kvh * n_sub + sub_of(j)) * 16);
+#pragma unroll
+      for (int g = 0; g < NGB; g += 4) {
+        const float4 x = p[g / 4], y = p[2 + g / 4];
+        ks_next[g] = x.x; ks_next[g + 1] = x.y; ks_next[g + 2] = x.z; ks_next[g + 3] = x.w;
+        vs_next[g] = y.x; vs_next[g + 1] = y.y; vs_next[g + 2] = y.z; vs_next[g + 3] = y.w;
+      }
+    };
+    pdl_wait();  // the scales belong to this call's images
+    if (grp < n_blk) fetch_scales(grp);
+    for (int j = grp; j < n_blk; j += NG) {
       const int sub = sub_of(j);
       const bool is_tile = sub < s.p.n_tsub;
       const int64_t kpos0 = is_tile ? (int64_t)KB * sub : win_pos0 + (int64_t)KB * (sub - s.p.n_tsub);
       const int nkeys = is_tile ? KB : min(KB, a.win_len - KB * (sub - s.p.n_tsub));
       const bool full_vis = kpos0 + KB - 1 <= pmin && nkeys == KB;
-      if (j == 0) pdl_wait();  // the scales below belong to this call's images
-      const float* scp = s.scale + ((int64_t)kvh * n_sub + sub) * 16 + half * HG;
-      float ks[HG], vs[HG];
+      // keys of the block this row sees
+      const int seen = !my_valid ? 0 : (int)max((int64_t)0, min((int64_t)nkeys, my_pos - kpos0 + 1));
+      float ks[NGB], vs[NGB];
 #pragma unroll
-      for (int g = 0; g < HG; ++g) {
+      for (int g = 0; g < NGB; ++g) {
         // (not zero, so that a hidden key's -inf stays; a factor that small makes every score 0 anyway)
-        ks[g] = fmaxf(scp[g] * qscale, 1e-37f);
-        vs[g] = scp[8 + g];
+        ks[g] = fmaxf(ks_next[g] * qscale, 1e-37f);
+        vs[g] = vs_next[g];
       }
-      bool bad = !mbar_wait_timed(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u, a.err, KVARN_DEVERR_WAIT, fail);
-      bad = __any_sync(0xffffffffu, bad || *fail != 0);
-      const uint32_t t_s = tmem + P::T_S + KB * (j & 1) + lb + HK * half;
-      float sv[HK];
-      float mloc = -INFINITY, uloc = -INFINITY;
-      if (!bad) {
-        tc_fence_after();
+      if (j + NG < n_blk) fetch_scales(j + NG);
+      if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_s + grp, (uint32_t)(j / NG) & 1u, a.err, KVARN_DEVERR_WAIT, fail))) break;
+      tc_fence_after();
+      float mblk = -INFINITY, ublk = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < HK; c += 32) tmem_ld32_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+      for (int c = 0; c < KB; c += 64) {
+        float sv[64];
+        tmem_ld32_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(sv));
+        tmem_ld32_nowait(t_s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
         tmem_wait_ld(sv);
         if (!full_vis) {
 #pragma unroll
-          for (int u = 0; u < HK; ++u) {
-            const int t = HK * half + u;
-            if (!(my_valid && t < nkeys && kpos0 + t <= my_pos)) sv[u] = -INFINITY;
-          }
+          for (int u = 0; u < 64; ++u)
+            if (c + u >= seen) sv[u] = -INFINITY;
         }
 #pragma unroll
-        for (int g = 0; g < HG; ++g) {
+        for (int g = 0; g < 4; ++g) {
           float m = sv[16 * g];
 #pragma unroll
           for (int u = 1; u < 15; u += 2) m = fmax3(m, sv[16 * g + u], sv[16 * g + u + 1]);
-          m = fmaxf(m, sv[16 * g + 15]) * ks[g];
-          mloc = fmaxf(mloc, m);
-          uloc = fmaxf(uloc, m + fast_lg2(vs[g]));
+          m = fmaxf(m, sv[16 * g + 15]) * ks[c / 16 + g];
+          mblk = fmaxf(mblk, m);
+          ublk = fmaxf(ublk, m + fast_lg2(vs[c / 16 + g]));
         }
       }
-      // the pair of threads of a row (warps w and w + 4) agrees on the maxima and on going on; slots
-      // alternate with the block's parity
-      const int par = j & 1;
-      xm[(par * 2 + half) * 128 + row] = make_float2(mloc, uloc);
-      if (lane == 0) xb[par * 8 + warp] = bad ? 1 : 0;
-      asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
-      const float2 other = xm[(par * 2 + (half ^ 1)) * 128 + row];
-      if (bad || xb[par * 8 + (warp ^ 4)] != 0) break;
-      const float mblk = fmaxf(mloc, other.x), ublk = fmaxf(uloc, other.y);
       const float m_new = mblk > m_ref + kLag ? mblk : m_ref;
-      const float alpha = m_ref != -INFINITY ? fast_ex2(m_ref - m_new) : 1.f;
-      const bool need = ublk > u_ref + kLag;
-      const float u_new = need ? ublk : u_ref;
-      const float alpha_o = u_ref != -INFINITY ? fast_ex2(u_ref - u_new) : 1.f;
+      l_part *= m_ref != -INFINITY ? fast_ex2(m_ref - m_new) : 1.f;
       m_ref = m_new;
-      u_ref = u_new;
+      // u after the block before, from the group that has it
+      float u_old = -INFINITY;
+      if (j > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_u + 4 * grp_before + (warp & 3), (uint32_t)((j - 1) / NG) & 1u,
+                                                     a.err, KVARN_DEVERR_WAIT, fail)))
+          break;
+        u_old = su[grp_before * 128 + row];
+      }
+      const bool need = ublk > u_old + kLag;
+      const float u_ref = need ? ublk : u_old;
+      su[grp * 128 + row] = u_ref;
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(bar_u + 4 * grp + (warp & 3));
       // a row with no visible key yet subtracts +inf and gets 0
       const bool none = m_ref == -INFINITY;
       const float msub = none ? INFINITY : m_ref;
       const float fu = none ? 0.f : fast_ex2(fminf(m_ref - u_ref + kHead, 126.f));
-      uint32_t hw[HK / 2], lw[HK / 2];
       float2 ls2 = make_float2(0.f, 0.f);
       const float2 nm2 = make_float2(-msub, -msub);
 #pragma unroll
-      for (int g = 0; g < HG; ++g) {
-        float f = vs[g] * fu;
-        if (f > 1e30f) f = 1e30f;  // belongs to probabilities below 2^-90
-        const float2 k2 = make_float2(ks[g], ks[g]), f2 = make_float2(f, f);
+      for (int c = 0; c < KB; c += 64) {
+        float sv[64];
+        tmem_ld32_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(sv));
+        tmem_ld32_nowait(t_s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+        tmem_wait_ld(sv);
+        if (!full_vis) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, nm2);
-          const float2 p = make_float2(fast_ex2(x.x), fast_ex2(x.y));
-          ls2 = __fadd2_rn(ls2, p);
-          const float2 w = __fmul2_rn(p, f2);
-          if constexpr (NP == 2) {
-            split_pair(w.x, w.y, hw[8 * g + e], lw[8 * g + e]);
-          } else {
-            const __half2 h = __floats2half2_rn(w.x, w.y);
-            hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int u = 0; u < 64; ++u)
+            if (c + u >= seen) sv[u] = -INFINITY;
+        }
+        uint32_t hw[32], lw[32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float f = vs[c / 16 + g] * fu;
+          if (f > 1e30f) f = 1e30f;  // belongs to probabilities below 2^-90
+          const float2 k2 = make_float2(ks[c / 16 + g], ks[c / 16 + g]), f2 = make_float2(f, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, nm2);
+            const float2 p = make_float2(fast_ex2(x.x), fast_ex2(x.y));
+            ls2 = __fadd2_rn(ls2, p);
+            const float2 w = __fmul2_rn(p, f2);
+            if constexpr (NP == 2) {
+              split_pair(w.x, w.y, hw[8 * g + e], lw[8 * g + e]);
+            } else {
+              const __half2 h = __floats2half2_rn(w.x, w.y);
+              hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
           }
         }
+        // w replaces the scores of these 64 keys: hi in the first 32 columns, lo in the others
+        tmem_st32_nowait(t_s + c, hw);
+        if constexpr (NP == 2) tmem_st32_nowait(t_s + c + 32, lw);
       }
-      l_part = fmaf(l_part, alpha, ls2.x + ls2.y);
-      // w replaces this thread's scores: hi in the first half of its columns, lo in the second
-#pragma unroll
-      for (int c = 0; c < HK / 2; c += 16) {
-        tmem_st16(t_s + c, *reinterpret_cast<uint32_t(*)[16]>(hw + c));
-        if constexpr (NP == 2) tmem_st16(t_s + HK / 2 + c, *reinterpret_cast<uint32_t(*)[16]>(lw + c));
-      }
+      l_part += ls2.x + ls2.y;
       // O belongs to the previous block's product until that completes
       if (j > 0 && __any_sync(0xffffffffu, need)) {
-        if (mbar_wait_timed(bar_o, (uint32_t)(j - 1) & 1u, a.err, KVARN_DEVERR_WAIT, fail)) {
-          tc_fence_after();
+        const float alpha = need && u_old != -INFINITY ? fast_ex2(u_old - u_ref) : 1.f;
+        // its last V image is read when it is complete
+        const int n_t = max(0, min(n_blk, vis_t - b0));
+        const int im = j <= n_t ? j - 1 : n_t + 2 * (j - n_t) - 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_ve + im % NV, (uint32_t)(im / NV) & 1u, a.err, KVARN_DEVERR_WAIT, fail)))
+          break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float v[32];
+          tmem_ld32(t_o + lb + c0, v);
 #pragma unroll
-          for (int c0 = 0; c0 < D / 2; c0 += 32) {
-            float v[32];
-            tmem_ld32(t_o + lb + half * (D / 2) + c0, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= alpha_o;
-            tmem_st32(t_o + lb + half * (D / 2) + c0, v);
-          }
+          for (int i = 0; i < 32; ++i) v[i] *= alpha;
+          tmem_st32(t_o + lb + c0, v);
         }
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive1(bar_p + (j & 1));
+      if (lane == 0) mbar_arrive1(bar_p + grp);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const bool ok = *fail == 0;
-  if (tid < 256) xm[half * 128 + row].x = l_part;
+  if (warp < 4 * NG) xm[(warp >> 2) * 128 + row] = make_float2(m_ref, l_part);
   __syncthreads();
-  // ---- epilogue: this thread's half of the row's channels
+  // ---- epilogue: half of a row's channels per thread
   if (tid < 256) {
-    const float l = xm[row].x + xm[128 + row].x;
-    const bool any = n_blk > 0 && m_ref != -INFINITY;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) m = fmaxf(m, xm[g * 128 + row].x);
+    const bool any = n_blk > 0 && m != -INFINITY;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float2 v = xm[g * 128 + row];
+      l += any ? v.y * fast_ex2(v.x - m) : v.y;  // (a NaN l without a maximum stays)
+    }
     // O is in units of 2^(u - kHead), l in units of 2^m
-    float f = any ? fast_ex2(u_ref - kHead - m_ref) : 0.f;
+    const float u = n_blk > 0 ? su[((n_blk - 1) % NG) * 128 + row] : 0.f;
+    float f = any ? fast_ex2(u - kHead - m) : 0.f;
     if (s.p.shares == 1) f = l != 0.f ? f / l : 0.f;
     if (!ok) f = NAN;
     const int64_t orow = (int64_t)my_i * a.Hq + hq;
@@ -554,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Att8Args s) 
       }
     }
     if (s.p.shares > 1 && my_valid && half == 0)
-      s.ml[prow] = ok ? make_float2(any ? m_ref : -INFINITY, l) : make_float2(0.f, NAN);
+      s.ml[prow] = ok ? make_float2(any ? m : -INFINITY, l) : make_float2(0.f, NAN);
   }
   tc_fence_before();
   __syncthreads();
@@ -589,7 +687,7 @@ __global__ void __launch_bounds__(256) join8_kernel(const Att8Args s) {
 
 Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D) {
   Plan8 p;
-  const int KB = D == 256 ? 64 : 128, G = Hq / Hkv, ppc = 128 / G;
+  const int KB = PC8<64, 1>::KB, G = Hq / Hkv, ppc = 128 / G;
   p.n_tsub = n_tblk * (kTile / KB);
   p.n_wsub = (win_vis + KB - 1) / KB;
   p.head_imgs = 2LL * p.n_tsub + 4LL * p.n_wsub;
@@ -625,7 +723,7 @@ cudaError_t launch_p8(const Att8Args& s, cudaStream_t st) {
   image8_kernel<D, F><<<dim3(blocks, s.a.Hkv), 256, 0, st>>>(s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  LaunchCfg L(dim3(s.p.row_blocks, s.a.Hkv, s.p.shares), dim3(kThreads), P::SMEM, st, KVARN_LAUNCH_PDL);
+  LaunchCfg L(dim3(s.p.row_blocks, s.a.Hkv, s.p.shares), dim3(P::THREADS), P::SMEM, st, KVARN_LAUNCH_PDL);
   e = cudaLaunchKernelEx(&L.cfg, attend8_kernel<D, NP>, s);
   if (e != cudaSuccess || s.p.shares == 1) return e;
   const int64_t rows = (int64_t)s.a.C * s.a.Hq;
