@@ -8,8 +8,8 @@
 //                     K [key][channel] and V^T [channel][key] in the 128-byte-swizzled K-major layout
 //                     the tensor cores read, plus the scales of each 16-token group.
 //   attention kernel  one CTA per KV head, 128 score rows (the G heads of the group x 128 / G
-//                     positions) and, when there are few rows, a share of the keys. 8 softmax warps,
-//                     an MMA warp and a copy warp.
+//                     positions) and, when there are few rows, a share of the keys: 8 or 12 softmax
+//                     warps, two MMA warps and two copy warps.
 //   merge kernel      joins the key shares, when there are several.
 //
 // A scale is constant over 16 keys, so it multiplies scores and probabilities and the codes are used as
@@ -39,20 +39,26 @@ constexpr float kLag = 7.f;   // references move when exceeded by this power of 
 
 template <int D, int NP>
 struct PC8 {
-  static constexpr int KB = 64;                   // keys of a block
+  static constexpr int KB = 64;                   // image rows of a block: 64 keys of a tile,
+  static constexpr int KW = 32;                   // or 32 window keys, hi parts and then lo parts
   static constexpr int SUB = kTile / KB;          // blocks of a tile
   static constexpr int IMG = KB * D * 2;          // bytes of an operand image
   static constexpr int NGB = KB / kGrp;           // scale groups of a block
-  static constexpr int NG = D == 256 ? 2 : 3;     // softmax groups (of 4 warps), a block's scores each
-  static constexpr int THREADS = 128 * NG + 64;   // and an MMA and a copy warp
+  // Softmax groups of 4 warps, each with 64 columns of scores. Where tensor memory has room, P has
+  // columns of its own, and S of a group's next block is formed while its softmax runs; at head_dim
+  // 256 P replaces the scores.
+  static constexpr bool SEP = D <= 128;
+  static constexpr int NG = D == 256 || (D == 128 && NP == 2) ? 2 : 3;
+  static constexpr int PW = SEP ? NP * KB / 2 : 0;  // columns of a group's P
+  static constexpr int THREADS = 128 * NG + 128;    // and two MMA warps and two copy warps
   static constexpr bool QL_SMEM = D == 256 && NP == 2;
-  static constexpr int NK = D == 64 ? 8 : D == 128 ? 6 : QL_SMEM ? 2 : 3;  // image slots of the K and of the V ring
-  static constexpr int NV = NK;
+  static constexpr int R = D <= 128 ? 6 : QL_SMEM ? 2 : 3;  // image slots of the K and of the V ring
+  static constexpr int LP = D <= 128 ? 2 : 1;     // blocks of one copy: few waits, where the ring is deep
   static constexpr int QL_BYTES = QL_SMEM ? 128 * D * 2 : 0;
   static constexpr int OFF_K = QL_BYTES;
-  static constexpr int OFF_V = OFF_K + NK * IMG;
-  static constexpr int OFF_BAR = OFF_V + NV * IMG;
-  static constexpr int OFF_X = OFF_BAR + 512;              // float2 [NG][128]: (m, l) of a row's threads
+  static constexpr int OFF_V = OFF_K + R * IMG;
+  static constexpr int OFF_BAR = OFF_V + R * IMG;
+  static constexpr int OFF_X = OFF_BAR + 256;              // float2 [NG][128]: (m, l) of a row's threads
   static constexpr int OFF_U = OFF_X + NG * 128 * 8;       // float [NG][128]: reference u after a group's block
   static constexpr int OFF_MISC = OFF_U + NG * 128 * 4;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;        // + slack to align the base to 1024
@@ -60,38 +66,39 @@ struct PC8 {
   static constexpr int T_QH = 0;
   [[maybe_unused]] static constexpr int T_QL = D / 2;
   static constexpr int T_S = D == 256 ? 128 : D / 2 * NP;
-  static constexpr int T_O = T_S + NG * KB;
+  static constexpr int T_P = SEP ? T_S + NG * KB : T_S;    // group g's at T_P + g * (PW or KB)
+  static constexpr int PSTEP = SEP ? PW : KB;
+  static constexpr int T_O = T_S + NG * (KB + PW);
   static constexpr int TMEM = 512;
   static_assert(T_O + D <= TMEM && SMEM <= 227 * 1024, "TMEM and shared memory");
-  static_assert(8 * (2 * NK + 2 * NV + 2 * NG + 1 + 4 * NG) <= 512, "barriers");
+  static_assert(8 * (4 * R + 1) <= 256 && R % LP == 0, "barriers");
 };
 
-// Workspace of a call: images [Hkv][blocks] of 2 (tiles) or 4 (window) operands, the groups'
-// scales, and the key shares' partial results.
+// Workspace of a call: images [Hkv][pairs of blocks][K, K, V, V], the groups' scales, and the key shares'
+// partial results.
 struct Plan8 {
   int n_tsub, n_wsub;     // blocks of visible tiles and window rows
   int row_blocks, shares;
-  int64_t head_imgs;      // operand images per KV head
+  int64_t head_imgs;      // operand images per KV head, two per block
   size_t off_scale, off_ml, off_acc, bytes;
 };
 
-template <int KB>
-__host__ __device__ inline int64_t image_index(const Plan8& p, int sub) {
-  return sub < p.n_tsub ? 2LL * sub : 2LL * p.n_tsub + 4LL * (sub - p.n_tsub);
+// Hand-overs between the warps of a CTA go over its hardware barriers (some 20 cycles; a satisfied test
+// of an mbarrier costs 60 to 200 beside the tensor core's reads of shared memory). A warp that gave up
+// on a copy or a product raises `fail` and still takes part in every hand-over, so that none is left
+// waiting; what it computes from then on is discarded.
+enum : int { kBarPair = 2, kBarRead = 6, kBarP = 9, kBarU = 12 };  // + warp % 4, and + group three times
+template <int THREADS>
+__device__ __forceinline__ void hand_over(int id) {
+  asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
+template <int THREADS>
+__device__ __forceinline__ void take_over(int id) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
 
-// Slot of a ring of N and the parity of its current use.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
+// Place of a block's K image among its head's; the V image is two further.
+__host__ __device__ inline int64_t image_index(int sub) { return 4LL * (sub >> 1) + (sub & 1); }
 
 struct Att8Args {
   Prefill8Args a;
@@ -157,20 +164,21 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = is_v ? 0u : 0x7E007E00u;  // 0, or NaN
       }
-      uint8_t* img = head + (image_index<KB>(s.p, j * SUB + tok / KB) + (is_v ? 1 : 0)) * P::IMG;
+      uint8_t* img = head + (image_index(j * SUB + tok / KB) + (is_v ? 2 : 0)) * P::IMG;
       const int rr = is_v ? row : row % KB, kk = is_v ? k % KB : k, rows = is_v ? D : KB;
       *reinterpret_cast<uint4*>(img + sw_off(rr, kk, rows)) = make_uint4(h[0], h[1], h[2], h[3]);
       *reinterpret_cast<uint4*>(img + sw_off(rr, kk + 8, rows)) = make_uint4(h[4], h[5], h[6], h[7]);
     }
     return;
   }
-  // 16 window rows: pairs hi + lo of row / 2^e, one e for the 16
+  // 16 window rows: pairs hi + lo of row / 2^e, one e for the 16. A block holds 32 window keys: its
+  // image's first 32 rows (columns, of V^T) the hi parts, the other 32 the lo parts.
   __shared__ unsigned amax_s;
   __shared__ unsigned bad_s;  // bit t: row t holds a NaN or an infinity
   const int wx = blockIdx.x - n_tblk, g = wx >> 1;
   const bool is_v = wx & 1;
   const int t0 = kGrp * g;  // first window row
-  const int sub = s.p.n_tsub + t0 / KB, gb = (t0 % KB) / kGrp;
+  const int sub = s.p.n_tsub + t0 / P::KW, r0 = t0 % P::KW;
   auto row_of = [&](const float* base, int t) {
     return base + ((int64_t)kvh * a.win_cap + (a.win_start + t0 + t) % a.win_cap) * D;
   };
@@ -193,8 +201,9 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
   __syncthreads();
   const float f = pow2_to(__uint_as_float(amax_s), 8);
   const unsigned bad = bad_s;
-  if (tid == 0) s.scale[((int64_t)kvh * n_sub + sub) * 16 + (is_v ? 8 : 0) + gb] = pow2_inverse(f);
-  uint8_t* img = head + (image_index<KB>(s.p, sub) + (is_v ? 2 : 0)) * P::IMG;
+  if (tid < 2)  // (the lo rows have their hi rows' scale)
+    s.scale[((int64_t)kvh * n_sub + sub) * 16 + (is_v ? 8 : 0) + r0 / kGrp + 2 * tid] = pow2_inverse(f);
+  uint8_t* img = head + (image_index(sub) + (is_v ? 2 : 0)) * P::IMG;
   for (int u = tid; u < 2 * D; u += 256) {  // 8 elements along the summed index: channels of K, tokens of V
     const int row = is_v ? u % D : u / (D / 8), k = is_v ? (u / D) * 8 : (u % (D / 8)) * 8;
     float v[8];
@@ -210,9 +219,10 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_pair(v[2 * i], v[2 * i + 1], h[i], l[i]);
-    const uint32_t o = is_v ? sw_off(row, t0 % KB + k, D) : sw_off(t0 % KB + row, k, KB);
-    *reinterpret_cast<uint4*>(img + o) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(img + P::IMG + o) = make_uint4(l[0], l[1], l[2], l[3]);
+    const uint32_t oh = is_v ? sw_off(row, r0 + k, D) : sw_off(r0 + row, k, KB);
+    const uint32_t ol = is_v ? sw_off(row, P::KW + r0 + k, D) : sw_off(P::KW + r0 + row, k, KB);
+    *reinterpret_cast<uint4*>(img + oh) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(img + ol) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -220,19 +230,16 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
 template <int D, int NP>
 __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const Att8Args s) {
   using P = PC8<D, NP>;
-  constexpr int KB = P::KB, NK = P::NK, NV = P::NV, NGB = P::NGB, NG = P::NG;
+  constexpr int KB = P::KB, KW = P::KW, R = P::R, NGB = P::NGB, NG = P::NG;
   const Prefill8Args& a = s.a;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                        ~uintptr_t(1023));
-  uint64_t* bar_kf = reinterpret_cast<uint64_t*>(sm + P::OFF_BAR);  // [NK] K image landed
-  uint64_t* bar_ke = bar_kf + NK;   // [NK] K slot read
-  uint64_t* bar_vf = bar_ke + NK;   // [NV]
-  uint64_t* bar_ve = bar_vf + NV;   // [NV]
-  uint64_t* bar_s = bar_ve + NV;    // [NG] S of the group's block complete
-  uint64_t* bar_p = bar_s + NG;     // [NG] w in TMEM, O rescaled (one arrival per softmax warp)
-  uint64_t* bar_o = bar_p + NG;     // every product complete
-  uint64_t* bar_u = bar_o + 1;      // [NG][4] u after the group's block published by warp w % 4
+  uint64_t* bar_fk = reinterpret_cast<uint64_t*>(sm + P::OFF_BAR);  // [R] K image landed
+  uint64_t* bar_dk = bar_fk + R;    // [R] S of its block complete
+  uint64_t* bar_fv = bar_dk + R;    // [R] V image landed
+  uint64_t* bar_dv = bar_fv + R;    // [R] PV of its block complete
+  uint64_t* bar_o = bar_dv + R;     // every product complete (one arrival per MMA warp)
   float2* xm = reinterpret_cast<float2*>(sm + P::OFF_X);
   float* su = reinterpret_cast<float*>(sm + P::OFF_U);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + P::OFF_MISC);
@@ -251,17 +258,18 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   // blocks this CTA sees: tiles up to pmax, window blocks up to pmax; its share of them
   const int n_sub = s.p.n_tsub + s.p.n_wsub;
   int vis_t = (int)min((int64_t)s.p.n_tsub, pmax / KB + 1);
-  int vis_w = pmax >= win_pos0 ? (int)min((int64_t)s.p.n_wsub, (pmax - win_pos0) / KB + 1) : 0;
+  int vis_w = pmax >= win_pos0 ? (int)min((int64_t)s.p.n_wsub, (pmax - win_pos0) / KW + 1) : 0;
   const int vis = vis_t + vis_w;
-  const int b0 = (int)((int64_t)vis * share / s.p.shares), b1 = (int)((int64_t)vis * (share + 1) / s.p.shares);
+  const int pairs = (vis + 1) / 2;  // shares are whole pairs of blocks
+  const int b0 = 2 * (int)((int64_t)pairs * share / s.p.shares);
+  const int b1 = min(vis, 2 * (int)((int64_t)pairs * (share + 1) / s.p.shares));
   const int n_blk = b1 - b0;
   auto sub_of = [&](int j) { const int v = b0 + j; return v < vis_t ? v : s.p.n_tsub + (v - vis_t); };
   const uint8_t* head = a.ws + (int64_t)kvh * s.p.head_imgs * P::IMG;
 
   if (tid == 0) {
-    for (int i = 0; i < 2 * NK + 2 * NV + NG; ++i) mbar_init_n(bar_kf + i, 1);
-    for (int i = 0; i < NG; ++i) mbar_init_n(bar_p + i, 4);
-    for (int i = 0; i < 1 + 4 * NG; ++i) mbar_init_n(bar_o + i, 1);
+    for (int i = 0; i < 4 * R; ++i) mbar_init_n(bar_fk + i, 1);
+    mbar_init_n(bar_o, 2);
     mbar_fence_init();
     *fail = 0;
   }
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
         m = fmaxf(fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
       }
     xm[half * 128 + row].x = m;
-    asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+    take_over<64>(kBarPair + (warp & 3));
     const float up = pow2_to(fmaxf(m, xm[(half ^ 1) * 128 + row].x), 10);
     qscale = fabsf(a.scale) * pow2_inverse(up);
     const float p2 = copysignf(up, a.scale);  // maxima are taken before the (positive) scales
@@ -315,156 +323,106 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   tc_fence_after();
 
   float m_ref = -INFINITY, l_part = 0.f;
-  if (warp == 4 * NG + 1) {
-    // ---------------- copies: one thread keeps both rings full
+  if (warp >= 4 * NG + 2) {
+    // ---------------- copies: one thread for the K images, one for the V images
     if (lane == 0 && n_blk > 0) {
-      const int n_t = max(0, min(n_blk, vis_t - b0));  // tile blocks, one image each; window blocks two
-      const int total = n_t + 2 * (n_blk - n_t);
-      const int w0 = s.p.n_tsub + max(b0 - vis_t, 0);  // first window block
-      auto image = [&](int i, bool v) -> const uint8_t* {
-        const int64_t x = i < n_t ? 2LL * (b0 + i) + (v ? 1 : 0)
-                                  : image_index<KB>(s.p, w0 + ((i - n_t) >> 1)) + ((i - n_t) & 1) + (v ? 2 : 0);
-        return head + x * P::IMG;
-      };
-      int nk = 0, nv = 0;  // images requested
-      uint64_t t0 = 0;
+      const bool is_v = warp == 4 * NG + 3;
+      uint64_t* full = is_v ? bar_fv : bar_fk;
+      uint64_t* done = is_v ? bar_dv : bar_dk;
+      unsigned char* ring = sm + (is_v ? P::OFF_V : P::OFF_K);
+      const uint8_t* src = head + (is_v ? 2 * P::IMG : 0);
       pdl_wait();  // the images of this call are complete
-      while (nk < total || nv < total) {
-        bool moved = false;
-        if (nk < total && (nk < NK || mbar_done(bar_ke + nk % NK, (uint32_t)(nk / NK - 1) & 1u))) {
-          mbar_arrive_tx(bar_kf + nk % NK, P::IMG);
-          bulk_in(sm + P::OFF_K + (nk % NK) * P::IMG, image(nk, false), P::IMG, bar_kf + nk % NK);
-          ++nk;
-          moved = true;
-        }
-        if (nv < total && (nv < NV || mbar_done(bar_ve + nv % NV, (uint32_t)(nv / NV - 1) & 1u))) {
-          mbar_arrive_tx(bar_vf + nv % NV, P::IMG);
-          bulk_in(sm + P::OFF_V + (nv % NV) * P::IMG, image(nv, true), P::IMG, bar_vf + nv % NV);
-          ++nv;
-          moved = true;
-        }
-        if (moved) {
-          t0 = 0;
-        } else {
-          if (*fail) break;
-          const uint64_t now = global_ns();
-          if (t0 == 0) t0 = now;
-          if (now - t0 > kWaitLimitNs) {
-            *fail = 1;
-            report(a.err, KVARN_DEVERR_WAIT);
-            break;
-          }
-        }
+      int t = 0;
+      for (; t < n_blk; t += P::LP) {  // (a pair's second image is copied even if no row sees it)
+        const int sl = t % R, last = t - R + P::LP - 1;  // the last block that used the slots
+        if (t >= R) mbar_wait_timed(done + last % R, (uint32_t)(last / R) & 1u, a.err, KVARN_DEVERR_WAIT, fail);
+        mbar_arrive_tx(full + sl, P::LP * P::IMG);
+        bulk_in(ring + sl * P::IMG, src + image_index(sub_of(t)) * P::IMG, P::LP * P::IMG, full + sl);
       }
       // every copy has landed before the CTA can retire
-      for (int i = max(0, nk - NK); i < nk; ++i)
-        mbar_wait_timed(bar_kf + i % NK, (uint32_t)(i / NK) & 1u, a.err, KVARN_DEVERR_WAIT);
-      for (int i = max(0, nv - NV); i < nv; ++i)
-        mbar_wait_timed(bar_vf + i % NV, (uint32_t)(i / NV) & 1u, a.err, KVARN_DEVERR_WAIT);
+      for (int i = max(0, t - R); i < t; i += P::LP)
+        mbar_wait_timed(full + i % R, (uint32_t)(i / R) & 1u, a.err, KVARN_DEVERR_WAIT);
     }
     __syncwarp();
-  } else if (warp == 4 * NG) {
-    // ---------------- products. The whole warp runs the loop, so that operand addresses stay uniform,
-    // and one elected lane issues. A step is PV(j) and then S(j + NG), into the columns P(j) leaves;
-    // its three barriers are tested at once and nothing else is done per step: time that this warp
-    // spends between products is time the tensor pipe stands still once its short queue is empty.
+  } else if (warp >= 4 * NG) {
+    // ---------------- products: one warp issues S, the other PV, each waiting for its own operands while
+    // the tensor pipe works on the other's (a satisfied wait costs some 200 cycles beside the softmax
+    // warps, more than the pipe's short queue lasts). The whole warp runs the loop, so that operand
+    // addresses stay uniform, and one elected lane issues; the loops are unrolled over the rings, so that
+    // slots, addresses and descriptors are constants.
     if (n_blk > 0) {
-      const uint64_t dk = sdesc(smem_addr(sm + P::OFF_K)), dv = sdesc(smem_addr(sm + P::OFF_V));
-      [[maybe_unused]] const uint64_t dq = sdesc(smem_addr(sm));  // lo part of the query (head_dim 256)
       constexpr uint32_t kStep = P::IMG >> 4;
-      const int n_t = max(0, min(n_blk, vis_t - b0));  // tile blocks, one image each; window blocks two
-      Ring<NK> rk;
-      Ring<NV> rv;
-      Ring<NG> rs, rp;  // score columns: S to write, P to read
-      // S of a block from the image in slot rk, its first (hi) or second (lo) part
-      auto s_products = [&](bool lo_part) {
-        const uint64_t kd = dk + rk.slot * kStep;
-        const uint32_t t_s = tmem + P::T_S + KB * rs.slot;
+      auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail); };
+      constexpr int U = (R % NG == 0) ? R : R * NG;
+      if (warp == 4 * NG) {
+        const uint64_t dk = sdesc(smem_addr(sm + P::OFF_K));
+        [[maybe_unused]] const uint64_t dq = sdesc(smem_addr(sm));  // lo part of the query (head_dim 256)
+        for (int t0 = 0; t0 < n_blk; t0 += U) {
 #pragma unroll
-        for (int h = NP - 1; h >= 0; --h) {  // the query's lo part first: while the sums are small
-          if (h == 1 && lo_part) continue;   // lo x lo (2^-22) is dropped
+          for (int u = 0; u < U; ++u) {
+            const int t = t0 + u;
+            if (t >= n_blk) break;
+            const int sl = u % R, ss = u % NG;
+            if (u % P::LP == 0) wait(bar_fk + sl, (uint32_t)(t / R) & 1u);
+            // the columns are free when the group has read its scores from them, or, where P replaced the
+            // scores, when the product that reads P is complete
+            if (!P::SEP && t >= NG) wait(bar_dv + (t - NG) % R, (uint32_t)((t - NG) / R) & 1u);
+            __syncwarp();
+            if (P::SEP && t >= NG) take_over<160>(kBarRead + ss);
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t kd = dk + sl * kStep;
+              const uint32_t t_s = tmem + P::T_S + KB * ss;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
-            const uint32_t acc = lo_part || h < NP - 1 || kk > 0;
-            if (P::QL_SMEM && h == 1)
-              mma_ss(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>(), acc);
-            else
-              mma_ts(t_s, tmem + (h == 1 ? P::T_QL : P::T_QH) + 8 * kk, bd, idesc_f16<KB>(), acc);
+              for (int h = NP - 1; h >= 0; --h) {  // the query's lo part first: while the sums are small
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
+                  const uint32_t acc = h < NP - 1 || kk > 0;
+                  if (P::QL_SMEM && h == 1)
+                    mma_ss(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>(), acc);
+                  else
+                    mma_ts(t_s, tmem + (h == 1 ? P::T_QL : P::T_QH) + 8 * kk, bd, idesc_f16<KB>(), acc);
+                }
+              }
+              mma_commit(bar_dk + sl);
+            }
+            __syncwarp();
           }
         }
-        mma_commit(bar_ke + rk.slot);
-      };
-      auto o_products = [&](bool lo_part, bool first) {
-        const uint64_t vd = dv + rv.slot * kStep;
-        const uint32_t t_p = tmem + P::T_S + KB * rp.slot;  // 32 columns hi, then 32 lo
+      } else {
+        const uint64_t dv = sdesc(smem_addr(sm + P::OFF_V));
+        for (int t0 = 0; t0 < n_blk; t0 += U) {
 #pragma unroll
-        for (int kk = 0; kk < KB / 16; ++kk) {
-          const uint64_t bd = sdesc_add(vd, kk * 32);
-          mma_ts(t_o, t_p + 8 * kk, bd, idesc_f16<D>(), !first || kk > 0);
-          if (NP == 2 && !lo_part) mma_ts(t_o, t_p + 32 + 8 * kk, bd, idesc_f16<D>(), 1);
-        }
-        mma_commit(bar_ve + rv.slot);
-      };
-      auto all_done = [&](bool a0) { return __all_sync(0xffffffffu, a0); };
-      auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
-        return all_done(mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail));
-      };
-      // S of block j whose barriers were not tested yet
-      auto issue_s = [&](int j) -> bool {
-        for (int p = 0; p < (j < n_t ? 1 : 2); ++p) {
-          if (!wait(bar_kf + rk.slot, rk.phase)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            s_products(p == 1);
-            if (p == 1 || j < n_t) mma_commit(bar_s + rs.slot);
+          for (int u = 0; u < U; ++u) {
+            const int t = t0 + u;
+            if (t >= n_blk) break;
+            const int sl = u % R, ss = u % NG;
+            if (u % P::LP == 0) {
+              wait(bar_fv + sl, (uint32_t)(t / R) & 1u);
+              __syncwarp();
+            }
+            take_over<160>(kBarP + ss);
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t vd = dv + sl * kStep;
+              const uint32_t t_p = tmem + P::T_P + P::PSTEP * ss;  // 32 columns hi, then 32 lo
+#pragma unroll
+              for (int kk = 0; kk < KB / 16; ++kk) {
+                const uint64_t bd = sdesc_add(vd, kk * 32);
+                mma_ts(t_o, t_p + 8 * kk, bd, idesc_f16<D>(), t > 0 || kk > 0);
+                if (NP == 2) mma_ts(t_o, t_p + 32 + 8 * kk, bd, idesc_f16<D>(), 1);
+              }
+              mma_commit(bar_dv + sl);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          rk.next();
         }
-        rs.next();
-        return true;
-      };
-      bool ok = true;
-      for (int j = 0; ok && j < min(NG, n_blk); ++j) ok = issue_s(j);
-      int j = 0;
-      for (; ok && j + NG < n_t; ++j) {  // tile blocks whose successors are tile blocks
-        const bool r0 = mbar_test_parity(bar_p + rp.slot, rp.phase);
-        const bool r1 = mbar_test_parity(bar_vf + rv.slot, rv.phase);
-        const bool r2 = mbar_test_parity(bar_kf + rk.slot, rk.phase);
-        if (!all_done(r0 && r1 && r2) &&
-            !(wait(bar_p + rp.slot, rp.phase) && wait(bar_vf + rv.slot, rv.phase) && wait(bar_kf + rk.slot, rk.phase))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          o_products(false, j == 0);
-          s_products(false);
-          mma_commit(bar_s + rs.slot);
-        }
-        __syncwarp();
-        rp.next();
-        rv.next();
-        rk.next();
-        rs.next();
       }
-      for (; ok && j < n_blk; ++j) {  // and the rest
-        if (!wait(bar_p + rp.slot, rp.phase)) break;
-        for (int p = 0; ok && p < (j < n_t ? 1 : 2); ++p) {
-          if (!wait(bar_vf + rv.slot, rv.phase)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) o_products(p == 1, j == 0 && p == 0);
-          __syncwarp();
-          rv.next();
-        }
-        rp.next();
-        if (ok && j + NG < n_blk) ok = issue_s(j + NG);
-      }
-      // everything issued has completed before the CTA goes on: one commit behind it all
+      // everything issued has completed before the CTA goes on: a commit behind it all
       if (elect_one()) mma_commit(bar_o);
       __syncwarp();
-      if (!all_done(mbar_wait_timed(bar_o, 0, a.err, KVARN_DEVERR_WAIT))) *fail = 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_o, 0, a.err, KVARN_DEVERR_WAIT))) *fail = 1;
     }
     __syncwarp();
   } else {
@@ -472,11 +430,15 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     // so that the latencies of one are covered by the others' arithmetic. m and l are a thread's own;
     // u, which scales O, is decided block after block and handed from group to group.
     const int grp = warp >> 2, grp_before = (grp + NG - 1) % NG;
-    const uint32_t t_s = tmem + P::T_S + KB * grp + lb;
-    // a block's scales are read from L2 while the block before it is worked on
+    const uint32_t t_s = tmem + P::T_S + KB * grp + lb, t_p = tmem + P::T_P + P::PSTEP * grp + lb;
+    // a block's scales are read from L2 while the group's block before it is worked on
+    const int n_t = max(0, min(n_blk, vis_t - b0));  // tile blocks; window blocks follow
+    // of them, the leading ones that every row of the CTA sees whole
+    const int n_full = (int)max((int64_t)0, min((int64_t)n_t, (pmin + 1) / KB - b0));
+    const float* scales = s.scale + (int64_t)kvh * n_sub * 16;
     float ks_next[NGB] = {}, vs_next[NGB] = {};
     auto fetch_scales = [&](int j) {
-      const float4* p = reinterpret_cast<const float4*>(s.scale + ((int64_t)kvh * n_sub + sub_of(j)) * 16);
+      const float4* p = reinterpret_cast<const float4*>(scales + 16 * (j < n_t ? b0 + j : sub_of(j)));
 #pragma unroll
       for (int g = 0; g < NGB; g += 4) {
         const float4 x = p[g / 4], y = p[2 + g / 4];
@@ -486,14 +448,8 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     };
     pdl_wait();  // the scales belong to this call's images
     if (grp < n_blk) fetch_scales(grp);
+    auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail); };
     for (int j = grp; j < n_blk; j += NG) {
-      const int sub = sub_of(j);
-      const bool is_tile = sub < s.p.n_tsub;
-      const int64_t kpos0 = is_tile ? (int64_t)KB * sub : win_pos0 + (int64_t)KB * (sub - s.p.n_tsub);
-      const int nkeys = is_tile ? KB : min(KB, a.win_len - KB * (sub - s.p.n_tsub));
-      const bool full_vis = kpos0 + KB - 1 <= pmin && nkeys == KB;
-      // keys of the block this row sees
-      const int seen = !my_valid ? 0 : (int)max((int64_t)0, min((int64_t)nkeys, my_pos - kpos0 + 1));
       float ks[NGB], vs[NGB];
 #pragma unroll
       for (int g = 0; g < NGB; ++g) {
@@ -502,96 +458,102 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
         vs[g] = vs_next[g];
       }
       if (j + NG < n_blk) fetch_scales(j + NG);
-      if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_s + grp, (uint32_t)(j / NG) & 1u, a.err, KVARN_DEVERR_WAIT, fail))) break;
+      wait(bar_dk + j % R, (uint32_t)(j / R) & 1u);
+      __syncwarp();
       tc_fence_after();
+      float sv[KB];
+      tmem_ld32_nowait(t_s, *reinterpret_cast<uint32_t(*)[32]>(sv));
+      tmem_ld32_nowait(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+      // P's columns are free when the product that read the group's block before is complete
+      const int jb = j - NG;
+      const bool p_free = !P::SEP || j < NG || mbar_done(bar_dv + jb % R, (uint32_t)(jb / R) & 1u);
+      tmem_wait_ld(sv);
+      if (P::SEP) {
+        tc_fence_before();
+        if (j + NG < n_blk) hand_over<160>(kBarRead + grp);
+      }
+      if (j >= n_full) {  // keys of the block that this row sees
+        const int sub = sub_of(j);
+        const bool is_tile = sub < s.p.n_tsub;
+        const int64_t kpos0 = is_tile ? (int64_t)KB * sub : win_pos0 + (int64_t)KW * (sub - s.p.n_tsub);
+        const int nkeys = is_tile ? KB : min(KW, a.win_len - KW * (sub - s.p.n_tsub));
+        if (!is_tile) {
+#pragma unroll
+          for (int u = 0; u < KW; ++u) sv[u] += sv[KW + u];  // hi and lo part of a key
+        }
+        const int seen = !my_valid ? 0 : (int)max((int64_t)0, min((int64_t)nkeys, my_pos - kpos0 + 1));
+#pragma unroll
+        for (int u = 0; u < KB; ++u)
+          if (u >= seen) sv[u] = -INFINITY;
+      }
       float mblk = -INFINITY, ublk = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < KB; c += 64) {
-        float sv[64];
-        tmem_ld32_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(sv));
-        tmem_ld32_nowait(t_s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-        tmem_wait_ld(sv);
-        if (!full_vis) {
+      for (int g = 0; g < NGB; ++g) {
+        float m = sv[16 * g];
 #pragma unroll
-          for (int u = 0; u < 64; ++u)
-            if (c + u >= seen) sv[u] = -INFINITY;
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float m = sv[16 * g];
-#pragma unroll
-          for (int u = 1; u < 15; u += 2) m = fmax3(m, sv[16 * g + u], sv[16 * g + u + 1]);
-          m = fmaxf(m, sv[16 * g + 15]) * ks[c / 16 + g];
-          mblk = fmaxf(mblk, m);
-          ublk = fmaxf(ublk, m + fast_lg2(vs[c / 16 + g]));
-        }
+        for (int u = 1; u < 15; u += 2) m = fmax3(m, sv[16 * g + u], sv[16 * g + u + 1]);
+        m = fmaxf(m, sv[16 * g + 15]) * ks[g];
+        mblk = fmaxf(mblk, m);
+        ublk = fmaxf(ublk, m + fast_lg2(vs[g]));
       }
-      const float m_new = mblk > m_ref + kLag ? mblk : m_ref;
-      l_part *= m_ref != -INFINITY ? fast_ex2(m_ref - m_new) : 1.f;
-      m_ref = m_new;
       // u after the block before, from the group that has it
       float u_old = -INFINITY;
       if (j > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_u + 4 * grp_before + (warp & 3), (uint32_t)((j - 1) / NG) & 1u,
-                                                     a.err, KVARN_DEVERR_WAIT, fail)))
-          break;
+        take_over<256>(kBarU + grp_before);
         u_old = su[grp_before * 128 + row];
       }
       const bool need = ublk > u_old + kLag;
       const float u_ref = need ? ublk : u_old;
       su[grp * 128 + row] = u_ref;
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(bar_u + 4 * grp + (warp & 3));
+      if (j + 1 < n_blk) hand_over<256>(kBarU + grp);
+      const float m_new = mblk > m_ref + kLag ? mblk : m_ref;
+      l_part *= m_ref != -INFINITY ? fast_ex2(m_ref - m_new) : 1.f;
+      m_ref = m_new;
       // a row with no visible key yet subtracts +inf and gets 0
       const bool none = m_ref == -INFINITY;
       const float msub = none ? INFINITY : m_ref;
       const float fu = none ? 0.f : fast_ex2(fminf(m_ref - u_ref + kHead, 126.f));
       float2 ls2 = make_float2(0.f, 0.f);
       const float2 nm2 = make_float2(-msub, -msub);
+      uint32_t hw[KB / 2], lw[KB / 2];
 #pragma unroll
-      for (int c = 0; c < KB; c += 64) {
-        float sv[64];
-        tmem_ld32_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(sv));
-        tmem_ld32_nowait(t_s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-        tmem_wait_ld(sv);
-        if (!full_vis) {
+      for (int g = 0; g < NGB; ++g) {
+        float f = vs[g] * fu;
+        if (f > 1e30f) f = 1e30f;  // belongs to probabilities below 2^-90
+        const float2 k2 = make_float2(ks[g], ks[g]), f2 = make_float2(f, f);
 #pragma unroll
-          for (int u = 0; u < 64; ++u)
-            if (c + u >= seen) sv[u] = -INFINITY;
-        }
-        uint32_t hw[32], lw[32];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float f = vs[c / 16 + g] * fu;
-          if (f > 1e30f) f = 1e30f;  // belongs to probabilities below 2^-90
-          const float2 k2 = make_float2(ks[c / 16 + g], ks[c / 16 + g]), f2 = make_float2(f, f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, nm2);
-            const float2 p = make_float2(fast_ex2(x.x), fast_ex2(x.y));
-            ls2 = __fadd2_rn(ls2, p);
-            const float2 w = __fmul2_rn(p, f2);
-            if constexpr (NP == 2) {
-              split_pair(w.x, w.y, hw[8 * g + e], lw[8 * g + e]);
-            } else {
-              const __half2 h = __floats2half2_rn(w.x, w.y);
-              hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+        for (int e = 0; e < 8; ++e) {
+          const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, nm2);
+          const float2 p = make_float2(fast_ex2(x.x), fast_ex2(x.y));
+          ls2 = __fadd2_rn(ls2, p);
+          const float2 w = __fmul2_rn(p, f2);
+          if constexpr (NP == 2) {
+            split_pair(w.x, w.y, hw[8 * g + e], lw[8 * g + e]);
+          } else {
+            const __half2 h = __floats2half2_rn(w.x, w.y);
+            hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
-        // w replaces the scores of these 64 keys: hi in the first 32 columns, lo in the others
-        tmem_st32_nowait(t_s + c, hw);
-        if constexpr (NP == 2) tmem_st32_nowait(t_s + c + 32, lw);
       }
+      if (j >= n_t) {  // a window key's weight meets both parts of its value
+#pragma unroll
+        for (int e = 0; e < KW / 2; ++e) {
+          hw[KW / 2 + e] = hw[e];
+          if constexpr (NP == 2) lw[KW / 2 + e] = lw[e];
+        }
+      }
+      if (!p_free) wait(bar_dv + jb % R, (uint32_t)(jb / R) & 1u);
+      __syncwarp();
+      if (P::SEP) tc_fence_after();
+      // w: hi in 32 columns, lo in the 32 after
+      tmem_st32_nowait(t_p, hw);
+      if constexpr (NP == 2) tmem_st32_nowait(t_p + 32, lw);
       l_part += ls2.x + ls2.y;
       // O belongs to the previous block's product until that completes
       if (j > 0 && __any_sync(0xffffffffu, need)) {
         const float alpha = need && u_old != -INFINITY ? fast_ex2(u_old - u_ref) : 1.f;
-        // its last V image is read when it is complete
-        const int n_t = max(0, min(n_blk, vis_t - b0));
-        const int im = j <= n_t ? j - 1 : n_t + 2 * (j - n_t) - 1;
-        if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_ve + im % NV, (uint32_t)(im / NV) & 1u, a.err, KVARN_DEVERR_WAIT, fail)))
-          break;
+        wait(bar_dv + (j - 1) % R, (uint32_t)((j - 1) / R) & 1u);
+        __syncwarp();
         tc_fence_after();
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -604,8 +566,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       }
       tmem_wait_st();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(bar_p + grp);
+      hand_over<160>(kBarP + grp);
     }
   }
   tc_fence_before();
@@ -689,8 +650,8 @@ Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D) {
   Plan8 p;
   const int KB = PC8<64, 1>::KB, G = Hq / Hkv, ppc = 128 / G;
   p.n_tsub = n_tblk * (kTile / KB);
-  p.n_wsub = (win_vis + KB - 1) / KB;
-  p.head_imgs = 2LL * p.n_tsub + 4LL * p.n_wsub;
+  p.n_wsub = (win_vis + 2 * PC8<64, 1>::KW - 1) / (2 * PC8<64, 1>::KW) * 2;
+  p.head_imgs = 2LL * (p.n_tsub + p.n_wsub);
   p.row_blocks = (C + ppc - 1) / ppc;
   const int64_t ctas = (int64_t)p.row_blocks * Hkv;
   int64_t shares = ctas > 0 ? sm_count() / ctas : 1;
@@ -719,7 +680,7 @@ cudaError_t launch_p8(const Att8Args& s, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  const int blocks = s.p.n_tsub / P::SUB + 2 * s.p.n_wsub * P::NGB;
+  const int blocks = s.p.n_tsub / P::SUB + 2 * s.p.n_wsub * (P::KW / kGrp);
   image8_kernel<D, F><<<dim3(blocks, s.a.Hkv), 256, 0, st>>>(s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

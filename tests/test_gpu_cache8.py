@@ -313,7 +313,7 @@ def test_prefill_head_groups(G):
 
 @pytest.mark.parametrize("tiles,window,C,pos0", [
     (0, 1, 1, 0), (0, 130, 130, 0), (1, 0, 128, 0), (1, 0, 1, 127), (3, 5, 20, 0), (3, 300, 64, 100),
-    (3, 300, 64, 3 * T - 10), (30, 0, 3, 30 * T - 3), (30, 64, 1, 30 * T + 63), (61, 17, 2, 900),
+    (3, 300, 64, 3 * T - 10), (0, 500, 90, 410), (1, 500, 3, 625), (30, 0, 3, 30 * T - 3), (30, 64, 1, 30 * T + 63), (61, 17, 2, 900),
     (5, 129, 500, 5 * T + 129 - 500)])
 @pytest.mark.parametrize("D", [128, 256])
 def test_prefill_lengths_and_positions(tiles, window, C, pos0, D):
