@@ -120,6 +120,14 @@ __device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// mbar_wait_timed that looks at the clock only after a while: reading the global timer takes longer than
+// most waits.
+__device__ __forceinline__ bool mbar_wait8(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* stop = nullptr) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_test_parity(bar, parity)) return true;
+  return mbar_wait_timed(bar, parity, err, KVARN_DEVERR_WAIT, stop);
+}
 // Global -> shared copy (16-byte aligned addresses, size a multiple of 16) that
 // completes on bar, whose transaction count was announced by mbar_arrive_tx.
 __device__ __forceinline__ void bulk_in(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   const int grp = (warp * C::NT) >> 1;  // scale entry of this warp's tokens
 
   auto scores = [&](int i) {  // scores of tile i's tokens 8 NT warp .., and their row maxima
-    ok &= mbar_wait_timed(bar + i % kStages, (uint32_t)(i / kStages) & 1u, a.err, KVARN_DEVERR_WAIT);
+    ok &= mbar_wait8(bar + i % kStages, (uint32_t)(i / kStages) & 1u, a.err);
     const unsigned char* rec = smem + (i % kStages) * C::SLOT;
     const float kc = reinterpret_cast<const float*>(rec + R::kKScale)[grp] * c1;
     vs = reinterpret_cast<const float*>(rec + R::kVScale)[grp];

@@ -58,7 +58,7 @@ struct PC8 {
   static constexpr int OFF_K = QL_BYTES;
   static constexpr int OFF_V = OFF_K + R * IMG;
   static constexpr int OFF_BAR = OFF_V + R * IMG;
-  static constexpr int OFF_X = OFF_BAR + 256;              // float2 [NG][128]: (m, l) of a row's threads
+  static constexpr int OFF_X = OFF_BAR + 256;              // float2 [NG][128]: (u, l) of a row's threads
   static constexpr int OFF_U = OFF_X + NG * 128 * 8;       // float [NG][128]: reference u after a group's block
   static constexpr int OFF_MISC = OFF_U + NG * 128 * 4;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;        // + slack to align the base to 1024
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   __syncthreads();
   tc_fence_after();
 
-  float m_ref = -INFINITY, l_part = 0.f;
+  float u_own = -INFINITY, l_part = 0.f;  // softmax threads: sum of probabilities, in units of 2^u_own
   if (warp >= 4 * NG + 2) {
     // ---------------- copies: one thread for the K images, one for the V images
     if (lane == 0 && n_blk > 0) {
@@ -335,13 +335,13 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       int t = 0;
       for (; t < n_blk; t += P::LP) {  // (a pair's second image is copied even if no row sees it)
         const int sl = t % R, last = t - R + P::LP - 1;  // the last block that used the slots
-        if (t >= R) mbar_wait_timed(done + last % R, (uint32_t)(last / R) & 1u, a.err, KVARN_DEVERR_WAIT, fail);
+        if (t >= R) mbar_wait8(done + last % R, (uint32_t)(last / R) & 1u, a.err, fail);
         mbar_arrive_tx(full + sl, P::LP * P::IMG);
         bulk_in(ring + sl * P::IMG, src + image_index(sub_of(t)) * P::IMG, P::LP * P::IMG, full + sl);
       }
       // every copy has landed before the CTA can retire
       for (int i = max(0, t - R); i < t; i += P::LP)
-        mbar_wait_timed(full + i % R, (uint32_t)(i / R) & 1u, a.err, KVARN_DEVERR_WAIT);
+        mbar_wait8(full + i % R, (uint32_t)(i / R) & 1u, a.err);
     }
     __syncwarp();
   } else if (warp >= 4 * NG) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     // slots, addresses and descriptors are constants.
     if (n_blk > 0) {
       constexpr uint32_t kStep = P::IMG >> 4;
-      auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail); };
+      auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait8(bar, par, a.err, fail); };
       constexpr int U = (R % NG == 0) ? R : R * NG;
       if (warp == 4 * NG) {
         const uint64_t dk = sdesc(smem_addr(sm + P::OFF_K));
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       // everything issued has completed before the CTA goes on: a commit behind it all
       if (elect_one()) mma_commit(bar_o);
       __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait_timed(bar_o, 0, a.err, KVARN_DEVERR_WAIT))) *fail = 1;
+      if (!__all_sync(0xffffffffu, mbar_wait8(bar_o, 0, a.err))) *fail = 1;
     }
     __syncwarp();
   } else {
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     };
     pdl_wait();  // the scales belong to this call's images
     if (grp < n_blk) fetch_scales(grp);
-    auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait_timed(bar, par, a.err, KVARN_DEVERR_WAIT, fail); };
+    auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait8(bar, par, a.err, fail); };
     for (int j = grp; j < n_blk; j += NG) {
       float ks[NGB], vs[NGB];
 #pragma unroll
@@ -486,15 +486,16 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
         for (int u = 0; u < KB; ++u)
           if (u >= seen) sv[u] = -INFINITY;
       }
-      float mblk = -INFINITY, ublk = -INFINITY;
+      // largest score of each group of keys, and of the row's weighted scores
+      float mg[NGB], lv[NGB], ublk = -INFINITY;
 #pragma unroll
       for (int g = 0; g < NGB; ++g) {
         float m = sv[16 * g];
 #pragma unroll
         for (int u = 1; u < 15; u += 2) m = fmax3(m, sv[16 * g + u], sv[16 * g + u + 1]);
-        m = fmaxf(m, sv[16 * g + 15]) * ks[g];
-        mblk = fmaxf(mblk, m);
-        ublk = fmaxf(ublk, m + fast_lg2(vs[g]));
+        mg[g] = fmaxf(m, sv[16 * g + 15]) * ks[g];
+        lv[g] = fast_lg2(vs[g]);
+        ublk = fmaxf(ublk, mg[g] + lv[g]);
       }
       // u after the block before, from the group that has it
       float u_old = -INFINITY;
@@ -506,27 +507,23 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       const float u_ref = need ? ublk : u_old;
       su[grp * 128 + row] = u_ref;
       if (j + 1 < n_blk) hand_over<256>(kBarU + grp);
-      const float m_new = mblk > m_ref + kLag ? mblk : m_ref;
-      l_part *= m_ref != -INFINITY ? fast_ex2(m_ref - m_new) : 1.f;
-      m_ref = m_new;
-      // a row with no visible key yet subtracts +inf and gets 0
-      const bool none = m_ref == -INFINITY;
-      const float msub = none ? INFINITY : m_ref;
-      const float fu = none ? 0.f : fast_ex2(fminf(m_ref - u_ref + kHead, 126.f));
-      float2 ls2 = make_float2(0.f, 0.f);
-      const float2 nm2 = make_float2(-msub, -msub);
+      // (a row with no visible key yet has scores of -inf only, and any reference does)
+      const float u = u_ref == -INFINITY ? 0.f : u_ref;
+      l_part *= u_own != -INFINITY ? fast_ex2(u_own - u_ref) : 1.f;
+      u_own = u_ref;
       uint32_t hw[KB / 2], lw[KB / 2];
 #pragma unroll
       for (int g = 0; g < NGB; ++g) {
-        float f = vs[g] * fu;
-        if (f > 1e30f) f = 1e30f;  // belongs to probabilities below 2^-90
-        const float2 k2 = make_float2(ks[g], ks[g]), f2 = make_float2(f, f);
+        // a group whose weights vanish beside the row's largest (2^-kHead of a step of fp16) is given more
+        // weight, none of which reaches the product, so that l still counts its probabilities
+        const float le = fmaxf(lv[g], u - fmaxf(mg[g], -1e30f) - (kHead + 50.f));
+        const float2 k2 = make_float2(ks[g], ks[g]), c2 = make_float2(le + kHead - u, le + kHead - u);
+        float2 ls2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, nm2);
-          const float2 p = make_float2(fast_ex2(x.x), fast_ex2(x.y));
-          ls2 = __fadd2_rn(ls2, p);
-          const float2 w = __fmul2_rn(p, f2);
+          const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, c2);
+          const float2 w = make_float2(fast_ex2(x.x), fast_ex2(x.y));
+          ls2 = __fadd2_rn(ls2, w);
           if constexpr (NP == 2) {
             split_pair(w.x, w.y, hw[8 * g + e], lw[8 * g + e]);
           } else {
@@ -534,6 +531,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
             hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
+        l_part = fmaf(ls2.x + ls2.y, fast_ex2(-le - kHead), l_part);
       }
       if (j >= n_t) {  // a window key's weight meets both parts of its value
 #pragma unroll
@@ -548,7 +546,6 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       // w: hi in 32 columns, lo in the 32 after
       tmem_st32_nowait(t_p, hw);
       if constexpr (NP == 2) tmem_st32_nowait(t_p + 32, lw);
-      l_part += ls2.x + ls2.y;
       // O belongs to the previous block's product until that completes
       if (j > 0 && __any_sync(0xffffffffu, need)) {
         const float alpha = need && u_old != -INFINITY ? fast_ex2(u_old - u_ref) : 1.f;
@@ -573,22 +570,19 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   __syncthreads();
   tc_fence_after();
   const bool ok = *fail == 0;
-  if (warp < 4 * NG) xm[(warp >> 2) * 128 + row] = make_float2(m_ref, l_part);
+  if (warp < 4 * NG) xm[(warp >> 2) * 128 + row] = make_float2(u_own, l_part);
   __syncthreads();
   // ---- epilogue: half of a row's channels per thread
   if (tid < 256) {
-    float m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) m = fmaxf(m, xm[g * 128 + row].x);
-    const bool any = n_blk > 0 && m != -INFINITY;
+    // O and the sum l in units of 2^u, u after the last block
+    const float u = n_blk > 0 ? su[((n_blk - 1) % NG) * 128 + row] : -INFINITY;
+    float l = 0.f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const float2 v = xm[g * 128 + row];
-      l += any ? v.y * fast_ex2(v.x - m) : v.y;  // (a NaN l without a maximum stays)
+      l += v.x != -INFINITY ? v.y * fast_ex2(v.x - u) : v.y;  // (no reference: 0, or NaN of NaN scores)
     }
-    // O is in units of 2^(u - kHead), l in units of 2^m
-    const float u = n_blk > 0 ? su[((n_blk - 1) % NG) * 128 + row] : 0.f;
-    float f = any ? fast_ex2(u - kHead - m) : 0.f;
+    float f = pow2_inverse(256.f);  // 2^-kHead
     if (s.p.shares == 1) f = l != 0.f ? f / l : 0.f;
     if (!ok) f = NAN;
     const int64_t orow = (int64_t)my_i * a.Hq + hq;
@@ -613,7 +607,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       }
     }
     if (s.p.shares > 1 && my_valid && half == 0)
-      s.ml[prow] = ok ? make_float2(any ? m : -INFINITY, l) : make_float2(0.f, NAN);
+      s.ml[prow] = ok ? make_float2(u, l) : make_float2(0.f, NAN);
   }
   tc_fence_before();
   __syncthreads();
