@@ -20,7 +20,7 @@
 // The weighted probabilities have a reference exponent u of their own (their running
 // maximum), so that any ratio between the value scales keeps its 22 bits.
 //
-// Records arrive by bulk copies, kStages of them in flight per CTA. Their code order is
+// Records arrive by bulk copies into a ring of slots. Their code order is
 // made for this kernel: a warp's 16-byte reads cover 512 consecutive bytes, and what a
 // lane reads is what it needs of the B fragments of four products, up to an order of the
 // summed index (channels, or tokens) that both operands share.
@@ -33,26 +33,30 @@ namespace kvarn {
 namespace {
 
 constexpr float kNone = -3.0e38f;  // reference exponent before the first tile
-constexpr int kStages = 3;
 constexpr int kPRow = 576;          // bytes per head of the probability buffer (4 bytes x 2 parts x 64 pairs + pad)
 constexpr float kHead = 14.f;       // weighted probabilities reach 2^14: lo parts stay normal fp16 numbers
 
 template <int D_>
 struct D8 {
   static constexpr int D = D_;
-  static constexpr int NW = D == 256 ? 16 : 8;   // warps per CTA
+  static constexpr int NW = 8;                   // warps per CTA
   static constexpr int NTHR = 32 * NW;
   static constexpr int NT = 16 / NW;             // 8-token column tiles of the scores per warp
   static constexpr int NC = D / 8 / NW;          // 8-channel column tiles of the values per warp
   static constexpr int NJ = D / 64;              // 64-channel runs
-  static constexpr int SLOT = Rec8<D>::kBytes;
-  static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 2 : 1;  // resident per SM
+  // A record arrives as two copies, K codes with the scales behind them, and V codes, each in a slot of a
+  // ring: two (four, at head_dim 64) CTAs per SM have some 100 KB in flight or in use, and a CTA's
+  // exchanges are covered by the other's work
+  static constexpr int HALF = kTile * D;         // bytes of K or of V codes
+  static constexpr int SLOT = HALF + 128;
+  static constexpr int SLOTS = D == 256 ? 3 : 6;
+  static constexpr int CTAS = D == 64 ? 4 : 2;   // resident per SM
   static constexpr int WROWS = 8 * NW;           // window rows per window item
-  static constexpr int OFF_P = kStages * SLOT;
+  static constexpr int OFF_P = SLOTS * SLOT;
   static constexpr int OFF_MX = OFF_P + 8 * kPRow;              // float2 [8][NW]: (max s, max s + log2 vscale)
   static constexpr int OFF_L = OFF_MX + 8 * NW * 8;             // float [NW][8]
   static constexpr int OFF_BAR = OFF_L + 8 * NW * 4;
-  static constexpr int OFF_FLG = OFF_BAR + 8 * kStages;         // int: a wait ran out or a record was refused
+  static constexpr int OFF_FLG = OFF_BAR + 8 * SLOTS;         // int: a wait ran out or a record was refused
   static constexpr int SMEM = (OFF_FLG + 8 + 127) / 128 * 128;
   static_assert(SLOT % 128 == 0 && OFF_P % 128 == 0, "alignment");
   static_assert(8 * (WROWS + 4) * 4 <= 8 * kPRow, "window probabilities fit");
@@ -226,23 +230,31 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     return;
   }
   const int64_t* table = a.tile_table + ((int64_t)b * a.Hkv + kvh) * a.max_tiles + first;
-  auto request = [&](int i) {  // one thread: tile i of the item into its stage
-    uint64_t* br = bar + i % kStages;
-    const int64_t off = table[i];
+  auto request = [&](int n) {  // one thread: copy n of the item (K, then V of each tile) into its slot
+    if (n >= 2 * nt) return;
+    uint64_t* br = bar + n % C::SLOTS;
+    unsigned char* dst = smem + (n % C::SLOTS) * C::SLOT;
+    const int64_t off = table[n >> 1];
     if ((off & 15) || off < 0 || off > a.tiles_bytes - R::kBytes) {
       report(a.err, KVARN_DEVERR_RECORD);
       *flag = 1;
       mbar_arrive1(br);
       return;
     }
-    mbar_arrive_tx(br, R::kBytes);
-    bulk_in(smem + (i % kStages) * C::SLOT, a.tiles + off, R::kBytes, br);
+    if (n & 1) {
+      mbar_arrive_tx(br, C::HALF);
+      bulk_in(dst, a.tiles + off + R::kVCodes, C::HALF, br);
+    } else {
+      mbar_arrive_tx(br, C::HALF + 8 * kGrps);
+      bulk_in(dst, a.tiles + off + R::kKCodes, C::HALF, br);
+      bulk_in(dst + C::HALF, a.tiles + off + R::kKScale, 8 * kGrps, br);
+    }
   };
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init_n(bar + i, 1);
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init_n(bar + i, 1);
     mbar_fence_init();
     *flag = 0;
-    for (int i = 0; i < min(nt, kStages); ++i) request(i);
+    for (int i = 0; i < C::SLOTS; ++i) request(i);
   }
   if (early) pdl_wait();
   pdl_trigger();
@@ -285,18 +297,19 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   bool ok = true;
   const int grp = (warp * C::NT) >> 1;  // scale entry of this warp's tokens
 
+  auto landed = [&](int n) { return mbar_wait8(bar + n % C::SLOTS, (uint32_t)(n / C::SLOTS) & 1u, a.err); };
   auto scores = [&](int i) {  // scores of tile i's tokens 8 NT warp .., and their row maxima
-    ok &= mbar_wait8(bar + i % kStages, (uint32_t)(i / kStages) & 1u, a.err);
-    const unsigned char* rec = smem + (i % kStages) * C::SLOT;
-    const float kc = reinterpret_cast<const float*>(rec + R::kKScale)[grp] * c1;
-    vs = reinterpret_cast<const float*>(rec + R::kVScale)[grp];
+    ok &= landed(2 * i);
+    const unsigned char* rec = smem + (2 * i % C::SLOTS) * C::SLOT;
+    const float kc = reinterpret_cast<const float*>(rec + C::HALF)[grp] * c1;
+    vs = reinterpret_cast<const float*>(rec + C::HALF)[kGrps + grp];
     float mw = -INFINITY;
 #pragma unroll
     for (int t = 0; t < C::NT; ++t) {
       float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j) {
-        const uint4 w = *reinterpret_cast<const uint4*>(rec + R::kKCodes +
+        const uint4 w = *reinterpret_cast<const uint4*>(rec +
                                                         ((warp * C::NT + t) * C::NJ + j) * 512 + lane * 16);
         uint32_t b0, b1;
         codes_to_half<F>(w.x, b0, b1); mma_f16(c, qa[4 * j], b0, b1);
@@ -315,7 +328,10 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   scores(0);
   for (int i = 0; i < nt; ++i) {
     __syncthreads();  // row maxima of tile i are in; tile i - 1 and its probabilities are used up
-    if (tid == 0 && i > 0 && i - 1 + kStages < nt) request(i - 1 + kStages);
+    if (tid == 0) {  // the slots of V of tile i - 1 and of K of tile i are free
+      if (i > 0) request(2 * i - 1 + C::SLOTS);
+      request(2 * i + C::SLOTS);
+    }
     float Mn = M, Un = U;
 #pragma unroll
     for (int w = 0; w < C::NW; w += 2) {
@@ -361,7 +377,8 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[c][r] *= ao;
     }
-    const unsigned char* V = smem + (i % kStages) * C::SLOT + R::kVCodes;
+    ok &= landed(2 * i + 1);
+    const unsigned char* V = smem + ((2 * i + 1) % C::SLOTS) * C::SLOT;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 w[C::NC];
