@@ -32,7 +32,7 @@ __device__ __forceinline__ void tile_place(int tid, int& grp, int& col) {
 // fp32 step of x / s and on the same side of (or equal to) every midpoint of two codes as
 // the exact quotient. y is refined once from the reciprocal (Markstein's correction); a
 // y that falls on a short value although the remainder is not zero moves one step off it.
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
+__device__ __noinline__ float quotient(float x, float s, float inv) {
   const float y0 = x * inv;
   const float y = fmaf(fmaf(-y0, s, x), inv, y0);
   const float e = fmaf(-y, s, x);  // sign of (x / s - y), s > 0
@@ -40,6 +40,18 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
   if ((u & 0xFFFu) == 0u && e != 0.f && (u << 1) != 0u)
     return __uint_as_float((e > 0.f) == (y > 0.f) ? u + 1u : u - 1u);
   return copysignf(y, x);  // (the correction turns -0 into 0)
+}
+// The same for four values. x * inv is within two steps of the quotient, and the midpoints end in 12
+// zero bits: only a product within three steps of such a value (one in 600) needs the care above.
+__device__ __forceinline__ void quotients(const float4& x, float s, float inv, float (&y)[4]) {
+  y[0] = x.x * inv; y[1] = x.y * inv; y[2] = x.z * inv; y[3] = x.w * inv;
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) near |= ((__float_as_uint(y[i]) + 3u) & 0xFFFu) < 7u;
+  if (near) {
+    y[0] = quotient(x.x, s, inv); y[1] = quotient(x.y, s, inv);
+    y[2] = quotient(x.z, s, inv); y[3] = quotient(x.w, s, inv);
+  }
 }
 
 template <int F>
@@ -98,8 +110,8 @@ __device__ __forceinline__ void compress_tensor(const float* __restrict__ src, i
   uint32_t w[16];
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
-    const float y[4] = {finite ? quotient(x[t].x, s, inv) : 0.f, finite ? quotient(x[t].y, s, inv) : 0.f,
-                        finite ? quotient(x[t].z, s, inv) : 0.f, finite ? quotient(x[t].w, s, inv) : 0.f};
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    if (finite) quotients(x[t], s, inv, y);
     w[t] = encode4<F>(y);
   }
   if constexpr (IS_V) {

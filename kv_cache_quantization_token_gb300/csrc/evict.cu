@@ -5,15 +5,22 @@
 // selection finds the weight T of the lightest tile that stays and how many tiles of weight
 // exactly T do (the lowest indices); a running count then moves each tile to its place.
 //
-// One CTA per sequence: all its KV heads share n, so n_tiles can be updated in place after a
-// barrier, and groups of threads (one per KV head) go through the passes in step. The data is
-// a few hundred KB at most, read from L1 after the first pass; latency bounds the call.
+// One CTA per KV head; the CTAs of a sequence form a cluster (of 8 at most; more heads are taken in turn),
+// so that n_tiles can be updated in place once all of them have read it. A histogram pass counts with
+// shared-memory atomics, a run of 32 x 256 tiles is ranked with two scans, and an entry moves only after
+// all entries up to its run's eighth have been read. The data is a few hundred KB at most, read from L1
+// after the first pass; latency bounds the call.
+#include <cooperative_groups.h>
+
 #include "cache8.cuh"
 
 namespace kvarn {
 namespace {
 
-constexpr int kThreads = 1024;
+namespace cg = cooperative_groups;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRun = 32;    // tiles per thread of a run: one bit each of a word
+constexpr int kBatch = 8;   // tiles per thread read before any is moved
 
 // Unsigned keys in the order of the weights: -0 as 0, NaN as +infinity.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -21,130 +28,176 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// GT: threads per KV head, a power of two of at least 32.
-template <int GT>
+// Exclusive sums of count[0 .. 255] in place; returns the total. One value per thread.
+__device__ __forceinline__ unsigned scan(unsigned* count, unsigned* warp_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __syncthreads();
+  const unsigned v = count[tid];
+  unsigned x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned o = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += o;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  unsigned base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const unsigned t = warp_sum[w];
+    base += w < warp ? t : 0u;
+    total += t;
+  }
+  count[tid] = base + x - v;
+  __syncthreads();
+  return total;
+}
+
 __global__ void __launch_bounds__(kThreads) evict_kernel(const int64_t* table, const float* mass,
                                                          const int32_t* n_tiles, int64_t* table_out,
                                                          float* mass_out, int32_t* n_out,
                                                          int64_t* evicted, int Hkv, int max_tiles,
                                                          int keep, int sinks, int recent) {
-  constexpr int GROUPS = kThreads / GT, GW = GT / 32;
-  __shared__ unsigned hist[GROUPS][256];
-  __shared__ unsigned found[GROUPS][2];         // digit prefix, how many are still to take
-  __shared__ unsigned count[GROUPS][2][GW];     // per warp: tiles of weight T, tiles that stay
+  __shared__ unsigned hist[256], count[kRun * kWarps], warp_sum[kWarps];
+  __shared__ unsigned found[2];  // digit prefix, how many are still to take
+  static_assert(kRun * kWarps == kThreads, "one count per thread");
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x, tid = threadIdx.x, gi = tid / GT, gt = tid % GT;
-  const int lane = tid & 31, gw = gt >> 5;
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned below = (1u << lane) - 1u;
   const int n = min(max(n_tiles[b], 0), max_tiles);
-  __syncthreads();  // every thread has n
-  if (tid == 0) n_out[b] = min(n, keep);
+  cg::this_cluster().sync();  // every CTA of the sequence has n
+  if (blockIdx.x == 0 && tid == 0) n_out[b] = min(n, keep);
   const int lo = sinks, hi = n - recent, take = keep - sinks - recent;
-  for (int h0 = 0; h0 < Hkv; h0 += GROUPS) {
-    const bool live = h0 + gi < Hkv;
-    const int64_t base = ((int64_t)b * Hkv + (live ? h0 + gi : 0)) * max_tiles;
+  for (int h = blockIdx.x; h < Hkv; h += gridDim.x) {
+    const int64_t base = ((int64_t)b * Hkv + h) * max_tiles;
     const int64_t* tab = table + base;
     const float* wt = mass + base;
     int64_t* tab_o = table_out + base;
     float* wt_o = mass_out + base;
     int64_t* ev = evicted ? evicted + base : nullptr;
-    if (n <= keep) {  // the same for all heads of the sequence
-      if (live)
-        for (int i = gt; i < max_tiles; i += GT) {
-          const int64_t t = i < n ? tab[i] : -1;
-          const float w = i < n ? wt[i] : 0.f;
-          tab_o[i] = t;
-          wt_o[i] = w;
-          if (ev) ev[i] = -1;
-        }
+    if (n <= keep) {
+      for (int i = tid; i < max_tiles; i += kThreads) {
+        const int64_t t = i < n ? tab[i] : -1;
+        const float w = i < n ? wt[i] : 0.f;
+        tab_o[i] = t;
+        wt_o[i] = w;
+        if (ev) ev[i] = -1;
+      }
       continue;
     }
     unsigned prefix = 0, rem = (unsigned)take;
-    if (take > 0) {
 #pragma unroll 1
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = gt; i < 256; i += GT) hist[gi][i] = 0u;
-        __syncthreads();
-        if (live)
-          for (int i = lo + gt; i < hi; i += GT) {
-            const uint32_t k = weight_key(wt[i]);
-            if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[gi][(k >> shift) & 255u], 1u);
-          }
-        __syncthreads();
-        if (gw == 0) {
-          // lane l holds digits 255 - 8 l .. 248 - 8 l: the digit at which the running count reaches rem
-          unsigned c[8], sum = 0;
+    for (int shift = 24; take > 0 && shift >= 0; shift -= 8) {
+      hist[tid] = 0u;
+      __syncthreads();
+#pragma unroll 4
+      for (int i = lo + tid; i < hi; i += kThreads) {
+        const uint32_t k = weight_key(wt[i]);
+        if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (warp == 0) {
+        // lane l holds digits 255 - 8 l .. 248 - 8 l: the digit at which the running count reaches rem
+        unsigned c[8], sum = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum += c[i] = hist[gi][255 - 8 * lane - i];
-          unsigned before = sum;
+        for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+        unsigned before = sum;
 #pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const unsigned o = __shfl_up_sync(0xffffffffu, before, d);
-            if (lane >= d) before += o;
-          }
-          before -= sum;
-          if (before < rem && before + sum >= rem) {
-            unsigned left = rem - before;
-            int i = 0;
-            while (left > c[i]) left -= c[i++];
-            found[gi][0] = (prefix << 8) | (unsigned)(255 - 8 * lane - i);
-            found[gi][1] = left;
-          }
+        for (int d = 1; d < 32; d <<= 1) {
+          const unsigned o = __shfl_up_sync(0xffffffffu, before, d);
+          if (lane >= d) before += o;
         }
-        __syncthreads();
-        if (live) {
-          prefix = found[gi][0];
-          rem = found[gi][1];
+        before -= sum;
+        if (before < rem && before + sum >= rem) {
+          unsigned left = rem - before, digit = 0, rest = 0;
+          bool open = true;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (open && left <= c[i]) {
+              digit = 255 - 8 * lane - i;
+              rest = left;
+              open = false;
+            }
+            left -= c[i];
+          }
+          found[0] = (prefix << 8) | digit;
+          found[1] = rest;
         }
       }
+      __syncthreads();
+      prefix = found[0];
+      rem = found[1];
     }
     unsigned ties = 0, stay = 0;  // tiles of weight T, and tiles that stay, before this run
-    for (int i0 = 0; i0 < n; i0 += GT) {
-      const int i = i0 + gt;
-      const bool in = live && i < n;
-      const int64_t t = in ? tab[i] : 0;
-      const float w = in ? wt[i] : 0.f;
-      const uint32_t k = weight_key(w);
-      const bool mid = in && i >= lo && i < hi;
-      const unsigned tie_mask = __ballot_sync(0xffffffffu, mid && take > 0 && k == prefix);
-      if (lane == 0) count[gi][0][gw] = __popc(tie_mask);
+    for (int r0 = 0; r0 < n; r0 += kRun * kThreads) {
+      const int chunks = min(kRun, (n - r0 + kThreads - 1) / kThreads);
+      unsigned tie_bits = 0, stay_bits = 0;  // bit c: this thread's tile of chunk c
       __syncthreads();
-      unsigned tb = ties + __popc(tie_mask & below), all = 0;
-      for (int x = 0; x < GW; ++x) {
-        const unsigned v = count[gi][0][x];
-        tb += x < gw ? v : 0u;
-        all += v;
+      count[tid] = 0u;
+      __syncthreads();
+#pragma unroll 4
+      for (int c = 0; c < chunks; ++c) {
+        const int i = r0 + c * kThreads + tid;
+        const bool in = i < n, mid = i >= lo && i < hi;
+        const uint32_t k = mid ? weight_key(wt[i]) : 0u;
+        const bool tie = mid && take > 0 && k == prefix;
+        if (tie) tie_bits |= 1u << c;
+        if (in && (!mid || (take > 0 && k > prefix))) stay_bits |= 1u << c;
+        const unsigned m = __ballot_sync(0xffffffffu, tie);
+        if (lane == 0) count[c * kWarps + warp] = __popc(m);
       }
-      ties += all;
-      const bool stays = in && (!mid || (take > 0 && (k > prefix || (k == prefix && tb < rem))));
-      const unsigned stay_mask = __ballot_sync(0xffffffffu, stays);
-      if (lane == 0) count[gi][1][gw] = __popc(stay_mask);
-      __syncthreads();  // every tile of the run has been read
-      unsigned at = stay + __popc(stay_mask & below);
-      all = 0;
-      for (int x = 0; x < GW; ++x) {
-        const unsigned v = count[gi][1][x];
-        at += x < gw ? v : 0u;
-        all += v;
+      const unsigned all_ties = scan(count, warp_sum);
+      for (int c = 0; c < chunks; ++c) {
+        const bool tie = tie_bits >> c & 1u;
+        const unsigned m = __ballot_sync(0xffffffffu, tie);
+        if (tie && ties + count[c * kWarps + warp] + __popc(m & below) < rem) stay_bits |= 1u << c;
       }
-      stay += all;
-      if (stays) {
-        tab_o[at] = t;
-        wt_o[at] = w;
-      } else if (in && ev) {
-        ev[i - at] = t;
+      ties += all_ties;
+      __syncthreads();
+      count[tid] = 0u;
+      __syncthreads();
+      for (int c = 0; c < chunks; ++c) {
+        const unsigned m = __ballot_sync(0xffffffffu, stay_bits >> c & 1u);
+        if (lane == 0) count[c * kWarps + warp] = __popc(m);
       }
+      const unsigned all_stay = scan(count, warp_sum);
+      for (int c0 = 0; c0 < chunks; c0 += kBatch) {
+        int64_t t[kBatch];
+        float w[kBatch];
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          const int i = r0 + (c0 + c) * kThreads + tid;
+          const bool in = c0 + c < chunks && i < n;
+          t[c] = in ? tab[i] : 0;
+          w[c] = in ? wt[i] : 0.f;
+        }
+        __syncthreads();  // read: entries of this batch may move
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          if (c0 + c >= chunks) break;
+          const int i = r0 + (c0 + c) * kThreads + tid;
+          const bool stays = stay_bits >> (c0 + c) & 1u;
+          const unsigned m = __ballot_sync(0xffffffffu, stays);
+          const unsigned at = stay + count[(c0 + c) * kWarps + warp] + __popc(m & below);
+          if (stays) {
+            tab_o[at] = t[c];
+            wt_o[at] = w[c];
+          } else if (i < n && ev) {
+            ev[i - at] = t[c];
+          }
+        }
+      }
+      stay += all_stay;
     }
     __syncthreads();
-    if (live)
-      for (int i = gt; i < max_tiles; i += GT) {
-        if (i >= keep) {
-          tab_o[i] = -1;
-          wt_o[i] = 0.f;
-        }
-        if (ev && i >= n - keep) ev[i] = -1;
+    for (int i = tid; i < max_tiles; i += kThreads) {
+      if (i >= keep) {
+        tab_o[i] = -1;
+        wt_o[i] = 0.f;
       }
+      if (ev && i >= n - keep) ev[i] = -1;
+    }
     __syncthreads();
   }
 }
@@ -155,16 +208,18 @@ cudaError_t launch_evict(const int64_t* table, const float* mass, const int32_t*
                          int64_t* table_out, float* mass_out, int32_t* n_out, int64_t* evicted,
                          int B, int Hkv, int max_tiles, int keep, int sinks, int recent,
                          unsigned flags, cudaStream_t st) {
-  LaunchCfg L(dim3(B), dim3(kThreads), 0, st, flags);
-#define KVARN_GO(GT)                                                                               \
-  cudaLaunchKernelEx(&L.cfg, evict_kernel<GT>, table, mass, n_tiles, table_out, mass_out, n_out,  \
-                     evicted, Hkv, max_tiles, keep, sinks, recent)
-  if (Hkv <= 1) return KVARN_GO(1024);
-  if (Hkv <= 2) return KVARN_GO(512);
-  if (Hkv <= 4) return KVARN_GO(256);
-  if (Hkv <= 8) return KVARN_GO(128);
-  return KVARN_GO(64);
-#undef KVARN_GO
+  const unsigned heads = Hkv < 8 ? Hkv : 8;
+  LaunchCfg L(dim3(heads, B), dim3(kThreads), 0, st, flags);
+  cudaLaunchAttribute attr[2] = {L.attr[0], {}};
+  unsigned na = L.cfg.numAttrs;
+  attr[na].id = cudaLaunchAttributeClusterDimension;
+  attr[na].val.clusterDim.x = heads;
+  attr[na].val.clusterDim.y = 1;
+  attr[na].val.clusterDim.z = 1;
+  L.cfg.attrs = attr;
+  L.cfg.numAttrs = na + 1;
+  return cudaLaunchKernelEx(&L.cfg, evict_kernel, table, mass, n_tiles, table_out, mass_out, n_out, evicted,
+                            Hkv, max_tiles, keep, sinks, recent);
 }
 
 }  // namespace kvarn

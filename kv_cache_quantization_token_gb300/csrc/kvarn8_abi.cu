@@ -198,7 +198,7 @@ int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const i
                       int64_t* table_out, float* mass_out, int32_t* n_tiles_out, int64_t* evicted, int B,
                       int Hkv, int max_tiles, int keep, int sinks, int recent, unsigned launch_flags,
                       kvarn_stream_t stream) {
-  if (B < 0 || Hkv <= 0 || Hkv > 65535 || max_tiles < 0 || keep < 1 || sinks < 0 || recent < 0 ||
+  if (B < 0 || B > 65535 || Hkv <= 0 || Hkv > 65535 || max_tiles < 0 || keep < 1 || sinks < 0 || recent < 0 ||
       (int64_t)sinks + recent > keep || !flags_ok(launch_flags))
     return KVARN_ERR_BAD_ARG;
   if (B == 0) return KVARN_OK;
