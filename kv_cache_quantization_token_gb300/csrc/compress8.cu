@@ -149,7 +149,7 @@ __device__ __forceinline__ void compress_tensor(const float* __restrict__ src, i
   }
   if (col == 0) reinterpret_cast<float*>(rec + (IS_V ? R::kVScale : R::kKScale))[grp] = s;
   if (IS_V && tid < 4) reinterpret_cast<uint4*>(rec + R::kVScale + 4 * kGrps)[tid] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 template <int D, int F>

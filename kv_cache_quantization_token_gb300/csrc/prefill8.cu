@@ -103,7 +103,7 @@ __host__ __device__ inline int64_t image_index(int sub) { return 4LL * (sub >> 1
 struct Att8Args {
   Prefill8Args a;
   Plan8 p;
-  float* scale;  // [Hkv][blocks][2][8]
+  float* scale;  // [Hkv][blocks][8 scales of K, 8 binary logarithms of scales of V]
   float2* ml;    // [shares][C][Hq]
   float* acc;    // [shares][C][Hq][D]
 };
@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
     if (tid < 16) {
       const int g = tid & 7;
       float* sc = s.scale + ((int64_t)kvh * n_sub + (int64_t)j * SUB + g / P::NGB) * 16;
-      sc[(tid >> 3) * 8 + g % P::NGB] =
-          (dead >> g & 1) ? 1.f : *reinterpret_cast<const float*>(rec + R::kKScale + 4 * tid);
+      const float x = (dead >> g & 1) ? 1.f : *reinterpret_cast<const float*>(rec + R::kKScale + 4 * tid);
+      sc[(tid >> 3) * 8 + g % P::NGB] = tid < 8 ? x : fast_lg2(x);
     }
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
   const float f = pow2_to(__uint_as_float(amax_s), 8);
   const unsigned bad = bad_s;
   if (tid < 2)  // (the lo rows have their hi rows' scale)
-    s.scale[((int64_t)kvh * n_sub + sub) * 16 + (is_v ? 8 : 0) + r0 / kGrp + 2 * tid] = pow2_inverse(f);
+    s.scale[((int64_t)kvh * n_sub + sub) * 16 + (is_v ? 8 : 0) + r0 / kGrp + 2 * tid] =
+        is_v ? fast_lg2(pow2_inverse(f)) : pow2_inverse(f);
   uint8_t* img = head + (image_index(sub) + (is_v ? 2 : 0)) * P::IMG;
   for (int u = tid; u < 2 * D; u += 256) {  // 8 elements along the summed index: channels of K, tokens of V
     const int row = is_v ? u % D : u / (D / 8), k = is_v ? (u / D) * 8 : (u % (D / 8)) * 8;
@@ -436,37 +437,38 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     // of them, the leading ones that every row of the CTA sees whole
     const int n_full = (int)max((int64_t)0, min((int64_t)n_t, (pmin + 1) / KB - b0));
     const float* scales = s.scale + (int64_t)kvh * n_sub * 16;
-    float ks_next[NGB] = {}, vs_next[NGB] = {};
+    float ks_next[NGB] = {}, lv_next[NGB] = {};
     auto fetch_scales = [&](int j) {
       const float4* p = reinterpret_cast<const float4*>(scales + 16 * (j < n_t ? b0 + j : sub_of(j)));
 #pragma unroll
       for (int g = 0; g < NGB; g += 4) {
         const float4 x = p[g / 4], y = p[2 + g / 4];
         ks_next[g] = x.x; ks_next[g + 1] = x.y; ks_next[g + 2] = x.z; ks_next[g + 3] = x.w;
-        vs_next[g] = y.x; vs_next[g + 1] = y.y; vs_next[g + 2] = y.z; vs_next[g + 3] = y.w;
+        lv_next[g] = y.x; lv_next[g + 1] = y.y; lv_next[g + 2] = y.z; lv_next[g + 3] = y.w;
       }
     };
     pdl_wait();  // the scales belong to this call's images
     if (grp < n_blk) fetch_scales(grp);
     auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait8(bar, par, a.err, fail); };
+    int sl = grp, sl_before = 0;  // ring slot of block j and of the group's block before, and their parities
+    uint32_t ph = 0, ph_before = 0;
     for (int j = grp; j < n_blk; j += NG) {
-      float ks[NGB], vs[NGB];
+      float ks[NGB], lv[NGB];
 #pragma unroll
       for (int g = 0; g < NGB; ++g) {
         // (not zero, so that a hidden key's -inf stays; a factor that small makes every score 0 anyway)
         ks[g] = fmaxf(ks_next[g] * qscale, 1e-37f);
-        vs[g] = vs_next[g];
+        lv[g] = lv_next[g];
       }
       if (j + NG < n_blk) fetch_scales(j + NG);
-      wait(bar_dk + j % R, (uint32_t)(j / R) & 1u);
+      wait(bar_dk + sl, ph);
       __syncwarp();
       tc_fence_after();
       float sv[KB];
       tmem_ld32_nowait(t_s, *reinterpret_cast<uint32_t(*)[32]>(sv));
       tmem_ld32_nowait(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
       // P's columns are free when the product that read the group's block before is complete
-      const int jb = j - NG;
-      const bool p_free = !P::SEP || j < NG || mbar_done(bar_dv + jb % R, (uint32_t)(jb / R) & 1u);
+      const bool p_free = !P::SEP || j < NG || mbar_done(bar_dv + sl_before, ph_before);
       tmem_wait_ld(sv);
       if (P::SEP) {
         tc_fence_before();
@@ -487,14 +489,13 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
           if (u >= seen) sv[u] = -INFINITY;
       }
       // largest score of each group of keys, and of the row's weighted scores
-      float mg[NGB], lv[NGB], ublk = -INFINITY;
+      float mg[NGB], ublk = -INFINITY;
 #pragma unroll
       for (int g = 0; g < NGB; ++g) {
         float m = sv[16 * g];
 #pragma unroll
         for (int u = 1; u < 15; u += 2) m = fmax3(m, sv[16 * g + u], sv[16 * g + u + 1]);
         mg[g] = fmaxf(m, sv[16 * g + 15]) * ks[g];
-        lv[g] = fast_lg2(vs[g]);
         ublk = fmaxf(ublk, mg[g] + lv[g]);
       }
       // u after the block before, from the group that has it
@@ -540,9 +541,16 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
           if constexpr (NP == 2) lw[KW / 2 + e] = lw[e];
         }
       }
-      if (!p_free) wait(bar_dv + jb % R, (uint32_t)(jb / R) & 1u);
+      if (!p_free) wait(bar_dv + sl_before, ph_before);
       __syncwarp();
       if (P::SEP) tc_fence_after();
+      sl_before = sl;
+      ph_before = ph;
+      sl += NG;
+      if (sl >= R) {
+        sl -= R;
+        ph ^= 1u;
+      }
       // w: hi in 32 columns, lo in the 32 after
       tmem_st32_nowait(t_p, hw);
       if constexpr (NP == 2) tmem_st32_nowait(t_p + 32, lw);
