@@ -87,7 +87,7 @@ struct Plan8 {
 // of an mbarrier costs 60 to 200 beside the tensor core's reads of shared memory). A warp that gave up
 // on a copy or a product raises `fail` and still takes part in every hand-over, so that none is left
 // waiting; what it computes from then on is discarded.
-enum : int { kBarPair = 2, kBarRead = 6, kBarP = 9, kBarU = 12 };  // + warp % 4, and + group three times
+enum : int { kBarPair = 2, kBarRead = 6, kBarTurn = 6, kBarP = 9, kBarU = 12 };  // + warp % 4, group, MMA warp
 template <int THREADS>
 __device__ __forceinline__ void hand_over(int id) {
   asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
@@ -346,76 +346,105 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     }
     __syncwarp();
   } else if (warp >= 4 * NG) {
-    // ---------------- products: one warp issues S, the other PV, each waiting for its own operands while
-    // the tensor pipe works on the other's (a satisfied wait costs some 200 cycles beside the softmax
-    // warps, more than the pipe's short queue lasts). The whole warp runs the loop, so that operand
-    // addresses stay uniform, and one elected lane issues; the loops are unrolled over the rings, so that
-    // slots, addresses and descriptors are constants.
+    // ---------------- products, by two warps: each waits for its operands while the tensor pipe works on
+    // what the other issued (a satisfied wait costs some 200 cycles beside the softmax warps, more than the
+    // pipe's short queue lasts). The whole warp runs the loop, so that operand addresses stay uniform, and
+    // one elected lane issues; the loops are unrolled over the rings, so that slots, addresses and
+    // descriptors are constants.
     if (n_blk > 0) {
+      const uint64_t dk = sdesc(smem_addr(sm + P::OFF_K)), dv = sdesc(smem_addr(sm + P::OFF_V));
+      [[maybe_unused]] const uint64_t dq = sdesc(smem_addr(sm));  // lo part of the query (head_dim 256)
       constexpr uint32_t kStep = P::IMG >> 4;
       auto wait = [&](uint64_t* bar, uint32_t par) { mbar_wait8(bar, par, a.err, fail); };
-      constexpr int U = (R % NG == 0) ? R : R * NG;
-      if (warp == 4 * NG) {
-        const uint64_t dk = sdesc(smem_addr(sm + P::OFF_K));
-        [[maybe_unused]] const uint64_t dq = sdesc(smem_addr(sm));  // lo part of the query (head_dim 256)
-        for (int t0 = 0; t0 < n_blk; t0 += U) {
+      // S of a block from the K image in slot sl into columns ss
+      auto s_products = [&](int sl, int ss) {
+        const uint64_t kd = dk + sl * kStep;
+        const uint32_t t_s = tmem + P::T_S + KB * ss;
+#pragma unroll
+        for (int h = NP - 1; h >= 0; --h) {  // the query's lo part first: while the sums are small
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
+            const uint32_t acc = h < NP - 1 || kk > 0;
+            if (P::QL_SMEM && h == 1)
+              mma_ss(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>(), acc);
+            else
+              mma_ts(t_s, tmem + (h == 1 ? P::T_QL : P::T_QH) + 8 * kk, bd, idesc_f16<KB>(), acc);
+          }
+        }
+        mma_commit(bar_dk + sl);
+      };
+      // O += P V: the V image in slot sl, P in columns ss (32 columns hi, then 32 lo)
+      auto o_products = [&](int sl, int ss, bool first) {
+        const uint64_t vd = dv + sl * kStep;
+        const uint32_t t_p = tmem + P::T_P + P::PSTEP * ss;
+#pragma unroll
+        for (int kk = 0; kk < KB / 16; ++kk) {
+          const uint64_t bd = sdesc_add(vd, kk * 32);
+          mma_ts(t_o, t_p + 8 * kk, bd, idesc_f16<D>(), !first || kk > 0);
+          if (NP == 2) mma_ts(t_o, t_p + 32 + 8 * kk, bd, idesc_f16<D>(), 1);
+        }
+        mma_commit(bar_dv + sl);
+      };
+      constexpr int U0 = (R % NG == 0) ? R : R * NG;
+      if constexpr (!P::SEP) {
+        // the pipe's order alone keeps S(t) behind PV(t - NG), whose P is in the same columns: the warps take
+        // turns at steps of the two, handing over once a step is issued
+        constexpr int U = U0 % 2 == 0 ? U0 : 2 * U0;
+        const int me = warp - 4 * NG, n_steps = n_blk + NG;
+        for (int t0 = 0; t0 < n_steps; t0 += U) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
+            const int t = t0 + u;
+            if (t >= n_steps) break;
+            if ((u & 1) != me) continue;
+            const int sl = u % R, ss = u % NG, sv = (u + R * NG - NG) % R;
+            if (t >= NG) wait(bar_fv + sv, (uint32_t)((t - NG) / R) & 1u);
+            if (t < n_blk && R > 2) wait(bar_fk + sl, (uint32_t)(t / R) & 1u);
+            __syncwarp();
+            if (t >= NG) take_over<160>(kBarP + ss);
+            if (t > 0) take_over<64>(kBarTurn + me);
+            tc_fence_after();
+            if (t >= NG && elect_one()) o_products(sv, ss, t == NG);
+            __syncwarp();
+            if (t < n_blk && R == 2) {  // (a ring of two: its K image is as late as this)
+              wait(bar_fk + sl, (uint32_t)(t / R) & 1u);
+              __syncwarp();
+              tc_fence_after();
+            }
+            if (t < n_blk && elect_one()) s_products(sl, ss);
+            __syncwarp();
+            tc_fence_before();
+            if (t + 1 < n_steps) hand_over<64>(kBarTurn + (me ^ 1));
+          }
+        }
+      } else if (warp == 4 * NG) {  // S, into columns whose scores have been read
+        for (int t0 = 0; t0 < n_blk; t0 += U0) {
+#pragma unroll
+          for (int u = 0; u < U0; ++u) {
             const int t = t0 + u;
             if (t >= n_blk) break;
             const int sl = u % R, ss = u % NG;
             if (u % P::LP == 0) wait(bar_fk + sl, (uint32_t)(t / R) & 1u);
-            // the columns are free when the group has read its scores from them, or, where P replaced the
-            // scores, when the product that reads P is complete
-            if (!P::SEP && t >= NG) wait(bar_dv + (t - NG) % R, (uint32_t)((t - NG) / R) & 1u);
             __syncwarp();
-            if (P::SEP && t >= NG) take_over<160>(kBarRead + ss);
+            if (t >= NG) take_over<160>(kBarRead + ss);
             tc_fence_after();
-            if (elect_one()) {
-              const uint64_t kd = dk + sl * kStep;
-              const uint32_t t_s = tmem + P::T_S + KB * ss;
-#pragma unroll
-              for (int h = NP - 1; h >= 0; --h) {  // the query's lo part first: while the sums are small
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint64_t bd = sdesc_add(kd, (kk >> 2) * KB * 128 + (kk & 3) * 32);
-                  const uint32_t acc = h < NP - 1 || kk > 0;
-                  if (P::QL_SMEM && h == 1)
-                    mma_ss(t_s, sdesc_add(dq, (kk >> 2) * 128 * 128 + (kk & 3) * 32), bd, idesc_f16<KB>(), acc);
-                  else
-                    mma_ts(t_s, tmem + (h == 1 ? P::T_QL : P::T_QH) + 8 * kk, bd, idesc_f16<KB>(), acc);
-                }
-              }
-              mma_commit(bar_dk + sl);
-            }
+            if (elect_one()) s_products(sl, ss);
             __syncwarp();
           }
         }
-      } else {
-        const uint64_t dv = sdesc(smem_addr(sm + P::OFF_V));
-        for (int t0 = 0; t0 < n_blk; t0 += U) {
+      } else {  // PV
+        for (int t0 = 0; t0 < n_blk; t0 += U0) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
+          for (int u = 0; u < U0; ++u) {
             const int t = t0 + u;
             if (t >= n_blk) break;
             const int sl = u % R, ss = u % NG;
-            if (u % P::LP == 0) {
-              wait(bar_fv + sl, (uint32_t)(t / R) & 1u);
-              __syncwarp();
-            }
+            if (u % P::LP == 0) wait(bar_fv + sl, (uint32_t)(t / R) & 1u);
+            __syncwarp();
             take_over<160>(kBarP + ss);
             tc_fence_after();
-            if (elect_one()) {
-              const uint64_t vd = dv + sl * kStep;
-              const uint32_t t_p = tmem + P::T_P + P::PSTEP * ss;  // 32 columns hi, then 32 lo
-#pragma unroll
-              for (int kk = 0; kk < KB / 16; ++kk) {
-                const uint64_t bd = sdesc_add(vd, kk * 32);
-                mma_ts(t_o, t_p + 8 * kk, bd, idesc_f16<D>(), t > 0 || kk > 0);
-                if (NP == 2) mma_ts(t_o, t_p + 32 + 8 * kk, bd, idesc_f16<D>(), 1);
-              }
-              mma_commit(bar_dv + sl);
-            }
+            if (elect_one()) o_products(sl, ss, t == 0);
             __syncwarp();
           }
         }
