@@ -171,7 +171,6 @@ cudaError_t launch_expand8(int D, int format, const uint8_t* tiles, int64_t tile
 struct Decode8Plan {
   int span;        // consecutive tiles of a tile item (one CTA)
   int tile_items;  // ceil(max_tiles / span)
-  int win_rows;    // window rows of a window item
   int items;       // tile items + window items
   size_t off_acc;  // workspace offsets: (m, l) per (sequence, head, item) at 0, then the
   size_t off_tile; // accumulators, then (m, l) per (sequence, KV head, tile, head of the group)
@@ -211,6 +210,9 @@ struct Prefill8Args {
   float scale;  // softmax scale * log2(e)
   unsigned* err;
 };
+// Prefill of a few positions by the decode kernels.
+void chunk8_plan(int C, int Hq, int Hkv, int D, int n_tiles, int win_len, Decode8Plan* p);
+cudaError_t launch_chunk8(const Decode8Plan& p, const Prefill8Args& a, cudaStream_t st);
 size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D);
 cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st);
 

@@ -109,30 +109,61 @@ struct Split8Args {
   float* acc;      // [B][Hq][items][D]
   float2* tile_ml; // [B][Hkv][max_tiles][8], or NULL
   int span, tile_items, items;
+  // a chunk of positions (CHUNK): B positions of one sequence instead of B sequences
+  int64_t pos0;
+  int n_tiles, win_start, win_len;
 };
 
+// Score row g of a CTA: with CHUNK the (position, head) pairs of a KV head, eight per CTA, are rows of one
+// sequence that see the cache up to their own position; otherwise the G heads of sequence blockIdx.z.
+struct Row8 {
+  bool valid;
+  int64_t index;  // among the [B][Hq] rows of queries and outputs
+  int64_t seen;   // cached tokens that the row sees
+};
+template <bool CHUNK>
+__device__ __forceinline__ Row8 row8(const Split8Args& s, int kvh, int g) {
+  const Decode8Args& a = s.a;
+  if constexpr (CHUNK) {
+    const int r = 8 * blockIdx.z + g, i = r / a.G;
+    const bool valid = i < a.B;
+    return Row8{valid, valid ? (int64_t)i * a.Hq + (int64_t)kvh * a.G + r % a.G : 0, valid ? s.pos0 + i + 1 : 0};
+  } else {
+    return Row8{g < a.G, (int64_t)blockIdx.z * a.Hq + (int64_t)kvh * a.G + min(g, a.G - 1), INT64_MAX};
+  }
+}
+
 // A run of window rows: fp32 rows against fp32 queries and probabilities, every operand a
-// pair of tf32 numbers.
-template <int D>
-__device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* smem, int item, int kvh,
-                                            int b, int64_t part) {
+// pair of tf32 numbers. A row with a NaN or an infinity counts as NaN scores and zero values.
+template <int D, bool CHUNK>
+__device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* smem, int item, int kvh) {
   using C = D8<D>;
   const Decode8Args& a = s.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   float* P = reinterpret_cast<float*>(smem + C::OFF_P);
   float2* mx = reinterpret_cast<float2*>(smem + C::OFF_MX);
+  volatile int* dead = reinterpret_cast<volatile int*>(smem);  // [WROWS]
   constexpr int PS = C::WROWS + 4;
-  const int wlen = min(max(a.win_len[b], 0), a.win_cap);
+  const int b = CHUNK ? 0 : blockIdx.z;
+  const Row8 me = row8<CHUNK>(s, kvh, g);
+  const int wlen = CHUNK ? s.win_len : min(max(a.win_len[b], 0), a.win_cap);
   const int r0 = C::WROWS * (item - s.tile_items);
   const int n = min(C::WROWS, wlen - r0);
   pdl_trigger();
   if (n <= 0) {
-    if (tid < a.G) s.ml[part + (int64_t)tid * s.items] = make_float2(-INFINITY, 0.f);
+    if (tid < 8) {
+      const Row8 r = row8<CHUNK>(s, kvh, tid);
+      if (r.valid) s.ml[r.index * s.items + item] = make_float2(-INFINITY, 0.f);
+    }
     return;
   }
-  const int start = ((a.win_start[b] % a.win_cap) + a.win_cap) % a.win_cap;
+  const int start = CHUNK ? s.win_start : ((a.win_start[b] % a.win_cap) + a.win_cap) % a.win_cap;
   const int64_t head = ((int64_t)b * a.Hkv + kvh) * a.win_cap;
-  auto row = [&](int t) { return (head + (start + r0 + t) % a.win_cap) * (int64_t)D; };
+  auto row = [&](int t) { return (head + ((int64_t)start + r0 + t) % a.win_cap) * (int64_t)D; };
+  // rows of this item that score row g sees
+  const int seen = CHUNK ? (int)max((int64_t)0, min((int64_t)n, me.seen - (int64_t)128 * s.n_tiles - r0)) : n;
+  if (tid < C::WROWS) dead[tid] = 0;
+  __syncthreads();
   // the values this warp's channels need, under way while the scores are formed
   float v[C::NW][C::NC][2];
 #pragma unroll
@@ -146,14 +177,24 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
       v[k][c][1] = t1 < n ? v1[8 * c] : 0.f;
     }
   }
+#pragma unroll
+  for (int k = 0; k < C::NW; ++k)
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (!isfinite(v[k][c][h])) {
+          dead[8 * k + q + 4 * h] = 1;
+          v[k][c][h] = 0.f;
+        }
   const bool have = 8 * warp + g < n;
   const float* kr = a.win_k + (have ? row(8 * warp + g) : 0) + 4 * q;
-  const int64_t qrow = ((int64_t)b * a.Hq + (int64_t)kvh * a.G + min(g, a.G - 1)) * D + 4 * q;
+  const int64_t qrow = me.index * D + 4 * q;
   float sc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int m = 0; m < D / 16; ++m) {
     const float4 kx = have ? *reinterpret_cast<const float4*>(kr + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 qx = g < a.G ? io_ld4(a.q, a.io, qrow + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 qx = me.valid ? io_ld4(a.q, a.io, qrow + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t qa[4], kh[2], kl[2];
@@ -166,15 +207,16 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
     }
   }
   const int t0 = 8 * warp + 2 * q;
-  const float s0 = t0 < n ? (sc[0] + sc[2]) * a.scale : -INFINITY;
-  const float s1 = t0 + 1 < n ? (sc[1] + sc[3]) * a.scale : -INFINITY;
+  __syncthreads();  // dead rows are known
+  const float s0 = t0 < seen ? (dead[t0] ? NAN : (sc[0] + sc[2]) * a.scale) : -INFINITY;
+  const float s1 = t0 + 1 < seen ? (dead[t0 + 1] ? NAN : (sc[1] + sc[3]) * a.scale) : -INFINITY;
   const float mw = quad_max(fmaxf(s0, s1));
   if (q == 0) mx[g * C::NW + warp].x = mw;
   __syncthreads();
   float M = kNone;
 #pragma unroll
   for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mx[g * C::NW + w].x);
-  const float p0 = t0 < n ? fast_ex2(s0 - M) : 0.f, p1 = t0 + 1 < n ? fast_ex2(s1 - M) : 0.f;
+  const float p0 = t0 < seen ? fast_ex2(s0 - M) : 0.f, p1 = t0 + 1 < seen ? fast_ex2(s1 - M) : 0.f;
   *reinterpret_cast<float2*>(P + g * PS + t0) = make_float2(p0, p1);
   const float l = cta_row_sum<C::NW>(quad_sum(p0 + p1), reinterpret_cast<float*>(smem + C::OFF_L), warp, g, q);
   float o[C::NC][4] = {};
@@ -192,27 +234,27 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
       mma_tf32(o[c], pa, vl[0], vl[1]);
     }
   }
-  if (g < a.G) {
-    float* dst = s.acc + (part + (int64_t)g * s.items) * D + 8 * C::NC * warp + 2 * q;
+  if (me.valid) {
+    const int64_t part = me.index * s.items + item;
+    float* dst = s.acc + part * D + 8 * C::NC * warp + 2 * q;
 #pragma unroll
     for (int c = 0; c < C::NC; ++c)
       *reinterpret_cast<float2*>(dst + 8 * c) = make_float2(o[c][0] + o[c][2], o[c][1] + o[c][3]);
-    if (warp == 0 && q == 0) s.ml[part + (int64_t)g * s.items] = make_float2(M, l);
+    if (warp == 0 && q == 0) s.ml[part] = make_float2(M, l);
   }
 }
 
-template <int D, int F>
+template <int D, int F, bool CHUNK>
 __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const Split8Args s) {
   using C = D8<D>;
   using R = Rec8<D>;
   extern __shared__ __align__(128) unsigned char smem[];
   const Decode8Args& a = s.a;
-  const int item = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int item = blockIdx.x, kvh = blockIdx.y, b = CHUNK ? 0 : blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int64_t part = ((int64_t)b * a.Hq + (int64_t)kvh * a.G) * s.items + item;
   if (item >= s.tile_items) {
     pdl_wait();
-    window_item<D>(s, smem, item, kvh, b, part);
+    window_item<D, CHUNK>(s, smem, item, kvh);
     return;
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -229,11 +271,15 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     entry[0] = __ldcg(table);
     if (first + 1 < a.max_tiles) entry[1] = __ldcg(table + 1);
   }
-  const int nt = min(max(min(max(a.n_tiles[b], 0), a.max_tiles) - first, 0), s.span);
+  const int n_tiles = CHUNK ? s.n_tiles : min(max(a.n_tiles[b], 0), a.max_tiles);
+  const int nt = min(max(n_tiles - first, 0), s.span);
   if (nt == 0) {
     if (early) pdl_wait();
     pdl_trigger();
-    if (tid < a.G) s.ml[part + (int64_t)tid * s.items] = make_float2(-INFINITY, 0.f);
+    if (tid < 8) {
+      const Row8 r = row8<CHUNK>(s, kvh, tid);
+      if (r.valid) s.ml[r.index * s.items + item] = make_float2(-INFINITY, 0.f);
+    }
     return;
   }
   auto request = [&](int n) {  // one thread: copy n of the item (K, then V of each tile) into its slot
@@ -242,8 +288,10 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     unsigned char* dst = smem + (n % C::SLOTS) * C::SLOT;
     const int64_t off = n < 4 ? ((n >> 1) ? entry[1] : entry[0]) : table[n >> 1];
     if ((off & 15) || off < 0 || off > a.tiles_bytes - R::kBytes) {
+      // a record that is not read: zero codes under scales of NaN, which only rows that see it meet
       report(a.err, KVARN_DEVERR_RECORD);
-      *flag = 1;
+      for (int k = 0; k < C::HALF; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 2 * kGrps; ++k) reinterpret_cast<float*>(dst + C::HALF)[k] = NAN;
       mbar_arrive1(br);
       return;
     }
@@ -269,15 +317,18 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   // of product (j, r); hi in the registers of row g, lo in those of row g + 8
   uint32_t qa[4 * C::NJ][4];
   float c1;
+  [[maybe_unused]] int64_t seen = 0;  // cached tokens that row g sees (CHUNK)
   {
+    const Row8 me = row8<CHUNK>(s, kvh, g);
+    seen = me.seen;
     float x[C::NJ][16];
-    const int64_t qrow = ((int64_t)b * a.Hq + (int64_t)kvh * a.G + min(g, a.G - 1)) * D + 16 * q;
+    const int64_t qrow = me.index * D + 16 * q;
     float mxq = 0.f;
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float4 v = g < a.G ? io_ld4(a.q, a.io, qrow + 64 * j + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = me.valid ? io_ld4(a.q, a.io, qrow + 64 * j + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
         x[j][4 * r] = v.x; x[j][4 * r + 1] = v.y; x[j][4 * r + 2] = v.z; x[j][4 * r + 3] = v.w;
         mxq = fmaxf(fmaxf(mxq, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
       }
@@ -325,6 +376,11 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
       }
       sc[t][0] = (c[0] + c[2]) * kc;
       sc[t][1] = (c[1] + c[3]) * kc;
+      if constexpr (CHUNK) {
+        const int64_t pos = (int64_t)128 * (first + i) + 8 * (warp * C::NT + t) + 2 * q;
+        if (pos >= seen) sc[t][0] = -INFINITY;
+        if (pos + 1 >= seen) sc[t][1] = -INFINITY;
+      }
       mw = fmaxf(mw, fmaxf(sc[t][0], sc[t][1]));
     }
     mw = quad_max(mw);
@@ -359,7 +415,10 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
       const float p0 = fast_ex2(sc[t][0] - M), p1 = fast_ex2(sc[t][1] - M);
       lt += p0 + p1;
       uint32_t hi, lo;
-      split_pair(p0 * fw, p1 * fw, hi, lo);
+      if constexpr (CHUNK)  // (a token that is not seen has weight 0, whatever its scale)
+        split_pair(sc[t][0] == -INFINITY ? 0.f : p0 * fw, sc[t][1] == -INFINITY ? 0.f : p1 * fw, hi, lo);
+      else
+        split_pair(p0 * fw, p1 * fw, hi, lo);
       // tokens 8 n + 2 q, + 1 in the order the second product's A fragments are read
       const int n = warp * C::NT + t;
       *reinterpret_cast<uint2*>(P + g * kPRow + (((n >> 3) * 4 + 2 * (n & 1) + (q >> 1)) * 4 + ((n & 7) >> 1)) * 16 +
@@ -408,14 +467,16 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   if (!ok) *flag = 1;
   l = cta_row_sum<C::NW>(quad_sum(l), lbuf, warp, g, q);  // its barriers also publish the flag
   const bool bad = *flag != 0;
-  if (g < a.G) {
+  const Row8 me = row8<CHUNK>(s, kvh, g);
+  if (me.valid) {
+    const int64_t part = me.index * s.items + item;
     const float f = fast_ex2(U - kHead - M);
-    float* dst = s.acc + (part + (int64_t)g * s.items) * D + 8 * C::NC * warp + 2 * q;
+    float* dst = s.acc + part * D + 8 * C::NC * warp + 2 * q;
 #pragma unroll
     for (int c = 0; c < C::NC; ++c)
       *reinterpret_cast<float2*>(dst + 8 * c) = make_float2((o[c][0] + o[c][2]) * f, (o[c][1] + o[c][3]) * f);
     if (warp == 0 && q == 0)
-      s.ml[part + (int64_t)g * s.items] = bad ? make_float2(0.f, NAN) : make_float2(M, l);
+      s.ml[part] = bad ? make_float2(0.f, NAN) : make_float2(M, l);
   }
 }
 
@@ -518,20 +579,19 @@ __global__ void __launch_bounds__(256) merge8_kernel(const Split8Args s, int mas
   }
 }
 
-template <int D, int F>
-cudaError_t launch_d8(const Decode8Plan& p, const Decode8Args& a, void* ws, cudaStream_t st) {
+template <int D, int F, bool CHUNK>
+cudaError_t launch_d8(const Decode8Plan& p, Split8Args& s, void* ws, cudaStream_t st) {
   using C = D8<D>;
+  const Decode8Args& a = s.a;
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(split8_kernel<D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(split8_kernel<D, F, CHUNK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  Split8Args s;
-  s.a = a;
   unsigned char* w = static_cast<unsigned char*>(ws);
   s.ml = reinterpret_cast<float2*>(w);
   s.acc = reinterpret_cast<float*>(w + p.off_acc);
@@ -540,8 +600,8 @@ cudaError_t launch_d8(const Decode8Plan& p, const Decode8Args& a, void* ws, cuda
   s.tile_items = p.tile_items;
   s.items = p.items;
   if (p.items > 0) {
-    LaunchCfg L(dim3(p.items, a.Hkv, a.B), dim3(C::NTHR), C::SMEM, st, a.flags);
-    e = cudaLaunchKernelEx(&L.cfg, split8_kernel<D, F>, s);
+    LaunchCfg L(dim3(p.items, a.Hkv, CHUNK ? (a.B * a.G + 7) / 8 : a.B), dim3(C::NTHR), C::SMEM, st, a.flags);
+    e = cudaLaunchKernelEx(&L.cfg, split8_kernel<D, F, CHUNK>, s);
     if (e != cudaSuccess) return e;
   }
   const int mass_blocks = a.mass_out ? (a.max_tiles + 255) / 256 : 0;
@@ -550,38 +610,68 @@ cudaError_t launch_d8(const Decode8Plan& p, const Decode8Args& a, void* ws, cuda
   return cudaLaunchKernelEx(&L.cfg, merge8_kernel<D>, s, mass_blocks);
 }
 
-}  // namespace
+template <bool CHUNK>
+cudaError_t launch_any(const Decode8Plan& p, Split8Args& s, void* ws, cudaStream_t st) {
+  const bool e = s.a.format == KVARN_CODE8_E4M3;
+  switch (s.a.D) {
+    case 64: return e ? launch_d8<64, 1, CHUNK>(p, s, ws, st) : launch_d8<64, 0, CHUNK>(p, s, ws, st);
+    case 128: return e ? launch_d8<128, 1, CHUNK>(p, s, ws, st) : launch_d8<128, 0, CHUNK>(p, s, ws, st);
+    case 256: return e ? launch_d8<256, 1, CHUNK>(p, s, ws, st) : launch_d8<256, 0, CHUNK>(p, s, ws, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
 
-void decode8_plan(int B, int Hq, int Hkv, int D, int max_tiles, int win_capacity, Decode8Plan* p) {
+// groups: CTAs that read a KV head's records; rows: query rows; seqs: sequences of lengths of their own.
+void make_plan(int64_t groups, int64_t rows, int seqs, int D, int max_tiles, int win_rows, size_t tile_pairs,
+               Decode8Plan* p) {
   const int ctas = D == 64 ? D8<64>::CTAS : D == 128 ? D8<128>::CTAS : D8<256>::CTAS;
   const int64_t slots = (int64_t)sm_count() * ctas;
-  const int64_t work = (int64_t)B * Hkv * max_tiles;
+  const int64_t work = groups * max_tiles;
   // Whole waves of resident CTAs, as long as an item has at most 16 tiles. Several sequences, whose
   // lengths differ as a rule, take two waves at least: a wave of items as long as the longest
   // sequence's leaves the SMs of the short ones idle (5 ragged sequences of up to 250 tiles, head_dim
   // 64: 24.7 -> 20.5 us; 8 equal ones of 256 tiles, head_dim 256: 92.9 -> 97.6 us).
   int64_t waves = (work + 16 * slots - 1) / (16 * slots);
-  if (waves < (B > 1 ? 2 : 1)) waves = B > 1 ? 2 : 1;
+  if (waves < (seqs > 1 ? 2 : 1)) waves = seqs > 1 ? 2 : 1;
   const int64_t span = (work + waves * slots - 1) / (waves * slots);
   p->span = (int)(span < 1 ? 1 : span);
   p->tile_items = (max_tiles + p->span - 1) / p->span;
-  p->win_rows = D == 256 ? D8<256>::WROWS : D8<128>::WROWS;
-  p->items = p->tile_items + (win_capacity + p->win_rows - 1) / p->win_rows;
-  const size_t rows = (size_t)B * Hq * p->items;
+  constexpr int kRows = D8<64>::WROWS;
+  static_assert(kRows == D8<128>::WROWS && kRows == D8<256>::WROWS, "window rows per item");
+  p->items = p->tile_items + (int)(((int64_t)win_rows + kRows - 1) / kRows);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  p->off_acc = up(rows * sizeof(float2));
-  p->off_tile = p->off_acc + up(rows * D * sizeof(float));
-  p->ws_bytes = p->off_tile + up((size_t)B * Hkv * max_tiles * 8 * sizeof(float2));
+  p->off_acc = up((size_t)rows * p->items * sizeof(float2));
+  p->off_tile = p->off_acc + up((size_t)rows * p->items * D * sizeof(float));
+  p->ws_bytes = p->off_tile + up(tile_pairs * sizeof(float2));
+}
+
+}  // namespace
+
+void decode8_plan(int B, int Hq, int Hkv, int D, int max_tiles, int win_capacity, Decode8Plan* p) {
+  make_plan((int64_t)B * Hkv, (int64_t)B * Hq, B, D, max_tiles, win_capacity, (size_t)B * Hkv * max_tiles * 8, p);
 }
 
 cudaError_t launch_decode8(const Decode8Plan& p, const Decode8Args& a, void* ws, cudaStream_t st) {
-  const bool e = a.format == KVARN_CODE8_E4M3;
-  switch (a.D) {
-    case 64: return e ? launch_d8<64, 1>(p, a, ws, st) : launch_d8<64, 0>(p, a, ws, st);
-    case 128: return e ? launch_d8<128, 1>(p, a, ws, st) : launch_d8<128, 0>(p, a, ws, st);
-    case 256: return e ? launch_d8<256, 1>(p, a, ws, st) : launch_d8<256, 0>(p, a, ws, st);
-    default: return cudaErrorInvalidValue;
-  }
+  Split8Args s{};
+  s.a = a;
+  return launch_any<false>(p, s, ws, st);
+}
+
+// A few positions of one sequence, eight (position, head) rows of a KV head to a CTA.
+void chunk8_plan(int C, int Hq, int Hkv, int D, int n_tiles, int win_len, Decode8Plan* p) {
+  make_plan((int64_t)Hkv * ((C * (Hq / Hkv) + 7) / 8), (int64_t)C * Hq, 1, D, n_tiles, win_len, 0, p);
+}
+
+cudaError_t launch_chunk8(const Decode8Plan& p, const Prefill8Args& a, cudaStream_t st) {
+  Split8Args s{};
+  s.a = Decode8Args{a.q, a.tiles, a.tile_table, nullptr, a.win_k, a.win_v, nullptr, nullptr, nullptr, nullptr, a.out,
+                    a.tiles_bytes, a.io, a.win_cap, a.C, a.Hq, a.Hkv, a.G, a.D, a.table_stride, a.format, a.scale, 0,
+                    a.err};
+  s.pos0 = a.pos0;
+  s.n_tiles = a.n_tiles;
+  s.win_start = a.win_start;
+  s.win_len = a.win_len;
+  return launch_any<true>(p, s, a.ws, st);
 }
 
 }  // namespace kvarn
