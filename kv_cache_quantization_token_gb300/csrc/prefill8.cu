@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
 
   // query rows into TMEM: scaled by a power of two, fp16 (hi and lo); two threads per row
-  float qscale = 0.f;
   if (tid < 256) {
     const int64_t at = ((int64_t)my_i * a.Hq + hq) * D + half * (D / 2);
     float m = 0.f;
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     xm[half * 128 + row].x = m;
     take_over<64>(kBarPair + (warp & 3));
     const float up = pow2_to(fmaxf(m, xm[(half ^ 1) * 128 + row].x), 10);
-    qscale = fabsf(a.scale) * pow2_inverse(up);
+    if (half == 0) xm[row].y = fabsf(a.scale) * pow2_inverse(up);
     const float p2 = copysignf(up, a.scale);  // maxima are taken before the (positive) scales
 #pragma unroll 1
     for (int c0 = 0; c0 < D / 2; c0 += 32) {
@@ -323,6 +322,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   __syncthreads();
   tc_fence_after();
 
+  const float qscale = xm[row].y;  // what turns a product into a score, but for the key's scale
   float u_own = -INFINITY, l_part = 0.f;  // softmax threads: sum of probabilities, in units of 2^u_own
   if (warp >= 4 * NG + 2) {
     // ---------------- copies: one thread for the K images, one for the V images

@@ -322,6 +322,17 @@ def test_prefill_lengths_and_positions(tiles, window, C, pos0, D):
     _check_prefill(c, q, pos0, c.prefill(q, pos0))
 
 
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hkv,C,tiles,window", [(8, 320, 21, 70), (2, 200, 33, 0), (1, 130, 5, 500)])
+def test_prefill_of_many_blocks(Hkv, C, tiles, window, D, io):
+    """Enough keys that every ring of the kernel wraps, with all keys in one CTA and in several shares."""
+    c = Cache8(D + C, [tiles], [window], Hkv, D, "e4m3", 64)
+    q = _query(C, (C, 4 * Hkv, D), io)
+    pos0 = T * tiles + window - C
+    _check_prefill(c, q, pos0, c.prefill(q, pos0))
+
+
 def test_prefill_scales_of_either_sign_and_zero():
     c = Cache8(32, [3], [20], 2, 128)
     q = _query(2, (40, 4, 128), "f32")
