@@ -135,11 +135,12 @@ int kvarn_decode_attention8(const void* q, int io_type, const uint8_t* tiles, in
   if (mass_in && !mass_out) return KVARN_ERR_BAD_ARG;
   if (!(softmax_scale == softmax_scale)) return KVARN_ERR_BAD_ARG;
   if (B == 0) return KVARN_OK;
-  if (!q || !out || !ws || !n_tiles) return KVARN_ERR_NULL;
+  if (!q || !out || !n_tiles) return KVARN_ERR_NULL;
   if (max_tiles > 0 && (!tiles || !tile_table)) return KVARN_ERR_NULL;
   if (win_capacity > 0 && (!win_k || !win_v || !win_start || !win_len)) return KVARN_ERR_NULL;
   kvarn::Decode8Plan p;
   kvarn::decode8_plan(B, Hq, Hkv, head_dim, max_tiles, win_capacity, &p);
+  if (p.ws_bytes > 0 && !ws) return KVARN_ERR_NULL;
   if (ws_bytes < p.ws_bytes) return KVARN_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(out, 16) || (max_tiles > 0 && !aligned(tiles, 16)) ||
       (win_capacity > 0 && (!aligned(win_k, 16) || !aligned(win_v, 16))) || !aligned(ws, 256))

@@ -36,6 +36,10 @@ namespace {
 
 constexpr float kHead = 8.f;  // w is about 2^8: lo parts of fp16 pairs stay normal
 constexpr float kLag = 7.f;   // references move when exceeded by this power of two
+// The tensor core drops what falls below an accumulator's last bit, for fp32 work eight times per block,
+// some 1e-8 of O each time: O is emptied into global memory with rounded sums every so many blocks (15,500
+// tokens, fp32: 8e-6 off without, 4e-6 with; 2.5 us each time).
+constexpr int kEmpty = 96;
 
 template <int D, int NP>
 struct PC8 {
@@ -60,7 +64,8 @@ struct PC8 {
   static constexpr int OFF_BAR = OFF_V + R * IMG;
   static constexpr int OFF_X = OFF_BAR + 256;              // float2 [NG][128]: (u, l) of a row's threads
   static constexpr int OFF_U = OFF_X + NG * 128 * 8;       // float [NG][128]: reference u after a group's block
-  static constexpr int OFF_MISC = OFF_U + NG * 128 * 4;
+  static constexpr int OFF_UE = OFF_U + NG * 128 * 4;      // float [128]: reference of the emptied sums
+  static constexpr int OFF_MISC = OFF_UE + 128 * 4;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;        // + slack to align the base to 1024
   // tensor memory columns
   static constexpr int T_QH = 0;
@@ -80,7 +85,7 @@ struct Plan8 {
   int n_tsub, n_wsub;     // blocks of visible tiles and window rows
   int row_blocks, shares;
   int64_t head_imgs;      // operand images per KV head, two per block
-  size_t off_scale, off_ml, off_acc, bytes;
+  size_t off_scale, off_ml, off_acc, off_sum, bytes;
 };
 
 // Hand-overs between the warps of a CTA go over its hardware barriers (some 20 cycles; a satisfied test
@@ -106,6 +111,7 @@ struct Att8Args {
   float* scale;  // [Hkv][blocks][8 scales of K, 8 binary logarithms of scales of V]
   float2* ml;    // [shares][C][Hq]
   float* acc;    // [shares][C][Hq][D]
+  float4* sum;   // what O is emptied into: [CTA][D / 4][128 rows], one 512-byte line per warp and step
 };
 
 // ---------------------------------------------------------------------------
@@ -126,14 +132,18 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
     const int64_t off = a.tile_table[(int64_t)kvh * a.table_stride + j];
     const bool good = !(off & 15) && off >= 0 && off <= a.tiles_bytes - R::kBytes;
     if (!good && tid == 0) report(a.err, KVARN_DEVERR_RECORD);
-    const unsigned char* rec = a.tiles + (good ? off : 0);
+    const unsigned char* rec = a.tiles + (good ? off : 0);  // (read only if good)
     // 16 D units of 16 codes: K (16 channels of a token), then V (16 tokens of a channel)
     constexpr int UNITS = 16 * D / 256;
     uint4 w[UNITS];
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) w[i] = *reinterpret_cast<const uint4*>(rec + 16 * (tid + 256 * i));
-    const float4* sp = reinterpret_cast<const float4*>(rec + R::kKScale);
-    const float4 f[4] = {sp[0], sp[1], sp[2], sp[3]};
+    for (int i = 0; i < UNITS; ++i)
+      w[i] = good ? *reinterpret_cast<const uint4*>(rec + 16 * (tid + 256 * i)) : make_uint4(0, 0, 0, 0);
+    float4 f[4] = {};
+    if (good) {
+      const float4* sp = reinterpret_cast<const float4*>(rec + R::kKScale);
+      f[0] = sp[0]; f[1] = sp[1]; f[2] = sp[2]; f[3] = sp[3];
+    }
     const float* fs = &f[0].x;
     unsigned dead = 0;  // groups whose tokens poison what sees them
 #pragma unroll
@@ -243,6 +253,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   uint64_t* bar_o = bar_dv + R;     // every product complete (one arrival per MMA warp)
   float2* xm = reinterpret_cast<float2*>(sm + P::OFF_X);
   float* su = reinterpret_cast<float*>(sm + P::OFF_U);
+  [[maybe_unused]] float* su_empty = reinterpret_cast<float*>(sm + P::OFF_UE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + P::OFF_MISC);
   volatile int* fail = reinterpret_cast<volatile int*>(sm + P::OFF_MISC + 4);
 
@@ -255,6 +266,9 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   const int64_t my_pos = a.pos0 + my_i;
   const int64_t pmin = a.pos0 + i0, pmax = a.pos0 + min(a.C, i0 + ppc) - 1;
   const int hq = kvh * a.G + min(my_g, a.G - 1);
+  const int64_t out_row = ((int64_t)share * a.C + my_i) * a.Hq + hq;  // among the key shares' results
+  [[maybe_unused]] float4* sums =
+      s.sum + (((int64_t)share * gridDim.y + kvh) * gridDim.x + blockIdx.x) * (D / 4) * 128;
   const int64_t win_pos0 = 128LL * a.n_tiles;
   // blocks this CTA sees: tiles up to pmax, window blocks up to pmax; its share of them
   const int n_sub = s.p.n_tsub + s.p.n_wsub;
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
             if (t >= NG) take_over<160>(kBarP + ss);
             if (t > 0) take_over<64>(kBarTurn + me);
             tc_fence_after();
-            if (t >= NG && elect_one()) o_products(sv, ss, t == NG);
+            if (t >= NG && elect_one()) o_products(sv, ss, NP == 2 ? (t - NG) % kEmpty == 0 : t == NG);
             __syncwarp();
             if (t < n_blk && R == 2) {  // (a ring of two: its K image is as late as this)
               wait(bar_fk + sl, (uint32_t)(t / R) & 1u);
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
             __syncwarp();
             take_over<160>(kBarP + ss);
             tc_fence_after();
-            if (elect_one()) o_products(sl, ss, t == 0);
+            if (elect_one()) o_products(sl, ss, NP == 2 ? t % kEmpty == 0 : t == 0);
             __syncwarp();
           }
         }
@@ -584,7 +598,28 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       tmem_st32_nowait(t_p, hw);
       if constexpr (NP == 2) tmem_st32_nowait(t_p + 32, lw);
       // O belongs to the previous block's product until that completes
-      if (j > 0 && __any_sync(0xffffffffu, need)) {
+      if (NP == 2 && j > 0 && j % kEmpty == 0) {
+        wait(bar_dv + (j - 1) % R, (uint32_t)((j - 1) / R) & 1u);
+        __syncwarp();
+        tc_fence_after();
+        const float u_sum = su_empty[row], again = j > kEmpty && u_sum != -INFINITY ? fast_ex2(u_sum - u_old) : 0.f;
+        float4* dst = sums + row;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float v[32];
+          float4 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            y[i] = again != 0.f ? __ldcg(dst + (c0 / 4 + i) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+          tmem_ld32(t_o + lb + c0, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            __stcg(dst + (c0 / 4 + i) * 128,
+                   make_float4(fmaf(y[i].x, again, v[4 * i]), fmaf(y[i].y, again, v[4 * i + 1]),
+                               fmaf(y[i].z, again, v[4 * i + 2]), fmaf(y[i].w, again, v[4 * i + 3])));
+        }
+        su_empty[row] = u_old;
+      } else if (j > 0 && __any_sync(0xffffffffu, need)) {
         const float alpha = need && u_old != -INFINITY ? fast_ex2(u_old - u_ref) : 1.f;
         wait(bar_dv + (j - 1) % R, (uint32_t)((j - 1) / R) & 1u);
         __syncwarp();
@@ -623,7 +658,10 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
     if (s.p.shares == 1) f = l != 0.f ? f / l : 0.f;
     if (!ok) f = NAN;
     const int64_t orow = (int64_t)my_i * a.Hq + hq;
-    const int64_t prow = (int64_t)share * a.C * a.Hq + orow;
+    // what O was emptied of, in units of 2^su_empty
+    const bool emptied = NP == 2 && n_blk > kEmpty;
+    const float u_sum = emptied ? su_empty[row] : -INFINITY;
+    const float again = u_sum != -INFINITY ? fast_ex2(u_sum - u) : 0.f;
 #pragma unroll 1
     for (int c0 = 0; c0 < D / 2; c0 += 32) {
       float v[32];
@@ -634,17 +672,25 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
         for (int i = 0; i < 32; ++i) v[i] = 0.f;
       }
       if (my_valid) {
+        if (again != 0.f) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 y = __ldcg(sums + (half * (D / 8) + (c0 + i) / 4) * 128 + row);
+            v[i] = fmaf(y.x, again, v[i]); v[i + 1] = fmaf(y.y, again, v[i + 1]);
+            v[i + 2] = fmaf(y.z, again, v[i + 2]); v[i + 3] = fmaf(y.w, again, v[i + 3]);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const float4 o = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
           const int c = half * (D / 2) + c0 + i;
           if (s.p.shares == 1) io_st4(a.out, a.io, orow * D + c, o);
-          else *reinterpret_cast<float4*>(s.acc + prow * D + c) = o;
+          else *reinterpret_cast<float4*>(s.acc + out_row * D + c) = o;
         }
       }
     }
     if (s.p.shares > 1 && my_valid && half == 0)
-      s.ml[prow] = ok ? make_float2(u, l) : make_float2(0.f, NAN);
+      s.ml[out_row] = ok ? make_float2(u, l) : make_float2(0.f, NAN);
   }
   tc_fence_before();
   __syncthreads();
@@ -677,7 +723,7 @@ __global__ void __launch_bounds__(256) join8_kernel(const Att8Args s) {
   io_st4(a.out, a.io, r * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
-Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D) {
+Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D, bool fp32) {
   Plan8 p;
   const int KB = PC8<64, 1>::KB, G = Hq / Hkv, ppc = 128 / G;
   p.n_tsub = n_tblk * (kTile / KB);
@@ -686,7 +732,7 @@ Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D) {
   p.row_blocks = (C + ppc - 1) / ppc;
   const int64_t ctas = (int64_t)p.row_blocks * Hkv;
   int64_t shares = ctas > 0 ? sm_count() / ctas : 1;
-  const int64_t most = (p.n_tsub + p.n_wsub + 1) / 2;  // two blocks per share at least
+  const int64_t most = (p.n_tsub + p.n_wsub) / 4;  // two pairs of blocks per share at least
   if (shares > most) shares = most;
   if (shares > 64) shares = 64;
   p.shares = shares < 1 ? 1 : (int)shares;
@@ -695,7 +741,9 @@ Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D) {
   p.off_ml = p.off_scale + up((size_t)Hkv * (p.n_tsub + p.n_wsub) * 64);
   const size_t rows = p.shares > 1 ? (size_t)p.shares * C * Hq : 0;
   p.off_acc = p.off_ml + up(rows * sizeof(float2));
-  p.bytes = p.off_acc + up(rows * D * sizeof(float));
+  p.off_sum = p.off_acc + up(rows * D * sizeof(float));
+  const bool emptied = fp32 && p.n_tsub + p.n_wsub > kEmpty;
+  p.bytes = p.off_sum + (emptied ? up((size_t)ctas * p.shares * 128 * D * sizeof(float)) : 0);
   return p;
 }
 
@@ -748,7 +796,7 @@ size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D
     return p.ws_bytes;
   }
   // shares (and with them the partial results) grow as the visible blocks do
-  return plan8(C, n_tiles, win_len, Hq, Hkv, D).bytes;
+  return plan8(C, n_tiles, win_len, Hq, Hkv, D, true).bytes;
 }
 
 cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st) {
@@ -764,10 +812,11 @@ cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st) {
   const int win_vis = (int)(w < 0 ? 0 : w < a.win_len ? w : a.win_len);
   Att8Args s;
   s.a = a;
-  s.p = plan8(a.C, n_tblk, win_vis, a.Hq, a.Hkv, a.D);
+  s.p = plan8(a.C, n_tblk, win_vis, a.Hq, a.Hkv, a.D, a.io == KVARN_IO_F32);
   s.scale = reinterpret_cast<float*>(a.ws + s.p.off_scale);
   s.ml = reinterpret_cast<float2*>(a.ws + s.p.off_ml);
   s.acc = reinterpret_cast<float*>(a.ws + s.p.off_acc);
+  s.sum = reinterpret_cast<float4*>(a.ws + s.p.off_sum);
   switch (a.D) {
     case 64: return launch_p8d<64>(s, st);
     case 128: return launch_p8d<128>(s, st);

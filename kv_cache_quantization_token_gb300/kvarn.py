@@ -458,6 +458,8 @@ def _call(device, fn, stream, *args):
             return _call(device, fn, stream, *args)
     if stream is None:
         stream = torch.cuda.current_stream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
     rc = getattr(_lib or _L(), fn)(*args, stream.cuda_stream)
     if rc != 0:
         raise KvarnError(fn, rc)

@@ -127,6 +127,7 @@ def test_evict_refusals(lib):
                dict(B=1, ev=ctypes.c_void_p(2 << 20))):
         assert _evict(lib, **kw) == -4, kw
     assert _evict(lib, B=1, t=ctypes.c_void_p((1 << 20) + 4)) == -2
+    assert _evict(lib, B=65536) == -4
 
 
 def test_host_tensors_are_refused():

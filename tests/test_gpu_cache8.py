@@ -208,6 +208,62 @@ def test_decode_weights_accumulate(D):
     assert torch.equal(c.decode(q), out)                   # the weights do not change the output
 
 
+def test_decode_without_tiles_or_window():
+    lay = kvarn.layout8(64)
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    q = _query(1, (2, 4, 64), "f16")
+    n = torch.zeros(2, dtype=torch.int32, device=DEV)
+    table = torch.empty(2, 2, 0, dtype=torch.int64, device=DEV)
+    win = torch.empty(2, 2, 0, 64, device=DEV)
+    out = torch.full_like(q, 7.0)
+    kvarn.decode_attention8(q, none, table, n, win, win, n, n, lay, out=out)
+    assert int(out.count_nonzero()) == 0
+    c = Cache8(5, [0, 0], [30, 128], 2, 64)
+    args = list(c.args())
+    args[0], args[1] = none, table
+    _check_decode(c, q, kvarn.decode_attention8(q, *args))
+    c = Cache8(6, [2, 1], [0, 0], 2, 64)
+    args = list(c.args())
+    args[3] = args[4] = win
+    _check_decode(c, q, kvarn.decode_attention8(q, *args))
+
+
+def test_calls_run_on_the_stream_that_they_are_given():
+    c = Cache8(97, [12], [77], 2, 128)
+    q = _query(3, (1, 8, 128), "f32")
+    qc = _query(4, (60, 8, 128), "f32")
+    want, want_c = c.decode(q), c.prefill(qc, 12 * T + 17)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    busy = torch.cuda.Event()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)
+        busy.record()
+    outs = [torch.zeros_like(q), torch.zeros_like(qc)]
+    c.decode(q, out=outs[0], stream=st)
+    c.prefill(qc, 12 * T + 17, out=outs[1], stream=st)
+    assert not busy.query()  # nothing waited
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want_c)
+
+
+def test_decode_on_two_streams_at_once():
+    cs = [Cache8(98 + i, [60, 20], [30, 99], 4, 128) for i in range(2)]
+    qs = [_query(i, (2, 16, 128), "bf16") for i in range(2)]
+    want = [c.decode(q) for c, q in zip(cs, qs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    ws = [torch.empty(kvarn.decode8_workspace_bytes(2, 16, 4, 128, c.max_tiles, c.cap), dtype=torch.uint8, device=DEV)
+          for c in cs]
+    outs = [torch.empty_like(q) for q in qs]
+    for _ in range(20):
+        for c, q, s, w, o in zip(cs, qs, streams, ws, outs):
+            c.decode(q, ws=w, out=o, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
 def test_decode_scales_of_either_sign_and_zero():
     c = Cache8(31, [3], [20], 2, 128)
     q = _query(2, (1, 8, 128), "f32")
@@ -340,10 +396,11 @@ def test_prefill_scales_of_either_sign_and_zero():
         _check_prefill(c, q, 200, c.prefill(q, 200, softmax_scale=s), scale=s)
 
 
+@pytest.mark.parametrize("C", [9, 100])  # on the decode kernels, and on the images
 @pytest.mark.parametrize("D", [64, 256])
-def test_prefill_non_finite_rows_reach_only_the_rows_that_see_them(D):
+def test_prefill_non_finite_rows_reach_only_the_rows_that_see_them(D, C):
     c = Cache8(62, [2], [60], 2, D, "i8", 16)
-    C, pos0 = 100, 2 * T + 60 - 100
+    pos0 = 2 * T + 34 - C                    # the chunk ends four positions past the bad row
     q = _query(8, (C, 4, D), "f32")
     want = c.prefill(q, pos0)
     for arr, bad in ((c.win_v, float("inf")), (c.win_k, float("nan")), (c.win_v, float("nan"))):
@@ -360,16 +417,18 @@ def test_prefill_non_finite_rows_reach_only_the_rows_that_see_them(D):
     k[100] = np.nan
     kvarn.compress_tile8(torch.from_numpy(k).to(DEV), torch.from_numpy(v).to(DEV), torch.zeros(1, dtype=torch.int64, device=DEV),
                          c.tiles, c.table[0, 1, 1:2].contiguous(), c.lay)
-    out = c.prefill(q, 150)
-    seen = T + 96 - 150  # the group's first token
+    pos0 = min(T + 93, 2 * T + 60 - C)
+    seen = T + 96 - pos0                     # the chunk's row at the group's first token
+    out = c.prefill(q, pos0)
     assert bool(out[seen:, 2:].isnan().all()) and bool(out[:seen].isfinite().all())
     assert bool(out[:, :2].isfinite().all())
 
 
-def test_prefill_bad_offsets_poison_what_sees_them():
+@pytest.mark.parametrize("C", [8, 200])
+def test_prefill_bad_offsets_poison_what_sees_them(C):
     c = Cache8(52, [4], [9], 2, 128)
-    q = _query(3, (200, 8, 128), "bf16")
-    pos0 = 4 * T + 9 - 200
+    q = _query(3, (C, 8, 128), "bf16")
+    pos0 = 3 * T - 4 if C == 8 else 4 * T + 9 - C
     want = c.prefill(q, pos0)
     for off in (-16, 8, c.tiles.numel() - c.lay.record_bytes + 16, 1 << 62):
         t = c.table[0].clone()
@@ -379,6 +438,30 @@ def test_prefill_bad_offsets_poison_what_sees_them():
         first = 3 * T - pos0
         assert torch.equal(out[:, :4], want[:, :4]) and bool(out[first:, 4:].isnan().all())
         assert bool(out[:first, 4:].isfinite().all())
+
+
+@pytest.mark.parametrize("C", [4, 100])
+def test_a_pool_smaller_than_a_record_is_not_read(C):
+    lay = kvarn.layout8(128)
+    pool = torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    win = torch.randn(1, 128, 128, device=DEV)
+    table = torch.zeros(1, 1, dtype=torch.int64, device=DEV)
+    out = kvarn.prefill_attention8(_query(1, (C, 1, 128), "f32"), 128, pool, table, 1, win, win, 0, 128, lay)
+    assert kvarn.device_error() == kvarn.DEVERR_RECORD and bool(out.isnan().all())
+    one = torch.ones(1, dtype=torch.int32, device=DEV)
+    out = kvarn.decode_attention8(_query(1, (1, 1, 128), "f32"), pool, table[None], one, win[None], win[None], one, one, lay)
+    assert kvarn.device_error() == kvarn.DEVERR_RECORD and bool(out.isnan().all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("C,G", [(5, 8), (6, 8), (11, 4), (64, 1), (13, 5), (16, 4)])
+def test_prefill_around_the_change_of_kernels(C, G, io):
+    """Chunks just below and above the row count from which the images pay; also at 0 tiles."""
+    for tiles, window in ((70, 90), (0, 130)):
+        c = Cache8(C + G, [tiles], [window], 3, 64, "i8", 32)
+        q = _query(C, (C, 3 * G, 64), io)
+        pos0 = T * tiles + window - C
+        _check_prefill(c, q, pos0, c.prefill(q, pos0))
 
 
 def test_prefill_of_one_position_agrees_with_decode():
