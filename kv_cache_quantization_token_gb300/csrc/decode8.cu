@@ -51,6 +51,10 @@ struct D8 {
   static constexpr int SLOT = HALF + 128;
   static constexpr int SLOTS = D == 256 ? 3 : 6;
   static constexpr int CTAS = D == 64 ? 4 : 2;   // resident per SM
+  // The tensor core drops what falls below a sum's last bit. Where registers allow, a score is two sums
+  // and a tile's values a sum of their own, joined with rounding (at head_dim 256 they spill: 224 us of
+  // batched decode become 245).
+  static constexpr bool FRESH = D <= 128;
   static constexpr int WROWS = 8 * NW;           // window rows per window item
   static constexpr int OFF_P = SLOTS * SLOT;
   static constexpr int OFF_MX = OFF_P + 8 * kPRow;              // float2 [8][NW]: (max s, max s + log2 vscale)
@@ -363,7 +367,8 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     float mw = -INFINITY;
 #pragma unroll
     for (int t = 0; t < C::NT; ++t) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+      float (&e)[4] = C::FRESH ? d : c;
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j) {
         const uint4 w = *reinterpret_cast<const uint4*>(rec +
@@ -371,11 +376,11 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
         uint32_t b0, b1;
         codes_to_half<F>(w.x, b0, b1); mma_f16(c, qa[4 * j], b0, b1);
         codes_to_half<F>(w.y, b0, b1); mma_f16(c, qa[4 * j + 1], b0, b1);
-        codes_to_half<F>(w.z, b0, b1); mma_f16(c, qa[4 * j + 2], b0, b1);
-        codes_to_half<F>(w.w, b0, b1); mma_f16(c, qa[4 * j + 3], b0, b1);
+        codes_to_half<F>(w.z, b0, b1); mma_f16(e, qa[4 * j + 2], b0, b1);
+        codes_to_half<F>(w.w, b0, b1); mma_f16(e, qa[4 * j + 3], b0, b1);
       }
-      sc[t][0] = (c[0] + c[2]) * kc;
-      sc[t][1] = (c[1] + c[3]) * kc;
+      sc[t][0] = ((c[0] + d[0]) + (c[2] + d[2])) * kc;
+      sc[t][1] = ((c[1] + d[1]) + (c[3] + d[3])) * kc;
       if constexpr (CHUNK) {
         const int64_t pos = (int64_t)128 * (first + i) + 8 * (warp * C::NT + t) + 2 * q;
         if (pos >= seen) sc[t][0] = -INFINITY;
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
       Un = fmaxf(Un, fmaxf(v.y, v.w));
     }
     const float al = fast_ex2(M - Mn), ao = fast_ex2(U - Un);
-    const bool moved = Un != U;
+    [[maybe_unused]] const bool moved = Un != U;
     M = Mn;
     U = Un;
     // weight of a value code: probability * scale, in units of 2^(U - kHead); a factor past the
@@ -436,14 +441,16 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
       for (int w = 0; w < C::NW; ++w) t += lbuf[w * 8 + g];
       s.tile_ml[(((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + i) * 8 + g] = make_float2(M, t);
     }
-    if (__any_sync(0xffffffffu, moved)) {
+    ok &= landed(2 * i + 1);
+    const unsigned char* V = smem + ((2 * i + 1) % C::SLOTS) * C::SLOT;
+    float fresh[C::NC][4] = {};
+    float (&ot)[C::NC][4] = C::FRESH ? fresh : o;
+    if (!C::FRESH && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int c = 0; c < C::NC; ++c)
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[c][r] *= ao;
     }
-    ok &= landed(2 * i + 1);
-    const unsigned char* V = smem + ((2 * i + 1) % C::SLOTS) * C::SLOT;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 w[C::NC];
@@ -458,9 +465,15 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
         for (int c = 0; c < C::NC; ++c) {
           uint32_t b0, b1;
           codes_to_half<F>((&w[c].x)[r], b0, b1);
-          mma_f16(o[c], pa, b0, b1);
+          mma_f16(ot[c], pa, b0, b1);
         }
       }
+    }
+    if constexpr (C::FRESH) {
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[c][r] = fmaf(o[c][r], ao, fresh[c][r]);
     }
     if (i + 1 < nt) scores(i + 1);
   }

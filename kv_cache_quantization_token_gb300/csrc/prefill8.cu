@@ -39,7 +39,7 @@ constexpr float kLag = 7.f;   // references move when exceeded by this power of 
 // The tensor core drops what falls below an accumulator's last bit, for fp32 work eight times per block,
 // some 1e-8 of O each time: O is emptied into global memory with rounded sums every so many blocks (15,500
 // tokens, fp32: 8e-6 off without, 4e-6 with; 2.5 us each time).
-constexpr int kEmpty = 96;
+constexpr int kEmpty = 48;
 
 template <int D, int NP>
 struct PC8 {
@@ -115,6 +115,13 @@ struct Att8Args {
 };
 
 // ---------------------------------------------------------------------------
+// 32 bytes to an aligned sector.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t (&h)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+               "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+               : "memory");
+}
+
 // images: of tile blockIdx.x of KV head blockIdx.y, or (past the tiles) of 16 window rows of K or of V
 template <int D, int F>
 __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
@@ -176,8 +183,16 @@ __global__ void __launch_bounds__(256) image8_kernel(const Att8Args s) {
       }
       uint8_t* img = head + (image_index(j * SUB + tok / KB) + (is_v ? 2 : 0)) * P::IMG;
       const int rr = is_v ? row : row % KB, kk = is_v ? k % KB : k, rows = is_v ? D : KB;
-      *reinterpret_cast<uint4*>(img + sw_off(rr, kk, rows)) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(img + sw_off(rr, kk + 8, rows)) = make_uint4(h[4], h[5], h[6], h[7]);
+      // the two 16-byte chunks of the unit share a 32-byte sector, swapped in odd rows of the swizzle
+      if (rr & 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t t = h[e];
+          h[e] = h[4 + e];
+          h[4 + e] = t;
+        }
+      }
+      st_sector(img + (sw_off(rr, kk, rows) & ~31u), h);
     }
     return;
   }
