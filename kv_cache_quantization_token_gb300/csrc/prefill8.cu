@@ -3,25 +3,37 @@
 //
 //   out[i][h] = sum_j softmax_j(scale q[i][h] . k_j) v_j over keys j with position(j) <= pos0 + i
 //
-//   image kernel      one CTA per (128-key block, KV head): codes, exact in fp16, or window rows as
-//                     fp16 pairs hi + lo scaled by a power of two per 16 rows, as operand images
-//                     K [key][channel] and V^T [channel][key] in the 128-byte-swizzled K-major layout
-//                     the tensor cores read, plus the scales of each 16-token group.
-//   attention kernel  one CTA per KV head, 128 score rows (the G heads of the group x 128 / G
-//                     positions) and, when there are few rows, a share of the keys: 8 or 12 softmax
-//                     warps, two MMA warps and two copy warps.
+//   image kernel      a CTA per tile and KV head, or per 16 window rows of K or of V: codes, exact in fp16,
+//                     or window rows as fp16 pairs hi + lo scaled by a power of two per 16 rows, as operand
+//                     images of 64-key blocks, K [key][channel] and V^T [channel][key], in the
+//                     128-byte-swizzled K-major layout the tensor cores read, plus the scales.
+//   attention kernel  a CTA per KV head, 128 score rows (the G heads of the group x 128 / G positions) and,
+//                     when there are few rows, a share of the keys: 8 or 12 softmax warps, two MMA warps and
+//                     two copy warps.
 //   merge kernel      joins the key shares, when there are several.
+// Chunks of few rows run on the decode kernels instead (few_rows() below).
 //
 // A scale is constant over 16 keys, so it multiplies scores and probabilities and the codes are used as
-// they are: S = Q K^T with the query rows scaled by a power of two, then per group of 16 keys
-//   p = 2^(S kscale c - m),  l += p,  w = p vscale 2^(m - u),  O += w V
-// with running references m (scores) and u (weighted scores), both moved only when exceeded by several
-// powers of two, so that O is rarely rescaled.
-// Precision: fp32 queries and their probabilities are pairs hi + lo of fp16 (22 bits), two products per
-// code operand. 16-bit queries are exact in one fp16 operand, and then w is rounded to fp16 once (2^-12
-// relative, a quarter or less of the rounding of the output): one product. Window rows are always pairs.
-// The query and w are read from tensor memory (the A operand), so shared memory feeds B operands only; at
-// head_dim 256 the lo part of the query lives in shared memory.
+// they are: S = Q K^T with the query rows scaled by a power of two, then with one reference u per row
+//   w = 2^(S kscale c + log2 vscale - u),  O += w V,  l += (sum of w over the 16 keys) / vscale
+// so that a weight costs one multiply-add and one exponential. u is the largest weighted score so far,
+// moved only when exceeded by several powers of two, so that O is rarely rescaled; whatever the ratio of
+// the value scales, the largest terms of O keep their bits.
+// Precision: fp32 queries and their weights are pairs hi + lo of fp16 (22 bits), two products per code
+// operand. 16-bit queries are exact in one fp16 operand, and then w is rounded to fp16 once (2^-11 of each
+// weight at most, an eighth of bf16's rounding of the output, as much as fp16's): one product. Window rows
+// are always pairs. The query and w are read from tensor memory (the A operand), so shared memory feeds B
+// operands only; at head_dim 256 the lo part of the query lives in shared memory.
+//
+// What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 122 us, 1,050 TFLOP/s, 55%
+// of the measured bf16 rate; images 17 us of it): the softmax warps. A 64-key block costs the tensor pipe 512
+// cycles and 12 softmax warps some 450 instructions per warp, and the SM issues 2.4 per cycle. What made it
+// faster, from 207 us: window rows by 16 (their 128-row CTAs were the tail of the image grid), softmax
+// groups that take blocks in turn instead of halves of one block, MMA warps that do their waiting beside each
+// other's products, hardware barriers for hand-overs, copies of two blocks at a time, one reference instead
+// of two. With fp32 (two products of each kind) the tensor pipe bounds it: 181 us against 122 of products.
+// Not kept: P in the columns of its scores (S of the next block then waits for PV), one MMA warp, four
+// softmax groups (96 registers each), 128-key blocks.
 //
 // A cached row with a NaN or an infinity gets a NaN key and a zero value in the images: a score row that
 // sees it becomes NaN, one that does not is untouched (0 x NaN never enters the value product).
