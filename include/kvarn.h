@@ -539,6 +539,12 @@ typedef struct kvarn_layout8 {
   int64_t off_k_codes, off_v_codes, off_k_scale, off_v_scale;
 } kvarn_layout8_t;
 
+/*
+ * Limits of the calls below: at most 2^29 tiles of a head and window rows, 65535
+ * sequences and KV heads (KVARN_ERR_BAD_ARG), Hq a multiple of Hkv, 8 query heads
+ * per KV head at most (KVARN_ERR_UNSUPPORTED). Scores are fp32 numbers.
+ */
+
 /* Fills *out (host pointer). KVARN_ERR_UNSUPPORTED for head dims other than 64,
  * 128 and 256, other formats, or block_tokens other than 16, 32, 64 and 128. */
 int kvarn_layout8(int head_dim, int code_format, int block_tokens, kvarn_layout8_t* out);
@@ -546,8 +552,9 @@ int kvarn_layout8(int head_dim, int code_format, int block_tokens, kvarn_layout8
 /*
  * Element type of the queries and the outputs of the 8-bit cache's attention
  * calls. KVARN_IO_F32 keeps about 22 bits of every operand. With the 16-bit
- * types the queries enter the products exactly (bf16: down to 2^-25 of the
- * row's largest) and the output is rounded once.
+ * types the queries enter the products to within 2^-33 of their row's largest
+ * element and the output is rounded once; chunked prefill then also rounds the
+ * softmax weights, to fp16.
  */
 #define KVARN_IO_F32 0
 #define KVARN_IO_F16 1
@@ -612,12 +619,13 @@ int kvarn_decode_attention8(const void* q, int io_type, const uint8_t* tiles, in
  * Chunked-prefill attention over the 8-bit cache: the result that
  * kvarn_prefill_attention defines (same positions, window and causal rule), over
  * records of a kvarn_layout8_t, with queries and outputs [C][Hq][D] of type
- * io_type. A row that sees a NaN or an infinity in a cached K or V row is NaN;
- * rows before it are not touched by it. tile_table entries are multiples of 16; one
+ * io_type. A row that sees a NaN or an infinity in a cached K or V row, or has one
+ * in its query, is NaN; rows before it are not touched by it. tile_table entries are multiples of 16; one
  * outside the pool makes the rows that see it NaN and sets KVARN_DEVERR_RECORD.
- *   ws       : at least kvarn_prefill8_workspace_bytes(C, n_tiles, win_len, Hq, Hkv,
- *              head_dim) bytes, 256-byte aligned, no initialisation. Calls
- *              sharing ws must not overlap.
+ *   ws       : at least kvarn_prefill8_workspace_bytes() bytes for these very
+ *              sizes (two kinds of kernels serve small and large chunks, so a
+ *              smaller chunk or cache can need more), 256-byte aligned, no
+ *              initialisation. Calls sharing ws must not overlap.
  * After tiles were evicted (kvarn_evict_tiles) positions count the cached tokens
  * that are left: pos0 = 128 n_tiles + win_len - C for the newest C tokens.
  */
@@ -647,7 +655,7 @@ int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t po
  *   keep       : >= 1, sinks and recent >= 0, sinks + recent <= keep.
  * One launch, deterministic, no workspace; can be captured. After it, tile i no longer
  * holds positions [128 i, 128 i + 128): see kvarn_prefill_attention8.
- * launch_flags: 0 or KVARN_LAUNCH_PDL.
+ * launch_flags: 0 or KVARN_LAUNCH_PDL (other bits give KVARN_ERR_BAD_ARG).
  */
 int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const int32_t* n_tiles,
                       int64_t* table_out, float* mass_out, int32_t* n_tiles_out, int64_t* evicted,

@@ -34,6 +34,9 @@ int heads_ok(int Hq, int Hkv, int D) {
   return KVARN_OK;
 }
 
+// Tiles of a head and window rows stay below this, so that the kernels' 32-bit counts of them hold.
+constexpr int kMost = 1 << 29;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 }  // namespace
@@ -103,7 +106,8 @@ int kvarn_expand_tile8(const uint8_t* tiles, int64_t tiles_bytes, const int64_t*
 static int decode8_check(int B, int Hq, int Hkv, int D, int max_tiles, int win_capacity) {
   const int rc = heads_ok(Hq, Hkv, D);
   if (rc != KVARN_OK) return rc;
-  if (B < 0 || max_tiles < 0 || win_capacity < 0 || B > 65535) return KVARN_ERR_BAD_ARG;
+  if (B < 0 || max_tiles < 0 || win_capacity < 0 || B > 65535 || max_tiles > kMost || win_capacity > kMost)
+    return KVARN_ERR_BAD_ARG;
   // the grids' first dimension and the workspace stay in range
   if ((int64_t)Hkv * ((max_tiles + 255) / 256) + Hq > 0x7fffffff) return KVARN_ERR_BAD_ARG;
   return KVARN_OK;
@@ -143,7 +147,9 @@ int kvarn_decode_attention8(const void* q, int io_type, const uint8_t* tiles, in
   if (p.ws_bytes > 0 && !ws) return KVARN_ERR_NULL;
   if (ws_bytes < p.ws_bytes) return KVARN_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(out, 16) || (max_tiles > 0 && !aligned(tiles, 16)) ||
-      (win_capacity > 0 && (!aligned(win_k, 16) || !aligned(win_v, 16))) || !aligned(ws, 256))
+      (win_capacity > 0 && (!aligned(win_k, 16) || !aligned(win_v, 16))) || !aligned(ws, 256) ||
+      !aligned(tile_table, 8) || !aligned(n_tiles, 4) || !aligned(win_start, 4) || !aligned(win_len, 4) ||
+      !aligned(mass_in, 4) || !aligned(mass_out, 4))
     return KVARN_ERR_ALIGN;
   const size_t n_mass = (size_t)B * Hkv * max_tiles * sizeof(float);
   if (mass_in && mass_in != mass_out && overlap(mass_in, n_mass, mass_out, n_mass)) return KVARN_ERR_BAD_ARG;
@@ -159,7 +165,7 @@ int kvarn_prefill8_workspace_bytes(int C, int n_tiles, int win_len, int Hq, int 
   if (!bytes) return KVARN_ERR_NULL;
   const int rc = heads_ok(Hq, Hkv, head_dim);
   if (rc != KVARN_OK) return rc;
-  if (C < 0 || n_tiles < 0 || win_len < 0) return KVARN_ERR_BAD_ARG;
+  if (C < 0 || n_tiles < 0 || win_len < 0 || n_tiles > kMost || win_len > kMost) return KVARN_ERR_BAD_ARG;
   *bytes = kvarn::prefill8_ws_bytes(C, n_tiles, win_len, Hq, Hkv, head_dim);
   return KVARN_OK;
 }
@@ -175,7 +181,8 @@ int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t po
   if (!layout) return KVARN_ERR_NULL;
   if (!layout_ok(layout) || layout->head_dim != head_dim) return KVARN_ERR_UNSUPPORTED;
   if (!io_ok(io_type) || C < 0 || pos0 < 0 || n_tiles < 0 || win_len < 0 || win_capacity < 0 ||
-      tiles_bytes < 0 || table_stride < n_tiles || win_len > win_capacity)
+      tiles_bytes < 0 || table_stride < n_tiles || win_len > win_capacity || n_tiles > kMost ||
+      win_capacity > kMost)
     return KVARN_ERR_BAD_ARG;
   if (pos0 > (int64_t)KVARN_TILE_TOKENS * n_tiles + win_len - C) return KVARN_ERR_BAD_ARG;
   if (!(softmax_scale == softmax_scale)) return KVARN_ERR_BAD_ARG;
@@ -185,7 +192,7 @@ int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t po
   if (win_len > 0 && (!win_k || !win_v)) return KVARN_ERR_NULL;
   if (ws_bytes < kvarn::prefill8_ws_bytes(C, n_tiles, win_len, Hq, Hkv, head_dim)) return KVARN_ERR_WORKSPACE;
   if (!aligned(q_chunk, 16) || !aligned(out, 16) || (n_tiles > 0 && !aligned(tiles, 16)) ||
-      (win_len > 0 && (!aligned(win_k, 16) || !aligned(win_v, 16))) || !aligned(ws, 256))
+      (win_len > 0 && (!aligned(win_k, 16) || !aligned(win_v, 16))) || !aligned(ws, 256) || !aligned(tile_table, 8))
     return KVARN_ERR_ALIGN;
   const int start = win_capacity > 0 ? (int)((((int64_t)win_start % win_capacity) + win_capacity) % win_capacity) : 0;
   const kvarn::Prefill8Args a{q_chunk, tiles, tile_table, win_k, win_v, static_cast<uint8_t*>(ws), out, pos0,
@@ -199,8 +206,8 @@ int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const i
                       int64_t* table_out, float* mass_out, int32_t* n_tiles_out, int64_t* evicted, int B,
                       int Hkv, int max_tiles, int keep, int sinks, int recent, unsigned launch_flags,
                       kvarn_stream_t stream) {
-  if (B < 0 || B > 65535 || Hkv <= 0 || Hkv > 65535 || max_tiles < 0 || keep < 1 || sinks < 0 || recent < 0 ||
-      (int64_t)sinks + recent > keep || !flags_ok(launch_flags))
+  if (B < 0 || B > 65535 || Hkv <= 0 || Hkv > 65535 || max_tiles < 0 || max_tiles > kMost || keep < 1 ||
+      sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep || (launch_flags & ~KVARN_LAUNCH_PDL))
     return KVARN_ERR_BAD_ARG;
   if (B == 0) return KVARN_OK;
   if (!n_tiles || !n_tiles_out) return KVARN_ERR_NULL;

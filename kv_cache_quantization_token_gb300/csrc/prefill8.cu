@@ -335,9 +335,10 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
       }
     xm[half * 128 + row].x = m;
     take_over<64>(kBarPair + (warp & 3));
-    const float up = pow2_to(fmaxf(m, xm[(half ^ 1) * 128 + row].x), 10);
+    const float mq = fmaxf(m, xm[(half ^ 1) * 128 + row].x), up = pow2_to(mq, 10);
     if (half == 0) xm[row].y = fabsf(a.scale) * pow2_inverse(up);
-    const float p2 = copysignf(up, a.scale);  // maxima are taken before the (positive) scales
+    // (maxima are taken before the positive scales; a row with an infinity becomes NaN)
+    const float p2 = mq == INFINITY ? NAN : copysignf(up, a.scale);
 #pragma unroll 1
     for (int c0 = 0; c0 < D / 2; c0 += 32) {
       uint32_t hw[16], lw[16];

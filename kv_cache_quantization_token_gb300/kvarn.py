@@ -465,6 +465,18 @@ def _call(device, fn, stream, *args):
         raise KvarnError(fn, rc)
 
 
+def _scratch(nbytes, like, stream):
+    """Workspace on like's device, in the memory of the stream that will use it: it is
+    given back on return, and only later work of that stream may take it."""
+    with torch.cuda.stream(stream):  # (None: the current stream)
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=like.device)
+
+
+def _result(like, stream):
+    with torch.cuda.stream(stream):
+        return torch.empty_like(like)
+
+
 def _rows8(k, v, rows, tiles, records, names):
     _dev(k, names[0], torch.float32)
     device = k.get_device()
@@ -535,9 +547,9 @@ def decode_attention8(q, tiles, tile_table, n_tiles, win_k, win_v, win_start, wi
     if ws is None:
         with torch.cuda.device(device):  # the split of the work depends on the device
             need = decode8_workspace_bytes(B, Hq, Hkv, D, max_tiles, cap)
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        ws = _scratch(need, q, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(q, stream)
     _fit(device, ("ws", ws, torch.uint8), ("out", out, q.dtype))
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
@@ -563,7 +575,8 @@ def prefill_attention8(q_chunk, pos0, tiles, tile_table, n_tiles, win_k, win_v, 
                        lay: Layout8, softmax_scale=None, ws=None, out=None, stream=None):
     """prefill_attention over 8-bit records: q_chunk and out fp32, fp16 or bf16
     [C][Hq][D], the other arguments as prefill_attention's; ws a uint8 device
-    workspace of prefill8_workspace_bytes() (allocated here when None)."""
+    workspace of prefill8_workspace_bytes() for these very sizes (allocated here
+    when None)."""
     io, device = _io(q_chunk, "q_chunk")
     _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64),
          ("win_k", win_k, torch.float32), ("win_v", win_v, torch.float32))
@@ -576,11 +589,11 @@ def prefill_attention8(q_chunk, pos0, tiles, tile_table, n_tiles, win_k, win_v, 
     if win_k.shape != win_v.shape or (Hw, Dw) != (Hkv, D):
         raise ValueError("prefill_attention8: inconsistent shapes")
     if out is None:
-        out = torch.empty_like(q_chunk)
+        out = _result(q_chunk, stream)
     if ws is None:
         with torch.cuda.device(device):
             need = prefill8_workspace_bytes(C, n_tiles, win_len, Hq, Hkv, D)
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q_chunk.device)
+        ws = _scratch(need, q_chunk, stream)
     _fit(device, ("ws", ws, torch.uint8), ("out", out, q_chunk.dtype))
     if out.shape != q_chunk.shape:
         raise ValueError("out must have q_chunk's shape")

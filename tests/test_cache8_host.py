@@ -73,6 +73,11 @@ def test_decode_refusals(lib):
     for k in ("q", "tiles", "wk", "wv", "out"):
         assert _decode(lib, **{k: ODD}) == -2, k
     assert _decode(lib, ws=ctypes.c_void_p((1 << 20) + 128)) == -2
+    for k in ("table", "n", "ws_", "wl"):
+        assert _decode(lib, **{k: ctypes.c_void_p((1 << 20) + 2)}) == -2, k
+    assert _decode(lib, table=ctypes.c_void_p((1 << 20) + 4)) == -2
+    assert _decode(lib, mo=ctypes.c_void_p((1 << 20) + 2)) == -2
+    assert _decode(lib, mt=(1 << 29) + 1) == -4 and _decode(lib, cap=(1 << 29) + 1) == -4
     for kw in (dict(io=3), dict(io=-1), dict(tiles_bytes=-1), dict(cap=-1), dict(B=-1), dict(B=65536), dict(Hq=30),
                dict(Hq=0), dict(Hkv=0), dict(mt=-1), dict(flags=4), dict(flags=2), dict(scale=f32(float("nan"))),
                dict(mi=P), dict(mi=P, mo=ctypes.c_void_p((1 << 20) + 4))):
@@ -106,6 +111,13 @@ def test_prefill_refusals(lib):
         assert _prefill(lib, **kw) == -4, kw
     assert _prefill(lib, Hq=72) == -3 and _prefill(lib, D=64) == -3 and _prefill(lib, D=100) == -3
     assert _prefill(lib, wsb=1 << 10) == -5
+    assert _prefill(lib, table=ctypes.c_void_p((1 << 20) + 4)) == -2
+    many, most = (1 << 29) + 1, ctypes.c_size_t()
+    assert _prefill(lib, nt=many, stride=many) == -4 and _prefill(lib, cap=many) == -4
+    query = lib.kvarn_prefill8_workspace_bytes
+    assert query(512, many, 0, 32, 8, 128, ctypes.byref(most)) == -4 and query(512, 0, many, 32, 8, 128, ctypes.byref(most)) == -4
+    # the largest sizes are counted without wrapping: images of every tile, fp16 K and V
+    assert query(512, 1 << 29, 1 << 29, 32, 8, 256, ctypes.byref(most)) == 0 and most.value > 8 * 2 * 128 * 512 << 29
     assert _prefill(lib, C=0) == 0
 
 
@@ -127,7 +139,8 @@ def test_evict_refusals(lib):
                dict(B=1, ev=ctypes.c_void_p(2 << 20))):
         assert _evict(lib, **kw) == -4, kw
     assert _evict(lib, B=1, t=ctypes.c_void_p((1 << 20) + 4)) == -2
-    assert _evict(lib, B=65536) == -4
+    assert _evict(lib, B=65536) == -4 and _evict(lib, mt=(1 << 29) + 1) == -4
+    assert _evict(lib, flags=kvarn.LAUNCH_PDL | kvarn.LAUNCH_PREFETCH) == -4
 
 
 def test_host_tensors_are_refused():

@@ -247,6 +247,27 @@ def test_calls_run_on_the_stream_that_they_are_given():
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want_c)
 
 
+def test_workspaces_allocated_for_a_stream_stay_its_own(monkeypatch):
+    """A workspace that a call allocates is not handed to another stream while the call may run."""
+    c = Cache8(97, [12], [77], 2, 128)
+    calls, real = [], kvarn._call
+    monkeypatch.setattr(kvarn, "_call", lambda *a: (calls.append(a), real(*a))[1])
+    st = torch.cuda.Stream()
+    for q, run in ((_query(3, (1, 8, 128), "f32"), lambda q: c.decode(q, stream=st)),
+                   (_query(4, (60, 8, 128), "f32"), lambda q: c.prefill(q, 12 * T + 17, stream=st))):
+        want = run(q)
+        st.synchronize()
+        calls.clear()
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        out = run(q)
+        sizes = [x for x in calls[0] if isinstance(x, int)]
+        mine = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes if 256 <= n < 1 << 28 for _ in range(3)]
+        assert not {t.data_ptr() for t in mine} & set(sizes)
+        st.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_decode_on_two_streams_at_once():
     cs = [Cache8(98 + i, [60, 20], [30, 99], 4, 128) for i in range(2)]
     qs = [_query(i, (2, 16, 128), "bf16") for i in range(2)]
@@ -422,6 +443,27 @@ def test_prefill_non_finite_rows_reach_only_the_rows_that_see_them(D, C):
     out = c.prefill(q, pos0)
     assert bool(out[seen:, 2:].isnan().all()) and bool(out[:seen].isfinite().all())
     assert bool(out[:, :2].isfinite().all())
+
+
+@pytest.mark.parametrize("C", [9, 100])
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+def test_prefill_non_finite_queries_are_nan(io, C):
+    """Also where every product of an infinite query with a key has the same sign."""
+    c = Cache8(63, [2], [20], 2, 128, "i8", 32)
+    k, v = rows(np.random.default_rng(3), T, 128)
+    k[:, 5] = 1
+    for i in range(2):
+        kvarn.compress_tile8(torch.from_numpy(k).to(DEV), torch.from_numpy(v).to(DEV),
+                             torch.zeros(1, dtype=torch.int64, device=DEV), c.tiles, c.table[0, 1, i:i + 1].contiguous(),
+                             c.lay)
+    for pos0 in (T, 2 * T + 20 - C):
+        q = _query(8, (C, 4, 128), io)
+        want = c.prefill(q, pos0)
+        q[1, 2, 5], q[2, 2, 5], q[3, 3, 7], q[5, 0, 0] = -np.inf, np.inf, np.nan, -np.inf
+        out = c.prefill(q, pos0)
+        bad = torch.zeros(C, 4, dtype=torch.bool, device=DEV)
+        bad[1, 2] = bad[2, 2] = bad[3, 3] = bad[5, 0] = True
+        assert bool(out[bad].isnan().all()) and torch.equal(out[~bad], want[~bad])
 
 
 @pytest.mark.parametrize("C", [8, 200])
