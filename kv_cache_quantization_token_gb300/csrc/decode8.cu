@@ -91,10 +91,11 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo with hi a tf32 number; lo keeps the rest (tf32 reads its top 11 bits).
+// x = hi + lo, both rounded to the 11 bits that a tf32 operand is read with: within 2^-22 of x.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xFFFFE000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
+  const uint32_t u = __float_as_uint(x), r = u + 0x1000u;
+  hi = ((r & 0x7F800000u) == 0x7F800000u ? u : r) & 0xFFFFE000u;  // (not up to infinity)
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, shfl_xor(v, 1));
@@ -204,7 +205,9 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
   const bool have = 8 * warp + g < n;
   const float* kr = a.win_k + (have ? row(8 * warp + g) : 0) + 4 * q;
   const int64_t qrow = me.index * D + 4 * q;
-  float sc[4] = {0.f, 0.f, 0.f, 0.f};
+  // sums of their own for the parts of K and for odd and even steps: the tensor core cuts off what falls below
+  // a sum's last bit, and no product waits for the one before
+  float sh[2][4] = {}, sl[2][4] = {};
 #pragma unroll 4
   for (int m = 0; m < D / 16; ++m) {
     const float4 kx = have ? *reinterpret_cast<const float4*>(kr + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -216,14 +219,19 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
       split_tf32(h ? qx.w : qx.y, qa[2], qa[3]);
       split_tf32(h ? kx.z : kx.x, kh[0], kl[0]);
       split_tf32(h ? kx.w : kx.y, kh[1], kl[1]);
-      mma_tf32(sc, qa, kh[0], kh[1]);
-      mma_tf32(sc, qa, kl[0], kl[1]);
+      mma_tf32(sh[h], qa, kh[0], kh[1]);
+      mma_tf32(sl[h], qa, kl[0], kl[1]);
     }
   }
+  float sc[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    sc[e] = ((sl[0][e] + sl[1][e]) + ((sh[0][e + 2] + sl[0][e + 2]) + (sh[1][e + 2] + sl[1][e + 2]))) +
+            (sh[0][e] + sh[1][e]);
   const int t0 = 8 * warp + 2 * q;
   __syncthreads();  // dead rows are known
-  const float s0 = t0 < seen ? (dead[t0] ? NAN : (sc[0] + sc[2]) * a.scale) : -INFINITY;
-  const float s1 = t0 + 1 < seen ? (dead[t0 + 1] ? NAN : (sc[1] + sc[3]) * a.scale) : -INFINITY;
+  const float s0 = t0 < seen ? (dead[t0] ? NAN : sc[0] * a.scale) : -INFINITY;
+  const float s1 = t0 + 1 < seen ? (dead[t0 + 1] ? NAN : sc[1] * a.scale) : -INFINITY;
   const float mw = quad_max(fmaxf(s0, s1));
   if (q == 0) mx[g * C::NW + warp].x = mw;
   __syncthreads();
@@ -233,7 +241,7 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
   const float p0 = t0 < seen ? fast_ex2(s0 - M) : 0.f, p1 = t0 + 1 < seen ? fast_ex2(s1 - M) : 0.f;
   *reinterpret_cast<float2*>(P + g * PS + t0) = make_float2(p0, p1);
   const float l = cta_row_sum<C::NW>(quad_sum(p0 + p1), reinterpret_cast<float*>(smem + C::OFF_L), warp, g, q);
-  float o[C::NC][4] = {};
+  float o[C::NC][4] = {}, ol[C::NC][4] = {};
 #pragma unroll
   for (int k = 0; k < C::NW; ++k) {
     uint32_t pa[4];
@@ -245,9 +253,13 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
       split_tf32(v[k][c][0], vh[0], vl[0]);
       split_tf32(v[k][c][1], vh[1], vl[1]);
       mma_tf32(o[c], pa, vh[0], vh[1]);
-      mma_tf32(o[c], pa, vl[0], vl[1]);
+      mma_tf32(ol[c], pa, vl[0], vl[1]);
     }
   }
+#pragma unroll
+  for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[c][r] += ol[c][r];
   if (me.valid) {
     const int64_t part = me.index * s.items + item;
     float* dst = s.acc + part * D + 8 * C::NC * warp + 2 * q;

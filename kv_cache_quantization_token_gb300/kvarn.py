@@ -456,23 +456,29 @@ def _call(device, fn, stream, *args):
     if torch.cuda.current_device() != device:
         with torch.cuda.device(device):
             return _call(device, fn, stream, *args)
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    if stream is None:  # (the handle itself: a Stream object takes a microsecond to make)
+        handle = torch._C._cuda_getCurrentRawStream(device)
     elif stream.device.index != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
-    rc = getattr(_lib or _L(), fn)(*args, stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    rc = getattr(_lib or _L(), fn)(*args, handle)
     if rc != 0:
         raise KvarnError(fn, rc)
 
 
-def _scratch(nbytes, like, stream):
-    """Workspace on like's device, in the memory of the stream that will use it: it is
-    given back on return, and only later work of that stream may take it."""
-    with torch.cuda.stream(stream):  # (None: the current stream)
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=like.device)
+def _scratch(nbytes, device, stream):
+    """A workspace in the memory of the stream that will use it: it is given back on
+    return, and only later work of that stream may take it."""
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def _result(like, stream):
+    if stream is None:
+        return torch.empty_like(like)
     with torch.cuda.stream(stream):
         return torch.empty_like(like)
 
@@ -547,7 +553,7 @@ def decode_attention8(q, tiles, tile_table, n_tiles, win_k, win_v, win_start, wi
     if ws is None:
         with torch.cuda.device(device):  # the split of the work depends on the device
             need = decode8_workspace_bytes(B, Hq, Hkv, D, max_tiles, cap)
-        ws = _scratch(need, q, stream)
+        ws = _scratch(need, q.device, stream)
     if out is None:
         out = _result(q, stream)
     _fit(device, ("ws", ws, torch.uint8), ("out", out, q.dtype))
@@ -593,7 +599,7 @@ def prefill_attention8(q_chunk, pos0, tiles, tile_table, n_tiles, win_k, win_v, 
     if ws is None:
         with torch.cuda.device(device):
             need = prefill8_workspace_bytes(C, n_tiles, win_len, Hq, Hkv, D)
-        ws = _scratch(need, q_chunk, stream)
+        ws = _scratch(need, q_chunk.device, stream)
     _fit(device, ("ws", ws, torch.uint8), ("out", out, q_chunk.dtype))
     if out.shape != q_chunk.shape:
         raise ValueError("out must have q_chunk's shape")
