@@ -25,12 +25,12 @@
 // lane reads is what it needs of the B fragments of four products, up to an order of the
 // summed index (channels, or tokens) that both operands share.
 //
-// A CTA's warps split a tile's tokens for the scores and its channels for the values,
-// with one exchange of row maxima and one of probabilities per tile through shared memory.
+// A CTA's warps split a tile's tokens for the scores and its channels for the values, with one exchange of
+// row maxima and one of probabilities per step of one or two tiles through shared memory.
 //
-// HBM bounds it in batches: 32 ragged sequences of up to 32k tokens, head_dim 256, 1.37 GB in 222 us
-// (6.2 TB/s, 91% of the measured copy rate; one CTA per SM with whole records in its stages took 311);
-// 4 of 64k tokens, head_dim 128, 0.54 GB in 97 us (82%), where the instructions per code (conversion,
+// HBM bounds it in batches: 32 ragged sequences of up to 32k tokens, head_dim 256, 1.37 GB in 218 us
+// (6.3 TB/s, 93% of the measured copy rate; one CTA per SM with whole records in its stages took 311);
+// 4 of 64k tokens, head_dim 128, 0.54 GB in 94 us (84%), where the instructions per code (conversion,
 // products, exchanges: 1.6 per cycle and SM) take as long as the copy. One sequence of 16k tokens, 34 MB,
 // takes 14 us against a floor of 5: a CTA has four tiles, and the chain of launch, count, table, copy, four
 // rounds of exchanges and the merge is latency.
@@ -59,17 +59,20 @@ struct D8 {
   // exchanges are covered by the other's work
   static constexpr int HALF = kTile * D;         // bytes of K or of V codes
   static constexpr int SLOT = HALF + 128;
-  static constexpr int SLOTS = D == 256 ? 3 : 6;
+  // Tiles of a step: two halve the exchanges (4 of 64k tokens, head_dim 128: 97.1 -> 94.4 us; 5 ragged ones,
+  // head_dim 64: 21.1 -> 20.5); at head_dim 256 neither slots nor registers are left for it.
+  static constexpr int TP = D <= 128 ? 2 : 1;
+  static constexpr int SLOTS = D == 256 ? 3 : D == 64 ? 5 : 6;
   static constexpr int CTAS = D == 64 ? 4 : 2;   // resident per SM
   // The tensor core drops what falls below a sum's last bit. Where registers allow, a score is two sums
-  // and a tile's values a sum of their own, joined with rounding (at head_dim 256 they spill: 224 us of
+  // and a step's values a sum of their own, joined with rounding (at head_dim 256 they spill: 224 us of
   // batched decode become 245).
   static constexpr bool FRESH = D <= 128;
   static constexpr int WROWS = 8 * NW;           // window rows per window item
   static constexpr int OFF_P = SLOTS * SLOT;
-  static constexpr int OFF_MX = OFF_P + 8 * kPRow;              // float2 [8][NW]: (max s, max s + log2 vscale)
-  static constexpr int OFF_L = OFF_MX + 8 * NW * 8;             // float [NW][8]
-  static constexpr int OFF_BAR = OFF_L + 8 * NW * 4;
+  static constexpr int OFF_MX = OFF_P + TP * 8 * kPRow;              // float2 [8][NW]: (max s, max s + log2 vscale)
+  static constexpr int OFF_L = OFF_MX + 8 * NW * 8;             // float [TP][NW][8]
+  static constexpr int OFF_BAR = OFF_L + TP * 8 * NW * 4;
   static constexpr int OFF_FLG = OFF_BAR + 8 * SLOTS;         // int: a wait ran out or a record was refused
   static constexpr int SMEM = (OFF_FLG + 8 + 127) / 128 * 128;
   static_assert(SLOT % 128 == 0 && OFF_P % 128 == 0, "alignment");
@@ -179,19 +182,53 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
   const int seen = CHUNK ? (int)max((int64_t)0, min((int64_t)n, me.seen - (int64_t)128 * s.n_tiles - r0)) : n;
   if (tid < C::WROWS) dead[tid] = 0;
   __syncthreads();
-  // the values this warp's channels need, under way while the scores are formed
+  // the values this warp's channels need: under way while the scores are formed, where registers allow
   float v[C::NW][C::NC][2];
+  auto load_values = [&] {
 #pragma unroll
-  for (int k = 0; k < C::NW; ++k) {
-    const int t0 = 8 * k + q, t1 = t0 + 4;
-    const float* v0 = a.win_v + (t0 < n ? row(t0) : 0) + 8 * C::NC * warp + g;
-    const float* v1 = a.win_v + (t1 < n ? row(t1) : 0) + 8 * C::NC * warp + g;
+    for (int k = 0; k < C::NW; ++k) {
+      const int t0 = 8 * k + q, t1 = t0 + 4;
+      const float* v0 = a.win_v + (t0 < n ? row(t0) : 0) + 8 * C::NC * warp + g;
+      const float* v1 = a.win_v + (t1 < n ? row(t1) : 0) + 8 * C::NC * warp + g;
 #pragma unroll
-    for (int c = 0; c < C::NC; ++c) {
-      v[k][c][0] = t0 < n ? v0[8 * c] : 0.f;
-      v[k][c][1] = t1 < n ? v1[8 * c] : 0.f;
+      for (int c = 0; c < C::NC; ++c) {
+        v[k][c][0] = t0 < n ? v0[8 * c] : 0.f;
+        v[k][c][1] = t1 < n ? v1[8 * c] : 0.f;
+      }
     }
+  };
+  if constexpr (D <= 128) load_values();
+  const bool have = 8 * warp + g < n;
+  const float* kr = a.win_k + (have ? row(8 * warp + g) : 0) + 4 * q;
+  const int64_t qrow = me.index * D + 4 * q;
+  // sums of their own for the parts of K and for odd and even steps: the tensor core cuts off what falls below
+  // a sum's last bit, and no product waits for the one before
+  float sh[2][4] = {}, sl[2][4] = {};
+  // loads of K and of the queries under way together, beside those of V where they come first (3 tiles and a
+  // window, head_dim 128: 7.6 us; all of them at once 8.2, in the order of use 8.9)
+  constexpr int RUN = D == 64 ? 2 : D == 128 ? 4 : 8;
+#pragma unroll 1
+  for (int m0 = 0; m0 < D / 16; m0 += RUN) {
+    float4 kx[RUN], qx[RUN];
+#pragma unroll
+    for (int m = 0; m < RUN; ++m) {
+      kx[m] = have ? *reinterpret_cast<const float4*>(kr + 16 * (m0 + m)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      qx[m] = me.valid ? io_ld4(a.q, a.io, qrow + 16 * (m0 + m)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int m = 0; m < RUN; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t qa[4], kh[2], kl[2];
+        split_tf32(h ? qx[m].z : qx[m].x, qa[0], qa[1]);
+        split_tf32(h ? qx[m].w : qx[m].y, qa[2], qa[3]);
+        split_tf32(h ? kx[m].z : kx[m].x, kh[0], kl[0]);
+        split_tf32(h ? kx[m].w : kx[m].y, kh[1], kl[1]);
+        mma_tf32(sh[h], qa, kh[0], kh[1]);
+        mma_tf32(sl[h], qa, kl[0], kl[1]);
+      }
   }
+  if constexpr (D == 256) load_values();
 #pragma unroll
   for (int k = 0; k < C::NW; ++k)
 #pragma unroll
@@ -202,27 +239,6 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
           dead[8 * k + q + 4 * h] = 1;
           v[k][c][h] = 0.f;
         }
-  const bool have = 8 * warp + g < n;
-  const float* kr = a.win_k + (have ? row(8 * warp + g) : 0) + 4 * q;
-  const int64_t qrow = me.index * D + 4 * q;
-  // sums of their own for the parts of K and for odd and even steps: the tensor core cuts off what falls below
-  // a sum's last bit, and no product waits for the one before
-  float sh[2][4] = {}, sl[2][4] = {};
-#pragma unroll 4
-  for (int m = 0; m < D / 16; ++m) {
-    const float4 kx = have ? *reinterpret_cast<const float4*>(kr + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 qx = me.valid ? io_ld4(a.q, a.io, qrow + 16 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t qa[4], kh[2], kl[2];
-      split_tf32(h ? qx.z : qx.x, qa[0], qa[1]);
-      split_tf32(h ? qx.w : qx.y, qa[2], qa[3]);
-      split_tf32(h ? kx.z : kx.x, kh[0], kl[0]);
-      split_tf32(h ? kx.w : kx.y, kh[1], kl[1]);
-      mma_tf32(sh[h], qa, kh[0], kh[1]);
-      mma_tf32(sl[h], qa, kl[0], kl[1]);
-    }
-  }
   float sc[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
@@ -241,7 +257,8 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
   const float p0 = t0 < seen ? fast_ex2(s0 - M) : 0.f, p1 = t0 + 1 < seen ? fast_ex2(s1 - M) : 0.f;
   *reinterpret_cast<float2*>(P + g * PS + t0) = make_float2(p0, p1);
   const float l = cta_row_sum<C::NW>(quad_sum(p0 + p1), reinterpret_cast<float*>(smem + C::OFF_L), warp, g, q);
-  float o[C::NC][4] = {}, ol[C::NC][4] = {};
+  float o[C::NC][4] = {}, olo[C::NC][4] = {};
+  float (&ol)[C::NC][4] = D <= 128 ? olo : o;
 #pragma unroll
   for (int k = 0; k < C::NW; ++k) {
     uint32_t pa[4];
@@ -256,10 +273,12 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
       mma_tf32(ol[c], pa, vl[0], vl[1]);
     }
   }
+  if constexpr (D <= 128) {
 #pragma unroll
-  for (int c = 0; c < C::NC; ++c)
+    for (int c = 0; c < C::NC; ++c)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[c][r] += ol[c][r];
+      for (int r = 0; r < 4; ++r) o[c][r] += olo[c][r];
+  }
   if (me.valid) {
     const int64_t part = me.index * s.items + item;
     float* dst = s.acc + part * D + 8 * C::NC * warp + 2 * q;
@@ -308,11 +327,14 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     }
     return;
   }
-  auto request = [&](int n) {  // one thread: copy n of the item (K, then V of each tile) into its slot
-    if (n >= 2 * nt) return;
+  constexpr int TP = C::TP;
+  auto request = [&](int n) {  // one thread: copy n of the item (K of a step's tiles, then V) into its slot
+    const int tile = n / (2 * TP) * TP + n % TP;
+    if (n < 0 || tile >= nt) return;
+    const bool is_v = n % (2 * TP) >= TP;
     uint64_t* br = bar + n % C::SLOTS;
     unsigned char* dst = smem + (n % C::SLOTS) * C::SLOT;
-    const int64_t off = n < 4 ? ((n >> 1) ? entry[1] : entry[0]) : table[n >> 1];
+    const int64_t off = tile < 2 ? (tile ? entry[1] : entry[0]) : table[tile];
     if ((off & 15) || off < 0 || off > a.tiles_bytes - R::kBytes) {
       // a record that is not read: zero codes under scales of NaN, which only rows that see it meet
       report(a.err, KVARN_DEVERR_RECORD);
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
       mbar_arrive1(br);
       return;
     }
-    if (n & 1) {
+    if (is_v) {
       mbar_arrive_tx(br, C::HALF);
       bulk_in(dst, a.tiles + off + R::kVCodes, C::HALF, br);
     } else {
@@ -375,51 +397,68 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
 
   float M = kNone, U = kNone, l = 0.f;
   float o[C::NC][4] = {};
-  float sc[C::NT][2];
-  float vs = 0.f;
+  float sc[TP][C::NT][2];
+  float vs[TP];
   bool ok = true;
   const int grp = (warp * C::NT) >> 1;  // scale entry of this warp's tokens
 
   auto landed = [&](int n) { return mbar_wait8(bar + n % C::SLOTS, (uint32_t)(n / C::SLOTS) & 1u, a.err); };
-  auto scores = [&](int i) {  // scores of tile i's tokens 8 NT warp .., and their row maxima
-    ok &= landed(2 * i);
-    const unsigned char* rec = smem + (2 * i % C::SLOTS) * C::SLOT;
-    const float kc = reinterpret_cast<const float*>(rec + C::HALF)[grp] * c1;
-    vs = reinterpret_cast<const float*>(rec + C::HALF)[kGrps + grp];
-    float mw = -INFINITY;
+  // scores of step j (tiles TP j ..): of each tile the tokens 8 NT warp .., and their row maxima
+  auto scores = [&](int j) {
+    float mw = -INFINITY, uw = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < C::NT; ++t) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
-      float (&e)[4] = C::FRESH ? d : c;
+    for (int x = 0; x < TP; ++x) {
+      if (TP > 1 && x > 0 && TP * j + x >= nt) {  // an odd item's last step
 #pragma unroll
-      for (int j = 0; j < C::NJ; ++j) {
-        const uint4 w = *reinterpret_cast<const uint4*>(rec +
-                                                        ((warp * C::NT + t) * C::NJ + j) * 512 + lane * 16);
-        uint32_t b0, b1;
-        codes_to_half<F>(w.x, b0, b1); mma_f16(c, qa[4 * j], b0, b1);
-        codes_to_half<F>(w.y, b0, b1); mma_f16(c, qa[4 * j + 1], b0, b1);
-        codes_to_half<F>(w.z, b0, b1); mma_f16(e, qa[4 * j + 2], b0, b1);
-        codes_to_half<F>(w.w, b0, b1); mma_f16(e, qa[4 * j + 3], b0, b1);
+        for (int t = 0; t < C::NT; ++t) sc[x][t][0] = sc[x][t][1] = -INFINITY;
+        vs[x] = 0.f;
+        break;
       }
-      sc[t][0] = ((c[0] + d[0]) + (c[2] + d[2])) * kc;
-      sc[t][1] = ((c[1] + d[1]) + (c[3] + d[3])) * kc;
-      if constexpr (CHUNK) {
-        const int64_t pos = (int64_t)128 * (first + i) + 8 * (warp * C::NT + t) + 2 * q;
-        if (pos >= seen) sc[t][0] = -INFINITY;
-        if (pos + 1 >= seen) sc[t][1] = -INFINITY;
+      const int n = 2 * TP * j + x;
+      ok &= landed(n);
+      const unsigned char* rec = smem + (n % C::SLOTS) * C::SLOT;
+      const float kc = reinterpret_cast<const float*>(rec + C::HALF)[grp] * c1;
+      vs[x] = reinterpret_cast<const float*>(rec + C::HALF)[kGrps + grp];
+      float mt = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+        float (&e)[4] = C::FRESH ? d : c;
+#pragma unroll
+        for (int k = 0; k < C::NJ; ++k) {
+          const uint4 w = *reinterpret_cast<const uint4*>(rec +
+                                                          ((warp * C::NT + t) * C::NJ + k) * 512 + lane * 16);
+          uint32_t b0, b1;
+          codes_to_half<F>(w.x, b0, b1); mma_f16(c, qa[4 * k], b0, b1);
+          codes_to_half<F>(w.y, b0, b1); mma_f16(c, qa[4 * k + 1], b0, b1);
+          codes_to_half<F>(w.z, b0, b1); mma_f16(e, qa[4 * k + 2], b0, b1);
+          codes_to_half<F>(w.w, b0, b1); mma_f16(e, qa[4 * k + 3], b0, b1);
+        }
+        sc[x][t][0] = ((c[0] + d[0]) + (c[2] + d[2])) * kc;
+        sc[x][t][1] = ((c[1] + d[1]) + (c[3] + d[3])) * kc;
+        if constexpr (CHUNK) {
+          const int64_t pos = (int64_t)128 * (first + TP * j + x) + 8 * (warp * C::NT + t) + 2 * q;
+          if (pos >= seen) sc[x][t][0] = -INFINITY;
+          if (pos + 1 >= seen) sc[x][t][1] = -INFINITY;
+        }
+        mt = fmaxf(mt, fmaxf(sc[x][t][0], sc[x][t][1]));
       }
-      mw = fmaxf(mw, fmaxf(sc[t][0], sc[t][1]));
+      mw = fmaxf(mw, mt);
+      uw = fmaxf(uw, mt + fast_lg2(vs[x]));
     }
     mw = quad_max(mw);
-    if (q == 0) mx[g * C::NW + warp] = make_float2(mw, mw + fast_lg2(vs));
+    if (TP > 1) uw = quad_max(uw);
+    if (q == 0) mx[g * C::NW + warp] = make_float2(mw, TP > 1 ? uw : mw + fast_lg2(vs[0]));
   };
 
+  const int n_steps = (nt + TP - 1) / TP;
   scores(0);
-  for (int i = 0; i < nt; ++i) {
-    __syncthreads();  // row maxima of tile i are in; tile i - 1 and its probabilities are used up
-    if (tid == 0) {  // the slots of V of tile i - 1 and of K of tile i are free
-      if (i > 0) request(2 * i - 1 + C::SLOTS);
-      request(2 * i + C::SLOTS);
+  for (int j = 0; j < n_steps; ++j) {
+    __syncthreads();  // row maxima of step j are in; step j - 1 and its probabilities are used up
+    if (tid == 0) {   // the slots of V of step j - 1 and of K of step j are free
+#pragma unroll
+      for (int n = -TP; n < TP; ++n)
+        if (j > 0 || n >= 0) request(2 * TP * j + n + C::SLOTS);
     }
     float Mn = M, Un = U;
 #pragma unroll
@@ -434,37 +473,44 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     U = Un;
     // weight of a value code: probability * scale, in units of 2^(U - kHead); a factor past the
     // range belongs to probabilities below 2^-100
-    float fw = vs * fast_ex2(fminf(M - U + kHead, 126.f));
-    if (fw > 1e30f) fw = 1e30f;
-    float lt = 0.f;
+    const float fm = fast_ex2(fminf(M - U + kHead, 126.f));
+    float lt[TP];
 #pragma unroll
-    for (int t = 0; t < C::NT; ++t) {
-      const float p0 = fast_ex2(sc[t][0] - M), p1 = fast_ex2(sc[t][1] - M);
-      lt += p0 + p1;
-      uint32_t hi, lo;
-      if constexpr (CHUNK)  // (a token that is not seen has weight 0, whatever its scale)
-        split_pair(sc[t][0] == -INFINITY ? 0.f : p0 * fw, sc[t][1] == -INFINITY ? 0.f : p1 * fw, hi, lo);
-      else
-        split_pair(p0 * fw, p1 * fw, hi, lo);
-      // tokens 8 n + 2 q, + 1 in the order the second product's A fragments are read
-      const int n = warp * C::NT + t;
-      *reinterpret_cast<uint2*>(P + g * kPRow + (((n >> 3) * 4 + 2 * (n & 1) + (q >> 1)) * 4 + ((n & 7) >> 1)) * 16 +
-                                (q & 1) * 8) = make_uint2(hi, lo);
+    for (int x = 0; x < TP; ++x) {
+      float fw = vs[x] * fm;
+      if (fw > 1e30f) fw = 1e30f;
+      lt[x] = 0.f;
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t) {
+        const float p0 = fast_ex2(sc[x][t][0] - M), p1 = fast_ex2(sc[x][t][1] - M);
+        lt[x] += p0 + p1;
+        uint32_t hi, lo;
+        if constexpr (CHUNK)  // (a token that is not seen has weight 0, whatever its scale)
+          split_pair(sc[x][t][0] == -INFINITY ? 0.f : p0 * fw, sc[x][t][1] == -INFINITY ? 0.f : p1 * fw, hi, lo);
+        else
+          split_pair(p0 * fw, p1 * fw, hi, lo);
+        // tokens 8 n + 2 q, + 1 in the order the second product's A fragments are read
+        const int n = warp * C::NT + t;
+        *reinterpret_cast<uint2*>(P + (8 * x + g) * kPRow +
+                                  (((n >> 3) * 4 + 2 * (n & 1) + (q >> 1)) * 4 + ((n & 7) >> 1)) * 16 + (q & 1) * 8) =
+            make_uint2(hi, lo);
+      }
     }
-    l = fmaf(l, al, lt);
+    l = fmaf(l, al, TP > 1 ? lt[0] + lt[TP - 1] : lt[0]);
     if (s.tile_ml) {
-      lt = quad_sum(lt);
-      if (q == 0) lbuf[warp * 8 + g] = lt;
+#pragma unroll
+      for (int x = 0; x < TP; ++x) {
+        lt[x] = quad_sum(lt[x]);
+        if (q == 0) lbuf[(x * C::NW + warp) * 8 + g] = lt[x];
+      }
     }
-    __syncthreads();  // probabilities of tile i are in
-    if (s.tile_ml && warp == 0 && q == 0) {
+    __syncthreads();  // probabilities of step j are in
+    if (s.tile_ml && warp < TP && TP * j + warp < nt && q == 0) {
       float t = 0.f;
 #pragma unroll
-      for (int w = 0; w < C::NW; ++w) t += lbuf[w * 8 + g];
-      s.tile_ml[(((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + i) * 8 + g] = make_float2(M, t);
+      for (int w = 0; w < C::NW; ++w) t += lbuf[(warp * C::NW + w) * 8 + g];
+      s.tile_ml[(((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + TP * j + warp) * 8 + g] = make_float2(M, t);
     }
-    ok &= landed(2 * i + 1);
-    const unsigned char* V = smem + ((2 * i + 1) % C::SLOTS) * C::SLOT;
     float fresh[C::NC][4] = {};
     float (&ot)[C::NC][4] = C::FRESH ? fresh : o;
     if (!C::FRESH && __any_sync(0xffffffffu, moved)) {
@@ -474,20 +520,27 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
         for (int r = 0; r < 4; ++r) o[c][r] *= ao;
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 w[C::NC];
+    for (int x = 0; x < TP; ++x) {
+      if (TP > 1 && x > 0 && TP * j + x >= nt) break;
+      const int n = 2 * TP * j + TP + x;
+      ok &= landed(n);
+      const unsigned char* V = smem + (n % C::SLOTS) * C::SLOT;
 #pragma unroll
-      for (int c = 0; c < C::NC; ++c)
-        w[c] = *reinterpret_cast<const uint4*>(V + ((warp * C::NC + c) * 2 + h) * 512 + lane * 16);
+      for (int h = 0; h < 2; ++h) {
+        uint4 w[C::NC];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint4 f = *reinterpret_cast<const uint4*>(P + g * kPRow + ((h * 4 + r) * 4 + q) * 16);
-        const uint32_t pa[4] = {f.x, f.y, f.z, f.w};
+        for (int c = 0; c < C::NC; ++c)
+          w[c] = *reinterpret_cast<const uint4*>(V + ((warp * C::NC + c) * 2 + h) * 512 + lane * 16);
 #pragma unroll
-        for (int c = 0; c < C::NC; ++c) {
-          uint32_t b0, b1;
-          codes_to_half<F>((&w[c].x)[r], b0, b1);
-          mma_f16(ot[c], pa, b0, b1);
+        for (int r = 0; r < 4; ++r) {
+          const uint4 f = *reinterpret_cast<const uint4*>(P + (8 * x + g) * kPRow + ((h * 4 + r) * 4 + q) * 16);
+          const uint32_t pa[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int c = 0; c < C::NC; ++c) {
+            uint32_t b0, b1;
+            codes_to_half<F>((&w[c].x)[r], b0, b1);
+            mma_f16(ot[c], pa, b0, b1);
+          }
         }
       }
     }
@@ -497,7 +550,7 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[c][r] = fmaf(o[c][r], ao, fresh[c][r]);
     }
-    if (i + 1 < nt) scores(i + 1);
+    if (j + 1 < n_steps) scores(j + 1);
   }
   if (!ok) *flag = 1;
   l = cta_row_sum<C::NW>(quad_sum(l), lbuf, warp, g, q);  // its barriers also publish the flag
