@@ -52,7 +52,12 @@ struct D8 {
   static constexpr int NW = 8;                   // warps per CTA
   static constexpr int NTHR = 32 * NW;
   static constexpr int NT = 16 / NW;             // 8-token column tiles of the scores per warp
-  static constexpr int NC = D / 8 / NW;          // 8-channel column tiles of the values per warp
+  // The values are split over the warps by channels, and where that leaves a warp one column tile of 8, by
+  // the halves of a tile's tokens too: what a warp reads of the probabilities is then read for more channels
+  // (24 ragged sequences, seven heads to a group: 60.0 -> 56.6 us).
+  static constexpr int TS = D == 64 ? 2 : 1;
+  static constexpr int NC = D / 8 / (NW / TS);   // column tiles of the values per warp
+  static constexpr int NCW = D / 8 / NW;         // the same for a window's values
   static constexpr int NJ = D / 64;              // 64-channel runs
   // A record arrives as two copies, K codes with the scales behind them, and V codes, each in a slot of a
   // ring: two (four, at head_dim 64) CTAs per SM have some 100 KB in flight or in use, and a CTA's
@@ -66,8 +71,8 @@ struct D8 {
   static constexpr int CTAS = D == 64 ? 4 : 2;   // resident per SM
   // The tensor core drops what falls below a sum's last bit. Where registers allow, a score is two sums
   // and a step's values a sum of their own, joined with rounding (at head_dim 256 they spill: 224 us of
-  // batched decode become 245).
-  static constexpr bool FRESH = D <= 128;
+  // batched decode become 245; at 64 they cost 5% and gain nothing).
+  static constexpr bool FRESH = D == 128;
   static constexpr int WROWS = 8 * NW;           // window rows per window item
   static constexpr int OFF_P = SLOTS * SLOT;
   static constexpr int OFF_MX = OFF_P + TP * 8 * kPRow;              // float2 [8][NW]: (max s, max s + log2 vscale)
@@ -183,15 +188,15 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
   if (tid < C::WROWS) dead[tid] = 0;
   __syncthreads();
   // the values this warp's channels need: under way while the scores are formed, where registers allow
-  float v[C::NW][C::NC][2];
+  float v[C::NW][C::NCW][2];
   auto load_values = [&] {
 #pragma unroll
     for (int k = 0; k < C::NW; ++k) {
       const int t0 = 8 * k + q, t1 = t0 + 4;
-      const float* v0 = a.win_v + (t0 < n ? row(t0) : 0) + 8 * C::NC * warp + g;
-      const float* v1 = a.win_v + (t1 < n ? row(t1) : 0) + 8 * C::NC * warp + g;
+      const float* v0 = a.win_v + (t0 < n ? row(t0) : 0) + 8 * C::NCW * warp + g;
+      const float* v1 = a.win_v + (t1 < n ? row(t1) : 0) + 8 * C::NCW * warp + g;
 #pragma unroll
-      for (int c = 0; c < C::NC; ++c) {
+      for (int c = 0; c < C::NCW; ++c) {
         v[k][c][0] = t0 < n ? v0[8 * c] : 0.f;
         v[k][c][1] = t1 < n ? v1[8 * c] : 0.f;
       }
@@ -232,7 +237,7 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
 #pragma unroll
   for (int k = 0; k < C::NW; ++k)
 #pragma unroll
-    for (int c = 0; c < C::NC; ++c)
+    for (int c = 0; c < C::NCW; ++c)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (!isfinite(v[k][c][h])) {
@@ -257,15 +262,15 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
   const float p0 = t0 < seen ? fast_ex2(s0 - M) : 0.f, p1 = t0 + 1 < seen ? fast_ex2(s1 - M) : 0.f;
   *reinterpret_cast<float2*>(P + g * PS + t0) = make_float2(p0, p1);
   const float l = cta_row_sum<C::NW>(quad_sum(p0 + p1), reinterpret_cast<float*>(smem + C::OFF_L), warp, g, q);
-  float o[C::NC][4] = {}, olo[C::NC][4] = {};
-  float (&ol)[C::NC][4] = D <= 128 ? olo : o;
+  float o[C::NCW][4] = {}, olo[C::NCW][4] = {};
+  float (&ol)[C::NCW][4] = D <= 128 ? olo : o;
 #pragma unroll
   for (int k = 0; k < C::NW; ++k) {
     uint32_t pa[4];
     split_tf32(P[g * PS + 8 * k + q], pa[0], pa[1]);
     split_tf32(P[g * PS + 8 * k + q + 4], pa[2], pa[3]);
 #pragma unroll
-    for (int c = 0; c < C::NC; ++c) {
+    for (int c = 0; c < C::NCW; ++c) {
       uint32_t vh[2], vl[2];
       split_tf32(v[k][c][0], vh[0], vl[0]);
       split_tf32(v[k][c][1], vh[1], vl[1]);
@@ -275,15 +280,15 @@ __device__ __forceinline__ void window_item(const Split8Args& s, unsigned char* 
   }
   if constexpr (D <= 128) {
 #pragma unroll
-    for (int c = 0; c < C::NC; ++c)
+    for (int c = 0; c < C::NCW; ++c)
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[c][r] += olo[c][r];
   }
   if (me.valid) {
     const int64_t part = me.index * s.items + item;
-    float* dst = s.acc + part * D + 8 * C::NC * warp + 2 * q;
+    float* dst = s.acc + part * D + 8 * C::NCW * warp + 2 * q;
 #pragma unroll
-    for (int c = 0; c < C::NC; ++c)
+    for (int c = 0; c < C::NCW; ++c)
       *reinterpret_cast<float2*>(dst + 8 * c) = make_float2(o[c][0] + o[c][2], o[c][1] + o[c][3]);
     if (warp == 0 && q == 0) s.ml[part] = make_float2(M, l);
   }
@@ -401,6 +406,7 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   float vs[TP];
   bool ok = true;
   const int grp = (warp * C::NT) >> 1;  // scale entry of this warp's tokens
+  const int cw = warp % (C::NW / C::TS);  // place among the channels
 
   auto landed = [&](int n) { return mbar_wait8(bar + n % C::SLOTS, (uint32_t)(n / C::SLOTS) & 1u, a.err); };
   // scores of step j (tiles TP j ..): of each tile the tokens 8 NT warp .., and their row maxima
@@ -526,11 +532,12 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
       ok &= landed(n);
       const unsigned char* V = smem + (n % C::SLOTS) * C::SLOT;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h0 = 0; h0 < 2 / C::TS; ++h0) {
+        const int h = C::TS == 2 ? warp / (C::NW / 2) : h0;
         uint4 w[C::NC];
 #pragma unroll
         for (int c = 0; c < C::NC; ++c)
-          w[c] = *reinterpret_cast<const uint4*>(V + ((warp * C::NC + c) * 2 + h) * 512 + lane * 16);
+          w[c] = *reinterpret_cast<const uint4*>(V + ((cw * C::NC + c) * 2 + h) * 512 + lane * 16);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const uint4 f = *reinterpret_cast<const uint4*>(P + (8 * x + g) * kPRow + ((h * 4 + r) * 4 + q) * 16);
@@ -555,14 +562,33 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   if (!ok) *flag = 1;
   l = cta_row_sum<C::NW>(quad_sum(l), lbuf, warp, g, q);  // its barriers also publish the flag
   const bool bad = *flag != 0;
+  float r[C::NC][2];
+#pragma unroll
+  for (int c = 0; c < C::NC; ++c) {
+    r[c][0] = o[c][0] + o[c][2];
+    r[c][1] = o[c][1] + o[c][3];
+  }
+  if constexpr (C::TS == 2) {  // the two halves of the tokens meet in the first slot, which nothing needs any more
+    float2* meet = reinterpret_cast<float2*>(smem) + (cw * C::NC) * 32 + lane;
+    if (warp >= C::NW / 2) {
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c) meet[32 * c] = make_float2(r[c][0], r[c][1]);
+    }
+    __syncthreads();
+    if (warp >= C::NW / 2) return;
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c) {
+      r[c][0] += meet[32 * c].x;
+      r[c][1] += meet[32 * c].y;
+    }
+  }
   const Row8 me = row8<CHUNK>(s, kvh, g);
   if (me.valid) {
     const int64_t part = me.index * s.items + item;
     const float f = fast_ex2(U - kHead - M);
-    float* dst = s.acc + part * D + 8 * C::NC * warp + 2 * q;
+    float* dst = s.acc + part * D + 8 * C::NC * cw + 2 * q;
 #pragma unroll
-    for (int c = 0; c < C::NC; ++c)
-      *reinterpret_cast<float2*>(dst + 8 * c) = make_float2((o[c][0] + o[c][2]) * f, (o[c][1] + o[c][3]) * f);
+    for (int c = 0; c < C::NC; ++c) *reinterpret_cast<float2*>(dst + 8 * c) = make_float2(r[c][0] * f, r[c][1] * f);
     if (warp == 0 && q == 0)
       s.ml[part] = bad ? make_float2(0.f, NAN) : make_float2(M, l);
   }
