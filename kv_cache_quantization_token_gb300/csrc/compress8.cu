@@ -5,10 +5,11 @@
 // with ties to even on the exact quotient; expansion is code * s.
 //
 // Both kernels move 128 D fp32 values and 128 D bytes per tensor and compute some ten
-// instructions per value, so memory bounds them. A thread holds 16 tokens x 4 channels in
-// registers, and rows are read and written as 16-byte pieces of whole lines.
-// 335 MB each: compressed in 66 us at head_dim 128 (5.1 TB/s), 64 us at 64 and 71 us at 256, expanded in 54
-// to 55 us (6.2 TB/s). Loading straight into registers, three CTAs per SM at 128, took 66, 68 and 98 us.
+// instructions per value, so memory bounds them. Compression holds 8 tokens x 4 channels in a thread's
+// registers, expansion 16 x 4, and rows are read and written as 16-byte pieces of whole lines.
+// 335 MB each: compressed in 63 us at head_dim 128 (5.3 TB/s), 63 us at 64 and 68 us at 256, expanded in 54
+// to 55 us (6.2 TB/s). With 16 tokens per thread, half the warps, compression took 66, 64 and 71; with
+// rows in a ring of half tensors 69, 80 and 75; loading straight into registers 66, 68 and 98.
 #include "cache8.cuh"
 
 namespace kvarn {
@@ -81,7 +82,7 @@ __device__ __forceinline__ uint32_t encode4(const float (&y)[4]) {
 // bulk copies while the codes of this one, whose rows are in registers, are formed.
 template <int D>
 struct C8 {
-  static constexpr int NTHR = 2 * D;             // 16 tokens x 4 channels each
+  static constexpr int NTHR = 4 * D;             // 8 tokens x 4 channels each
   static constexpr int IN = kTile * D * 4;       // rows of one tensor
   static constexpr int OFF_IMG = IN;             // its codes
   static constexpr int OFF_BAR = OFF_IMG + kTile * D;
@@ -148,15 +149,15 @@ compress8_kernel(const float* __restrict__ k_raw, const float* __restrict__ v_ra
   bool ok = true;
   for (int64_t x = blockIdx.x; x < n_pairs; x += gridDim.x, ++n) {
     const bool is_v = x & 1;
-    // K: the lanes of a warp run along the channels. V: 8 columns and the 4 groups of a 64-token run, whose
-    // 16-byte pieces of a channel's codes are one 64-byte line of the record.
+    // group of 8 tokens and column of 4 channels. K: the lanes of a warp run along the channels. V: 8 columns
+    // and 4 groups, whose 8-byte pieces of a channel's codes are half a line of the record.
     const int grp = is_v ? ((lane >> 3) + 4 * (tid / (4 * COLS))) : tid / COLS;
     const int col = is_v ? (lane & 7) + 8 * ((tid >> 5) % (COLS / 8)) : tid % COLS;
     ok = mbar_wait8(bar, n & 1u, err) && ok;
-    float4 r[16];
-    const float4* p = reinterpret_cast<const float4*>(smem) + (16 * grp) * COLS + col;
+    float4 r[8];
+    const float4* p = reinterpret_cast<const float4*>(smem) + (8 * grp) * COLS + col;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) r[t] = p[t * COLS];
+    for (int t = 0; t < 8; ++t) r[t] = p[t * COLS];
     const int64_t rec_off = ok ? meta[n & 1u] : -1;
     if (tid < kGrps) amax_s[tid] = 0u;
     if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the codes before are out
@@ -173,7 +174,7 @@ compress8_kernel(const float* __restrict__ k_raw, const float* __restrict__ v_ra
     float2 odd = make_float2(0.f, 0.f);  // 0, or NaN with a NaN or an infinity among the values
     const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
+    for (int t = 0; t < 8; ++t) {
       top = fmaxf(fmaxf(top, fabsf(r[t].x)), fabsf(r[t].y));
       top = fmaxf(fmaxf(top, fabsf(r[t].z)), fabsf(r[t].w));
       odd = __ffma2_rn(make_float2(r[t].x, r[t].y), zero, odd);
@@ -184,42 +185,41 @@ compress8_kernel(const float* __restrict__ k_raw, const float* __restrict__ v_ra
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
-    if ((lane & 7) == 0) atomicMax(&amax_s[grp], m);
+    if ((lane & 7) == 0) atomicMax(&amax_s[grp >> 1], m);
     __syncthreads();
-    const int g0 = grp & ~(block / 16 - 1);
+    const int g0 = (grp >> 1) & ~(block / 16 - 1);
     unsigned bm = 0u;
     for (int g = g0; g < g0 + block / 16; ++g) bm = max(bm, amax_s[g]);
     const bool finite = bm < 0x7F800000u;
     const float s = finite ? fmaxf(__uint_as_float(bm) / kQmax, kScaleFloor) : __int_as_float(0x7FFFFFFF);
     const float inv = 1.0f / s;
-    uint32_t w[16];
+    uint32_t w[8];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
+    for (int t = 0; t < 8; ++t) {
       float y[4] = {0.f, 0.f, 0.f, 0.f};
       if (finite) quotients(r[t], s, inv, y);
       w[t] = encode4<F>(y);
     }
     if (is_v) {
-      // 16 tokens of each of the thread's 4 channels, one 16-byte piece per channel
+      // 8 tokens of each of the thread's 4 channels, one 8-byte piece per channel
 #pragma unroll
       for (int i0 = 0; i0 < 4; ++i0) {
         const int i = i0 ^ (col & 1);  // neighbouring columns store to different banks
-        uint32_t o[4];
+        uint32_t o[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const uint32_t a = __byte_perm(w[4 * k], w[4 * k + 1], i | ((4 + i) << 4));
           const uint32_t b = __byte_perm(w[4 * k + 2], w[4 * k + 3], i | ((4 + i) << 4));
           o[k] = __byte_perm(a, b, 0x5410);
         }
         const int c = 4 * col + i;
-        *reinterpret_cast<uint4*>(img + (c >> 3) * 1024 + (grp >> 2) * 512 + (c & 7) * 64 + (grp & 3) * 16) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint2*>(img + (c >> 3) * 1024 + (grp >> 3) * 512 + (c & 7) * 64 + (grp & 7) * 8) =
+            make_uint2(o[0], o[1]);
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < 16; ++t)
-        *reinterpret_cast<uint32_t*>(img + (2 * grp + (t >> 3)) * (8 * D) + ((4 * col) >> 6) * 512 + (t & 7) * 64 +
-                                     ((4 * col) & 63)) = w[t];
+      for (int t = 0; t < 8; ++t)
+        *reinterpret_cast<uint32_t*>(img + grp * (8 * D) + ((4 * col) >> 6) * 512 + t * 64 + ((4 * col) & 63)) = w[t];
     }
     // the codes go out with one bulk copy (async proxy: fence the generic writes first)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -232,7 +232,7 @@ compress8_kernel(const float* __restrict__ k_raw, const float* __restrict__ v_ra
                    : "memory");
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-    if (col == 0) reinterpret_cast<float*>(rec + (is_v ? R::kVScale : R::kKScale))[grp] = s;
+    if (col == 0 && !(grp & 1)) reinterpret_cast<float*>(rec + (is_v ? R::kVScale : R::kKScale))[grp >> 1] = s;
     if (is_v && tid < 4) reinterpret_cast<uint4*>(rec + R::kVScale + 4 * kGrps)[tid] = make_uint4(0, 0, 0, 0);
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
