@@ -323,6 +323,21 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   const uint32_t t_o = tmem + P::T_O;
   const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
 
+  // copies, by one thread for the K images and one for the V images; the first fill of the rings is requested
+  // before the queries are prepared
+  const bool copies = warp >= 4 * NG + 2 && lane == 0, is_v = warp == 4 * NG + 3;
+  uint64_t* full = is_v ? bar_fv : bar_fk;
+  auto copy = [&](int t) {  // of blocks t .. t + LP - 1 (a pair's second image is copied even if no row sees it)
+    const int sl = t % R;
+    mbar_arrive_tx(full + sl, P::LP * P::IMG);
+    bulk_in(sm + (is_v ? P::OFF_V : P::OFF_K) + sl * P::IMG,
+            head + (image_index(sub_of(t)) + (is_v ? 2 : 0)) * P::IMG, P::LP * P::IMG, full + sl);
+  };
+  if (copies) {
+    pdl_wait();  // the images of this call are complete
+    for (int t = 0; t < min(n_blk, R); t += P::LP) copy(t);
+  }
+
   // query rows into TMEM: scaled by a power of two, fp16 (hi and lo); two threads per row
   if (tid < 256) {
     const int64_t at = ((int64_t)my_i * a.Hq + hq) * D + half * (D / 2);
@@ -367,20 +382,14 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend8_kernel(const A
   const float qscale = xm[row].y;  // what turns a product into a score, but for the key's scale
   float u_own = -INFINITY, l_part = 0.f;  // softmax threads: sum of probabilities, in units of 2^u_own
   if (warp >= 4 * NG + 2) {
-    // ---------------- copies: one thread for the K images, one for the V images
-    if (lane == 0 && n_blk > 0) {
-      const bool is_v = warp == 4 * NG + 3;
-      uint64_t* full = is_v ? bar_fv : bar_fk;
+    // ---------------- the copies that follow
+    if (copies) {
       uint64_t* done = is_v ? bar_dv : bar_dk;
-      unsigned char* ring = sm + (is_v ? P::OFF_V : P::OFF_K);
-      const uint8_t* src = head + (is_v ? 2 * P::IMG : 0);
-      pdl_wait();  // the images of this call are complete
-      int t = 0;
-      for (; t < n_blk; t += P::LP) {  // (a pair's second image is copied even if no row sees it)
-        const int sl = t % R, last = t - R + P::LP - 1;  // the last block that used the slots
-        if (t >= R) mbar_wait8(done + last % R, (uint32_t)(last / R) & 1u, a.err, fail);
-        mbar_arrive_tx(full + sl, P::LP * P::IMG);
-        bulk_in(ring + sl * P::IMG, src + image_index(sub_of(t)) * P::IMG, P::LP * P::IMG, full + sl);
+      int t = min((n_blk + P::LP - 1) / P::LP * P::LP, R);
+      for (; t < n_blk; t += P::LP) {
+        const int last = t - R + P::LP - 1;  // the last block that used the slots
+        mbar_wait8(done + last % R, (uint32_t)(last / R) & 1u, a.err, fail);
+        copy(t);
       }
       // every copy has landed before the CTA can retire
       for (int i = max(0, t - R); i < t; i += P::LP)
