@@ -32,8 +32,9 @@
 // (6.3 TB/s, 93% of the measured copy rate; one CTA per SM with whole records in its stages took 311);
 // 4 of 64k tokens, head_dim 128, 0.54 GB in 94 us (84%), where the instructions per code (conversion,
 // products, exchanges: 1.6 per cycle and SM) take as long as the copy. One sequence of 16k tokens, 34 MB,
-// takes 14 us against a floor of 5: a CTA has four tiles, and the chain of launch, count, table, copy, four
-// rounds of exchanges and the merge is latency.
+// takes 13 us against a floor of 5: an almost empty call takes 7.6 (launch, count, table, copy, exchanges,
+// merge: a chain of latencies), then HBM counts. One cluster per head that joins its items itself, instead of
+// the merge kernel, took 8.9 us where two kernels take 8.2.
 //
 // The same kernels serve chunks of a few positions (CHUNK): eight (position, head) rows to a CTA, each of
 // which sees the cache up to its own position.

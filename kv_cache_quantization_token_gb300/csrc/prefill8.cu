@@ -25,7 +25,7 @@
 // are always pairs. The query and w are read from tensor memory (the A operand), so shared memory feeds B
 // operands only; at head_dim 256 the lo part of the query lives in shared memory.
 //
-// What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 122 us, 1,050 TFLOP/s, 55%
+// What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 121 us, 1,056 TFLOP/s, 56%
 // of the measured bf16 rate; images 17 us of it): the softmax warps. A 64-key block costs the tensor pipe 512
 // cycles and 12 softmax warps some 450 instructions per warp, and the SM issues 2.4 per cycle. What made it
 // faster, from 207 us: window rows by 16 (their 128-row CTAs were the tail of the image grid), softmax
@@ -33,7 +33,8 @@
 // other's products, hardware barriers for hand-overs, copies of two blocks at a time, one reference instead
 // of two. With fp32 (two products of each kind) the tensor pipe bounds it: 181 us against 122 of products.
 // Not kept: P in the columns of its scores (S of the next block then waits for PV), one MMA warp, four
-// softmax groups (96 registers each), 128-key blocks.
+// softmax groups (96 registers each), 128-key blocks, one equal stretch of the work per SM (135 us: pipelines
+// fill and drain twice, every row block is joined), another order of keys per CTA.
 //
 // A cached row with a NaN or an infinity gets a NaN key and a zero value in the images: a score row that
 // sees it becomes NaN, one that does not is untouched (0 x NaN never enters the value product).
