@@ -50,9 +50,10 @@ namespace {
 constexpr float kHead = 8.f;  // w is about 2^8: lo parts of fp16 pairs stay normal
 constexpr float kLag = 7.f;   // references move when exceeded by this power of two
 // The tensor core drops what falls below an accumulator's last bit, for fp32 work eight times per block,
-// some 1e-8 of O each time: O is emptied into global memory with rounded sums every so many blocks (15,500
-// tokens, fp32: 8e-6 off without, 4e-6 with; 2.5 us each time).
-constexpr int kEmpty = 48;
+// some 1e-8 of O each time: O is emptied into global memory with rounded sums every so many blocks. 36 keep
+// fp32 results as close as a plain fp32 computation's (8 heads x 700 positions over 15,400 tokens: 2.2e-6 against
+// 2.3e-6; every 48 2.6e-6, never some 8e-6); 15,500 tokens take 183 us, with 48 181, with 24 189.
+constexpr int kEmpty = 36;
 
 template <int D, int NP>
 struct PC8 {
@@ -88,6 +89,7 @@ struct PC8 {
   static constexpr int PSTEP = SEP ? PW : KB;
   static constexpr int T_O = T_S + NG * (KB + PW);
   static constexpr int TMEM = 512;
+  static_assert(kEmpty % NG == 0, "one group empties O");
   static_assert(T_O + D <= TMEM && SMEM <= 227 * 1024, "TMEM and shared memory");
   static_assert(8 * (4 * R + 1) <= 256 && R % LP == 0, "barriers");
 };
