@@ -32,7 +32,7 @@
 // (6.3 TB/s, 93% of the measured copy rate; one CTA per SM with whole records in its stages took 311);
 // 4 of 64k tokens, head_dim 128, 0.54 GB in 94 us (84%), where the instructions per code (conversion,
 // products, exchanges: 1.6 per cycle and SM) take as long as the copy. One sequence of 16k tokens, 34 MB,
-// takes 13 us against a floor of 5: an almost empty call takes 7.6 (launch, count, table, copy, exchanges,
+// takes 12.5 us against a floor of 5: an almost empty call takes 7.6 (launch, count, table, copy, exchanges,
 // merge: a chain of latencies), then HBM counts. One cluster per head that joins its items itself, instead of
 // the merge kernel, took 8.9 us where two kernels take 8.2.
 //
@@ -81,6 +81,7 @@ struct D8 {
   static constexpr int OFF_BAR = OFF_L + TP * 8 * NW * 4;
   static constexpr int OFF_FLG = OFF_BAR + 8 * SLOTS;         // int: a wait ran out or a record was refused
   static constexpr int SMEM = (OFF_FLG + 8 + 127) / 128 * 128;
+  static_assert(SLOTS > TP && SLOTS + TP <= 4 * TP, "a step's requests belong to it and to the next");
   static_assert(SLOT % 128 == 0 && OFF_P % 128 == 0, "alignment");
   static_assert(8 * (WROWS + 4) * 4 <= 8 * kPRow, "window probabilities fit");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
@@ -316,11 +317,14 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   if (!early) pdl_wait();
   const int first = item * s.span;
   const int64_t* table = a.tile_table + ((int64_t)b * a.Hkv + kvh) * a.max_tiles + first;
-  // the first entries are read beside the count, not after it (all lie inside the table)
-  int64_t entry[2] = {0, 0};
+  // The requesting thread holds the table's entries of two steps: the first ones are read beside the count, not
+  // after it (all lie inside the table), the others a step before they are needed.
+  constexpr int TP = C::TP;
+  int64_t entry[2][TP] = {};
   if (tid == 0) {
-    entry[0] = __ldcg(table);
-    if (first + 1 < a.max_tiles) entry[1] = __ldcg(table + 1);
+#pragma unroll
+    for (int k = 0; k < 2 * TP; ++k)
+      if (first + k < a.max_tiles) entry[k / TP][k % TP] = __ldcg(table + k);
   }
   const int n_tiles = CHUNK ? s.n_tiles : min(max(a.n_tiles[b], 0), a.max_tiles);
   const int nt = min(max(n_tiles - first, 0), s.span);
@@ -333,14 +337,13 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     }
     return;
   }
-  constexpr int TP = C::TP;
-  auto request = [&](int n) {  // one thread: copy n of the item (K of a step's tiles, then V) into its slot
+  // one thread: copy n of the item (K of a step's tiles, then V) into its slot; off: the tile's entry
+  auto request = [&](int n, int64_t off) {
     const int tile = n / (2 * TP) * TP + n % TP;
     if (n < 0 || tile >= nt) return;
     const bool is_v = n % (2 * TP) >= TP;
     uint64_t* br = bar + n % C::SLOTS;
     unsigned char* dst = smem + (n % C::SLOTS) * C::SLOT;
-    const int64_t off = tile < 2 ? (tile ? entry[1] : entry[0]) : table[tile];
     if ((off & 15) || off < 0 || off > a.tiles_bytes - R::kBytes) {
       // a record that is not read: zero codes under scales of NaN, which only rows that see it meet
       report(a.err, KVARN_DEVERR_RECORD);
@@ -362,7 +365,8 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     for (int i = 0; i < C::SLOTS; ++i) mbar_init_n(bar + i, 1);
     mbar_fence_init();
     *flag = 0;
-    for (int i = 0; i < C::SLOTS; ++i) request(i);
+#pragma unroll
+    for (int i = 0; i < C::SLOTS; ++i) request(i, entry[i / (2 * TP)][i % TP]);
   }
   if (early) pdl_wait();
   pdl_trigger();
@@ -464,8 +468,13 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
     __syncthreads();  // row maxima of step j are in; step j - 1 and its probabilities are used up
     if (tid == 0) {   // the slots of V of step j - 1 and of K of step j are free
 #pragma unroll
-      for (int n = -TP; n < TP; ++n)
-        if (j > 0 || n >= 0) request(2 * TP * j + n + C::SLOTS);
+      for (int n = -TP; n < TP; ++n)  // (what they are filled with belongs to step j or j + 1)
+        if (j > 0 || n >= 0) request(2 * TP * j + n + C::SLOTS, entry[(n + C::SLOTS) / (2 * TP)][(n + C::SLOTS) % TP]);
+#pragma unroll
+      for (int k = 0; k < TP; ++k) {
+        entry[0][k] = entry[1][k];
+        if (TP * (j + 2) + k < nt) entry[1][k] = table[TP * (j + 2) + k];
+      }
     }
     float Mn = M, Un = U;
 #pragma unroll
