@@ -101,11 +101,14 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo, both rounded to the 11 bits that a tf32 operand is read with: within 2^-22 of x.
+// x = hi + lo, both brought to the 11 bits that a tf32 operand is read with: within 2^-21 of x. hi is rounded by an
+// addition to its bits. For lo, from which the tensor core cuts the rest, a product does it (0.36 to 0.72 of the
+// last kept bit is added before the cut), because of an infinity or a NaN lo has to stay NaN, so that every score it
+// enters is NaN whatever the signs: NaN is the largest int, an addition to its bits would wrap to -0.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   const uint32_t u = __float_as_uint(x), r = u + 0x1000u;
   hi = ((r & 0x7F800000u) == 0x7F800000u ? u : r) & 0xFFFFE000u;  // (not up to infinity)
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+  lo = __float_as_uint((x - __uint_as_float(hi)) * (1.f + 0x1.7p-12f));
 }
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, shfl_xor(v, 1));

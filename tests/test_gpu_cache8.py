@@ -341,6 +341,52 @@ def test_decode_non_finite_rows_and_queries():
     assert bool(out[1, :2].isnan().all()) and torch.equal(out[1, 2:], want[1, 2:])
 
 
+# bit patterns: what GPU arithmetic gives for a NaN, its negative, the last and the first of the NaNs, inf, -inf
+NON_FINITE = [0x7FFFFFFF, -1, 0x7F800001, 0x7FC00000, 0x7F800000, -0x800000]
+
+
+@pytest.mark.parametrize("bits", NON_FINITE)
+@pytest.mark.parametrize("tiles", [0, 2])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_non_finite_window_keys_poison_the_rows_that_see_them(D, tiles, bits):
+    """In decode and in prefill of few rows, whatever the signs of the products with the rest of the pair."""
+    c = Cache8(65, [tiles, tiles], [70, 6], 2, D)
+    q, qc = _query(4, (2, 8, D), "f32"), _query(5, (4, 8, D), "f32")
+    pos0 = T * tiles + 2
+    want, want_c = c.decode(q), c.prefill(qc, pos0, b=1)
+    for b, at in ((0, 69), (1, 4)):
+        for ch in (0, D // 2 + 5, D - 1):
+            word = c.win_k.view(torch.int32)[b, 1, (c.starts[b] + at) % c.cap]
+            old = int(word[ch])
+            word[ch] = bits
+            out = c.decode(q)
+            assert bool(out[b, 4:].isnan().all())
+            assert torch.equal(out[b, :4], want[b, :4]) and torch.equal(out[1 - b], want[1 - b])
+            if b == 1:  # the chunk's rows 2 and 3 see it
+                out = c.prefill(qc, pos0, b=1)
+                assert bool(out[2:, 4:].isnan().all())
+                assert torch.equal(out[:2], want_c[:2]) and torch.equal(out[:, :4], want_c[:, :4])
+            word[ch] = old
+
+
+@pytest.mark.parametrize("bits", NON_FINITE)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_non_finite_queries_over_a_window_alone_are_nan(D, bits):
+    c = Cache8(66, [0, 0], [70, 1], 2, D)
+    for seed in range(4):
+        q, qc = _query(seed, (2, 8, D), "f32"), _query(seed + 9, (4, 8, D), "f32")
+        want, want_c = c.decode(q), c.prefill(qc, 0)  # the chunk's first row sees one key
+        bad, bad_c = torch.zeros(2, 8, dtype=torch.bool, device=DEV), torch.zeros(4, 8, dtype=torch.bool, device=DEV)
+        for b, h, ch in ((0, 1, 0), (1, 2, D - 1), (1, 7, D // 2 + 5)):
+            q.view(torch.int32)[b, h, ch] = bits
+            bad[b, h] = True
+            for i in (0, 2):
+                qc.view(torch.int32)[i, h, ch] = bits
+                bad_c[i, h] = True
+        for out, ok, nan in ((c.decode(q), want, bad), (c.prefill(qc, 0), want_c, bad_c)):
+            assert bool(out[nan].isnan().all()) and torch.equal(out[~nan], ok[~nan])
+
+
 def test_decode_counts_past_their_arrays_are_clamped():
     c = Cache8(71, [3], [128], 2, 64)
     q = _query(6, (1, 4, 64), "f32")
