@@ -210,9 +210,9 @@ struct Prefill8Args {
   float scale;  // softmax scale * log2(e)
   unsigned* err;
 };
-// Prefill of a few positions by the decode kernels.
+// Prefill of a few positions by the decode kernels, over the first n_tiles tiles and win_len window rows of a's.
 void chunk8_plan(int C, int Hq, int Hkv, int D, int n_tiles, int win_len, Decode8Plan* p);
-cudaError_t launch_chunk8(const Decode8Plan& p, const Prefill8Args& a, cudaStream_t st);
+cudaError_t launch_chunk8(const Prefill8Args& a, int n_tiles, int win_len, cudaStream_t st);
 size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D);
 cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st);
 

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   if (tid == 0) {
 #pragma unroll
     for (int k = 0; k < 2 * TP; ++k)
-      if (first + k < a.max_tiles) entry[k / TP][k % TP] = __ldcg(table + k);
+      if (first + k < (CHUNK ? s.n_tiles : a.max_tiles)) entry[k / TP][k % TP] = __ldcg(table + k);
   }
   const int n_tiles = CHUNK ? s.n_tiles : min(max(a.n_tiles[b], 0), a.max_tiles);
   const int nt = min(max(n_tiles - first, 0), s.span);
@@ -789,15 +789,23 @@ void chunk8_plan(int C, int Hq, int Hkv, int D, int n_tiles, int win_len, Decode
   make_plan((int64_t)Hkv * ((C * (Hq / Hkv) + 7) / 8), (int64_t)C * Hq, 1, D, n_tiles, win_len, 0, p);
 }
 
-cudaError_t launch_chunk8(const Decode8Plan& p, const Prefill8Args& a, cudaStream_t st) {
+cudaError_t launch_chunk8(const Prefill8Args& a, int n_tiles, int win_len, cudaStream_t st) {
+  // the plan that the workspace was counted for; fewer tiles are spread over as many items at most
+  Decode8Plan p;
+  chunk8_plan(a.C, a.Hq, a.Hkv, a.D, a.n_tiles, a.win_len, &p);
+  if (n_tiles < a.n_tiles) {
+    p.span = (n_tiles + p.tile_items - 1) / p.tile_items;
+    p.tile_items = (n_tiles + p.span - 1) / p.span;
+  }
+  p.items = p.tile_items + (win_len + D8<64>::WROWS - 1) / D8<64>::WROWS;
   Split8Args s{};
   s.a = Decode8Args{a.q, a.tiles, a.tile_table, nullptr, a.win_k, a.win_v, nullptr, nullptr, nullptr, nullptr, a.out,
                     a.tiles_bytes, a.io, a.win_cap, a.C, a.Hq, a.Hkv, a.G, a.D, a.table_stride, a.format, a.scale, 0,
                     a.err};
   s.pos0 = a.pos0;
-  s.n_tiles = a.n_tiles;
+  s.n_tiles = n_tiles;
   s.win_start = a.win_start;
-  s.win_len = a.win_len;
+  s.win_len = win_len;
   return launch_any<true>(p, s, a.ws, st);
 }
 

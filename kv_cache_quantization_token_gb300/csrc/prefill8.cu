@@ -840,16 +840,13 @@ size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D
 }
 
 cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st) {
-  if (few_rows(a.C, a.G, a.Hkv, a.n_tiles)) {
-    Decode8Plan p;
-    chunk8_plan(a.C, a.Hq, a.Hkv, a.D, a.n_tiles, a.win_len, &p);
-    return launch_chunk8(p, a, st);
-  }
-  // blocks visible to the chunk's last position
+  // tiles and window rows that the chunk's last position sees: neither path reads others
   const int64_t pmax = a.pos0 + a.C - 1;
   const int n_tblk = (int)(pmax / kTile + 1 < a.n_tiles ? pmax / kTile + 1 : a.n_tiles);
   const int64_t w = pmax - 128LL * a.n_tiles + 1;
   const int win_vis = (int)(w < 0 ? 0 : w < a.win_len ? w : a.win_len);
+  // (the path follows from what the workspace was counted for, which does not know the position)
+  if (few_rows(a.C, a.G, a.Hkv, a.n_tiles)) return launch_chunk8(a, n_tblk, win_vis, st);
   Att8Args s;
   s.a = a;
   s.p = plan8(a.C, n_tblk, win_vis, a.Hq, a.Hkv, a.D, a.io == KVARN_IO_F32);

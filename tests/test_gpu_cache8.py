@@ -528,6 +528,22 @@ def test_prefill_bad_offsets_poison_what_sees_them(C):
         assert bool(out[:first, 4:].isfinite().all())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("C", [1, 6, 100])
+def test_prefill_reads_no_tile_behind_the_chunk(C, D):
+    """Few rows and many: an offset that no position sees is not an error, and the result is that of the visible part."""
+    c = Cache8(53, [40], [150], 2, D, "i8", 64)
+    q = _query(3, (C, 8, D), "f32")
+    for pos0 in (0, 3 * T - C, 3 * T + 1 - C, 20 * T + 5, 40 * T - C, 40 * T + 20 - C):
+        if pos0 < 0:
+            continue
+        t = c.table[0].clone()
+        t[:, (pos0 + C - 1) // T + 1:] = torch.tensor([[-16], [8]], device=DEV)
+        out = kvarn.prefill_attention8(q, pos0, c.tiles, t, 40, c.win_k[0], c.win_v[0], c.starts[0], 150, c.lay)
+        assert kvarn.device_error() == 0
+        _check_prefill(c, q, pos0, out)
+
+
 @pytest.mark.parametrize("C", [4, 100])
 def test_a_pool_smaller_than_a_record_is_not_read(C):
     lay = kvarn.layout8(128)
