@@ -1,5 +1,7 @@
 """What the 8-bit cache's calls and eviction refuse, on the host: nothing reaches a GPU."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -141,6 +143,18 @@ def test_evict_refusals(lib):
     assert _evict(lib, B=1, t=ctypes.c_void_p((1 << 20) + 4)) == -2
     assert _evict(lib, B=65536) == -4 and _evict(lib, mt=(1 << 29) + 1) == -4
     assert _evict(lib, flags=kvarn.LAUNCH_PDL | kvarn.LAUNCH_PREFETCH) == -4
+
+
+def test_compression_gives_up_as_a_whole_cta():
+    """A wait can run out for some threads of a CTA alone. What each of them saw must not decide a branch before the
+    CTA has joined it: the branches of the loop have barriers."""
+    with open(os.path.join(_build.CSRC, "compress8.cu")) as f:
+        body = f.read().split("compress8_kernel(")[1].split("\n}\n")[0]
+    verdict = re.findall(r"(?:if|=|&&|\|\|)[ (!]*mbar_wait8\(", body)
+    name = re.findall(r"const bool (\w+) = mbar_wait8\(", body)
+    assert len(verdict) == len(name) == 1
+    uses = re.findall(r"[^\n]*\b%s\b[^\n]*" % name[0], body)
+    assert len(uses) == 2 and "if (!__syncthreads_and(%s)) break;" % name[0] in uses[1]
 
 
 def test_host_tensors_are_refused():
