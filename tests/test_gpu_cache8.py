@@ -456,6 +456,36 @@ def test_prefill_of_many_blocks(Hkv, C, tiles, window, D, io):
     _check_prefill(c, q, pos0, c.prefill(q, pos0))
 
 
+@pytest.mark.parametrize("case", ["rising", "uneven", "falling"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill_of_long_fp32_contexts(D, case, monkeypatch):
+    """More than three times the blocks after which an fp32 accumulator is emptied, in one CTA. The row's largest
+    weighted score rises by about 2^9 before the second, the third and the last part ("rising"); value scales do so,
+    by 300 twice ("uneven"); or the largest comes first ("falling")."""
+    u = np.random.default_rng(D).choice([-1.0, 1.0], D)
+
+    def cache_rows(rng, n, D):
+        k, v = 0.3 * rng.standard_normal((n, D)), rng.standard_normal((n, D))
+        if case == "uneven":
+            v[2500:] *= 300
+            v[5000:] *= 300
+        for i, at in enumerate((1000, 3500, 5800, 7300)):  # scores 6 apart: emptyings are at 2304, 4608 and 6912 keys
+            k[at] += (6.0 * (i if case == "rising" else 4 - i if case == "falling" else 1) / D ** 0.5) * u
+        return k.astype(np.float32), v.astype(np.float32)
+
+    monkeypatch.setattr("tests.cache8_helpers.rows", cache_rows)
+    tiles, window, C, Hkv, G = 60, 40, 320, 8, 4  # 80 row blocks: no key shares
+    c = Cache8(D, [tiles], [window], Hkv, D, "i8", 16)
+    q = torch.from_numpy((np.random.default_rng(1).standard_normal((C, G * Hkv, D)) + u).astype(np.float32)).to(DEV)
+    pos0 = T * tiles + window - C
+    out = c.prefill(q, pos0)
+    qn = q.double().cpu().numpy()
+    for h in (0, 13, 31):
+        want, _, bound = attend(qn[:, h], c.k[0][h // G], c.v[0][h // G], D ** -0.5, pos0 + 1 + np.arange(C),
+                                c.vs[0][h // G], 2.0 ** -33)
+        check(out[:, h], want, bound, torch.float32)
+
+
 def test_prefill_scales_of_either_sign_and_zero():
     c = Cache8(32, [3], [20], 2, 128)
     q = _query(2, (40, 4, 128), "f32")
