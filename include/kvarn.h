@@ -649,7 +649,8 @@ int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t po
  *   n_tiles    : int32 [B] (clamped to 0..max_tiles).
  *   table_out, mass_out : the same shapes: the tiles that stay, in their old order,
  *                then -1 (mass: 0). May be tile_table and tile_mass themselves.
- *   n_tiles_out: int32 [B], min(n_tiles[b], keep). May be n_tiles itself.
+ *   n_tiles_out: int32 [B], min(n_tiles[b], keep). May be n_tiles itself. Both lie
+ *                apart from the arrays that are written.
  *   evicted    : int64 [B][Hkv][max_tiles] or NULL: the offsets that left, in their
  *                old order, then -1. Must not overlap the other arrays.
  *   keep       : >= 1, sinks and recent >= 0, sinks + recent <= keep.

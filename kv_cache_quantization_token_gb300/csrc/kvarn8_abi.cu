@@ -215,13 +215,18 @@ int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const i
   if (!aligned(tile_table, 8) || !aligned(table_out, 8) || !aligned(evicted, 8) || !aligned(tile_mass, 4) ||
       !aligned(mass_out, 4) || !aligned(n_tiles, 4) || !aligned(n_tiles_out, 4))
     return KVARN_ERR_ALIGN;
-  const size_t n = (size_t)B * Hkv * max_tiles, n8 = n * 8, n4 = n * 4;
+  const size_t n = (size_t)B * Hkv * max_tiles, n8 = n * 8, n4 = n * 4, nb = 4 * (size_t)B;
   if ((table_out != tile_table && overlap(table_out, n8, tile_table, n8)) ||
       (mass_out != tile_mass && overlap(mass_out, n4, tile_mass, n4)) ||
       overlap(table_out, n8, tile_mass, n4) || overlap(table_out, n8, mass_out, n4) ||
       overlap(tile_table, n8, mass_out, n4) ||
-      (n_tiles_out != n_tiles && overlap(n_tiles_out, 4 * (size_t)B, n_tiles, 4 * (size_t)B)))
+      (n_tiles_out != n_tiles && overlap(n_tiles_out, nb, n_tiles, nb)))
     return KVARN_ERR_BAD_ARG;
+  // the counts apart from what is written, and the written counts from what is read
+  for (const int32_t* c : {n_tiles, (const int32_t*)n_tiles_out})
+    if (overlap(c, nb, table_out, n8) || overlap(c, nb, mass_out, n4) || (evicted && overlap(c, nb, evicted, n8)))
+      return KVARN_ERR_BAD_ARG;
+  if (overlap(n_tiles_out, nb, tile_table, n8) || overlap(n_tiles_out, nb, tile_mass, n4)) return KVARN_ERR_BAD_ARG;
   if (evicted && (overlap(evicted, n8, tile_table, n8) || overlap(evicted, n8, table_out, n8) ||
                   overlap(evicted, n8, tile_mass, n4) || overlap(evicted, n8, mass_out, n4)))
     return KVARN_ERR_BAD_ARG;

@@ -145,6 +145,14 @@ def test_evict_refusals(lib):
     assert _evict(lib, flags=kvarn.LAUNCH_PDL | kvarn.LAUNCH_PREFETCH) == -4
 
 
+def test_evict_refuses_counts_inside_the_other_arrays(lib):
+    """Read while they are written, or written over them."""
+    inside = {k: ctypes.c_void_p((i << 20) + 8) for i, k in enumerate(("t", "m", "n", "to", "mo", "no", "ev"), 1)}
+    for count, others in (("n", ("to", "mo", "ev")), ("no", ("t", "m", "to", "mo", "ev"))):
+        for k in others:
+            assert _evict(lib, B=1, **{count: inside[k]}) == -4, (count, k)
+
+
 def test_compression_gives_up_as_a_whole_cta():
     """A wait can run out for some threads of a CTA alone. What each of them saw must not decide a branch before the
     CTA has joined it: the branches of the loop have barriers."""
