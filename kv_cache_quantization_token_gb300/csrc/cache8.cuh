@@ -44,13 +44,8 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& h01, uint32_
   }
 }
 
-// Element i of a row of io type IO (a KVARN_IO_* value known at run time).
-__device__ __forceinline__ float io_ld(const void* p, int io, int64_t i) {
-  if (io == KVARN_IO_F32) return reinterpret_cast<const float*>(p)[i];
-  if (io == KVARN_IO_F16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
-  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-}
-// Four consecutive elements from i (a multiple of 4, rows 16-byte aligned).
+// Four consecutive elements of a row of type io (a KVARN_IO_* value known at run time), from i on (a multiple
+// of 4, rows 16-byte aligned).
 __device__ __forceinline__ float4 io_ld4(const void* p, int io, int64_t i) {
   if (io == KVARN_IO_F32) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
   const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
@@ -61,11 +56,6 @@ __device__ __forceinline__ float4 io_ld4(const void* p, int io, int64_t i) {
   }
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
                      __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
-}
-__device__ __forceinline__ void io_st(void* p, int io, int64_t i, float v) {
-  if (io == KVARN_IO_F32) reinterpret_cast<float*>(p)[i] = v;
-  else if (io == KVARN_IO_F16) reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
-  else reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 __device__ __forceinline__ void io_st4(void* p, int io, int64_t i, float4 v) {
   if (io == KVARN_IO_F32) {
