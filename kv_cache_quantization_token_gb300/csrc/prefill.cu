@@ -52,7 +52,7 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
-#include "kvarn_common.cuh"
+#include "tcgen05.cuh"
 
 namespace kvarn {
 namespace {
@@ -62,66 +62,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// Byte offset of element (row, k) of a K-major fp16 operand of `rows` rows in
-// the 128-byte-swizzled canonical layout: 64-element K blocks, each `rows`
-// x 128 bytes, 16-byte chunks XOR-swizzled by (row & 7).
-__device__ __forceinline__ uint32_t sw_off(int row, int k, int rows) {
-  return (uint32_t)((k >> 6) * rows * 128 + row * 128 + ((((k & 63) >> 3) ^ (row & 7)) << 4) +
-                    (k & 7) * 2);
-}
-
-// tcgen05 shared-memory matrix descriptor: K-major, SWIZZLE_128B, 8-row
-// groups 1024 bytes apart (stride byte offset), version bits 46-48 = 0b001.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-// The descriptor of the operand `bytes` further on (16-byte multiple): the
-// start address field holds address / 16 in 14 bits, and every shared
-// address here stays below 256 KB, so the sum never carries out of the field.
-__device__ __forceinline__ uint64_t sdesc_add(uint64_t desc, uint32_t bytes) {
-  return desc + (uint64_t)(bytes >> 4);
-}
-// Instruction descriptor, kind::f16: D f32, A and B f16, both K-major, M = 128.
-template <int N>
-__device__ __forceinline__ uint32_t idesc() {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_f16(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate));
-}
-// The same product with the A operand (M = 128 rows, fp16 pairs packed two per
-// 32-bit column, element 2k in the low half) read from tensor memory.
-__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t id,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(b), "r"(id), "r"(accumulate));
-}
-// The TS product that always accumulates into D.
-__device__ __forceinline__ void mma_f16_ts_acc(uint32_t tmem_d, uint32_t tmem_a, uint64_t b,
-                                               uint32_t id) {
-  asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, 1;\n" ::"r"(tmem_d),
-               "r"(tmem_a), "l"(b), "r"(id));
-}
-// One lane of a converged warp (the same lane every time the warp is whole).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(pred));
-  return pred != 0;
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   su32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void mbar_init1(uint64_t* bar) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(bar)) : "memory");
 }
@@ -182,69 +122,6 @@ __device__ __forceinline__ void bulk_store_wait(void* gdst, const void* ssrc, ui
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
-// 32 consecutive fp32 TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
-      "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
-      "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
-      "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
-      "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
-      "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
-      : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// 16 consecutive 32-bit TMEM columns of this thread's lane (no wait).
-__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// 32 consecutive 32-bit TMEM columns of this thread's lane (no wait).
-__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 
 // x = hi + lo with hi, lo fp16: the pair carries about 22 significant bits.
@@ -757,10 +634,10 @@ __global__ void __launch_bounds__(320, 1) prefill_kernel(const PrefillArgs a) {
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
             const uint32_t qh = tmem + P::T_QH + 8 * kk, ql = tmem + P::T_QL + 8 * kk;
-            if (kk == 0) mma_f16_ts(t_s, qh, kh, idesc<128>(), 0);
-            else mma_f16_ts_acc(t_s, qh, sdesc_add(kh, off), idesc<128>());
-            mma_f16_ts_acc(t_s, ql, sdesc_add(kh, off), idesc<128>());
-            mma_f16_ts_acc(t_s, qh, sdesc_add(kl, off), idesc<128>());
+            if (kk == 0) mma_ts(t_s, qh, kh, idesc_f16<128>(), 0);
+            else mma_ts_acc(t_s, qh, sdesc_add(kh, off), idesc_f16<128>());
+            mma_ts_acc(t_s, ql, sdesc_add(kh, off), idesc_f16<128>());
+            mma_ts_acc(t_s, qh, sdesc_add(kl, off), idesc_f16<128>());
           }
           mma_commit(bar_s + b);
         }
@@ -789,10 +666,10 @@ __global__ void __launch_bounds__(320, 1) prefill_kernel(const PrefillArgs a) {
             for (int kq = 0; kq < 4; ++kq) {  // 16 keys each
               const uint32_t ph = t_p + 64 * h + 8 * kq, pl = ph + 32;
               const uint32_t off = h * kVHalf + kq * 32;
-              if (h == 0 && kq == 0) mma_f16_ts(t_o, ph, dvh, idesc<D>(), j > 0);
-              else mma_f16_ts_acc(t_o, ph, sdesc_add(dvh, off), idesc<D>());
-              mma_f16_ts_acc(t_o, pl, sdesc_add(dvh, off), idesc<D>());
-              mma_f16_ts_acc(t_o, ph, sdesc_add(dvl, off), idesc<D>());
+              if (h == 0 && kq == 0) mma_ts(t_o, ph, dvh, idesc_f16<D>(), j > 0);
+              else mma_ts_acc(t_o, ph, sdesc_add(dvh, off), idesc_f16<D>());
+              mma_ts_acc(t_o, pl, sdesc_add(dvh, off), idesc_f16<D>());
+              mma_ts_acc(t_o, ph, sdesc_add(dvl, off), idesc_f16<D>());
             }
             mma_commit(h == 0 ? bar_vh : bar_o);
           }
@@ -1085,7 +962,7 @@ __global__ void __launch_bounds__(320, 1) prefill_kernel_d256(const PrefillArgs 
         const int c = 128 * half + 32 * pass + 8 * c8;
         *reinterpret_cast<uint4*>(sQl + sw_off(row, c, 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-      tmem_st16_nowait(tmem + lb + P::T_QH + 64 * half + 16 * pass, hw);
+      tmem_st16(tmem + lb + P::T_QH + 64 * half + 16 * pass, hw);
     }
     tmem_wait_st();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1158,9 +1035,9 @@ __global__ void __launch_bounds__(320, 1) prefill_kernel_d256(const PrefillArgs 
             const uint32_t off_a = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
             const uint32_t off_b = (kk >> 2) * 64 * 128 + (kk & 3) * 32;
             const uint32_t qh = tmem + P::T_QH + 8 * kk;
-            if (kk == 0) mma_f16_ts(t_s, qh, dkh, idesc<64>(), 0);
-            else mma_f16_ts_acc(t_s, qh, sdesc_add(dkh, off_b), idesc<64>());
-            mma_f16(t_s, sdesc_add(dql, off_a), sdesc_add(dkh, off_b), idesc<64>(), 1);
+            if (kk == 0) mma_ts(t_s, qh, dkh, idesc_f16<64>(), 0);
+            else mma_ts_acc(t_s, qh, sdesc_add(dkh, off_b), idesc_f16<64>());
+            mma_ss(t_s, sdesc_add(dql, off_a), sdesc_add(dkh, off_b), idesc_f16<64>(), 1);
           }
           mma_commit(bar_khf);
         }
@@ -1172,7 +1049,7 @@ __global__ void __launch_bounds__(320, 1) prefill_kernel_d256(const PrefillArgs 
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off_b = (kk >> 2) * 64 * 128 + (kk & 3) * 32;
-            mma_f16_ts_acc(t_s, tmem + P::T_QH + 8 * kk, sdesc_add(dkl, off_b), idesc<64>());
+            mma_ts_acc(t_s, tmem + P::T_QH + 8 * kk, sdesc_add(dkl, off_b), idesc_f16<64>());
           }
           mma_commit(bar_s + (j & 1));
         }
@@ -1192,10 +1069,10 @@ __global__ void __launch_bounds__(320, 1) prefill_kernel_d256(const PrefillArgs 
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 16 keys each; keys 32 h .. are thread half h's
             const uint32_t ph = t_p + 32 * (kk >> 1) + 8 * (kk & 1), pl = ph + 16;
-            if (kk == 0) mma_f16_ts(t_o, ph, dvh, idesc<256>(), j > 0);
-            else mma_f16_ts_acc(t_o, ph, sdesc_add(dvh, 32 * kk), idesc<256>());
-            mma_f16_ts_acc(t_o, pl, sdesc_add(dvh, 32 * kk), idesc<256>());
-            mma_f16_ts_acc(t_o, ph, sdesc_add(dvl, 32 * kk), idesc<256>());
+            if (kk == 0) mma_ts(t_o, ph, dvh, idesc_f16<256>(), j > 0);
+            else mma_ts_acc(t_o, ph, sdesc_add(dvh, 32 * kk), idesc_f16<256>());
+            mma_ts_acc(t_o, pl, sdesc_add(dvh, 32 * kk), idesc_f16<256>());
+            mma_ts_acc(t_o, ph, sdesc_add(dvl, 32 * kk), idesc_f16<256>());
           }
           mma_commit(bar_o);
         }
@@ -1253,8 +1130,8 @@ __global__ void __launch_bounds__(320, 1) prefill_kernel_d256(const PrefillArgs 
         split2w(p0, p1, hw[e], lw[e]);
       }
       l_part = fmaf(l_part, alpha, ls);
-      tmem_st16_nowait(t_s, hw);
-      tmem_st16_nowait(t_s + 16, lw);
+      tmem_st16(t_s, hw);
+      tmem_st16(t_s + 16, lw);
       // O belongs to PV(j-1) until it completes
       if (j > 0 && __any_sync(0xffffffffu, need)) {
         if (mbar_wait_flag(bar_o, (uint32_t)(j - 1) & 1u, fail, a.err)) {

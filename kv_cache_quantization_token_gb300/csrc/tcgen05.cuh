@@ -1,4 +1,4 @@
-// tcgen05.cuh -- wrappers of the tensor-memory instructions the 8-bit prefill uses: operand
+// tcgen05.cuh -- wrappers of the tensor-memory instructions that both prefill paths use: operand
 // layout and descriptors, products with A in tensor or shared memory, loads and stores.
 #pragma once
 
@@ -35,6 +35,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(accumulate));
 }
+// The same product, always accumulating.
 __device__ __forceinline__ void mma_ts_acc(uint32_t d, uint32_t a, uint64_t b, uint32_t id) {
   asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, 1;\n" ::"r"(d), "r"(a), "l"(b), "r"(id));
 }
