@@ -818,19 +818,26 @@ cudaError_t launch_p8d(const Att8Args& s, cudaStream_t st) {
   return e ? launch_p8<D, 1, 1>(s, st) : launch_p8<D, 0, 1>(s, st);
 }
 
-// Chunks of few score rows per KV head go to the decode kernels, which need no images but go over the
-// records once for every eight rows: some 6 ns per tile-head and group of eight rows, against 28 ns per
-// tile-head and 9 us more for the images and their kernels (head_dim 128, 8 KV heads: 32 rows over 128
-// tiles 33 us against 46, 64 rows 56 against 47, 64 rows over 15 tiles 16 against 22).
-bool few_rows(int C, int G, int Hkv, int n_tiles) {
+// Chunks of few score rows per KV head go to the decode kernels, which need no images but go over the cache once
+// for every eight rows ("group"). Per tile-head they take some 5 ns a group (head_dim 64: 3, 256: 8) and per 128 window rows
+// 10 times that, fp32 rows through tf32 products; the images with their kernels take 5 tiles' worth of a group
+// per tile, 4 groups' worth per window row, and some 5 us more, and with fewer than 6 KV heads no less than with 6.
+// At head_dim 128, 8 KV heads, bf16 (us, decode kernels against images): 8 groups over 40 tiles 23.4 / 26.0, 12
+// 34.4 / 28.1; 5 over 128 tiles 36.3 / 38.1, 6 42.2 / 39.3; no tiles and 1,000 window rows, 4 groups 19.1 / 21.5, 6
+// 26.3 / 22.6, 64 221 / 29; 2 KV heads, 16 groups over 128 tiles 30.1 / 48.9, 24 42.1 / 38.4; head_dim 64, 8 over 15
+// tiles 11.3 / 13.7, 24 24.2 / 16.2; head_dim 256, 8 over 40 tiles 34.2 / 39.0, 12 50.3 / 43.6. Over 800 sizes (1 to 8 KV
+// heads, 4 to 64 groups, 0 to 128 tiles, 60 to 3,000 window rows) the choice costs 0.4% on the mean, 31% at worst.
+bool few_rows(int C, int G, int Hkv, int n_tiles, int win_len) {
   const int64_t groups = ((int64_t)C * G + 7) / 8;
-  return groups <= 5 || (groups <= 64 && (groups - 5) * Hkv * n_tiles <= 1500);
+  if (groups > 64) return false;
+  const int64_t work = groups * Hkv, heads = Hkv > 6 ? Hkv : 6;
+  return 12 * (work - 5 * heads) * n_tiles + (work - 4 * heads) * win_len <= 12 * 1600;
 }
 
 }  // namespace
 
 size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D) {
-  if (few_rows(C, Hq / Hkv, Hkv, n_tiles)) {
+  if (few_rows(C, Hq / Hkv, Hkv, n_tiles, win_len)) {
     Decode8Plan p;
     chunk8_plan(C, Hq, Hkv, D, n_tiles, win_len, &p);
     return p.ws_bytes;
@@ -846,7 +853,7 @@ cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st) {
   const int64_t w = pmax - 128LL * a.n_tiles + 1;
   const int win_vis = (int)(w < 0 ? 0 : w < a.win_len ? w : a.win_len);
   // (the path follows from what the workspace was counted for, which does not know the position)
-  if (few_rows(a.C, a.G, a.Hkv, a.n_tiles)) return launch_chunk8(a, n_tblk, win_vis, st);
+  if (few_rows(a.C, a.G, a.Hkv, a.n_tiles, a.win_len)) return launch_chunk8(a, n_tblk, win_vis, st);
   Att8Args s;
   s.a = a;
   s.p = plan8(a.C, n_tblk, win_vis, a.Hq, a.Hkv, a.D, a.io == KVARN_IO_F32);

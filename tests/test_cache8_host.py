@@ -123,6 +123,15 @@ def test_prefill_refusals(lib):
     assert _prefill(lib, C=0) == 0
 
 
+def test_the_window_counts_in_the_choice_of_kernels(lib):
+    """A chunk of 512 rows per KV head over a long window alone runs on images of it, whose size the workspace shows
+    (fp16 pairs of K and V in blocks of 32 keys), not on kernels that read the window again for every eight rows."""
+    images = lambda w: 8 * -(-w // 64) * 2 * 2 * 2 * 64 * 128
+    assert images(3000) <= kvarn.prefill8_workspace_bytes(128, 0, 3000, 32, 8, 128) < 2 * images(3000)
+    # few rows do without them
+    assert kvarn.prefill8_workspace_bytes(2, 0, 3000, 32, 8, 128) < images(3000) // 4
+
+
 def _evict(lib, **kw):
     a = dict(t=ctypes.c_void_p(1 << 20), m=ctypes.c_void_p(2 << 20), n=ctypes.c_void_p(3 << 20), to=ctypes.c_void_p(4 << 20),
              mo=ctypes.c_void_p(5 << 20), no=ctypes.c_void_p(6 << 20), ev=ctypes.c_void_p(7 << 20), B=0, Hkv=2, mt=10, keep=5,

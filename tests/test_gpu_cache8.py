@@ -598,6 +598,17 @@ def test_prefill_around_the_change_of_kernels(C, G, io):
         _check_prefill(c, q, pos0, c.prefill(q, pos0))
 
 
+@pytest.mark.parametrize("io", ["f32", "f16"])
+@pytest.mark.parametrize("Hkv,tiles,window", [(2, 0, 1500), (8, 0, 300), (1, 3, 900), (8, 9, 20)])
+def test_prefill_around_the_change_of_kernels_with_windows(Hkv, tiles, window, io):
+    """Chunks from a few rows to 64 groups of eight, over windows that decide which kernels serve them."""
+    c = Cache8(window, [tiles], [window], Hkv, 64, "i8", 32)
+    for C in (2, 8, 11, 20, 40, 64):
+        q = _query(C, (C, 4 * Hkv, 64), io)
+        pos0 = T * tiles + window - C
+        _check_prefill(c, q, pos0, c.prefill(q, pos0))
+
+
 def test_prefill_of_one_position_agrees_with_decode():
     c = Cache8(81, [33], [50], 4, 128, "e4m3", 64)
     q = _query(9, (1, 16, 128), "f32")
