@@ -575,6 +575,10 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
   if (!ok) *flag = 1;
   l = cta_row_sum<C::NW>(quad_sum(l), lbuf, warp, g, q);  // its barriers also publish the flag
   const bool bad = *flag != 0;
+  if (bad && tid == 0) {  // a copy whose wait ran out still writes to this CTA's memory: each is given as long again
+    for (int n = max(0, 2 * TP * n_steps - C::SLOTS); n < 2 * TP * n_steps; ++n)
+      if (n / (2 * TP) * TP + n % TP < nt) mbar_wait8(bar + n % C::SLOTS, (uint32_t)(n / C::SLOTS) & 1u, nullptr);
+  }
   float r[C::NC][2];
 #pragma unroll
   for (int c = 0; c < C::NC; ++c) {

@@ -174,6 +174,15 @@ def test_compression_gives_up_as_a_whole_cta():
     assert len(uses) == 2 and "if (!__syncthreads_and(%s)) break;" % name[0] in uses[1]
 
 
+def test_decode_waits_again_for_a_copy_that_it_gave_up_on():
+    """A copy whose wait ran out still writes to the CTA's shared memory: the CTA does not end before it is given as
+    long again."""
+    with open(os.path.join(_build.CSRC, "decode8.cu")) as f:
+        body = f.read().split("split8_kernel(")[1].split("\n}\n")[0]
+    end = body[body.index("const bool bad = *flag != 0;"):]
+    assert re.search(r"if \(bad && tid == 0\) \{[^}]*mbar_wait8\([^}]*nullptr\);\s*\}", end)
+
+
 def test_host_tensors_are_refused():
     lay = kvarn.layout8(128)
     x, i64 = torch.zeros(128, 128), torch.zeros(1, dtype=torch.int64)
