@@ -769,7 +769,7 @@ Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D, bool fp32) {
   p.n_tsub = n_tblk * (kTile / KB);
   p.n_wsub = (win_vis + 2 * PC8<64, 1>::KW - 1) / (2 * PC8<64, 1>::KW) * 2;
   p.head_imgs = 2LL * (p.n_tsub + p.n_wsub);
-  p.row_blocks = (C + ppc - 1) / ppc;
+  p.row_blocks = (int)(((int64_t)C + ppc - 1) / ppc);
   const int64_t ctas = (int64_t)p.row_blocks * Hkv;
   int64_t shares = ctas > 0 ? sm_count() / ctas : 1;
   const int64_t most = (p.n_tsub + p.n_wsub) / 4;  // two pairs of blocks per share at least

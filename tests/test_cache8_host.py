@@ -123,6 +123,14 @@ def test_prefill_refusals(lib):
     assert _prefill(lib, C=0) == 0
 
 
+def test_the_largest_chunks_are_counted_without_wrapping(lib):
+    n, below = ctypes.c_size_t(), ctypes.c_size_t()
+    query = lib.kvarn_prefill8_workspace_bytes
+    assert query((1 << 31) - 1, 1 << 24, 0, 8, 8, 64, ctypes.byref(n)) == 0
+    assert query((1 << 31) - 128, 1 << 24, 0, 8, 8, 64, ctypes.byref(below)) == 0
+    assert below.value <= n.value < 2 * below.value
+
+
 def test_the_window_counts_in_the_choice_of_kernels(lib):
     """A chunk of 512 rows per KV head over a long window alone runs on images of it, whose size the workspace shows
     (fp16 pairs of K and V in blocks of 32 keys), not on kernels that read the window again for every eight rows."""
