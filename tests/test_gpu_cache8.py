@@ -746,6 +746,39 @@ def test_a_cache_lives_prefill_decode_promote_evict(D, io):
     _check_prefill(c, q, pos0, c.prefill(q, pos0))
 
 
+@pytest.mark.parametrize("D", [64, 256])
+def test_records_and_rows_past_32_bit_offsets(D):
+    """A pool longer than 2^32 bytes and raw rows past 2^31 elements give what small ones give."""
+    c = Cache8(94, [9], [30], 2, D, "e4m3", 32)
+    rb, n = c.lay.record_bytes, 18
+    k, v = (torch.from_numpy(x).to(DEV) for x in rows(np.random.default_rng(5), n * T, D))
+    src, near = torch.arange(n, device=DEV) * T, c.table.view(-1)
+    kvarn.compress_tile8(k, v, src, c.tiles, near, c.lay)
+    out_k, out_v = torch.empty_like(k), torch.empty_like(v)
+    kvarn.expand_tile8(c.tiles, near, out_k, out_v, src, c.lay)
+
+    shift = (1 << 32) + 16 - (n // 2) * rb  # records on both sides of 2^32 and one across it
+    big = torch.empty(shift + n * rb, dtype=torch.uint8, device=DEV)
+    row0 = (1 << 31) // D + 3
+    raw_k, raw_v = (torch.empty(row0 + n * T, D, device=DEV) for _ in range(2))
+    raw_k[row0:], raw_v[row0:] = k, v
+    kvarn.compress_tile8(raw_k, raw_v, src + row0, big, near + shift, c.lay)
+    assert torch.equal(big[shift:], c.tiles)
+    raw_k[row0:], raw_v[row0:] = 0, 0
+    kvarn.expand_tile8(big, near + shift, raw_k, raw_v, src + row0, c.lay)
+    assert torch.equal(raw_k[row0:], out_k) and torch.equal(raw_v[row0:], out_v)
+    del raw_k, raw_v
+
+    table = c.table + shift
+    q = _query(1, (1, 8, D), "f32")
+    assert torch.equal(kvarn.decode_attention8(q, big, table, *c.args()[2:]), c.decode(q))
+    for C in (3, 200):
+        q = _query(2, (C, 8, D), "bf16")
+        pos0 = 9 * T + 30 - C
+        out = kvarn.prefill_attention8(q, pos0, big, table[0], 9, c.win_k[0], c.win_v[0], c.starts[0], 30, c.lay)
+        assert torch.equal(out, c.prefill(q, pos0))
+
+
 # ---------------------------------------------------------------- launches
 
 def test_decode_launch_modes_and_graphs_are_bit_identical():
