@@ -551,10 +551,13 @@ int kvarn_layout8(int head_dim, int code_format, int block_tokens, kvarn_layout8
 
 /*
  * Element type of the queries and the outputs of the 8-bit cache's attention
- * calls. KVARN_IO_F32 keeps about 22 bits of every operand. With the 16-bit
- * types the queries enter the products to within 2^-33 of their row's largest
- * element and the output is rounded once; chunked prefill then also rounds the
- * softmax weights, to fp16.
+ * calls. KVARN_IO_F32 keeps about 22 bits of every operand, of a query row down to
+ * 2^-33 of its largest element and, in chunked prefill, of a window row down to 2^-33
+ * of the largest element of its 16 rows. With the 16-bit types the queries enter the
+ * products to within 2^-33 of their row's largest element and the output is rounded
+ * once; chunked prefill of many rows then also rounds the softmax weights, to fp16
+ * (2^-11 of a weight at most: as much as fp16 rounds the output, an eighth of what bf16
+ * does). A caller who needs more passes fp32 queries.
  */
 #define KVARN_IO_F32 0
 #define KVARN_IO_F16 1
@@ -644,7 +647,10 @@ int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t po
  * `recent`, and of those between the keep - sinks - recent with the largest
  * weights (of equal weights the lower index; NaN counts as infinite, -0 as 0). Every
  * KV head loses the same number of tiles, its own choice of them. Works on the
- * tile tables of both caches; the records themselves are not touched.
+ * tile tables of both caches; the records themselves are not touched. The weights are
+ * the caller's: kvarn_decode_attention8 adds up what decode gives to each tile, and no
+ * other call reports any. Equal weights, such as zeros after a prompt alone, keep the
+ * oldest tiles.
  *   tile_table : int64 [B][Hkv][max_tiles]; tile_mass: fp32, the same shape.
  *   n_tiles    : int32 [B] (clamped to 0..max_tiles).
  *   table_out, mass_out : the same shapes: the tiles that stay, in their old order,

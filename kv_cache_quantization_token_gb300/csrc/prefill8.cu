@@ -21,17 +21,23 @@
 // the value scales, the largest terms of O keep their bits.
 // Precision: fp32 queries and their weights are pairs hi + lo of fp16 (22 bits), two products per code
 // operand. 16-bit queries are exact in one fp16 operand, and then w is rounded to fp16 once (2^-11 of each
-// weight at most, an eighth of bf16's rounding of the output, as much as fp16's): one product. Window rows
-// are always pairs. The query and w are read from tensor memory (the A operand), so shared memory feeds B
-// operands only; at head_dim 256 the lo part of the query lives in shared memory.
+// weight at most, an eighth of bf16's rounding of the output, as much as fp16's): one product. That shows in fp16
+// outputs: 301 positions of 15 / 3 heads of 64 are 2.5e-4 off the 64-bit result (relative L2) where the output's
+// rounding alone is 2.1e-4, and not in bf16 ones (1.67e-3 beside 1.66e-3). With pairs both are at the rounding alone,
+// but 25.3 us become 29.4 and 121 at 15,500 tokens 166; adding up the rounded weights instead of w gives 2.3e-4 for
+// 8%. So fp32 queries are the way to more bits. Window rows are always pairs. The query and w are read from tensor
+// memory (the A operand), so shared memory feeds B operands only; at head_dim 256 the lo part of the query lives in
+// shared memory.
 //
 // What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 121 us, 1,056 TFLOP/s, 56%
 // of the measured bf16 rate; images 17 us of it): the softmax warps. A 64-key block costs the tensor pipe 512
-// cycles and 12 softmax warps some 450 instructions per warp, and the SM issues 2.4 per cycle. What made it
-// faster, from 207 us: window rows by 16 (their 128-row CTAs were the tail of the image grid), softmax
-// groups that take blocks in turn instead of halves of one block, MMA warps that do their waiting beside each
+// cycles and each of four softmax warps 475 instructions (by counters, the other warps' share in them), of which the
+// SM issues 2.6 per cycle. Some 190 are the scores' own (an exponential each, and half a three-way maximum, packed
+// multiply-add, packed addition and conversion); the rest (scales and references per 16 keys, hand-overs, moves) has
+// not been taken apart. What made it faster, from 207 us: window rows by 16 (their 128-row CTAs were the tail of the
+// image grid), softmax groups that take blocks in turn instead of halves of one block, MMA warps that do their waiting beside each
 // other's products, hardware barriers for hand-overs, copies of two blocks at a time, one reference instead
-// of two. With fp32 (two products of each kind) the tensor pipe bounds it: 181 us against 122 of products.
+// of two. With fp32 (two products of each kind) the tensor pipe bounds it: 183 us against 122 of products.
 // Not kept: P in the columns of its scores (S of the next block then waits for PV), one MMA warp, four
 // softmax groups (96 registers each), 128-key blocks, one equal stretch of the work per SM (135 us: pipelines
 // fill and drain twice, every row block is joined), another order of keys per CTA.

@@ -615,7 +615,7 @@ def evict_tiles(tile_table, tile_mass, n_tiles, keep, sinks=0, recent=0, table_o
                 mass_out=None, n_tiles_out=None, evicted=None, stream=None, flags=0):
     """Drops tiles by accumulated weight (kvarn_evict_tiles): per KV head, of more
     than `keep` tiles stay the first `sinks`, the last `recent` and the heaviest
-    between. tile_table int64 and tile_mass fp32 [B][Hkv][max_tiles], n_tiles int32
+    between (tile_mass: what decode_attention8 adds up, or the caller's own). tile_table int64 and tile_mass fp32 [B][Hkv][max_tiles], n_tiles int32
     [B]. Outputs default to the inputs (in place); evicted (int64, tile_table's
     shape) receives the offsets that left. Returns (table, mass, n_tiles, evicted)."""
     _dev(tile_table, "tile_table", torch.int64)
