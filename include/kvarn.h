@@ -625,10 +625,10 @@ int kvarn_decode_attention8(const void* q, int io_type, const uint8_t* tiles, in
  * io_type. A row that sees a NaN or an infinity in a cached K or V row, or has one
  * in its query, is NaN; rows before it are not touched by it. tile_table entries are multiples of 16; one
  * outside the pool makes the rows that see it NaN and sets KVARN_DEVERR_RECORD.
- *   ws       : at least kvarn_prefill8_workspace_bytes() bytes for these very
- *              sizes (two kinds of kernels serve small and large chunks, so a
- *              smaller chunk or cache can need more), 256-byte aligned, no
- *              initialisation. Calls sharing ws must not overlap.
+ *   ws       : at least kvarn_prefill8_workspace_bytes() bytes, 256-byte aligned,
+ *              no initialisation. What the query gives for a chunk is enough for every
+ *              call of at most as many positions, tiles and window rows (of the same
+ *              heads). Calls sharing ws must not overlap.
  * After tiles were evicted (kvarn_evict_tiles) positions count the cached tokens
  * that are left: pos0 = 128 n_tiles + win_len - C for the newest C tokens.
  */

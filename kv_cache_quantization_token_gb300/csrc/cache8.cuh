@@ -204,6 +204,7 @@ struct Prefill8Args {
 void chunk8_plan(int C, int Hq, int Hkv, int D, int n_tiles, int win_len, Decode8Plan* p);
 cudaError_t launch_chunk8(const Prefill8Args& a, int n_tiles, int win_len, cudaStream_t st);
 size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D);
+size_t prefill8_ws_bound(int C, int n_tiles, int win_len, int Hq, int Hkv, int D);
 cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st);
 
 cudaError_t launch_evict(const int64_t* table, const float* mass, const int32_t* n_tiles,

@@ -166,7 +166,7 @@ int kvarn_prefill8_workspace_bytes(int C, int n_tiles, int win_len, int Hq, int 
   const int rc = heads_ok(Hq, Hkv, head_dim);
   if (rc != KVARN_OK) return rc;
   if (C < 0 || n_tiles < 0 || win_len < 0 || n_tiles > kMost || win_len > kMost) return KVARN_ERR_BAD_ARG;
-  *bytes = kvarn::prefill8_ws_bytes(C, n_tiles, win_len, Hq, Hkv, head_dim);
+  *bytes = kvarn::prefill8_ws_bound(C, n_tiles, win_len, Hq, Hkv, head_dim);
   return KVARN_OK;
 }
 

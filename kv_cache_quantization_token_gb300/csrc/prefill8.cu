@@ -833,11 +833,13 @@ cudaError_t launch_p8d(const Att8Args& s, cudaStream_t st) {
 // 26.3 / 22.6, 64 221 / 29; 2 KV heads, 16 groups over 128 tiles 30.1 / 48.9, 24 42.1 / 38.4; head_dim 64, 8 over 15
 // tiles 11.3 / 13.7, 24 24.2 / 16.2; head_dim 256, 8 over 40 tiles 34.2 / 39.0, 12 50.3 / 43.6. Over 800 sizes (1 to 8 KV
 // heads, 4 to 64 groups, 0 to 128 tiles, 60 to 3,000 window rows) the choice costs 0.4% on the mean, 31% at worst.
+constexpr int64_t kFewGroups = 64, kFewWork = 1600;
+int64_t row_groups(int C, int G) { return ((int64_t)C * G + 7) / 8; }
+int64_t few_heads(int Hkv) { return Hkv > 6 ? Hkv : 6; }
 bool few_rows(int C, int G, int Hkv, int n_tiles, int win_len) {
-  const int64_t groups = ((int64_t)C * G + 7) / 8;
-  if (groups > 64) return false;
-  const int64_t work = groups * Hkv, heads = Hkv > 6 ? Hkv : 6;
-  return 12 * (work - 5 * heads) * n_tiles + (work - 4 * heads) * win_len <= 12 * 1600;
+  const int64_t groups = row_groups(C, G), work = groups * Hkv, heads = few_heads(Hkv);
+  return groups <= kFewGroups &&
+         12 * (work - 5 * heads) * n_tiles + (work - 4 * heads) * win_len <= 12 * kFewWork;
 }
 
 }  // namespace
@@ -850,6 +852,30 @@ size_t prefill8_ws_bytes(int C, int n_tiles, int win_len, int Hq, int Hkv, int D
   }
   // shares (and with them the partial results) grow as the visible blocks do
   return plan8(C, n_tiles, win_len, Hq, Hkv, D, true).bytes;
+}
+
+// At least prefill8_ws_bytes of every call of at most C positions, n_tiles tiles and win_len window rows, whichever
+// kernels serve it: a workspace for a prompt's last chunk is one for all before it.
+size_t prefill8_ws_bound(int C, int n_tiles, int win_len, int Hq, int Hkv, int D) {
+  const int64_t n = n_tiles, w = win_len, heads = few_heads(Hkv), sms = sm_count();
+  const int64_t groups = row_groups(C, Hq / Hkv), work = (groups < kFewGroups ? groups : kFewGroups) * Hkv;
+  auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  // Decode kernels: 8 work' rows of tile_items + ceil(w' / 64) entries for a call's own work' <= work. tile_items is at
+  // most n' / 16 + slots / work' + 1 (make_plan), and where few_rows holds work' n' <= kFewWork + 5 heads n' and
+  // work' w' <= 12 kFewWork + 5 heads w'.
+  const int64_t slots = 4 * sms;  // resident CTAs, at most four per SM
+  const int64_t entries = 8 * (least(work * n, kFewWork + 5 * heads * n) / 16 + 1 +
+                               least(work * w, 12 * kFewWork + 5 * heads * w) / 64 + 1 + 2 * work + slots);
+  const size_t few = up((size_t)entries * sizeof(float2)) + up((size_t)entries * D * sizeof(float));
+  if (groups * Hkv <= 4 * heads) return few;  // (few_rows holds for every smaller call)
+  // Images: those of this call, and the results of key shares, of which there are only as many as fill the SMs
+  // once (128 rows to a CTA), and O's emptied sums, of a CTA's rows each.
+  const Plan8 p = plan8(C, n_tiles, win_len, Hq, Hkv, D, true);
+  const int64_t ctas = (int64_t)p.row_blocks * Hkv;
+  const size_t rows = 128 * (size_t)sms, sums = 128 * (size_t)(ctas > sms ? ctas : sms);
+  const size_t images = p.off_ml + up(rows * sizeof(float2)) + up(rows * D * sizeof(float)) + up(sums * D * sizeof(float));
+  return few > images ? few : images;
 }
 
 cudaError_t launch_prefill8(const Prefill8Args& a, cudaStream_t st) {

@@ -581,8 +581,8 @@ def prefill_attention8(q_chunk, pos0, tiles, tile_table, n_tiles, win_k, win_v, 
                        lay: Layout8, softmax_scale=None, ws=None, out=None, stream=None):
     """prefill_attention over 8-bit records: q_chunk and out fp32, fp16 or bf16
     [C][Hq][D], the other arguments as prefill_attention's; ws a uint8 device
-    workspace of prefill8_workspace_bytes() for these very sizes (allocated here
-    when None)."""
+    workspace of prefill8_workspace_bytes() for these sizes or larger ones
+    (allocated here when None)."""
     io, device = _io(q_chunk, "q_chunk")
     _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64),
          ("win_k", win_k, torch.float32), ("win_v", win_v, torch.float32))

@@ -1,6 +1,7 @@
 """What the 8-bit cache's calls and eviction refuse, on the host: nothing reaches a GPU."""
 import ctypes
 import os
+import random
 import re
 
 import pytest
@@ -129,6 +130,27 @@ def test_the_largest_chunks_are_counted_without_wrapping(lib):
     assert query((1 << 31) - 1, 1 << 24, 0, 8, 8, 64, ctypes.byref(n)) == 0
     assert query((1 << 31) - 128, 1 << 24, 0, 8, 8, 64, ctypes.byref(below)) == 0
     assert below.value <= n.value < 2 * below.value
+
+
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("Hkv,G", [(1, 1), (2, 8), (4, 3), (8, 4), (40, 2)])
+def test_a_workspace_serves_every_smaller_chunk(lib, Hkv, G, D):
+    """What the query gives is not refused for fewer positions, tiles or window rows, on either kind of kernels: an
+    unaligned output, looked at after the workspace, is."""
+    L, rng = kvarn.layout8(D), random.Random(Hkv * D)
+    log = lambda top: min(top, int(round(2 ** rng.uniform(0, 12)))) if rng.random() < 0.9 else 0
+    for _ in range(400):
+        n, w = log(900), log(3500)
+        C = max(1, min(log(2000), 128 * n + w))
+        size = kvarn.prefill8_workspace_bytes(C, n, w, Hkv * G, Hkv, D)
+        for _ in range(12):
+            n1, w1 = rng.choice([n, log(n)]), rng.choice([w, log(w)])
+            C1 = min(rng.choice([C, max(1, log(C)), rng.randint(1, C)]), 128 * n1 + w1)
+            if C1 == 0:
+                continue
+            rc = _prefill(lib, C=C1, pos0=128 * n1 + w1 - C1, nt=n1, stride=n1, wl=w1, cap=w1, Hq=Hkv * G, Hkv=Hkv, D=D,
+                          lay=ctypes.byref(L), wsb=size, out=ODD)
+            assert rc == -2, (rc, (C, n, w), (C1, n1, w1))
 
 
 def test_the_window_counts_in_the_choice_of_kernels(lib):
