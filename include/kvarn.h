@@ -118,7 +118,9 @@ typedef enum kvarn_status {
  *                          a compress source ran past n_rows.
  *   KVARN_DEVERR_WINDOW    kvarn_append_window would have overfilled a
  *                          sequence's ring (win_len + n_new > win_capacity);
- *                          that sequence's rows were not written.
+ *                          that sequence's rows were not written; or a
+ *                          token of kvarn_write_rows4 or kvarn_read_rows4
+ *                          lies outside its sequence's tile table.
  *   KVARN_DEVERR_SELFTEST  set by kvarn_selftest_bounded_wait.
  */
 #define KVARN_DEVERR_WAIT 1u
@@ -668,6 +670,189 @@ int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const i
                       int64_t* table_out, float* mass_out, int32_t* n_tiles_out, int64_t* evicted,
                       int B, int Hkv, int max_tiles, int keep, int sinks, int recent,
                       unsigned launch_flags, kvarn_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The 4-bit cache. The pages have no counterpart: 128-token tiles per KV head and
+ * byte-offset tile tables as above, but rows are quantised as they are written, token
+ * by token, so there is no staging window and nothing to promote: a decode step is
+ * kvarn_norm_rotate, kvarn_write_rows4, kvarn_decode_attention4. Records hold 4.5
+ * bits per value. kvarn_evict_tiles works on its tables.
+ *
+ * A value is code * scale, with one scale for each group of 32 consecutive channels of a
+ * token of a head, K and V on their own:
+ *   scale   the smallest number that has at most 8 significant bits, is a multiple of 2^-24
+ *           and at least 2^-24, and is not below (largest magnitude of the group) / 7;
+ *           stored as binary16, which holds it exactly
+ *   code    x / scale rounded to the nearest integer, ties to even: -7..7
+ * so that every value is a binary16 number exactly. A token of a head whose K or V row has
+ * a NaN, an infinity or a magnitude above KVARN_MAX4 is poison: its K scales are NaN, its V
+ * scales and all codes 0; it reads back as NaN, and every attention row that sees it is NaN.
+ *
+ * Record of one (tile, KV head), D = head_dim, 144 D bytes: four runs of 32 tokens, 36 D
+ * bytes each. In a run, for its token t (0..31), with W = min(D, 128):
+ *   off_k_codes  u16 [D/W][32][W/4]  channels c..c+3 (c a multiple of 4): unit
+ *                                    (c/W, t, c%W/4)
+ *   off_v_codes  u16 [D/32][32][8]   channels c..c+3: unit (c/32, t, c%32/4)
+ *   off_k_scale  binary16 [32][D/32] scale of channels [32 i, 32 i + 32) of token t
+ *   off_v_scale  binary16 [D/32][32] the same for V, token t in place
+ *                                    8 (t%8/2) + 2 (t/8) + t%2
+ * A unit holds code + 8 of four channels: the first at bits 6..9, the second at bits
+ * 10..13, the third at bits 2..5; of the fourth the low two bits at bits 14..15 and the
+ * high two at bits 0..1.
+ */
+#define KVARN_LAYOUT4_VERSION 1
+#define KVARN_MAX4 14336.0f
+
+typedef struct kvarn_layout4 {
+  int32_t version;        /* KVARN_LAYOUT4_VERSION            */
+  int32_t head_dim;       /* D                                */
+  int32_t tile_tokens;    /* 128                              */
+  int32_t run_tokens;     /* 32                               */
+  int32_t group_channels; /* 32                               */
+  int32_t reserved;       /* 0                                */
+  int64_t record_bytes;   /* 144 D                            */
+  int64_t run_bytes;      /* 36 D                             */
+  int64_t off_k_codes, off_v_codes, off_k_scale, off_v_scale; /* in a run */
+} kvarn_layout4_t;
+
+/* Fills *out (host pointer). KVARN_ERR_UNSUPPORTED for head dims other than 64, 128
+ * and 256. */
+int kvarn_layout4(int head_dim, kvarn_layout4_t* out);
+
+/*
+ * Writing rows: row (b, t) of k_new and v_new, t < counts[b], becomes cached token
+ * lens[b] + t of sequence b, in every KV head.
+ *   k_new, v_new : io_type [B][T][Hkv][D]; a row (b, t) starts k_stride (v_stride) elements
+ *                  after the one before, so that slices of a product that makes queries,
+ *                  keys and values at once can be passed. Strides are at least Hkv * D
+ *                  and, like the pointers, multiples of 16 bytes.
+ *   tile_table   : int64 [B][Hkv][max_tiles], byte offsets of records, multiples of 16.
+ *   lens         : int32 [B], tokens that sequence b holds before the call (not changed:
+ *                  kvarn_window_advance with promote 0 moves them on).
+ *   counts       : int32 [B] rows of each sequence (clamped to 0..T), or NULL: T.
+ *                  Rows behind them are not read.
+ * A token at or past 128 max_tiles, or of a negative lens[b], is not written and sets
+ * KVARN_DEVERR_WINDOW; one whose record is not inside the pool is not written and sets
+ * KVARN_DEVERR_RECORD. Bytes of other tokens stay as they are. Sequences must not share
+ * the records that are written. launch_flags: 0 or KVARN_LAUNCH_PDL.
+ */
+int kvarn_write_rows4(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                      int io_type, uint8_t* tiles, int64_t tiles_bytes, const int64_t* tile_table,
+                      const int32_t* lens, const int32_t* counts, int B, int T, int Hkv, int head_dim,
+                      int max_tiles, const kvarn_layout4_t* layout, unsigned launch_flags,
+                      kvarn_stream_t stream);
+
+/*
+ * Reading rows back: cached token first[b] + t of sequence b becomes row (b, t), t <
+ * counts[b], of k_out and v_out (code * scale, rounded once to io_type). Rows behind
+ * counts[b], and columns between the rows, are left as they are. Tokens outside the table
+ * are skipped (KVARN_DEVERR_WINDOW); one whose record is not inside the pool gives NaN
+ * rows (KVARN_DEVERR_RECORD). Arguments as kvarn_write_rows4's.
+ */
+int kvarn_read_rows4(const uint8_t* tiles, int64_t tiles_bytes, const int64_t* tile_table,
+                     const int32_t* first, const int32_t* counts, void* k_out, int64_t k_stride,
+                     void* v_out, int64_t v_stride, int io_type, int B, int T, int Hkv, int head_dim,
+                     int max_tiles, const kvarn_layout4_t* layout, unsigned launch_flags,
+                     kvarn_stream_t stream);
+
+/*
+ * Decode attention over the 4-bit cache: out[b][h] = sum_t softmax_t(scale q[b][h] . k_t) v_t
+ * over the lens[b] cached tokens of sequence b (lens is clamped to 0..128 max_tiles), q and out
+ * io_type [B][Hq][D], 16-byte aligned.
+ *   mass_in, mass_out : as in kvarn_decode_attention8: mass_out[b][h][i] = mass_in[b][h][i]
+ *                  plus the softmax weights that the heads of the group give to the
+ *                  tokens of tile i.
+ * At most 8 query heads per KV head (KVARN_ERR_UNSUPPORTED), 2^24 - 1 tiles of a head.
+ * A sequence of no tokens gets zeros. What is not written yet behind lens[b] in the last tile is
+ * read but has no effect, whatever its bits. tile_table entries that are misaligned or
+ * outside the pool make that head's output and masses NaN and set KVARN_DEVERR_RECORD. A NaN
+ * or an infinity in a query makes its row NaN. Precision: KVARN_IO_F32 keeps 22 bits of queries and
+ * weights; the cached values are exact. Deterministic; grids depend only on the sizes, so the
+ * call can be captured. launch_flags: 0 or KVARN_LAUNCH_PDL.
+ *   ws : at least kvarn_decode4_workspace_bytes() bytes, 256-byte aligned, no
+ *        initialisation. Calls sharing ws must not overlap.
+ */
+int kvarn_decode4_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int max_tiles, size_t* bytes);
+int kvarn_decode_attention4(const void* q, int io_type, const uint8_t* tiles, int64_t tiles_bytes,
+                            const int64_t* tile_table, const int32_t* lens, int B, int Hq, int Hkv,
+                            int head_dim, int max_tiles, float softmax_scale,
+                            const kvarn_layout4_t* layout, const float* mass_in, float* mass_out,
+                            void* ws, size_t ws_bytes, void* out, unsigned launch_flags,
+                            kvarn_stream_t stream);
+
+/*
+ * Chunked-prefill attention over the 4-bit cache: out[i][h] = sum_j softmax_j(scale q[i][h] .
+ * k_j) v_j over the cached tokens j <= pos0 + i of one sequence, C positions. The chunk's own
+ * rows have been written (kvarn_write_rows4), so the cache holds pos0 + C tokens at least.
+ *   q_chunk, out : io_type [C][Hq][D], 16-byte aligned.
+ *   tile_table   : int64 [Hkv][table_stride]; pos0 + C <= 128 table_stride.
+ * A row that sees a poisoned token or a record outside the pool (KVARN_DEVERR_RECORD), or has
+ * a NaN or an infinity in its query, is NaN; rows before it are not touched by it. With 16-bit types
+ * chunks of many rows round the softmax weights to fp16, as kvarn_prefill_attention8 does.
+ *   ws : at least kvarn_prefill4_workspace_bytes() bytes for these sizes or larger ones
+ *        (n_tiles >= ceil((pos0 + C) / 128)), 256-byte aligned, no initialisation. Calls
+ *        sharing ws must not overlap.
+ */
+int kvarn_prefill4_workspace_bytes(int C, int n_tiles, int Hq, int Hkv, int head_dim, size_t* bytes);
+int kvarn_prefill_attention4(const void* q_chunk, int io_type, int C, int64_t pos0,
+                             const uint8_t* tiles, int64_t tiles_bytes, const int64_t* tile_table,
+                             int table_stride, int Hq, int Hkv, int head_dim, float softmax_scale,
+                             const kvarn_layout4_t* layout, void* ws, size_t ws_bytes, void* out,
+                             kvarn_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Queries and keys of new tokens, made ready for any of the caches: RMS norm of each head,
+ * rotation by position, and an orthonormal Walsh-Hadamard transform of each head, each on
+ * request, in one pass over the rows.
+ *
+ * Rotation plan. Pair i (0 <= i < rotary_dim / 2) of a head is channels (i, i + rotary_dim / 2)
+ * (KVARN_PAIRS_HALVES) or (2 i, 2 i + 1) (KVARN_PAIRS_ADJACENT); it turns by the angle
+ * inv_freq[i] * position[pair_axis[i]] radians: (a, b) -> (a cos - b sin, a sin + b cos).
+ * Channels from rotary_dim on are not turned. A position has 1 to 4 axes (text: one;
+ * images and video: time, height, width). Angles are products in units of 2^-64 of a turn,
+ * with whole turns dropped exactly, so far positions keep their accuracy; positions may
+ * be negative.
+ *   rotary_dim : a multiple of 16, 16..256.
+ *   inv_freq   : host, double [rotary_dim / 2], finite.
+ *   pair_axis  : host, u8 [rotary_dim / 2], each below n_axes; NULL: all 0.
+ */
+#define KVARN_PAIRS_HALVES 0
+#define KVARN_PAIRS_ADJACENT 1
+#define KVARN_ROTARY_VERSION 1
+typedef struct kvarn_rotary {
+  int32_t version;    /* KVARN_ROTARY_VERSION       */
+  int32_t rotary_dim;
+  int32_t pairing;    /* KVARN_PAIRS_*              */
+  int32_t n_axes;
+  uint64_t turn[128]; /* inv_freq / 2 pi, in units of 2^-64 of a turn, whole turns dropped */
+  uint8_t axis[128];
+} kvarn_rotary_t;
+int kvarn_rotary(int rotary_dim, int pairing, const double* inv_freq, const uint8_t* pair_axis, int n_axes,
+                 kvarn_rotary_t* out);
+
+/*
+ * Per row (token, head): y = x; with eps >= 0, y = x / sqrt(mean(x^2) + eps) * weight (the sum
+ * of squares and all that follows in fp32, rounded once at the end); then the rotation of
+ * `rotary` (host pointer; NULL: none); then, with hadamard, y H / sqrt(D) (H as in
+ * kvarn_rotate_query: scores of transformed queries and keys are the same, and 4-bit keys
+ * lose less).
+ *   q, k         : io_type [n_tokens][Hq][D] and [n_tokens][Hkv][D]; tokens q_stride (k_stride)
+ *                  elements apart, at least Hq * D (Hkv * D). Pointers and strides are multiples
+ *                  of 16 bytes. Hkv = 0: queries alone (k, k_out NULL). Any number of heads.
+ *   q_weight, k_weight : io_type [D], 16-byte aligned, or NULL: ones. NULL without a norm.
+ *   eps          : >= 0, or negative: no norm.
+ *   positions    : int64 [rotary->n_axes][n_tokens]; not read without a rotation.
+ *   q_out, k_out : as q and k, with strides of their own; may be q and k themselves (same
+ *                  stride), and must not share rows with anything else. Between rows nothing is written.
+ * launch_flags: 0 or KVARN_LAUNCH_PDL.
+ */
+int kvarn_norm_rotate(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int io_type,
+                      int64_t n_tokens, int Hq, int Hkv, int head_dim, const void* q_weight,
+                      const void* k_weight, float eps, const int64_t* positions,
+                      const kvarn_rotary_t* rotary, int hadamard, void* q_out, int64_t q_out_stride,
+                      void* k_out, int64_t k_out_stride, unsigned launch_flags, kvarn_stream_t stream);
 
 #ifdef __cplusplus
 }

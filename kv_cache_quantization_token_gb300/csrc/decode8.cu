@@ -39,6 +39,7 @@
 // The same kernels serve chunks of a few positions (CHUNK): eight (position, head) rows to a CTA, each of
 // which sees the cache up to its own position.
 #include "cache8.cuh"
+#include "join.cuh"
 
 namespace kvarn {
 namespace {
@@ -616,98 +617,18 @@ __global__ void __launch_bounds__(D8<D>::NTHR, D8<D>::CTAS) split8_kernel(const 
 template <int D>
 __global__ void __launch_bounds__(256) merge8_kernel(const Split8Args s, int mass_blocks) {
   const Decode8Args& a = s.a;
-  __shared__ __align__(16) float4 part_s[256];
-  __shared__ float2 part_ml[16];
-  __shared__ float2 stat[8];
-  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.y;
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x >= a.Hq) {
     const int kvh = ((int)blockIdx.x - a.Hq) / mass_blocks, run = ((int)blockIdx.x - a.Hq) % mass_blocks;
-    if (warp < a.G) {  // (maximum, sum) of query head `warp` of the group
-      const float2* ml = s.ml + ((int64_t)b * a.Hq + kvh * a.G + warp) * s.items;
-      float M = -INFINITY, L = 0.f;
-      for (int i = lane; i < s.items; i += 32) M = fmaxf(M, ml[i].x);
-      for (int m = 16; m; m >>= 1) M = fmaxf(M, shfl_xor(M, m));
-      for (int i = lane; i < s.items; i += 32)
-        if (ml[i].y != 0.f) L += fast_ex2(ml[i].x - M) * ml[i].y;
-      for (int m = 16; m; m >>= 1) L += shfl_xor(L, m);
-      if (lane == 0) stat[warp] = make_float2(M, 1.f / L);
-    }
-    __syncthreads();
-    const int i = 256 * run + tid;
-    if (i < a.max_tiles) {
-      const int64_t at = ((int64_t)b * a.Hkv + kvh) * a.max_tiles + i;
-      float w = a.mass_in ? a.mass_in[at] : 0.f;
-      if (i < min(a.n_tiles[b], a.max_tiles)) {
-        float sum = 0.f;
-        for (int h = 0; h < a.G; ++h) {
-          const float2 t = s.tile_ml[at * 8 + h];
-          sum += fast_ex2(t.x - stat[h].x) * t.y * stat[h].y;
-        }
-        w += sum;
-      }
-      a.mass_out[at] = w;
-    }
+    const int64_t at = ((int64_t)b * a.Hkv + kvh) * a.max_tiles;
+    join_masses<1>(s.ml + ((int64_t)b * a.Hq + kvh * a.G) * s.items, s.items, s.tile_ml + at * 8, a.G, run,
+                   min(a.n_tiles[b], a.max_tiles), a.max_tiles, a.mass_in ? a.mass_in + at : nullptr, a.mass_out + at);
     return;
   }
-  // each part takes every PARTS-th item of the head with a maximum of its own; the parts meet in shared
-  // memory (one round of loads, none waiting for another)
-  constexpr int COLS = D / 4, PARTS = 256 / COLS;
-  const int h = blockIdx.x, col = tid % COLS, pt = tid / COLS;
-  const int64_t base = ((int64_t)b * a.Hq + h) * s.items;
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = pt; i0 < s.items; i0 += 4 * PARTS) {
-    float2 v[4];
-    float4 x[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * PARTS;
-      v[k] = i < s.items ? s.ml[base + i] : make_float2(-INFINITY, 0.f);
-      x[k] = i < s.items ? *reinterpret_cast<const float4*>(s.acc + (base + i) * D + 4 * col)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float m = M;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m = fmaxf(m, v[k].x);
-    if (m == -INFINITY) continue;  // empty items only
-    const float w0 = fast_ex2(M - m);
-    L *= w0; acc.x *= w0; acc.y *= w0; acc.z *= w0; acc.w *= w0;
-    M = m;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (v[k].y != 0.f) {  // an empty item wrote no accumulator
-        const float w = fast_ex2(v[k].x - m);
-        L = fmaf(w, v[k].y, L);
-        acc.x = fmaf(w, x[k].x, acc.x); acc.y = fmaf(w, x[k].y, acc.y);
-        acc.z = fmaf(w, x[k].z, acc.z); acc.w = fmaf(w, x[k].w, acc.w);
-      }
-  }
-  part_s[tid] = acc;
-  if (col == 0) part_ml[pt] = make_float2(M, L);
-  __syncthreads();
-  if (tid < COLS) {
-    M = -INFINITY;
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) M = fmaxf(M, part_ml[p].x);
-    L = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
-      const float2 v = part_ml[p];
-      if (v.y != 0.f) {
-        const float w = fast_ex2(v.x - M);
-        const float4 x = part_s[p * COLS + tid];
-        L = fmaf(w, v.y, L);
-        acc.x = fmaf(w, x.x, acc.x); acc.y = fmaf(w, x.y, acc.y);
-        acc.z = fmaf(w, x.z, acc.z); acc.w = fmaf(w, x.w, acc.w);
-      }
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    io_st4(a.out, a.io, ((int64_t)b * a.Hq + h) * D + 4 * tid,
-           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  }
+  const int64_t row = (int64_t)b * a.Hq + blockIdx.x;
+  join_items<D>(s.ml + row * s.items, s.acc + row * s.items * D, s.items, a.out, a.io, row);
 }
 
 template <int D, int F, bool CHUNK>

@@ -24,6 +24,7 @@ DEVERR_WINDOW = 4    # KVARN_DEVERR_WINDOW
 DEVERR_SELFTEST = 8  # KVARN_DEVERR_SELFTEST
 
 CODE8 = {"i8": 0, "e4m3": 1}  # KVARN_CODE8_*
+PAIRINGS = {"halves": 0, "adjacent": 1}  # KVARN_PAIRS_*
 IO_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # KVARN_IO_*
 
 _lib = None
@@ -58,6 +59,23 @@ class Layout8(ctypes.Structure):
                 ("record_bytes", ctypes.c_int64),
                 ("off_k_codes", ctypes.c_int64), ("off_v_codes", ctypes.c_int64),
                 ("off_k_scale", ctypes.c_int64), ("off_v_scale", ctypes.c_int64)]
+
+
+class Layout4(ctypes.Structure):
+    """Mirror of kvarn_layout4_t."""
+    _fields_ = [("version", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("tile_tokens", ctypes.c_int32), ("run_tokens", ctypes.c_int32),
+                ("group_channels", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("record_bytes", ctypes.c_int64), ("run_bytes", ctypes.c_int64),
+                ("off_k_codes", ctypes.c_int64), ("off_v_codes", ctypes.c_int64),
+                ("off_k_scale", ctypes.c_int64), ("off_v_scale", ctypes.c_int64)]
+
+
+class Rotary(ctypes.Structure):
+    """Mirror of kvarn_rotary_t."""
+    _fields_ = [("version", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("turn", ctypes.c_uint64 * 128), ("axis", ctypes.c_uint8 * 128)]
 
 
 def library_path() -> str:
@@ -120,6 +138,27 @@ def _L():
                                                  lay8, vp, sz, vp, vp]
         lib.kvarn_evict_tiles.argtypes = [vp, vp, vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int,
                                           c_int, u32, vp]
+        lay4, rot = ctypes.POINTER(Layout4), ctypes.POINTER(Rotary)
+        lib.kvarn_layout4.argtypes = [c_int, lay4]
+        lib.kvarn_write_rows4.argtypes = [vp, i64, vp, i64, c_int, vp, i64, vp, vp, vp, c_int, c_int, c_int,
+                                          c_int, c_int, lay4, u32, vp]
+        lib.kvarn_read_rows4.argtypes = [vp, i64, vp, vp, vp, vp, i64, vp, i64, c_int, c_int, c_int, c_int,
+                                         c_int, c_int, lay4, u32, vp]
+        lib.kvarn_decode4_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int, ctypes.POINTER(sz)]
+        lib.kvarn_decode_attention4.argtypes = [vp, c_int, vp, i64, vp, vp, c_int, c_int, c_int, c_int, c_int,
+                                                f32, lay4, vp, vp, vp, sz, vp, u32, vp]
+        lib.kvarn_prefill4_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int, ctypes.POINTER(sz)]
+        lib.kvarn_prefill_attention4.argtypes = [vp, c_int, c_int, i64, vp, i64, vp, c_int, c_int, c_int, c_int,
+                                                 f32, lay4, vp, sz, vp, vp]
+        lib.kvarn_rotary.argtypes = [c_int, c_int, ctypes.POINTER(ctypes.c_double),
+                                     ctypes.POINTER(ctypes.c_uint8), c_int, rot]
+        lib.kvarn_norm_rotate.argtypes = [vp, i64, vp, i64, c_int, i64, c_int, c_int, c_int, vp, vp, f32, vp, rot,
+                                          c_int, vp, i64, vp, i64, u32, vp]
+        for name in ("kvarn_layout4", "kvarn_write_rows4", "kvarn_read_rows4",
+                     "kvarn_decode4_workspace_bytes", "kvarn_decode_attention4",
+                     "kvarn_prefill4_workspace_bytes", "kvarn_prefill_attention4", "kvarn_rotary",
+                     "kvarn_norm_rotate"):
+            getattr(lib, name).restype = c_int
         for name in ("kvarn_layout8", "kvarn_compress_tile8", "kvarn_expand_tile8",
                      "kvarn_decode8_workspace_bytes", "kvarn_decode_attention8",
                      "kvarn_prefill8_workspace_bytes", "kvarn_prefill_attention8",
@@ -641,3 +680,264 @@ def evict_tiles(tile_table, tile_mass, n_tiles, keep, sinks=0, recent=0, table_o
           None if evicted is None else evicted.data_ptr(), B, Hkv, max_tiles, int(keep), int(sinks),
           int(recent), int(flags))
     return table_out, mass_out, n_tiles_out, evicted
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit cache, and queries and keys made ready for any cache
+
+def layout4(head_dim: int) -> Layout4:
+    """Layout of a 4-bit tile record: integers -7..7 with a scale for each 32
+    channels of a token of a head (4.5 bits per value)."""
+    L = Layout4()
+    _check("kvarn_layout4", _L().kvarn_layout4(head_dim, ctypes.byref(L)))
+    return L
+
+
+def _rows_of(t, name, dims, io_dtype=None, device=None):
+    """A CUDA tensor [..., heads, D] of `dims` dimensions whose heads lie side by side and whose
+    rows (all but the last two axes) are a constant stride apart, as a slice of a packed
+    product's result: its stride in elements."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in IO_TYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if io_dtype is not None and t.dtype is not io_dtype:
+        raise TypeError(f"{name} must be {io_dtype}, got {t.dtype}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    shape, stride = t.shape, t.stride()
+    width = shape[-2] * shape[-1]
+    if (shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1]):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    # (the stride of an axis of one element says nothing)
+    row, span = None, 1
+    for n, s in zip(shape[-3::-1], stride[-3::-1]):
+        if n != 1:
+            if row is None:
+                if s % span:
+                    raise ValueError(f"the rows of {name} must be a constant stride apart")
+                row = s // span
+            elif s != row * span:
+                raise ValueError(f"the rows of {name} must be a constant stride apart")
+        span *= n
+    return width if row is None else row
+
+
+def _cache4(tiles, tile_table, lay, D, device, what):
+    _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64))
+    if lay.head_dim != D:
+        raise ValueError(f"{what}: the layout is for head_dim {lay.head_dim}, the rows have {D}")
+
+
+def _counts4(counts, B, device):
+    if counts is None:
+        return None
+    _fit(device, ("counts", counts, torch.int32))
+    if counts.numel() != B:
+        raise ValueError("counts must have one entry per sequence")
+    return counts.data_ptr()
+
+
+def write_rows4(k_new, v_new, tiles, tile_table, lens, lay: Layout4, counts=None, stream=None, flags=0):
+    """Quantises rows into the 4-bit cache: k_new, v_new fp32, fp16 or bf16 [B][T][Hkv][D] (slices of
+    a packed tensor will do: heads contiguous, rows a constant stride apart); row (b, t), t <
+    counts[b] (int32 [B]; None: T), becomes token lens[b] + t (int32 [B], not changed) of sequence b.
+    tiles uint8 record pool; tile_table int64 [B][Hkv][max_tiles]."""
+    k_stride = _rows_of(k_new, "k_new", 4)
+    device = k_new.get_device()
+    v_stride = _rows_of(v_new, "v_new", 4, k_new.dtype, device)
+    B, T, Hkv, D = k_new.shape
+    _cache4(tiles, tile_table, lay, D, device, "write_rows4")
+    _fit(device, ("lens", lens, torch.int32))
+    if (v_new.shape != k_new.shape or tile_table.dim() != 3 or tuple(tile_table.shape[:2]) != (B, Hkv)
+            or lens.numel() != B):
+        raise ValueError("write_rows4: inconsistent shapes")
+    _call(device, "kvarn_write_rows4", stream, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+          IO_TYPES[k_new.dtype], tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(), lens.data_ptr(),
+          _counts4(counts, B, device), B, T, Hkv, D, tile_table.shape[2], ctypes.byref(lay), int(flags))
+
+
+def read_rows4(tiles, tile_table, first, k_out, v_out, lay: Layout4, counts=None, stream=None, flags=0):
+    """Cached tokens first[b] + t (int32 [B]) of the 4-bit cache as rows (b, t), t < counts[b], of k_out
+    and v_out (as k_new and v_new of write_rows4); other rows stay as they are."""
+    k_stride = _rows_of(k_out, "k_out", 4)
+    device = k_out.get_device()
+    v_stride = _rows_of(v_out, "v_out", 4, k_out.dtype, device)
+    B, T, Hkv, D = k_out.shape
+    _cache4(tiles, tile_table, lay, D, device, "read_rows4")
+    _fit(device, ("first", first, torch.int32))
+    if (v_out.shape != k_out.shape or tile_table.dim() != 3 or tuple(tile_table.shape[:2]) != (B, Hkv)
+            or first.numel() != B):
+        raise ValueError("read_rows4: inconsistent shapes")
+    _call(device, "kvarn_read_rows4", stream, tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(),
+          first.data_ptr(), _counts4(counts, B, device), k_out.data_ptr(), k_stride, v_out.data_ptr(), v_stride,
+          IO_TYPES[k_out.dtype], B, T, Hkv, D, tile_table.shape[2], ctypes.byref(lay), int(flags))
+
+
+def decode4_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles) -> int:
+    n = ctypes.c_size_t()
+    _check("kvarn_decode4_workspace_bytes",
+           _L().kvarn_decode4_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles, ctypes.byref(n)))
+    return n.value
+
+
+def decode_attention4(q, tiles, tile_table, lens, lay: Layout4, softmax_scale=None, mass_in=None,
+                      mass_out=None, ws=None, out=None, stream=None, flags=0):
+    """Attention of one query token per sequence over the first lens[b] (int32 [B]) cached tokens: q
+    and out fp32, fp16 or bf16 [B][Hq][D]; tile_table int64 [B][Hkv][max_tiles]. mass_in and mass_out
+    as decode_attention8's."""
+    io, device = _io(q, "q")
+    if q.dim() != 3 or not isinstance(tile_table, torch.Tensor) or tile_table.dim() != 3:
+        raise ValueError("decode_attention4: q [B][Hq][D], tile_table [B][Hkv][max_tiles] expected")
+    B, Hq, D = q.shape
+    _cache4(tiles, tile_table, lay, D, device, "decode_attention4")
+    _fit(device, ("lens", lens, torch.int32))
+    Bt, Hkv, max_tiles = tile_table.shape
+    if Bt != B or lens.numel() != B:
+        raise ValueError("decode_attention4: inconsistent shapes")
+    for name, m in (("mass_in", mass_in), ("mass_out", mass_out)):
+        if m is not None:
+            _fit(device, (name, m, torch.float32))
+            if m.shape != tile_table.shape:
+                raise ValueError(f"{name} must have tile_table's shape")
+    if ws is None:
+        with torch.cuda.device(device):  # the split of the work depends on the device
+            need = decode4_workspace_bytes(B, Hq, Hkv, D, max_tiles)
+        ws = _scratch(need, q.device, stream)
+    if out is None:
+        out = _result(q, stream)
+    _fit(device, ("ws", ws, torch.uint8), ("out", out, q.dtype))
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _call(device, "kvarn_decode_attention4", stream, q.data_ptr(), io, tiles.data_ptr(), tiles.numel(),
+          tile_table.data_ptr(), lens.data_ptr(), B, Hq, Hkv, D, max_tiles,
+          D ** -0.5 if softmax_scale is None else float(softmax_scale), ctypes.byref(lay),
+          None if mass_in is None else mass_in.data_ptr(),
+          None if mass_out is None else mass_out.data_ptr(), ws.data_ptr(), ws.numel(), out.data_ptr(),
+          int(flags))
+    return out
+
+
+def prefill4_workspace_bytes(C, n_tiles, Hq, Hkv, head_dim) -> int:
+    n = ctypes.c_size_t()
+    _check("kvarn_prefill4_workspace_bytes",
+           _L().kvarn_prefill4_workspace_bytes(int(C), int(n_tiles), Hq, Hkv, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def prefill_attention4(q_chunk, pos0, tiles, tile_table, lay: Layout4, softmax_scale=None, ws=None,
+                       out=None, stream=None):
+    """Causal attention of a chunk of one sequence whose rows are in the 4-bit cache: q_chunk and out fp32,
+    fp16 or bf16 [C][Hq][D] at positions pos0 + i; tile_table int64 [Hkv][stride]; ws a uint8 device
+    workspace of prefill4_workspace_bytes() for C positions and ceil((pos0 + C) / 128) tiles, or more of
+    either (allocated here when None)."""
+    io, device = _io(q_chunk, "q_chunk")
+    if q_chunk.dim() != 3 or not isinstance(tile_table, torch.Tensor) or tile_table.dim() != 2:
+        raise ValueError("prefill_attention4: q_chunk [C][Hq][D], tile_table [Hkv][stride] expected")
+    C, Hq, D = q_chunk.shape
+    Hkv, stride = tile_table.shape
+    _cache4(tiles, tile_table, lay, D, device, "prefill_attention4")
+    if out is None:
+        out = _result(q_chunk, stream)
+    if ws is None:
+        n_tiles = max(0, min(stride, -(-(int(pos0) + C) // TILE)))
+        with torch.cuda.device(device):
+            need = prefill4_workspace_bytes(C, n_tiles, Hq, Hkv, D)
+        ws = _scratch(need, q_chunk.device, stream)
+    _fit(device, ("ws", ws, torch.uint8), ("out", out, q_chunk.dtype))
+    if out.shape != q_chunk.shape:
+        raise ValueError("out must have q_chunk's shape")
+    _call(device, "kvarn_prefill_attention4", stream, q_chunk.data_ptr(), io, C, int(pos0),
+          tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(), stride, Hq, Hkv, D,
+          D ** -0.5 if softmax_scale is None else float(softmax_scale), ctypes.byref(lay),
+          ws.data_ptr(), ws.numel(), out.data_ptr())
+    return out
+
+
+def rotary(rotary_dim: int, theta: float = 10000.0, inv_freq=None, sections=None, pair_axis=None,
+           pairing: str = "halves") -> Rotary:
+    """Rotation plan of norm_rotate (kvarn_rotary): pair i of a head turns by inv_freq[i] (rotary_dim / 2
+    numbers; None: theta ** (-2 i / rotary_dim)) radians per position. Positions of several axes: sections,
+    pairs of each axis in order (their sum is rotary_dim / 2), or pair_axis, the axis of each pair.
+    pairing "halves": channels (i, i + rotary_dim / 2); "adjacent": (2 i, 2 i + 1)."""
+    if pairing not in PAIRINGS:
+        raise ValueError(f"pairing must be one of {sorted(PAIRINGS)}, got {pairing!r}")
+    pairs = rotary_dim // 2
+    if inv_freq is None:
+        inv_freq = [float(theta) ** (-2.0 * i / rotary_dim) for i in range(pairs)]
+    inv_freq = [float(f) for f in inv_freq]
+    if sections is not None:
+        if pair_axis is not None:
+            raise ValueError("sections or pair_axis, not both")
+        pair_axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    if len(inv_freq) != pairs or (pair_axis is not None and len(pair_axis) != pairs):
+        raise ValueError("inv_freq, sections and pair_axis must cover rotary_dim / 2 pairs")
+    axes, n_axes = None, 1
+    if pair_axis is not None:
+        if any(not 0 <= int(a) < 4 for a in pair_axis):
+            raise ValueError("a position has 1 to 4 axes")
+        n_axes = len(sections) if sections is not None else max(int(a) for a in pair_axis) + 1
+        axes = (ctypes.c_uint8 * max(pairs, 1))(*[int(a) for a in pair_axis])
+    R = Rotary()
+    _check("kvarn_rotary", _L().kvarn_rotary(rotary_dim, PAIRINGS[pairing],
+                                             (ctypes.c_double * max(pairs, 1))(*inv_freq), axes, n_axes,
+                                             ctypes.byref(R)))
+    return R
+
+
+def norm_rotate(q, k, positions, rot, q_weight=None, k_weight=None, eps=None, hadamard=False, q_out=None,
+                k_out=None, stream=None, flags=0):
+    """Queries and keys of new tokens made ready for a cache, in one pass: per head RMS norm (eps; None: no
+    norm) with weights [D], rotation by position (rot: rotary(...), or None), and on request an orthonormal
+    Walsh-Hadamard transform. q [T][Hq][D] and k [T][Hkv][D] (or None) fp32, fp16 or bf16, heads contiguous and
+    tokens a constant stride apart; positions int64 [T], or [axes][T]. Outputs are new tensors, or q_out and
+    k_out (q and k themselves: in place). Returns (q_out, k_out)."""
+    q_stride = _rows_of(q, "q", 3)
+    device = q.get_device()
+    T, Hq, D = q.shape
+    Hkv, k_stride, ko_stride = 0, 0, 0
+    if k is not None:
+        k_stride = _rows_of(k, "k", 3, q.dtype, device)
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("norm_rotate: inconsistent shapes")
+        Hkv = k.shape[1]
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("norm_rotate: k_out or k_weight without k")
+    if q_out is None:
+        q_out = _result_rows(q, stream)
+    qo_stride = _rows_of(q_out, "q_out", 3, q.dtype, device)
+    if k is not None:
+        if k_out is None:
+            k_out = _result_rows(k, stream)
+        ko_stride = _rows_of(k_out, "k_out", 3, q.dtype, device)
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise ValueError("norm_rotate: outputs must have the inputs' shapes")
+    if rot is not None:
+        _fit(device, ("positions", positions, torch.int64))
+        if positions.numel() != rot.n_axes * T or positions.shape[-1:] != (T,):
+            raise ValueError("positions must be [T], or [axes][T] with the plan's axes")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _fit(device, (name, w, q.dtype))
+            if w.numel() != D:
+                raise ValueError(f"{name} must have head_dim elements")
+            if eps is None:
+                raise ValueError(f"{name} without a norm (eps)")
+    if eps is not None and not eps >= 0:
+        raise ValueError("eps must not be negative")
+    _call(device, "kvarn_norm_rotate", stream, q.data_ptr(), q_stride, None if k is None else k.data_ptr(), k_stride,
+          IO_TYPES[q.dtype], T, Hq, Hkv, D, None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(), -1.0 if eps is None else float(eps),
+          None if rot is None else positions.data_ptr(), None if rot is None else ctypes.byref(rot), int(bool(hadamard)),
+          q_out.data_ptr(), qo_stride, None if k is None else k_out.data_ptr(), ko_stride, int(flags))
+    return q_out, k_out
+
+
+def _result_rows(like, stream):
+    """_result, contiguous whatever the strides of `like`."""
+    if stream is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
