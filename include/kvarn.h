@@ -815,7 +815,7 @@ int kvarn_prefill_attention4(const void* q_chunk, int io_type, int C, int64_t po
  * with whole turns dropped exactly, so far positions keep their accuracy; positions may
  * be negative.
  *   rotary_dim : a multiple of 16, 16..256.
- *   inv_freq   : host, double [rotary_dim / 2], finite.
+ *   inv_freq   : host, double [rotary_dim / 2], at most 1024 in magnitude.
  *   pair_axis  : host, u8 [rotary_dim / 2], each below n_axes; NULL: all 0.
  */
 #define KVARN_PAIRS_HALVES 0

@@ -32,6 +32,23 @@ int heads_ok(int Hq, int Hkv, int D) {
 constexpr int kMostTiles = (1 << 24) - 1;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// f / 2 pi in units of 2^-64 of a turn, whole turns dropped, to the last of them (|f| <= kMostFreq): f = m 2^e with
+// an integer m of 53 bits, times the first 128 bits of 1 / 2 pi.
+constexpr double kMostFreq = 1024.0;
+uint64_t turns(double f) {
+  constexpr uint64_t kHi = 0x28be60db9391054aULL, kLo = 0x7f09d5f47d4d3770ULL;
+  if (f == 0.0) return 0;
+  int e;
+  const uint64_t m = (uint64_t)ldexp(frexp(fabs(f), &e), 53);
+  e -= 53;
+  typedef unsigned __int128 u128;
+  const u128 low = (u128)m * kLo;
+  const u128 high = (u128)m * kHi + (uint64_t)(low >> 64);  // m / 2 pi, in units of 2^-64
+  // high 2^e is f / 2 pi in units of 2^-64; e <= 11 - 53
+  const uint64_t t = e <= -128 ? 0 : (uint64_t)(high >> -e);
+  return f < 0 ? 0 - t : t;
+}
+
 // Rows of `width` elements, `stride` apart, `n` of them.
 struct Rows {
   const char* p;
@@ -103,11 +120,11 @@ int kvarn_write_rows4(const void* k_new, int64_t k_stride, const void* v_new, in
                       uint8_t* tiles, int64_t tiles_bytes, const int64_t* tile_table, const int32_t* lens,
                       const int32_t* counts, int B, int T, int Hkv, int head_dim, int max_tiles,
                       const kvarn_layout4_t* layout, unsigned launch_flags, kvarn_stream_t stream) {
-  const kvarn::Rows4Args a{k_new, v_new, nullptr, nullptr, tiles, tile_table, lens, counts, k_stride, v_stride,
-                           tiles_bytes, io_type, B, T, Hkv, head_dim, max_tiles, launch_flags,
-                           kvarn::device_error_word()};
+  kvarn::Rows4Args a{k_new, v_new, nullptr, nullptr, tiles, tile_table, lens, counts, k_stride, v_stride,
+                     tiles_bytes, io_type, B, T, Hkv, head_dim, max_tiles, launch_flags, nullptr};
   const int rc = rows4_check(a, k_new, v_new, layout);
   if (rc != KVARN_OK || B == 0 || T == 0) return rc;
+  a.err = kvarn::device_error_word();
   return from_cuda(kvarn::launch_write4(a, (cudaStream_t)stream));
 }
 
@@ -115,15 +132,15 @@ int kvarn_read_rows4(const uint8_t* tiles, int64_t tiles_bytes, const int64_t* t
                      const int32_t* counts, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride, int io_type,
                      int B, int T, int Hkv, int head_dim, int max_tiles, const kvarn_layout4_t* layout,
                      unsigned launch_flags, kvarn_stream_t stream) {
-  const kvarn::Rows4Args a{nullptr, nullptr, k_out, v_out, const_cast<uint8_t*>(tiles), tile_table, first, counts,
-                           k_stride, v_stride, tiles_bytes, io_type, B, T, Hkv, head_dim, max_tiles, launch_flags,
-                           kvarn::device_error_word()};
+  kvarn::Rows4Args a{nullptr, nullptr, k_out, v_out, const_cast<uint8_t*>(tiles), tile_table, first, counts,
+                     k_stride, v_stride, tiles_bytes, io_type, B, T, Hkv, head_dim, max_tiles, launch_flags, nullptr};
   const int rc = rows4_check(a, k_out, v_out, layout);
   if (rc != KVARN_OK || B == 0 || T == 0) return rc;
   const int64_t rows = (int64_t)B * T, size = io_size(io_type), width = (int64_t)Hkv * head_dim * size;
   if (share(Rows{static_cast<const char*>(k_out), k_stride * size, width, rows},
             Rows{static_cast<const char*>(v_out), v_stride * size, width, rows}))
     return KVARN_ERR_BAD_ARG;
+  a.err = kvarn::device_error_word();
   return from_cuda(kvarn::launch_read4(a, (cudaStream_t)stream));
 }
 
@@ -220,16 +237,14 @@ int kvarn_rotary(int rotary_dim, int pairing, const double* inv_freq, const uint
     return KVARN_ERR_BAD_ARG;
   const int pairs = rotary_dim / 2;
   for (int i = 0; i < pairs; ++i)
-    if (!isfinite(inv_freq[i]) || (pair_axis && pair_axis[i] >= n_axes)) return KVARN_ERR_BAD_ARG;
+    if (!(fabs(inv_freq[i]) <= kMostFreq) || (pair_axis && pair_axis[i] >= n_axes)) return KVARN_ERR_BAD_ARG;
   memset(out, 0, sizeof(*out));
   out->version = KVARN_ROTARY_VERSION;
   out->rotary_dim = rotary_dim;
   out->pairing = pairing;
   out->n_axes = n_axes;
   for (int i = 0; i < pairs; ++i) {
-    double x = inv_freq[i] / 6.283185307179586476925286766559;
-    x -= floor(x);
-    out->turn[i] = x < 1.0 ? (uint64_t)(x * 18446744073709551616.0) : 0;
+    out->turn[i] = turns(inv_freq[i]);
     out->axis[i] = pair_axis ? pair_axis[i] : 0;
   }
   return KVARN_OK;

@@ -707,8 +707,11 @@ def _rows_of(t, name, dims, io_dtype=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     width = shape[-2] * shape[-1]
+    if t.is_contiguous() or t.numel() == 0:
+        return width
+    stride = t.stride()
     if (shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1]):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
     # (the stride of an axis of one element says nothing)
@@ -716,10 +719,8 @@ def _rows_of(t, name, dims, io_dtype=None, device=None):
     for n, s in zip(shape[-3::-1], stride[-3::-1]):
         if n != 1:
             if row is None:
-                if s % span:
-                    raise ValueError(f"the rows of {name} must be a constant stride apart")
-                row = s // span
-            elif s != row * span:
+                row = s // span if s % span == 0 else -1
+            if s != row * span:
                 raise ValueError(f"the rows of {name} must be a constant stride apart")
         span *= n
     return width if row is None else row
