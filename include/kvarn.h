@@ -763,7 +763,8 @@ int kvarn_read_rows4(const uint8_t* tiles, int64_t tiles_bytes, const int64_t* t
  *   mass_in, mass_out : as in kvarn_decode_attention8: mass_out[b][h][i] = mass_in[b][h][i]
  *                  plus the softmax weights that the heads of the group give to the
  *                  tokens of tile i.
- * At most 8 query heads per KV head (KVARN_ERR_UNSUPPORTED), 2^24 - 1 tiles of a head.
+ * At most 8 query heads per KV head (KVARN_ERR_UNSUPPORTED), 2^24 - 1 tiles of a head, 2^31 - 1
+ * entries of tile_table (KVARN_ERR_BAD_ARG).
  * A sequence of no tokens gets zeros. What is not written yet behind lens[b] in the last tile is
  * read but has no effect, whatever its bits. tile_table entries that are misaligned or
  * outside the pool make that head's output and masses NaN and set KVARN_DEVERR_RECORD. A NaN

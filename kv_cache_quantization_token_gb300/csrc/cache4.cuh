@@ -26,20 +26,19 @@ struct Run4 {
 // lie side by side.
 __device__ __forceinline__ int vscale_place(int t) { return 8 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1); }
 
-// Four codes + 8 (each 0..15) as a unit, and back.
-__device__ __forceinline__ uint32_t pack_unit(uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
-  return u0 << 6 | u1 << 10 | u2 << 2 | (u3 & 3u) << 14 | u3 >> 2;
-}
-
 // Two units of one register (low and high half) under scales s = (of the low unit, of the high
 // unit) as four pairs of fp16 values: x[j] = (channel j of the low unit, channel j of the high
 // unit). A code + 8 at bits 6..9 beside 0x4C00 is the fp16 number 16 + (code + 8), and
 // (24 + code) s - 24 s is code s: both products of the one multiply-add are exact (s has 8 bits, 24 s
-// has 10, code s 11) and so is its result. t = -24 s.
-__device__ __forceinline__ void unit_values(uint32_t w, __half2 s, __half2 t, uint32_t (&x)[4]) {
-  constexpr uint32_t kMask = 0x03C003C0u, kBase = 0x4C004C00u;
-  const uint32_t u[4] = {(w & kMask) | kBase, ((w >> 4) & kMask) | kBase, ((w << 4) & kMask) | kBase,
-                         (__byte_perm(w, 0u, 0x2301) & kMask) | kBase};
+// has 10, code s 11) and so is its result. t = -24 s; base is kUnitBase, better known at run time only (a kernel
+// argument): mask and base are one instruction then, while two constants take an instruction each (11 of
+// 15 operations of a word are integer ones with constants, 7 of 11 without: decode of four 64k sequences, head_dim
+// 128, executes a fifth less).
+constexpr uint32_t kUnitBase = 0x4C004C00u;
+__device__ __forceinline__ void unit_values(uint32_t w, __half2 s, __half2 t, uint32_t base, uint32_t (&x)[4]) {
+  constexpr uint32_t kMask = 0x03C003C0u;
+  const uint32_t u[4] = {(w & kMask) | base, ((w >> 4) & kMask) | base, ((w << 4) & kMask) | base,
+                         (__byte_perm(w, 0u, 0x2301) & kMask) | base};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u[j]), s, t);
@@ -122,9 +121,8 @@ cudaError_t launch_write4(const Rows4Args& a, cudaStream_t st);
 cudaError_t launch_read4(const Rows4Args& a, cudaStream_t st);
 
 struct Decode4Plan {
-  int span;    // consecutive tiles of an item (one CTA)
-  int items;   // ceil(max_tiles / span)
-  size_t off_acc;  // workspace: (m, l) per (row, item) at 0, then the accumulators, then (m, l) per
+  int ctas;        // of the split kernel
+  size_t off_acc;  // workspace: (m, l) of each piece's rows at 0, then their accumulators, then (m, l) per
   size_t off_tile; // (sequence, KV head, tile, run, head of the group)
   size_t ws_bytes;
 };

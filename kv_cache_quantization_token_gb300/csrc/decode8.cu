@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(256) merge8_kernel(const Split8Args s, int mas
   if ((int)blockIdx.x >= a.Hq) {
     const int kvh = ((int)blockIdx.x - a.Hq) / mass_blocks, run = ((int)blockIdx.x - a.Hq) % mass_blocks;
     const int64_t at = ((int64_t)b * a.Hkv + kvh) * a.max_tiles;
-    join_masses<1>(s.ml + ((int64_t)b * a.Hq + kvh * a.G) * s.items, s.items, s.tile_ml + at * 8, a.G, run,
+    join_masses<1>(s.ml + ((int64_t)b * a.Hq + kvh * a.G) * s.items, s.items, s.items, s.tile_ml + at * 8, a.G, run,
                    min(a.n_tiles[b], a.max_tiles), a.max_tiles, a.mass_in ? a.mass_in + at : nullptr, a.mass_out + at);
     return;
   }

@@ -7,8 +7,8 @@
 
 namespace kvarn {
 
-// The items of one row: ml[items], acc[items][D]; the result goes to out as row `row`.
-template <int D>
+// The items of one row: ml and acc [D] of item i lie at i * STRIDE; the result goes to out as row `row`.
+template <int D, int STRIDE = 1>
 __device__ __forceinline__ void join_items(const float2* ml, const float* acc, int items, void* out, int io, int64_t row) {
   __shared__ __align__(16) float4 part_s[256];
   __shared__ float2 part_ml[16];
@@ -25,8 +25,8 @@ __device__ __forceinline__ void join_items(const float2* ml, const float* acc, i
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = i0 + k * PARTS;
-      v[k] = i < items ? ml[i] : make_float2(-INFINITY, 0.f);
-      x[k] = i < items ? *reinterpret_cast<const float4*>(acc + (int64_t)i * D + 4 * col)
+      v[k] = i < items ? ml[(int64_t)i * STRIDE] : make_float2(-INFINITY, 0.f);
+      x[k] = i < items ? *reinterpret_cast<const float4*>(acc + (int64_t)i * STRIDE * D + 4 * col)
                        : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float m = M;
@@ -70,20 +70,20 @@ __device__ __forceinline__ void join_items(const float2* ml, const float* acc, i
   }
 }
 
-// Weights of 256 tiles (from 256 * block on) of one KV head: ml[G][items] of its query heads, tile_ml [tiles][PARTS][8]
-// (maximum, sum) of each tile's parts and heads; n tiles hold tokens, the others keep mass_in.
-template <int PARTS>
-__device__ __forceinline__ void join_masses(const float2* ml, int items, const float2* tile_ml, int G, int block, int n,
+// Weights of 256 tiles (from 256 * block on) of one KV head: ml of item i of its query head g at g * head + i * STRIDE,
+// tile_ml [tiles][PARTS][8] (maximum, sum) of each tile's parts and heads; n tiles hold tokens, the others keep mass_in.
+template <int PARTS, int STRIDE = 1>
+__device__ __forceinline__ void join_masses(const float2* ml, int64_t head, int items, const float2* tile_ml, int G, int block, int n,
                                             int max_tiles, const float* mass_in, float* mass_out) {
   __shared__ float2 stat[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp < G) {  // (maximum, sum) of query head `warp` of the group
-    const float2* row = ml + (int64_t)warp * items;
+    const float2* row = ml + warp * head;
     float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < items; i += 32) M = fmaxf(M, row[i].x);
+    for (int i = lane; i < items; i += 32) M = fmaxf(M, row[(int64_t)i * STRIDE].x);
     for (int m = 16; m; m >>= 1) M = fmaxf(M, shfl_xor(M, m));
     for (int i = lane; i < items; i += 32)
-      if (row[i].y != 0.f) L += fast_ex2(row[i].x - M) * row[i].y;
+      if (const float2 v = row[(int64_t)i * STRIDE]; v.y != 0.f) L += fast_ex2(v.x - M) * v.y;
     for (int m = 16; m; m >>= 1) L += shfl_xor(L, m);
     if (lane == 0) stat[warp] = make_float2(M, 1.f / L);
   }

@@ -148,8 +148,9 @@ static int decode4_check(int B, int Hq, int Hkv, int D, int max_tiles) {
   const int rc = heads_ok(Hq, Hkv, D);
   if (rc != KVARN_OK) return rc;
   if (B < 0 || max_tiles < 0 || B > 65535 || max_tiles > kMostTiles) return KVARN_ERR_BAD_ARG;
-  // the merge grid's first dimension stays in range
+  // the merge grid's first dimension and the count of all tiles stay in range
   if ((int64_t)Hkv * ((max_tiles + 255) / 256) + Hq > 0x7fffffff) return KVARN_ERR_BAD_ARG;
+  if (max_tiles > 0 && (int64_t)B * Hkv > 0x7fffffff / max_tiles) return KVARN_ERR_BAD_ARG;
   return KVARN_OK;
 }
 

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) image4_kernel(const Att8Args s) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t v[4];  // (channel e, channel e + 4)
-      unit_values(i ? w.y : w.x, sc, tc, v);
+      unit_values(i ? w.y : w.x, sc, tc, kUnitBase, v);
       h[4 * i] = __byte_perm(v[0], v[1], 0x5410);
       h[4 * i + 1] = __byte_perm(v[2], v[3], 0x5410);
       h[4 * i + 2] = __byte_perm(v[0], v[1], 0x7632);
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(256) image4_kernel(const Att8Args s) {
       const int t = t0 + 2 * i;
       if (t + 1 >= seen) sw = t < seen ? sw & 0xFFFFu : 0u;
       uint32_t v[4];
-      unit_values(w, as_half2(sw), minus24(as_half2(sw)), v);
+      unit_values(w, as_half2(sw), minus24(as_half2(sw)), kUnitBase, v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[e][i] = v[e];
     }
@@ -127,14 +127,11 @@ bool few_rows(int C, int G, int Hkv, int n_tiles) {
 
 // At least what every call of at most C positions over at most n_tiles tiles needs, whichever kernels serve it.
 size_t prefill4_ws_bytes(int C, int n_tiles, int Hq, int Hkv, int D) {
-  const int64_t n = n_tiles, heads = few_heads(Hkv), sms = sm_count();
+  const int64_t heads = few_heads(Hkv), sms = sm_count();
   const int64_t groups = row_groups(C, Hq / Hkv), work = (groups < kFewGroups ? groups : kFewGroups) * Hkv;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  // Decode kernels: 8 work' rows of items' entries for a call's own work' <= work; items' is at most n' / 32 +
-  // slots / work' + 1 (make_plan), and where few_rows holds work' n' <= kFewWork + 5 heads n'.
-  const int64_t slots = 6 * sms;  // resident CTAs, at most six per SM
-  const int64_t most = work * n < kFewWork + 5 * heads * n ? work * n : kFewWork + 5 * heads * n;
-  const int64_t entries = 8 * (most / 32 + 1 + slots + 2 * work);
+  // Decode kernels: eight rows for each of a call's pieces, at most a CTA's share each and one more per segment.
+  const int64_t entries = 8 * (4 * sms + work);  // (four CTAs per SM at most)
   const size_t few = up((size_t)entries * sizeof(float2)) + up((size_t)entries * D * sizeof(float));
   if (groups * Hkv <= 5 * heads) return few;  // (few_rows holds for every smaller call)
   // Images: those of this call, and the results of key shares, of which there are only as many as fill the SMs

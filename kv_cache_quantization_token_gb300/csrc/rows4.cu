@@ -25,23 +25,38 @@ __device__ __forceinline__ float least_scale(float amax) {
   return fmaxf(s, kStep);
 }
 
-// x / s to the nearest integer, ties to even, plus 8. inv ~ 1 / s finds it but next to a border; there
-// x - n s is exact (s has 8 bits, and next to (n + 1/2) s a difference of half of s needs no more bits than x),
-// and its comparison with s / 2 decides.
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
-  const float n = rintf(x * inv), r = fmaf(-n, s, x), a = fabsf(r), half = 0.5f * s;
-  const int i = (int)n;
-  const bool move = a > half || (a == half && (i & 1));
-  return (uint32_t)(i + 8 + (move ? (r > 0.f ? 1 : -1) : 0));
-}
-
-// Two units of eight channels.
+// Two units of eight channels: x / s to the nearest integer, ties to even, plus 8. The sum of x / s (with an approximate
+// 1 / s) and 1.5 * 2^23 + 8 holds the nearest integer in its low bits. It can be wrong next to a border, where
+// x - n s is exact (s has 8 bits, and a difference of about s / 2 needs no more bits than x) and not below s / 2; ties
+// of 16-bit rows are such a case in one warp of five, other rows hardly ever.
 __device__ __forceinline__ uint32_t units_of(const float (&x)[8], float s) {
-  const float inv = 1.0f / s;
+  constexpr float kRound = 12582920.f;
+  const float inv = __fdividef(1.f, s), half = 0.5f * s;
+  const float2 inv2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
   uint32_t u[8];
+  float r[8], most = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) u[e] = code_of(x[e], s, inv);
-  return pack_unit(u[0], u[1], u[2], u[3]) | pack_unit(u[4], u[5], u[6], u[7]) << 16;
+  for (int e = 0; e < 8; e += 2) {
+    const float2 x2 = make_float2(x[e], x[e + 1]);
+    const float2 t = __ffma2_rn(x2, inv2, make_float2(kRound, kRound));
+    const float2 n = __fadd2_rn(t, make_float2(-kRound, -kRound));
+    const float2 d = __ffma2_rn(n, s2, x2);
+    u[e] = __float_as_uint(t.x);
+    u[e + 1] = __float_as_uint(t.y);
+    r[e] = d.x;
+    r[e + 1] = d.y;
+    most = fmaxf(most, fmaxf(fabsf(d.x), fabsf(d.y)));
+  }
+  if (most >= half) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (fabsf(r[e]) > half || (fabsf(r[e]) == half && (u[e] & 1))) u[e] += r[e] > 0.f ? 1 : -1;
+  }
+  // (the bits above a code's four are constant: of 1.5 * 2^23 none among the low 16)
+  auto unit = [](const uint32_t* c) {
+    return (c[0] & 15u) << 6 | (c[1] & 15u) << 10 | (c[2] & 15u) << 2 | (c[3] & 3u) << 14 | (c[3] & 15u) >> 2;
+  };
+  return unit(u) | unit(u + 4) << 16;
 }
 
 __device__ __forceinline__ unsigned group_max(unsigned m) {  // over the four threads of 32 channels
@@ -162,7 +177,7 @@ __global__ void __launch_bounds__(256) read4_kernel(const Rows4Args a) {
     const __half2 s2 = __half2half2(s);
     uint32_t x[4];
     float y[8];
-    unit_values(w, s2, minus24(s2), x);
+    unit_values(w, s2, minus24(s2), kUnitBase, x);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = __half22float2(as_half2(x[j]));

@@ -418,7 +418,7 @@ def test_decode_launch_modes_and_graphs_are_bit_identical():
 def test_calls_run_on_the_stream_that_they_are_given():
     c = Cache4(36, [300], 2, 64)
     q = _query(11, (1, 4, 64), "f32")
-    want = c.decode(q)
+    want, want_pre = c.decode(q), c.prefill(q, 299)
     side, late = torch.cuda.Stream(), torch.zeros_like(q)
     row = _query(12, (1, 5, 2, 64), "f32")
     back = torch.zeros(2, 1, 5, 2, 64, device=DEV)
@@ -435,7 +435,7 @@ def test_calls_run_on_the_stream_that_they_are_given():
         turned, _ = kvarn.norm_rotate(late, None, None, None, hadamard=True, stream=side)
         assert bool((late == 0).all())
     side.synchronize()
-    assert torch.equal(out, want) and torch.equal(pre, want)
+    assert torch.equal(out, want) and torch.equal(pre, want_pre)
     assert torch.equal(back[0], back[1]) and bool((back != 0).any())
     assert torch.equal(turned, kvarn.norm_rotate(q, None, None, None, hadamard=True)[0])
 
@@ -620,8 +620,11 @@ def test_prefill_around_the_change_of_kernels(C, G, io):
 
 def test_prefill_of_one_position_agrees_with_decode_and_replays():
     c = Cache4(68, [777], 2, 128)
-    q = _query(9, (1, 8, 128), "f32")
-    assert torch.equal(c.prefill(q, 776), c.decode(q))
+    for Hq in (8, 12):  # (the same products, but for the order of the parts up to four heads to a group)
+        q = _query(9, (1, Hq, 128), "f32")
+        pre, dec = c.prefill(q, 776), c.decode(q)
+        _check_prefill(c, q, 776, pre)
+        assert torch.equal(pre, dec) if Hq == 12 else torch.allclose(pre, dec, rtol=0, atol=2.0 ** -15 * float(dec.abs().max()))
     for C in (4, 300):  # a workspace for more serves both
         q = _query(10, (C, 8, 128), "bf16")
         want = c.prefill(q, 777 - C)
