@@ -735,7 +735,8 @@ int kvarn_layout4(int head_dim, kvarn_layout4_t* out);
  * A token at or past 128 max_tiles, or of a negative lens[b], is not written and sets
  * KVARN_DEVERR_WINDOW; one whose record is not inside the pool is not written and sets
  * KVARN_DEVERR_RECORD. Bytes of other tokens stay as they are. Sequences must not share
- * the records that are written. launch_flags: 0 or KVARN_LAUNCH_PDL.
+ * the records that are written. At most 65535 sequences, and T * Hkv below 2^31 - 256
+ * (KVARN_ERR_BAD_ARG). launch_flags: 0 or KVARN_LAUNCH_PDL.
  */
 int kvarn_write_rows4(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
                       int io_type, uint8_t* tiles, int64_t tiles_bytes, const int64_t* tile_table,

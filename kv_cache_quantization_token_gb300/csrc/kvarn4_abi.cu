@@ -102,8 +102,8 @@ static int rows4_check(const kvarn::Rows4Args& a, const void* k, const void* v, 
     return KVARN_ERR_BAD_ARG;
   if (a.B == 0 || a.T == 0) return KVARN_OK;
   const int64_t rows = (int64_t)a.B * a.T, width = (int64_t)a.Hkv * a.D;
-  // the grid's first dimension stays in range
-  if (rows > INT64_MAX / 2 / a.Hkv || rows * a.Hkv > 0x7fffffffLL * (256 / (a.D / 8))) return KVARN_ERR_BAD_ARG;
+  // a sequence's (row, head) pairs are counted in 32 bits
+  if (a.B > 65535 || (int64_t)a.T * a.Hkv > 0x7fffff00) return KVARN_ERR_BAD_ARG;
   if (!k || !v || !a.first) return KVARN_ERR_NULL;
   if (a.max_tiles > 0 && (!a.tiles || !a.tile_table)) return KVARN_ERR_NULL;
   for (const int64_t s : {a.k_stride, a.v_stride}) {

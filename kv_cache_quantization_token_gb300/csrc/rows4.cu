@@ -2,9 +2,8 @@
 //
 //   s = least number of 8 significant bits >= max|x| / 7 over 32 channels,  code = x / s to nearest even
 //
-// A thread holds eight channels of K and the same eight of V of one row (token, head), so four threads meet for a
-// scale and the D / 8 threads of a row for whether it is poison; a warp reads 512 consecutive bytes of 16-bit
-// rows. Both roundings are decided exactly, without a division: 7 s and code * s are exact in fp32, so that a
+// A thread holds sixteen channels of K and the same sixteen of V of one row (token, head), so two threads meet for a
+// scale and the D / 16 threads of a row for whether it is poison. Both roundings are decided exactly, without a division: 7 s and code * s are exact in fp32, so that a
 // candidate is put right by comparisons (below).
 #include "cache4.cuh"
 
@@ -25,120 +24,138 @@ __device__ __forceinline__ float least_scale(float amax) {
   return fmaxf(s, kStep);
 }
 
-// Two units of eight channels: x / s to the nearest integer, ties to even, plus 8. The sum of x / s (with an approximate
-// 1 / s) and 1.5 * 2^23 + 8 holds the nearest integer in its low bits. It can be wrong next to a border, where
-// x - n s is exact (s has 8 bits, and a difference of about s / 2 needs no more bits than x) and not below s / 2; ties
-// of 16-bit rows are such a case in one warp of five, other rows hardly ever.
+// Two units of eight channels: x / s to the nearest integer, ties to even, plus 8. Added to 1.5 * 2^23 + 8, a
+// quotient leaves the nearest integer in the low bits. What of it is next to a border is decided
+//   of a 16-bit x by the correctly rounded quotient (an approximate one put right by its exact remainder): x and the
+//     borders have too few bits for another number to round onto one;
+//   of an fp32 x by x - n s, which is exact there (s has 8 bits, and a difference of about s / 2 needs no more
+//     bits than x) and not below s / 2: hardly ever.
+template <int IO>
 __device__ __forceinline__ uint32_t units_of(const float (&x)[8], float s) {
   constexpr float kRound = 12582920.f;
   const float inv = __fdividef(1.f, s), half = 0.5f * s;
-  const float2 inv2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
+  const float2 inv2 = make_float2(inv, inv), s2 = make_float2(-s, -s), round2 = make_float2(kRound, kRound);
   uint32_t u[8];
-  float r[8], most = 0.f;
+  [[maybe_unused]] float r[8], most = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
     const float2 x2 = make_float2(x[e], x[e + 1]);
-    const float2 t = __ffma2_rn(x2, inv2, make_float2(kRound, kRound));
-    const float2 n = __fadd2_rn(t, make_float2(-kRound, -kRound));
-    const float2 d = __ffma2_rn(n, s2, x2);
+    float2 t;
+    if constexpr (IO == KVARN_IO_F32) {
+      t = __ffma2_rn(x2, inv2, round2);
+      const float2 n = __fadd2_rn(t, make_float2(-kRound, -kRound)), d = __ffma2_rn(n, s2, x2);
+      r[e] = d.x;
+      r[e + 1] = d.y;
+      most = fmaxf(most, fmaxf(fabsf(d.x), fabsf(d.y)));
+    } else {
+      const float2 q = __fmul2_rn(x2, inv2), d = __ffma2_rn(q, s2, x2);
+      t = __fadd2_rn(__ffma2_rn(d, inv2, q), round2);
+    }
     u[e] = __float_as_uint(t.x);
     u[e + 1] = __float_as_uint(t.y);
-    r[e] = d.x;
-    r[e + 1] = d.y;
-    most = fmaxf(most, fmaxf(fabsf(d.x), fabsf(d.y)));
   }
-  if (most >= half) {
+  if (IO == KVARN_IO_F32 && most >= half) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (fabsf(r[e]) > half || (fabsf(r[e]) == half && (u[e] & 1))) u[e] += r[e] > 0.f ? 1 : -1;
   }
-  // (the bits above a code's four are constant: of 1.5 * 2^23 none among the low 16)
-  auto unit = [](const uint32_t* c) {
-    return (c[0] & 15u) << 6 | (c[1] & 15u) << 10 | (c[2] & 15u) << 2 | (c[3] & 3u) << 14 | (c[3] & 15u) >> 2;
-  };
-  return unit(u) | unit(u + 4) << 16;
+  // The bits of 1.5 * 2^23 lie above bit 21, and above bit 31 once shifted by ten: of the sums only the low halves count.
+  auto unit = [](const uint32_t* c) { return (((((c[1] << 4) + c[0]) << 4) + c[2]) << 2) + (c[3] << 14) + ((c[3] >> 2) & 3u); };
+  return __byte_perm(unit(u), unit(u + 4), 0x5410);
 }
 
-__device__ __forceinline__ unsigned group_max(unsigned m) {  // over the four threads of 32 channels
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+// Bits of the largest magnitude of a thread's eight elements, as an fp32 number's (a NaN's are above an infinity's,
+// those above every number's).
+template <int IO>
+__device__ __forceinline__ unsigned largest(const Eight<IO>& v) {
+  if constexpr (IO == KVARN_IO_F32) {
+    unsigned m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, (&v.w[e / 4].x)[e % 4] & 0x7FFFFFFFu);
+    return m;
+  } else {  // two 16-bit patterns at a time
+    const uint4 w = v.w[0];
+    constexpr unsigned kAbs = 0x7FFF7FFFu;
+    const unsigned m2 = __vmaxu2(__vmaxu2(w.x & kAbs, w.y & kAbs), __vmaxu2(w.z & kAbs, w.w & kAbs));
+    const unsigned m = max(m2 & 0xFFFFu, m2 >> 16);
+    return IO == KVARN_IO_F16 ? __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) : m << 16;
+  }
 }
 
-// Row (b, t) and head of a thread group, and where its token lies.
+__device__ __forceinline__ unsigned group_max(unsigned m) {  // over the two threads of 32 channels
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+}
+
+// Row t and head h of sequence blockIdx.y, of the threads that hold it, and where its token lies.
 struct Place {
   int64_t row;      // b * T + t
   int h;
   bool there;       // a row to be moved
   bool inside;      // its token has a place in the table
-  int64_t off;      // of the run's bytes in the pool, if its record lies inside
-  bool good;
+  bool good;        // the table's record lies inside the pool
   int r;            // token in the run
+  int64_t off;      // of the run's bytes
 };
 
 template <int D>
-__device__ __forceinline__ Place place_of(const Rows4Args& a, int64_t pair) {
+__device__ __forceinline__ Place place_of(const Rows4Args& a) {
+  constexpr int L = D / 16;
   Place p{};
-  const int64_t rows = (int64_t)a.B * a.T;
-  p.row = pair / a.Hkv;
-  p.h = (int)(pair - p.row * a.Hkv);
-  p.there = p.row < rows;
+  const int b = blockIdx.y, i = blockIdx.x * (256 / L) + threadIdx.x / L, t = i / a.Hkv;
+  p.h = i - t * a.Hkv;
+  p.row = (int64_t)b * a.T + t;
+  p.there = t < a.T && !(a.counts && t >= a.counts[b]);
   if (!p.there) return p;
-  const int b = (int)(p.row / a.T), t = (int)(p.row - (int64_t)b * a.T);
-  if (a.counts && t >= a.counts[b]) p.there = false;
   const int first = a.first[b];
-  const int64_t tok = (int64_t)first + t, tile = tok / kTile;
-  p.inside = first >= 0 && tile < a.max_tiles;
-  if (!p.there || !p.inside) return p;
+  const int64_t tok = (int64_t)first + t;
+  p.inside = first >= 0 && tok < (int64_t)kTile * a.max_tiles;
+  if (!p.inside) return p;
+  const int tile = (int)(tok / kTile);
   const int64_t off = a.tile_table[((int64_t)b * a.Hkv + p.h) * a.max_tiles + tile];
   p.good = !(off & 15) && off >= 0 && off <= a.tiles_bytes - Run4<D>::kRecord;
-  p.r = (int)(tok % kRun);
-  p.off = off + (tok % kTile) / kRun * Run4<D>::kBytes;
+  p.r = (int)tok % kRun;
+  p.off = off + (int)tok % kTile / kRun * Run4<D>::kBytes;
   return p;
 }
 
 template <int D, int IO>
 __global__ void __launch_bounds__(256) write4_kernel(const Rows4Args a) {
   using R = Run4<D>;
-  constexpr int L = D / 8;  // threads of a row
+  constexpr int L = D / 16;  // threads of a row
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31, c = 8 * (threadIdx.x % L);
-  const int64_t pair = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const Place p = place_of<D>(a, pair);
+  const int lane = threadIdx.x & 31, c = 16 * (threadIdx.x % L);
+  const Place p = place_of<D>(a);
   if (p.there && c == 0) {
     if (!p.inside) report(a.err, KVARN_DEVERR_WINDOW);
     else if (!p.good) report(a.err, KVARN_DEVERR_RECORD);
   }
   const bool move = p.there && p.inside && p.good;
-  float k[8] = {}, v[8] = {};
+  Eight<IO> ek[2]{}, ev[2]{};
   if (move) {
-    Eight<IO> ek, ev;
-    ek.load(a.k, p.row * a.k_stride + (int64_t)p.h * D + c);
-    ev.load(a.v, p.row * a.v_stride + (int64_t)p.h * D + c);
-    ek.get(k);
-    ev.get(v);
+    const int64_t at_k = p.row * a.k_stride + (int64_t)p.h * D + c, at_v = p.row * a.v_stride + (int64_t)p.h * D + c;
+    ek[0].load(a.k, at_k);
+    ek[1].load(a.k, at_k + 8);
+    ev[0].load(a.v, at_v);
+    ev[1].load(a.v, at_v + 8);
   }
-  unsigned mk = 0, mv = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    mk = max(mk, __float_as_uint(k[e]) & 0x7FFFFFFFu);
-    mv = max(mv, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-  }
-  mk = group_max(mk);
-  mv = group_max(mv);
-  // (a NaN's bits are above an infinity's, those above every number's)
+  const unsigned mk = group_max(max(largest<IO>(ek[0]), largest<IO>(ek[1])));
+  const unsigned mv = group_max(max(largest<IO>(ev[0]), largest<IO>(ev[1])));
   const unsigned bad = __ballot_sync(0xffffffffu, max(mk, mv) > __float_as_uint(KVARN_MAX4));
-  const bool poison = L == 32 ? bad != 0 : ((bad >> (lane & ~(L - 1))) & ((1u << (L & 31)) - 1u)) != 0;
+  const bool poison = ((bad >> (lane & ~(L - 1))) & ((1u << L) - 1u)) != 0;
   if (!move) return;
-  const float sk = least_scale(__uint_as_float(poison ? 0u : mk)), sv = least_scale(__uint_as_float(poison ? 0u : mv));
-  if (poison) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
-  }
+  const float sk = least_scale(__uint_as_float(mk)), sv = least_scale(__uint_as_float(mv));
+  auto units = [&](const Eight<IO> (&e)[2], float s) {
+    float x[8], y[8];
+    e[0].get(x);
+    e[1].get(y);
+    const uint2 w = make_uint2(units_of<IO>(x, s), units_of<IO>(y, s));
+    return poison ? make_uint2(0x22222222u, 0x22222222u) : w;  // (a poisoned token's codes are 0)
+  };
   uint8_t* run = a.tiles + p.off;
-  *reinterpret_cast<uint32_t*>(run + R::kKCodes + (c / R::kWide) * (kRun * R::kWide / 2) + p.r * (R::kWide / 2) +
-                               c % R::kWide / 2) = units_of(k, sk);
-  *reinterpret_cast<uint32_t*>(run + R::kVCodes + (c / 32) * (kRun * 16) + p.r * 16 + c % 32 / 2) = units_of(v, sv);
+  *reinterpret_cast<uint2*>(run + R::kKCodes + (c / R::kWide) * (kRun * R::kWide / 2) + p.r * (R::kWide / 2) +
+                            c % R::kWide / 2) = units(ek, sk);
+  *reinterpret_cast<uint2*>(run + R::kVCodes + (c / 32) * (kRun * 16) + p.r * 16 + c % 32 / 2) = units(ev, sv);
   if (c % 32 == 0) {
     reinterpret_cast<__half*>(run + R::kKScale)[p.r * R::kGroups + c / 32] =
         poison ? __ushort_as_half(0x7FFF) : __float2half_rn(sk);
@@ -148,69 +165,94 @@ __global__ void __launch_bounds__(256) write4_kernel(const Rows4Args a) {
 }
 
 template <int D, int IO>
-__global__ void __launch_bounds__(256) read4_kernel(const Rows4Args a) {
+__global__ void __launch_bounds__(256) read4_kernel(const Rows4Args a, uint32_t base) {
   using R = Run4<D>;
-  constexpr int L = D / 8;
+  constexpr int L = D / 16;
   pdl_trigger();
   pdl_wait();
-  const int c = 8 * (threadIdx.x % L);
-  const int64_t pair = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const Place p = place_of<D>(a, pair);
+  // eight channels of the row's lower half and eight of its upper, so that a warp's stores cover whole sectors
+  const int c0 = 8 * (threadIdx.x % L);
+  const Place p = place_of<D>(a);
   if (!p.there) return;
-  if (c == 0) {
+  if (c0 == 0) {
     if (!p.inside) report(a.err, KVARN_DEVERR_WINDOW);
     else if (!p.good) report(a.err, KVARN_DEVERR_RECORD);
   }
   if (!p.inside) return;
-  uint32_t wk = 0, wv = 0;
-  __half sk = __ushort_as_half(0x7FFF), sv = __ushort_as_half(0);
-  if (p.good) {
-    const uint8_t* run = a.tiles + p.off;
-    wk = *reinterpret_cast<const uint32_t*>(run + R::kKCodes + (c / R::kWide) * (kRun * R::kWide / 2) +
-                                            p.r * (R::kWide / 2) + c % R::kWide / 2);
-    wv = *reinterpret_cast<const uint32_t*>(run + R::kVCodes + (c / 32) * (kRun * 16) + p.r * 16 + c % 32 / 2);
-    sk = reinterpret_cast<const __half*>(run + R::kKScale)[p.r * R::kGroups + c / 32];
-    sv = reinterpret_cast<const __half*>(run + R::kVScale)[c / 32 * kRun + vscale_place(p.r)];
-  }
-  if (__hisnan(sk)) sv = sk;
-  auto out = [&](uint32_t w, __half s, void* dst, int64_t stride) {
-    const __half2 s2 = __half2half2(s);
-    uint32_t x[4];
-    float y[8];
-    unit_values(w, s2, minus24(s2), kUnitBase, x);
+  uint32_t wk[2] = {}, wv[2] = {};
+  __half sk[2], sv[2];
+  const uint8_t* run = a.tiles + (p.good ? p.off : 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(as_half2(x[j]));
-      y[j] = f.x;
-      y[4 + j] = f.y;
+  for (int i = 0; i < 2; ++i) {
+    const int c = c0 + i * (D / 2);
+    sk[i] = __ushort_as_half(0x7FFF);
+    sv[i] = __ushort_as_half(0);
+    if (p.good) {
+      wk[i] = *reinterpret_cast<const uint32_t*>(run + R::kKCodes + (c / R::kWide) * (kRun * R::kWide / 2) +
+                                                 p.r * (R::kWide / 2) + c % R::kWide / 2);
+      wv[i] = *reinterpret_cast<const uint32_t*>(run + R::kVCodes + (c / 32) * (kRun * 16) + p.r * 16 + c % 32 / 2);
+      sk[i] = reinterpret_cast<const __half*>(run + R::kKScale)[p.r * R::kGroups + c / 32];
+      sv[i] = reinterpret_cast<const __half*>(run + R::kVScale)[c / 32 * kRun + vscale_place(p.r)];
     }
-    Eight<IO>::store(dst, p.row * stride + (int64_t)p.h * D + c, y);
+  }
+  auto out = [&](uint32_t w, __half s, void* dst, int64_t at) {
+    const __half2 s2 = __half2half2(s);
+    uint32_t x[4];  // (channel j, channel j + 4)
+    unit_values(w, s2, minus24(s2), base, x);
+    if constexpr (IO == KVARN_IO_F16) {  // the values as they are
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dst) + at) =
+          make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                     __byte_perm(x[2], x[3], 0x7632));
+    } else {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(as_half2(x[j]));
+        y[j] = f.x;
+        y[4 + j] = f.y;
+      }
+      Eight<IO>::store(dst, at, y);
+    }
   };
-  out(wk, sk, a.k_out, a.k_stride);
-  out(wv, sv, a.v_out, a.v_stride);
+  const int64_t at_k = p.row * a.k_stride + (int64_t)p.h * D + c0, at_v = p.row * a.v_stride + (int64_t)p.h * D + c0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    out(wk[i], sk[i], a.k_out, at_k + i * (D / 2));
+    out(wv[i], __hisnan(sk[i]) ? sk[i] : sv[i], a.v_out, at_v + i * (D / 2));
+  }
 }
 
 template <int D>
-cudaError_t launch_rows(bool write, const Rows4Args& a, cudaStream_t st) {
-  const int64_t pairs = (int64_t)a.B * a.T * a.Hkv, per = 256 / (D / 8);
-  LaunchCfg L(dim3((unsigned)((pairs + per - 1) / per)), dim3(256), 0, st, a.flags);
+LaunchCfg rows_grid(const Rows4Args& a, cudaStream_t st) {
+  const int64_t pairs = (int64_t)a.T * a.Hkv, per = 256 / (D / 16);
+  return LaunchCfg(dim3((unsigned)((pairs + per - 1) / per), a.B), dim3(256), 0, st, a.flags);
+}
+template <int D>
+cudaError_t write_rows(const Rows4Args& a, cudaStream_t st) {
+  const LaunchCfg& L = rows_grid<D>(a, st);
   switch (a.io) {
-    case KVARN_IO_F32: return cudaLaunchKernelEx(&L.cfg, write ? write4_kernel<D, 0> : read4_kernel<D, 0>, a);
-    case KVARN_IO_F16: return cudaLaunchKernelEx(&L.cfg, write ? write4_kernel<D, 1> : read4_kernel<D, 1>, a);
-    default: return cudaLaunchKernelEx(&L.cfg, write ? write4_kernel<D, 2> : read4_kernel<D, 2>, a);
+    case KVARN_IO_F32: return cudaLaunchKernelEx(&L.cfg, write4_kernel<D, 0>, a);
+    case KVARN_IO_F16: return cudaLaunchKernelEx(&L.cfg, write4_kernel<D, 1>, a);
+    default: return cudaLaunchKernelEx(&L.cfg, write4_kernel<D, 2>, a);
   }
 }
-cudaError_t launch_any(bool write, const Rows4Args& a, cudaStream_t st) {
-  switch (a.D) {
-    case 64: return launch_rows<64>(write, a, st);
-    case 128: return launch_rows<128>(write, a, st);
-    default: return launch_rows<256>(write, a, st);
+template <int D>
+cudaError_t read_rows(const Rows4Args& a, cudaStream_t st) {
+  const LaunchCfg& L = rows_grid<D>(a, st);
+  switch (a.io) {
+    case KVARN_IO_F32: return cudaLaunchKernelEx(&L.cfg, read4_kernel<D, 0>, a, kUnitBase);
+    case KVARN_IO_F16: return cudaLaunchKernelEx(&L.cfg, read4_kernel<D, 1>, a, kUnitBase);
+    default: return cudaLaunchKernelEx(&L.cfg, read4_kernel<D, 2>, a, kUnitBase);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_write4(const Rows4Args& a, cudaStream_t st) { return launch_any(true, a, st); }
-cudaError_t launch_read4(const Rows4Args& a, cudaStream_t st) { return launch_any(false, a, st); }
+cudaError_t launch_write4(const Rows4Args& a, cudaStream_t st) {
+  return a.D == 64 ? write_rows<64>(a, st) : a.D == 128 ? write_rows<128>(a, st) : write_rows<256>(a, st);
+}
+cudaError_t launch_read4(const Rows4Args& a, cudaStream_t st) {
+  return a.D == 64 ? read_rows<64>(a, st) : a.D == 128 ? read_rows<128>(a, st) : read_rows<256>(a, st);
+}
 
 }  // namespace kvarn

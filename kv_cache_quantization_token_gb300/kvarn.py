@@ -693,16 +693,30 @@ def layout4(head_dim: int) -> Layout4:
     return L
 
 
-def _rows_of(t, name, dims, io_dtype=None, device=None):
-    """A CUDA tensor [..., heads, D] of `dims` dimensions whose heads lie side by side and whose
+def _rows_of(t, name, dims, dtype=None, device=None):
+    """A CUDA tensor [..., heads, D] of `dims` (3 or 4) dimensions whose heads lie side by side and whose
     rows (all but the last two axes) are a constant stride apart, as a slice of a packed
     product's result: its stride in elements."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and (t.dtype in IO_TYPES if dtype is None else t.dtype is dtype)
+            and (device is None or t.get_device() == device)):
+        shape = t.shape  # (the usual strides, without more ado)
+        if len(shape) == dims:
+            if t.is_contiguous():
+                return shape[-1] * shape[-2]
+            if dims == 3:
+                row, head, one = t.stride()
+                if one == 1 and head == shape[2] and shape[0] > 1:
+                    return row
+    return _rows_checked(t, name, dims, dtype, device)
+
+
+def _rows_checked(t, name, dims, dtype, device):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in IO_TYPES:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if io_dtype is not None and t.dtype is not io_dtype:
-        raise TypeError(f"{name} must be {io_dtype}, got {t.dtype}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.dim() != dims:
@@ -726,10 +740,10 @@ def _rows_of(t, name, dims, io_dtype=None, device=None):
     return width if row is None else row
 
 
-def _cache4(tiles, tile_table, lay, D, device, what):
-    _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64))
+def _layout4_for(lay, D, what):
     if lay.head_dim != D:
         raise ValueError(f"{what}: the layout is for head_dim {lay.head_dim}, the rows have {D}")
+    return ctypes.byref(lay)
 
 
 def _counts4(counts, B, device):
@@ -741,40 +755,38 @@ def _counts4(counts, B, device):
     return counts.data_ptr()
 
 
+def _rows4(k, v, tiles, tile_table, first, lay, counts, names, what):
+    """What write_rows4 and read_rows4 check alike: the strides, sizes and pointers of a call."""
+    k_stride = _rows_of(k, names[0], 4)
+    device = k.get_device()
+    v_stride = _rows_of(v, names[1], 4, k.dtype, device)
+    _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64), (names[2], first, torch.int32))
+    shape, table = k.shape, tile_table.shape
+    B, T, Hkv, D = shape
+    if v.shape != shape or len(table) != 3 or table[0] != B or table[1] != Hkv or first.numel() != B:
+        raise ValueError(f"{what}: inconsistent shapes")
+    return device, k_stride, v_stride, _counts4(counts, B, device), (IO_TYPES[k.dtype], B, T, Hkv, D, table[2],
+                                                                     _layout4_for(lay, D, what))
+
+
 def write_rows4(k_new, v_new, tiles, tile_table, lens, lay: Layout4, counts=None, stream=None, flags=0):
     """Quantises rows into the 4-bit cache: k_new, v_new fp32, fp16 or bf16 [B][T][Hkv][D] (slices of
     a packed tensor will do: heads contiguous, rows a constant stride apart); row (b, t), t <
     counts[b] (int32 [B]; None: T), becomes token lens[b] + t (int32 [B], not changed) of sequence b.
     tiles uint8 record pool; tile_table int64 [B][Hkv][max_tiles]."""
-    k_stride = _rows_of(k_new, "k_new", 4)
-    device = k_new.get_device()
-    v_stride = _rows_of(v_new, "v_new", 4, k_new.dtype, device)
-    B, T, Hkv, D = k_new.shape
-    _cache4(tiles, tile_table, lay, D, device, "write_rows4")
-    _fit(device, ("lens", lens, torch.int32))
-    if (v_new.shape != k_new.shape or tile_table.dim() != 3 or tuple(tile_table.shape[:2]) != (B, Hkv)
-            or lens.numel() != B):
-        raise ValueError("write_rows4: inconsistent shapes")
-    _call(device, "kvarn_write_rows4", stream, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
-          IO_TYPES[k_new.dtype], tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(), lens.data_ptr(),
-          _counts4(counts, B, device), B, T, Hkv, D, tile_table.shape[2], ctypes.byref(lay), int(flags))
+    device, ks, vs, n, (io, *sizes) = _rows4(k_new, v_new, tiles, tile_table, lens, lay, counts,
+                                             ("k_new", "v_new", "lens"), "write_rows4")
+    _call(device, "kvarn_write_rows4", stream, k_new.data_ptr(), ks, v_new.data_ptr(), vs, io, tiles.data_ptr(),
+          tiles.numel(), tile_table.data_ptr(), lens.data_ptr(), n, *sizes, int(flags))
 
 
 def read_rows4(tiles, tile_table, first, k_out, v_out, lay: Layout4, counts=None, stream=None, flags=0):
     """Cached tokens first[b] + t (int32 [B]) of the 4-bit cache as rows (b, t), t < counts[b], of k_out
     and v_out (as k_new and v_new of write_rows4); other rows stay as they are."""
-    k_stride = _rows_of(k_out, "k_out", 4)
-    device = k_out.get_device()
-    v_stride = _rows_of(v_out, "v_out", 4, k_out.dtype, device)
-    B, T, Hkv, D = k_out.shape
-    _cache4(tiles, tile_table, lay, D, device, "read_rows4")
-    _fit(device, ("first", first, torch.int32))
-    if (v_out.shape != k_out.shape or tile_table.dim() != 3 or tuple(tile_table.shape[:2]) != (B, Hkv)
-            or first.numel() != B):
-        raise ValueError("read_rows4: inconsistent shapes")
-    _call(device, "kvarn_read_rows4", stream, tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(),
-          first.data_ptr(), _counts4(counts, B, device), k_out.data_ptr(), k_stride, v_out.data_ptr(), v_stride,
-          IO_TYPES[k_out.dtype], B, T, Hkv, D, tile_table.shape[2], ctypes.byref(lay), int(flags))
+    device, ks, vs, n, sizes = _rows4(k_out, v_out, tiles, tile_table, first, lay, counts,
+                                      ("k_out", "v_out", "first"), "read_rows4")
+    _call(device, "kvarn_read_rows4", stream, tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(), first.data_ptr(),
+          n, k_out.data_ptr(), ks, v_out.data_ptr(), vs, *sizes, int(flags))
 
 
 def decode4_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles) -> int:
@@ -790,18 +802,18 @@ def decode_attention4(q, tiles, tile_table, lens, lay: Layout4, softmax_scale=No
     and out fp32, fp16 or bf16 [B][Hq][D]; tile_table int64 [B][Hkv][max_tiles]. mass_in and mass_out
     as decode_attention8's."""
     io, device = _io(q, "q")
-    if q.dim() != 3 or not isinstance(tile_table, torch.Tensor) or tile_table.dim() != 3:
+    _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64), ("lens", lens, torch.int32))
+    shape, table = q.shape, tile_table.shape
+    if len(shape) != 3 or len(table) != 3:
         raise ValueError("decode_attention4: q [B][Hq][D], tile_table [B][Hkv][max_tiles] expected")
-    B, Hq, D = q.shape
-    _cache4(tiles, tile_table, lay, D, device, "decode_attention4")
-    _fit(device, ("lens", lens, torch.int32))
-    Bt, Hkv, max_tiles = tile_table.shape
+    B, Hq, D = shape
+    Bt, Hkv, max_tiles = table
     if Bt != B or lens.numel() != B:
         raise ValueError("decode_attention4: inconsistent shapes")
     for name, m in (("mass_in", mass_in), ("mass_out", mass_out)):
         if m is not None:
             _fit(device, (name, m, torch.float32))
-            if m.shape != tile_table.shape:
+            if m.shape != table:
                 raise ValueError(f"{name} must have tile_table's shape")
     if ws is None:
         with torch.cuda.device(device):  # the split of the work depends on the device
@@ -810,11 +822,11 @@ def decode_attention4(q, tiles, tile_table, lens, lay: Layout4, softmax_scale=No
     if out is None:
         out = _result(q, stream)
     _fit(device, ("ws", ws, torch.uint8), ("out", out, q.dtype))
-    if out.shape != q.shape:
+    if out.shape != shape:
         raise ValueError("out must have q's shape")
     _call(device, "kvarn_decode_attention4", stream, q.data_ptr(), io, tiles.data_ptr(), tiles.numel(),
           tile_table.data_ptr(), lens.data_ptr(), B, Hq, Hkv, D, max_tiles,
-          D ** -0.5 if softmax_scale is None else float(softmax_scale), ctypes.byref(lay),
+          D ** -0.5 if softmax_scale is None else float(softmax_scale), _layout4_for(lay, D, "decode_attention4"),
           None if mass_in is None else mass_in.data_ptr(),
           None if mass_out is None else mass_out.data_ptr(), ws.data_ptr(), ws.numel(), out.data_ptr(),
           int(flags))
@@ -835,11 +847,12 @@ def prefill_attention4(q_chunk, pos0, tiles, tile_table, lay: Layout4, softmax_s
     workspace of prefill4_workspace_bytes() for C positions and ceil((pos0 + C) / 128) tiles, or more of
     either (allocated here when None)."""
     io, device = _io(q_chunk, "q_chunk")
-    if q_chunk.dim() != 3 or not isinstance(tile_table, torch.Tensor) or tile_table.dim() != 2:
+    _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64))
+    shape, table = q_chunk.shape, tile_table.shape
+    if len(shape) != 3 or len(table) != 2:
         raise ValueError("prefill_attention4: q_chunk [C][Hq][D], tile_table [Hkv][stride] expected")
-    C, Hq, D = q_chunk.shape
-    Hkv, stride = tile_table.shape
-    _cache4(tiles, tile_table, lay, D, device, "prefill_attention4")
+    C, Hq, D = shape
+    Hkv, stride = table
     if out is None:
         out = _result(q_chunk, stream)
     if ws is None:
@@ -848,12 +861,12 @@ def prefill_attention4(q_chunk, pos0, tiles, tile_table, lay: Layout4, softmax_s
             need = prefill4_workspace_bytes(C, n_tiles, Hq, Hkv, D)
         ws = _scratch(need, q_chunk.device, stream)
     _fit(device, ("ws", ws, torch.uint8), ("out", out, q_chunk.dtype))
-    if out.shape != q_chunk.shape:
+    if out.shape != shape:
         raise ValueError("out must have q_chunk's shape")
-    _call(device, "kvarn_prefill_attention4", stream, q_chunk.data_ptr(), io, C, int(pos0),
-          tiles.data_ptr(), tiles.numel(), tile_table.data_ptr(), stride, Hq, Hkv, D,
-          D ** -0.5 if softmax_scale is None else float(softmax_scale), ctypes.byref(lay),
-          ws.data_ptr(), ws.numel(), out.data_ptr())
+    _call(device, "kvarn_prefill_attention4", stream, q_chunk.data_ptr(), io, C, int(pos0), tiles.data_ptr(),
+          tiles.numel(), tile_table.data_ptr(), stride, Hq, Hkv, D,
+          D ** -0.5 if softmax_scale is None else float(softmax_scale),
+          _layout4_for(lay, D, "prefill_attention4"), ws.data_ptr(), ws.numel(), out.data_ptr())
     return out
 
 
@@ -896,43 +909,49 @@ def norm_rotate(q, k, positions, rot, q_weight=None, k_weight=None, eps=None, ha
     tokens a constant stride apart; positions int64 [T], or [axes][T]. Outputs are new tensors, or q_out and
     k_out (q and k themselves: in place). Returns (q_out, k_out)."""
     q_stride = _rows_of(q, "q", 3)
-    device = q.get_device()
-    T, Hq, D = q.shape
-    Hkv, k_stride, ko_stride = 0, 0, 0
-    if k is not None:
-        k_stride = _rows_of(k, "k", 3, q.dtype, device)
-        if k.shape[0] != T or k.shape[2] != D:
-            raise ValueError("norm_rotate: inconsistent shapes")
-        Hkv = k.shape[1]
-    elif k_out is not None or k_weight is not None:
-        raise ValueError("norm_rotate: k_out or k_weight without k")
+    device, dtype, shape = q.get_device(), q.dtype, q.shape
+    T, Hq, D = shape
     if q_out is None:
         q_out = _result_rows(q, stream)
-    qo_stride = _rows_of(q_out, "q_out", 3, q.dtype, device)
+    qo_stride = _rows_of(q_out, "q_out", 3, dtype, device)
+    good = q_out.shape == shape
     if k is not None:
+        k_stride = _rows_of(k, "k", 3, dtype, device)
         if k_out is None:
             k_out = _result_rows(k, stream)
-        ko_stride = _rows_of(k_out, "k_out", 3, q.dtype, device)
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise ValueError("norm_rotate: outputs must have the inputs' shapes")
+        ko_stride = _rows_of(k_out, "k_out", 3, dtype, device)
+        shape = k.shape
+        Hkv, k_in, k_to = shape[1], k.data_ptr(), k_out.data_ptr()
+        good = good and shape[0] == T and shape[2] == D and k_out.shape == shape
+    else:
+        if k_out is not None or k_weight is not None:
+            raise ValueError("norm_rotate: k_out or k_weight without k")
+        Hkv, k_stride, ko_stride, k_in, k_to = 0, 0, 0, None, None
+    if not good:
+        raise ValueError("norm_rotate: inconsistent shapes")
+    at = plan = None
     if rot is not None:
         _fit(device, ("positions", positions, torch.int64))
-        if positions.numel() != rot.n_axes * T or positions.shape[-1:] != (T,):
+        axes = positions.shape
+        if axes[-1:] != (T,) or positions.numel() != rot.n_axes * T:
             raise ValueError("positions must be [T], or [axes][T] with the plan's axes")
+        at, plan = positions.data_ptr(), ctypes.byref(rot)
+    weights = []
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _fit(device, (name, w, q.dtype))
-            if w.numel() != D:
-                raise ValueError(f"{name} must have head_dim elements")
-            if eps is None:
-                raise ValueError(f"{name} without a norm (eps)")
+        if w is None:
+            weights.append(None)
+            continue
+        _fit(device, (name, w, dtype))
+        if w.numel() != D:
+            raise ValueError(f"{name} must have head_dim elements")
+        if eps is None:
+            raise ValueError(f"{name} without a norm (eps)")
+        weights.append(w.data_ptr())
     if eps is not None and not eps >= 0:
         raise ValueError("eps must not be negative")
-    _call(device, "kvarn_norm_rotate", stream, q.data_ptr(), q_stride, None if k is None else k.data_ptr(), k_stride,
-          IO_TYPES[q.dtype], T, Hq, Hkv, D, None if q_weight is None else q_weight.data_ptr(),
-          None if k_weight is None else k_weight.data_ptr(), -1.0 if eps is None else float(eps),
-          None if rot is None else positions.data_ptr(), None if rot is None else ctypes.byref(rot), int(bool(hadamard)),
-          q_out.data_ptr(), qo_stride, None if k is None else k_out.data_ptr(), ko_stride, int(flags))
+    _call(device, "kvarn_norm_rotate", stream, q.data_ptr(), q_stride, k_in, k_stride, IO_TYPES[dtype], T, Hq, Hkv, D,
+          weights[0], weights[1], -1.0 if eps is None else float(eps), at, plan, int(bool(hadamard)), q_out.data_ptr(),
+          qo_stride, k_to, ko_stride, int(flags))
     return q_out, k_out
 
 
