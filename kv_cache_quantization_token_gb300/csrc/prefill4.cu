@@ -17,110 +17,139 @@
 namespace kvarn {
 namespace {
 
+// Registers x[0..3] of four neighbouring lanes, transposed: lane q of the four gets x[q] of each, in their order.
+__device__ __forceinline__ void transpose_quad(uint32_t (&x)[4]) {
+  const int q = threadIdx.x & 3;
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1)  // lanes m apart exchange the registers whose index has the other bit
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & m)) {
+        const bool high = q & m;
+        const uint32_t give = high ? x[i] : x[i | m], got = __shfl_xor_sync(0xffffffffu, give, m);
+        x[i] = high ? got : x[i];
+        x[i | m] = high ? x[i | m] : got;
+      }
+}
+
+// What bounds it: writing 64 KB for the 18 that it reads (15,500 tokens, 8 heads of 128: 63 MB to L2).
 template <int D>
-__global__ void __launch_bounds__(256) image4_kernel(const Att8Args s) {
+__global__ void __launch_bounds__(256) image4_kernel(const Att8Args s, uint32_t base) {
   using P = PC8<D, 1>;
   using R = Run4<D>;
   constexpr int KB = P::KB, SUB = P::SUB;
-  __shared__ __align__(16) unsigned char rec[R::kRecord];
+  // a tile's V codes and V scales
+  constexpr int V_RUN = R::kKScale - R::kVCodes, S_RUN = R::kBytes - R::kVScale;
+  __shared__ __align__(16) unsigned char codes[kRuns * V_RUN], scales[kRuns * S_RUN];
   const Prefill8Args& a = s.a;
-  const int kvh = blockIdx.y, tid = threadIdx.x, j = blockIdx.x;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = blockIdx.x;
   pdl_trigger();
   uint8_t* head = a.ws + (int64_t)kvh * s.p.head_imgs * P::IMG;
   const int64_t off = a.tile_table[(int64_t)kvh * a.table_stride + j];
   const bool good = !(off & 15) && off >= 0 && off <= a.tiles_bytes - R::kRecord;
   if (!good && tid == 0) report(a.err, KVARN_DEVERR_RECORD);
-  for (int i = tid; i < R::kRecord / 16; i += 256) {
-    // (no record: codes and V scales of zero, K scales of NaN)
-    const int at = 16 * i % R::kBytes;
-    const uint32_t none = at >= R::kKScale && at < R::kVScale ? 0x7FFF7FFFu : 0u;
-    *reinterpret_cast<uint4*>(rec + 16 * i) =
-        good ? *reinterpret_cast<const uint4*>(a.tiles + off + 16 * i) : make_uint4(none, none, none, none);
+  const unsigned char* rec = a.tiles + (good ? off : 0);  // (read only if good; without a record: zero codes, K scales of NaN)
+  // K, straight from memory: 16 channels of a token, in order; all loads of V under way before them
+  constexpr int NV = kRuns * V_RUN / 16 / 256, NK = kTile * D / 16 / 256;
+  uint4 v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = 16 * (tid + 256 * i);
+    v[i] = good ? *reinterpret_cast<const uint4*>(rec + at / V_RUN * R::kBytes + R::kVCodes + at % V_RUN) : make_uint4(0, 0, 0, 0);
   }
-  __syncthreads();
-  // 16 channels of a token of K, in order
-#pragma unroll 2
-  for (int x = tid; x < kTile * D / 16; x += 256) {
-    const int piece = x & 3, t = (x >> 2) % kTile, c = 64 * (x / (4 * kTile)) + 16 * piece;
+  uint4 vs = make_uint4(0, 0, 0, 0);
+  const int at_s = 16 * tid;
+  if (good && at_s < kRuns * S_RUN)
+    vs = *reinterpret_cast<const uint4*>(rec + at_s / S_RUN * R::kBytes + R::kVScale + at_s % S_RUN);
+  uint2 kw[NK];
+  __half ks[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int x = tid + 256 * i, t = (x >> 2) % kTile, c = 64 * (x / (4 * kTile)) + 16 * (x & 3);
     const unsigned char* run = rec + t / kRun * R::kBytes;
-    const int r = t % kRun;
-    const uint2 w = *reinterpret_cast<const uint2*>(run + R::kKCodes + (c / R::kWide) * (kRun * R::kWide / 2) +
-                                                    r * (R::kWide / 2) + c % R::kWide / 2);
-    const __half2 sc = __half2half2(reinterpret_cast<const __half*>(run + R::kKScale)[r * R::kGroups + c / 32]);
-    const __half2 tc = minus24(sc);
+    kw[i] = good ? *reinterpret_cast<const uint2*>(run + R::kKCodes + (c / R::kWide) * (kRun * R::kWide / 2) +
+                                                   t % kRun * (R::kWide / 2) + c % R::kWide / 2)
+                 : make_uint2(0, 0);
+    ks[i] = good ? reinterpret_cast<const __half*>(run + R::kKScale)[t % kRun * R::kGroups + c / 32] : __ushort_as_half(0x7FFF);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(codes + 16 * (tid + 256 * i)) = v[i];
+  if (at_s < kRuns * S_RUN) *reinterpret_cast<uint4*>(scales + at_s) = vs;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int x = tid + 256 * i, t = (x >> 2) % kTile, c = 64 * (x / (4 * kTile)) + 16 * (x & 3);
+    const __half2 sc = __half2half2(ks[i]), tc = minus24(sc);
     uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t v[4];  // (channel e, channel e + 4)
-      unit_values(i ? w.y : w.x, sc, tc, kUnitBase, v);
-      h[4 * i] = __byte_perm(v[0], v[1], 0x5410);
-      h[4 * i + 1] = __byte_perm(v[2], v[3], 0x5410);
-      h[4 * i + 2] = __byte_perm(v[0], v[1], 0x7632);
-      h[4 * i + 3] = __byte_perm(v[2], v[3], 0x7632);
-    }
-    const int row = t % KB;
-    if (row & 1) {  // the two 16-byte chunks share a 32-byte sector, swapped in odd rows of the swizzle
+    for (int k = 0; k < 2; ++k) {
+      uint32_t y[4];  // (channel e, channel e + 4)
+      unit_values(k ? kw[i].y : kw[i].x, sc, tc, base, y);
+      // (the two 16-byte chunks share a 32-byte sector, swapped in odd rows of the swizzle)
+      const int to = (k ^ (t & 1)) ? 4 : 0;
+      const uint32_t z[4] = {__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                             __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t y = h[e];
-        h[e] = h[4 + e];
-        h[4 + e] = y;
+        if (k == 0) h[e] = h[4 + e] = z[e];
+        else if (to) h[4 + e] = z[e];
+        else h[e] = z[e];
       }
     }
-    st_sector(head + image_index(j * SUB + t / KB) * P::IMG + (sw_off(row, c, KB) & ~31u), h);
+    st_sector(head + image_index(j * SUB + t / KB) * P::IMG + (sw_off(t % KB, c, KB) & ~31u), h);
   }
-  // 16 tokens of four channels of V
+  __syncthreads();
+  // V, 32 tokens x 32 channels to a warp: read transposed, a lane has two tokens of each eight for four channels; the four
+  // lanes of a quad then hold eight tokens of a channel, a chunk of its row, each
   const int64_t seen = a.pos0 + a.C - (int64_t)kTile * j;  // tokens of the tile that any row sees
-  for (int x = tid; x < D / 4 * (kTile / 16); x += 256) {
-    const int tb = x & 3, u = (x >> 2) % (D / 4), t0 = 64 * (x / D) + 16 * tb, c = 4 * u;
-    const unsigned char* run = rec + t0 / kRun * R::kBytes;
-    const int r = t0 % kRun;
-    uint32_t h[4][8];  // [channel][pair of tokens]
+  const int g = lane >> 2, q = lane & 3;
+  for (int x = warp; x < kRuns * (D / 32); x += 8) {
+    const int r = x / (D / 32), c = x % (D / 32);
+    uint32_t w[4], y[4][4];
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(smem_addr(codes + r * V_RUN + c * 512 + lane * 16))
+                 : "memory");
+    const uint4 sv = *reinterpret_cast<const uint4*>(scales + r * S_RUN + c * 64 + q * 16);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(run + R::kVCodes + (c / 32) * (kRun * 16) + (r + 2 * i) * 16) +
-                          c % 32 / 4;
-      const uint32_t w = (uint32_t)p[0] | (uint32_t)p[8] << 16;
-      uint32_t sw = *reinterpret_cast<const uint32_t*>(run + R::kVScale + (c / 32) * 64 + 2 * vscale_place(r + 2 * i));
-      const int t = t0 + 2 * i;
+    for (int m = 0; m < 4; ++m) {
+      const int t = kRun * r + 8 * m + 2 * q;
+      uint32_t sw = (&sv.x)[m];
       if (t + 1 >= seen) sw = t < seen ? sw & 0xFFFFu : 0u;
-      uint32_t v[4];
-      unit_values(w, as_half2(sw), minus24(as_half2(sw)), kUnitBase, v);
+      uint32_t z[4];
+      unit_values(w[m], as_half2(sw), minus24(as_half2(sw)), base, z);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e][i] = v[e];
+      for (int e = 0; e < 4; ++e) y[e][m] = z[e];
     }
-    uint8_t* img = head + (image_index(j * SUB + t0 / KB) + 2) * P::IMG;
+    uint8_t* img = head + (image_index(j * SUB + kRun * r / KB) + 2) * P::IMG;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int row = c + e;
-      if (row & 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t y = h[e][i];
-          h[e][i] = h[e][4 + i];
-          h[e][4 + i] = y;
-        }
-      }
-      st_sector(img + (sw_off(row, t0 % KB, D) & ~31u), h[e]);
+      transpose_quad(y[e]);
+      *reinterpret_cast<uint4*>(img + sw_off(32 * c + 4 * g + e, kRun * r % KB + 8 * q, D)) =
+          make_uint4(y[e][0], y[e][1], y[e][2], y[e][3]);
     }
   }
 }
 
 template <int D, int NP>
 cudaError_t launch_p4(const Att8Args& s, cudaStream_t st) {
-  image4_kernel<D><<<dim3(s.p.n_tsub / PC8<D, 1>::SUB, s.a.Hkv), 256, 0, st>>>(s);
+  image4_kernel<D><<<dim3(s.p.n_tsub / PC8<D, 1>::SUB, s.a.Hkv), 256, 0, st>>>(s, kUnitBase);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_attend<D, NP, false>(s, st);
 }
 
-// Chunks of few score rows per KV head go to the decode kernels, which need no images but go over the cache once
-// for every eight rows ("group").
-constexpr int64_t kFewGroups = 64, kFewWork = 1600;
+// Chunks of few score rows per KV head go to the decode kernels, which need no images but go over the cache once for
+// every eight rows ("group"): some 4 ns of all SMs per group and tile-head, where the images and their kernels take 6
+// groups' worth per tile-head, with fewer than 8 KV heads no less than with 8, and some 4 us more. At head_dim 128, 8 KV
+// heads, bf16 (us, decode kernels against images): 8 groups over 64 tiles 26 / 26, 12 33 / 28; 6 over 128 tiles 33 / 33, 8
+// 41 / 33; 2 KV heads, 24 groups over 128 tiles 33 / 34, 32 41 / 34; head_dim 64, 8 over 64 tiles 18 / 19, 256 40 / 39. Over
+// 774 sizes (1 to 8 KV heads, 1 to 48 groups, 4 to 128 tiles, both kinds of type) the choice costs 0.3% on the mean, 26%
+// at worst.
+constexpr int64_t kFewGroups = 64, kFewWork = 800;
 int64_t row_groups(int C, int G) { return ((int64_t)C * G + 7) / 8; }
-int64_t few_heads(int Hkv) { return Hkv > 6 ? Hkv : 6; }
+int64_t few_heads(int Hkv) { return Hkv > 8 ? Hkv : 8; }
 bool few_rows(int C, int G, int Hkv, int n_tiles) {
   const int64_t groups = row_groups(C, G);
-  return groups <= kFewGroups && (groups * Hkv - 5 * few_heads(Hkv)) * n_tiles <= kFewWork;
+  return groups <= kFewGroups && (groups * Hkv - 6 * few_heads(Hkv)) * n_tiles <= kFewWork;
 }
 
 }  // namespace
@@ -133,7 +162,7 @@ size_t prefill4_ws_bytes(int C, int n_tiles, int Hq, int Hkv, int D) {
   // Decode kernels: eight rows for each of a call's pieces, at most a CTA's share each and one more per segment.
   const int64_t entries = 8 * (4 * sms + work);  // (four CTAs per SM at most)
   const size_t few = up((size_t)entries * sizeof(float2)) + up((size_t)entries * D * sizeof(float));
-  if (groups * Hkv <= 5 * heads) return few;  // (few_rows holds for every smaller call)
+  if (groups * Hkv <= 6 * heads) return few;  // (few_rows holds for every smaller call)
   // Images: those of this call, and the results of key shares, of which there are only as many as fill the SMs
   // once (128 rows to a CTA), and O's emptied sums, of a CTA's rows each.
   const Plan8 p = plan8(C, n_tiles, 0, Hq, Hkv, D, true, false);
