@@ -11,6 +11,11 @@
 // An angle is position * frequency in units of 2^-64 of a turn: a 64-bit integer product drops whole turns
 // exactly, whatever the position, and costs three multiply-adds where an fp64 product and its reduction
 // would take GB300's slow fp64 units. The quarter turn nearest to it is taken off before it is rounded to fp32.
+//
+// What bounds it: instructions beside memory. 8,192 tokens of 32 + 8 heads of 128, bf16, packed (168 MB): 38.2 us, 4.4
+// TB/s (65% of the copy rate; the same kernel without norm and rotation 29). A CTA with the angles of several tokens in
+// shared memory took 47 to 58, with more than half of its instructions in addresses, starts and the exchange of partners;
+// sixteen channels to a thread instead of eight 38.2 instead of 41.
 #include "cache4.cuh"
 
 namespace kvarn {

@@ -3,8 +3,13 @@
 //   s = least number of 8 significant bits >= max|x| / 7 over 32 channels,  code = x / s to nearest even
 //
 // A thread holds sixteen channels of K and the same sixteen of V of one row (token, head), so two threads meet for a
-// scale and the D / 16 threads of a row for whether it is poison. Both roundings are decided exactly, without a division: 7 s and code * s are exact in fp32, so that a
-// candidate is put right by comparisons (below).
+// scale and the D / 16 threads of a row for whether it is poison. Both roundings are decided exactly, without a
+// division: 7 s and code * s are exact in fp32, so that a candidate is put right by comparisons (below).
+//
+// What bounds it: instructions and the latency of row, length and table one after another. 7,100 tokens of 8 heads of 128,
+// bf16 (37 MB in and out): writing 9.2 us, reading back 8.1, against 5.5 at the copy rate. Sixteen channels of K and of V
+// to a thread instead of eight brought writing from 13.7 to 9.3 (finding a row's place costs as much as coding eight
+// channels). Reading takes two runs of eight channels to a thread, so that a warp's stores cover whole sectors (9.8 -> 8.1).
 #include "cache4.cuh"
 
 namespace kvarn {
