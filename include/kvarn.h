@@ -788,7 +788,8 @@ int kvarn_decode_attention4(const void* q, int io_type, const uint8_t* tiles, in
  * k_j) v_j over the cached tokens j <= pos0 + i of one sequence, C positions. The chunk's own
  * rows have been written (kvarn_write_rows4), so the cache holds pos0 + C tokens at least.
  *   q_chunk, out : io_type [C][Hq][D], 16-byte aligned.
- *   tile_table   : int64 [Hkv][table_stride]; pos0 + C <= 128 table_stride.
+ *   tile_table   : int64 [Hkv][table_stride]; pos0 + C <= 128 table_stride. At most 2^24 - 1
+ *                  tiles of a head, 2^25 - 1 of all (KVARN_ERR_BAD_ARG).
  * A row that sees a poisoned token or a record outside the pool (KVARN_DEVERR_RECORD), or has
  * a NaN or an infinity in its query, is NaN; rows before it are not touched by it. With 16-bit types
  * chunks of many rows round the softmax weights to fp16, as kvarn_prefill_attention8 does.

@@ -30,6 +30,8 @@ int heads_ok(int Hq, int Hkv, int D) {
 
 // Token positions stay below 2^31.
 constexpr int kMostTiles = (1 << 24) - 1;
+// Tiles of all KV heads of a prefill: with up to 64 row groups to a head they are counted in 32 bits.
+constexpr int64_t kMostHeadTiles = (1 << 25) - 1;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // f / 2 pi in units of 2^-64 of a turn, whole turns dropped, to the last of them (|f| <= kMostFreq): f = m 2^e with
@@ -201,7 +203,7 @@ int kvarn_prefill4_workspace_bytes(int C, int n_tiles, int Hq, int Hkv, int head
   if (!bytes) return KVARN_ERR_NULL;
   const int rc = heads_ok(Hq, Hkv, head_dim);
   if (rc != KVARN_OK) return rc;
-  if (C < 0 || n_tiles < 0 || n_tiles > kMostTiles) return KVARN_ERR_BAD_ARG;
+  if (C < 0 || n_tiles < 0 || n_tiles > kMostTiles || (int64_t)Hkv * n_tiles > kMostHeadTiles) return KVARN_ERR_BAD_ARG;
   *bytes = kvarn::prefill4_ws_bytes(C, n_tiles, Hq, Hkv, head_dim);
   return KVARN_OK;
 }
@@ -221,6 +223,7 @@ int kvarn_prefill_attention4(const void* q_chunk, int io_type, int C, int64_t po
   if (C == 0) return KVARN_OK;
   if (!q_chunk || !out || !ws || !tiles || !tile_table) return KVARN_ERR_NULL;
   const int n_tiles = (int)((pos0 + C - 1) / KVARN_TILE_TOKENS + 1);
+  if ((int64_t)Hkv * n_tiles > kMostHeadTiles) return KVARN_ERR_BAD_ARG;
   if (ws_bytes < kvarn::prefill4_ws_bytes(C, n_tiles, Hq, Hkv, head_dim)) return KVARN_ERR_WORKSPACE;
   if (!aligned(q_chunk, 16) || !aligned(out, 16) || !aligned(tiles, 16) || !aligned(ws, 256) || !aligned(tile_table, 8))
     return KVARN_ERR_ALIGN;

@@ -97,6 +97,7 @@ def test_decode_refusals(lib):
     assert _decode(lib, Hq=72) == -3 and _decode(lib, D=96) == -3 and _decode(lib, D=64) == -3
     assert _decode(lib, wsb=256) == -5
     assert _decode(lib, B=0) == 0
+    assert _decode(lib, B=65535, Hq=8, mt=(1 << 12) + 1) == -4 and _decode(lib, B=128, mt=1 << 21) == -4  # 2^31 entries or more
     n, q = ctypes.c_size_t(), lib.kvarn_decode4_workspace_bytes
     assert q(1, 32, 8, 128, 8, None) == -1 and q(1, 32, 8, 96, 8, ctypes.byref(n)) == -3
     assert q(2, 32, 8, 128, 8, ctypes.byref(n)) == 0 and n.value % 256 == 0
@@ -126,6 +127,12 @@ def test_prefill_refusals(lib):
     assert _prefill(lib, Hq=72) == -3 and _prefill(lib, D=64) == -3 and _prefill(lib, D=100) == -3
     assert _prefill(lib, wsb=1 << 10) == -5
     assert _prefill(lib, C=0) == 0
+    # tiles of all heads are counted in 32 bits, with up to 64 groups of rows
+    many = dict(Hq=64, Hkv=64, C=1, stride=1 << 19, pos0=(1 << 26) - 1)
+    assert _prefill(lib, **many) == -4 and _prefill(lib, **{**many, "pos0": (1 << 26) - 129, "wsb": 256}) == -5
+    n = ctypes.c_size_t()
+    query = lib.kvarn_prefill4_workspace_bytes
+    assert query(1, 1 << 19, 64, 64, 128, ctypes.byref(n)) == -4 and query(1, (1 << 19) - 1, 64, 64, 128, ctypes.byref(n)) == 0
 
 
 def test_a_prefill_workspace_serves_smaller_chunks(lib):

@@ -300,6 +300,74 @@ def test_decode_of_long_sequences():
     assert bool((out[:3] == 0).all()) and bool((out[4:] == 0).all())
 
 
+def _shared(seed, D, H, lens, distinct=5):
+    """Ragged sequences whose tables name the same few tiles in any order: (pool's cache, table, lens, K and V rows by
+    (b, h))."""
+    c = Cache4(seed, [T * distinct], 1, D)
+    rng = np.random.default_rng(seed + 1)
+    tiles = max(-(-max(lens) // T), 1)
+    pick = rng.integers(0, distinct, (len(lens), H, tiles))
+    table = c.table[0, 0][torch.from_numpy(pick).to(DEV)].contiguous()
+
+    def rows_of(b, h, n):
+        return (x[0].reshape(distinct, T, D)[pick[b, h]].reshape(-1, D)[:n] for x in (c.k[0], c.v[0]))
+    return c, table, _dev(lens, torch.int32), rows_of
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D,G", [(64, 2), (64, 7), (128, 4), (128, 8), (256, 3), (256, 5)])
+def test_decode_of_ragged_batches(D, G, io):
+    """More tiles than CTAs: shares that begin and end inside sequences, that span several, and sequences of no
+    tokens between them; weights of all tiles."""
+    H = 3
+    rng = np.random.default_rng(D + G)
+    lens = [int(n) for n in rng.integers(0, 900, 60)]
+    lens[0] = lens[7] = lens[8] = lens[31] = lens[-1] = 0
+    lens[5], lens[20] = 6000, 128
+    c, table, ln, rows_of = _shared(D, D, H, lens)
+    q = _query(G, (len(lens), H * G, D), io)
+    m = torch.zeros(table.shape, device=DEV)
+    out = kvarn.decode_attention4(q, c.tiles, table, ln, c.lay, mass_out=m)
+    qn, mn = q.double().cpu().numpy(), m.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert bool((out[b] == 0).all()) and not mn[b].any()
+            continue
+        for h in range(H):
+            k, v = rows_of(b, h, n)
+            want, p, bound = attend(qn[b, h * G:(h + 1) * G], k, v, D ** -0.5, [n] * G, np.ones(n), 2.0 ** -39)
+            check(out[b, h * G:(h + 1) * G], want, bound, q.dtype)
+            w = np.zeros(table.shape[2] * T)
+            w[:n] = p.sum(0)
+            w = w.reshape(-1, T).sum(1)
+            assert (np.abs(mn[b, h] - w) <= 2.0 ** -12 * w + 1e-30).all()
+    assert torch.equal(out, kvarn.decode_attention4(q, c.tiles, table, ln, c.lay, flags=kvarn.LAUNCH_PDL))
+    # a batch of more sequences than threads: the same ones, apart by sequences of no tokens
+    far = torch.zeros(60 * 7, dtype=torch.int32, device=DEV)
+    far[::7] = ln
+    q7 = q.repeat_interleave(7, 0)
+    out7 = kvarn.decode_attention4(q7, c.tiles, table.repeat_interleave(7, 0), far, c.lay)
+    # (shares are cut elsewhere: the same but for the order of sums)
+    assert torch.allclose(out7[::7].float(), out.float(), rtol=2.0 ** -6 if io == "bf16" else 2.0 ** -14, atol=2.0 ** -9)
+    assert bool((out7.view(60, 7, -1)[:, 1:] == 0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill_of_few_rows_over_many_segments(D):
+    """A chunk on the decode kernels with more tiles than CTAs: shares that span row groups and heads."""
+    H, G, C, n = 8, 4, 31, 600
+    c, table, _, rows_of = _shared(D + 5, D, H, [n])
+    for io in ("f32", "bf16"):
+        q = _query(D, (C, H * G, D), io)
+        out = kvarn.prefill_attention4(q, n - C, c.tiles, table[0], c.lay)
+        for h in range(H):
+            k, v = rows_of(0, h, n)
+            qn = q[:, h * G:(h + 1) * G].double().cpu().numpy().reshape(C * G, D)
+            want, p, bound = attend(qn, k, v, D ** -0.5, np.repeat(n - C + 1 + np.arange(C), G), np.ones(n), 2.0 ** -33)
+            check(out[:, h * G:(h + 1) * G].reshape(C * G, D), want, bound, q.dtype, 0.0 if io == "f32" else 2.0 ** -11,
+                  p @ np.abs(v))
+
+
 @pytest.mark.parametrize("D,G", [(64, 3), (128, 8), (256, 4)])
 def test_decode_weights_accumulate(D, G):
     c = Cache4(20 + D, [450, 0, 128, 33], 2, D, max_tiles=6)
