@@ -649,9 +649,9 @@ int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t po
  * `recent`, and of those between the keep - sinks - recent with the largest
  * weights (of equal weights the lower index; NaN counts as infinite, -0 as 0). Every
  * KV head loses the same number of tiles, its own choice of them. Works on the
- * tile tables of both caches; the records themselves are not touched. The weights are
- * the caller's: kvarn_decode_attention8 adds up what decode gives to each tile, and no
- * other call reports any. Equal weights, such as zeros after a prompt alone, keep the
+ * tile tables of all caches; the records themselves are not touched. The weights are
+ * the caller's: kvarn_decode_attention8 and kvarn_decode_attention4 add up what decode gives to
+ * each tile, and no other call reports any. Equal weights, such as zeros after a prompt alone, keep the
  * oldest tiles.
  *   tile_table : int64 [B][Hkv][max_tiles]; tile_mass: fp32, the same shape.
  *   n_tiles    : int32 [B] (clamped to 0..max_tiles).
@@ -663,7 +663,9 @@ int kvarn_prefill_attention8(const void* q_chunk, int io_type, int C, int64_t po
  *                old order, then -1. Must not overlap the other arrays.
  *   keep       : >= 1, sinks and recent >= 0, sinks + recent <= keep.
  * One launch, deterministic, no workspace; can be captured. After it, tile i no longer
- * holds positions [128 i, 128 i + 128): see kvarn_prefill_attention8.
+ * holds positions [128 i, 128 i + 128): see kvarn_prefill_attention8. For the 4-bit cache
+ * n_tiles[b] is ceil(lens[b] / 128); with recent >= 1 the tile being written stays, and lens[b]
+ * falls by 128 for each tile that left.
  * launch_flags: 0 or KVARN_LAUNCH_PDL (other bits give KVARN_ERR_BAD_ARG).
  */
 int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const int32_t* n_tiles,

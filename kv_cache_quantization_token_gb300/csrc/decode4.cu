@@ -264,307 +264,307 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
   unsigned bad = 0;  // bit i: the run in slot i has no record
 #pragma unroll 1
   for (;;) {  // piece by piece
-  const int first = tile0, len = tokens4<CHUNK>(s, b);
-  const int nt = min(tiles4<CHUNK>(s, b) - first, end - now);
-  const int stop = first + nt;
-  const int64_t* table = a.tile_table + ((CHUNK ? 0 : (int64_t)b * a.Hkv) + kvh) * a.max_tiles + first;
-  // Runs of 32 tiles, one address per lane, NULL for one that does not lie in the pool.
-  auto address = [&](int j) -> const uint8_t* {
-    if (first + j >= stop) return nullptr;
-    const int64_t off = table[j];
-    return (off & 15) || off < 0 || off > a.tiles_bytes - R::kRecord ? nullptr : a.tiles + off + warp * RB;
-  };
-  const uint8_t* source = address(lane);
-  const int run0 = kTile * first + kRun * warp;  // first token of this warp
-  const int nr = min(nt, max((len - run0 + kTile - 1) / kTile, 0));  // runs of this warp that hold tokens
-  __syncwarp();
-  auto request = [&](int j, int sl) {
-    if (j >= nr) return;
-    const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(source), j & 31);
-    bad &= ~(1u << sl);
-    if (src == 0) bad |= 1u << sl;
-    if (lane == 0) {
-      if (src == 0) {
-        report(a.err, KVARN_DEVERR_RECORD);
-        mbar_arrive1(bar + sl);
-      } else {
-        mbar_arrive_tx(bar + sl, RB);
-        bulk_in(ring + sl * RB, reinterpret_cast<const uint8_t*>(src), RB, bar + sl);
-      }
-    }
-  };
-  auto next_slot = [&](int x) { return x + 1 == STG ? 0 : x + 1; };
-  for (int j = 0, x = sl; j < STG; ++j, x = next_slot(x)) request(j, x);
-
-  // B fragments of the query. Column g: part g % 2 of row g / 2, or (WIDE) row g, its parts in qb[0] and qb[1]. A
-  // product's channels are those that a word of K units gives to two registers.
-  uint32_t qb[NQ][BLK * WPB][4];
-  float c1[HL];             // of the rows whose scores this lane holds: HL q + 0 ..
-  [[maybe_unused]] int seen[HL];
-  {
-    const Row4 me = row4<CHUNK>(s, b, kvh, WIDE ? g : g >> 1);
-    float x[BLK * WPB][8];
-    float mx = 0.f;
-    auto load = [&](auto io) {  // (loads of a type that is known: under way together)
-      Eight<decltype(io)::value> e[BLK * WPB];
-#pragma unroll
-      for (int w = 0; w < BLK * WPB; ++w)
-        e[w].load(a.q, me.index * D + w / WPB * R::kWide + q * (R::kWide / 4) + 8 * (w % WPB));
-#pragma unroll
-      for (int w = 0; w < BLK * WPB; ++w) {
-        e[w].get(x[w]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!me.valid) x[w][i] = 0.f;
-          mx = fmaxf(mx, fabsf(x[w][i]));
+    const int first = tile0, len = tokens4<CHUNK>(s, b);
+    const int nt = min(tiles4<CHUNK>(s, b) - first, end - now);
+    const int stop = first + nt;
+    const int64_t* table = a.tile_table + ((CHUNK ? 0 : (int64_t)b * a.Hkv) + kvh) * a.max_tiles + first;
+    // Runs of 32 tiles, one address per lane, NULL for one that does not lie in the pool.
+    auto address = [&](int j) -> const uint8_t* {
+      if (first + j >= stop) return nullptr;
+      const int64_t off = table[j];
+      return (off & 15) || off < 0 || off > a.tiles_bytes - R::kRecord ? nullptr : a.tiles + off + warp * RB;
+    };
+    const uint8_t* source = address(lane);
+    const int run0 = kTile * first + kRun * warp;  // first token of this warp
+    const int nr = min(nt, max((len - run0 + kTile - 1) / kTile, 0));  // runs of this warp that hold tokens
+    __syncwarp();
+    auto request = [&](int j, int sl) {
+      if (j >= nr) return;
+      const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(source), j & 31);
+      bad &= ~(1u << sl);
+      if (src == 0) bad |= 1u << sl;
+      if (lane == 0) {
+        if (src == 0) {
+          report(a.err, KVARN_DEVERR_RECORD);
+          mbar_arrive1(bar + sl);
+        } else {
+          mbar_arrive_tx(bar + sl, RB);
+          bulk_in(ring + sl * RB, reinterpret_cast<const uint8_t*>(src), RB, bar + sl);
         }
       }
     };
-    if (a.io == KVARN_IO_F32) load(std::integral_constant<int, KVARN_IO_F32>());
-    else if (a.io == KVARN_IO_F16) load(std::integral_constant<int, KVARN_IO_F16>());
-    else load(std::integral_constant<int, KVARN_IO_BF16>());
-    mx = fmaxf(mx, shfl_xor(mx, 1));
-    mx = fmaxf(mx, shfl_xor(mx, 2));
-    // (a row with an infinity becomes NaN: without a lo part its scores could be infinite)
-    const float p2 = mx == INFINITY ? NAN : pow2_to(mx, 10);
+    auto next_slot = [&](int x) { return x + 1 == STG ? 0 : x + 1; };
+    for (int j = 0, x = sl; j < STG; ++j, x = next_slot(x)) request(j, x);
+
+    // B fragments of the query. Column g: part g % 2 of row g / 2, or (WIDE) row g, its parts in qb[0] and qb[1]. A
+    // product's channels are those that a word of K units gives to two registers.
+    uint32_t qb[NQ][BLK * WPB][4];
+    float c1[HL];             // of the rows whose scores this lane holds: HL q + 0 ..
+    [[maybe_unused]] int seen[HL];
+    {
+      const Row4 me = row4<CHUNK>(s, b, kvh, WIDE ? g : g >> 1);
+      float x[BLK * WPB][8];
+      float mx = 0.f;
+      auto load = [&](auto io) {  // (loads of a type that is known: under way together)
+        Eight<decltype(io)::value> e[BLK * WPB];
 #pragma unroll
-    for (int w = 0; w < BLK * WPB; ++w)
+        for (int w = 0; w < BLK * WPB; ++w)
+          e[w].load(a.q, me.index * D + w / WPB * R::kWide + q * (R::kWide / 4) + 8 * (w % WPB));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t hi, lo;
-        split_pair(x[w][j] * p2, x[w][j + 4] * p2, hi, lo);
-        qb[0][w][j] = !WIDE && (g & 1) ? lo : hi;
-        if constexpr (NQ == 2) qb[1][w][j] = lo;
+        for (int w = 0; w < BLK * WPB; ++w) {
+          e[w].get(x[w]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (!me.valid) x[w][i] = 0.f;
+            mx = fmaxf(mx, fabsf(x[w][i]));
+          }
+        }
+      };
+      if (a.io == KVARN_IO_F32) load(std::integral_constant<int, KVARN_IO_F32>());
+      else if (a.io == KVARN_IO_F16) load(std::integral_constant<int, KVARN_IO_F16>());
+      else load(std::integral_constant<int, KVARN_IO_BF16>());
+      mx = fmaxf(mx, shfl_xor(mx, 1));
+      mx = fmaxf(mx, shfl_xor(mx, 2));
+      // (a row with an infinity becomes NaN: without a lo part its scores could be infinite)
+      const float p2 = mx == INFINITY ? NAN : pow2_to(mx, 10);
+#pragma unroll
+      for (int w = 0; w < BLK * WPB; ++w)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t hi, lo;
+          split_pair(x[w][j] * p2, x[w][j + 4] * p2, hi, lo);
+          qb[0][w][j] = !WIDE && (g & 1) ? lo : hi;
+          if constexpr (NQ == 2) qb[1][w][j] = lo;
+        }
+      const float c = a.scale * pow2_inverse(pow2_to(mx, 10));
+#pragma unroll
+      for (int h = 0; h < HL; ++h) {
+        c1[h] = __shfl_sync(0xffffffffu, c, 8 * q + 4 * h);  // (column 2 q, or 2 q + h)
+        if constexpr (CHUNK) seen[h] = row4<CHUNK>(s, b, kvh, HL * q + h).seen;
       }
-    const float c = a.scale * pow2_inverse(pow2_to(mx, 10));
+    }
+
+    float M[HL], l[HL];
+    float o[D / 16][2][HL];
 #pragma unroll
     for (int h = 0; h < HL; ++h) {
-      c1[h] = __shfl_sync(0xffffffffu, c, 8 * q + 4 * h);  // (column 2 q, or 2 q + h)
-      if constexpr (CHUNK) seen[h] = row4<CHUNK>(s, b, kvh, HL * q + h).seen;
+      M[h] = kNone;
+      l[h] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][0][h] = o[i][1][h] = 0.f;
     }
-  }
-
-  float M[HL], l[HL];
-  float o[D / 16][2][HL];
+    const uint32_t ring_at = smem_addr(ring);
+    // this lane's places in a run: K units and scales of token g, V units, V scales
+    const uint32_t at_k = ring_at + g * (R::kWide / 2) + q * (R::kWide / 8);
+    const uint32_t at_ks = ring_at + R::kKScale + 2 * (g * R::kGroups + (WPB == 4 ? q : q >> 1));
+    const uint32_t at_v = ring_at + R::kVCodes + lane * 16, at_vs = ring_at + R::kVScale + q * 16;
+    // run j, which lies in slot sl; EDGE: some of its tokens are not seen, or it has no record
+    auto work_on = [&](int j, auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
+      const uint32_t run = sl * RB;
+      const int n_tok = len - run0 - kTile * j;  // tokens from the run's first on
+      const bool none = bad >> sl & 1;
+      // scores of tokens 8 x + g of the run for row HL q + h
+      float sc[HL][4];
 #pragma unroll
-  for (int h = 0; h < HL; ++h) {
-    M[h] = kNone;
-    l[h] = 0.f;
+      for (int mt = 0; mt < 2; ++mt) {
+        float e[2][4];  // sums of their own for every other product
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i][0][h] = o[i][1][h] = 0.f;
-  }
-  const uint32_t ring_at = smem_addr(ring);
-  // this lane's places in a run: K units and scales of token g, V units, V scales
-  const uint32_t at_k = ring_at + g * (R::kWide / 2) + q * (R::kWide / 8);
-  const uint32_t at_ks = ring_at + R::kKScale + 2 * (g * R::kGroups + (WPB == 4 ? q : q >> 1));
-  const uint32_t at_v = ring_at + R::kVCodes + lane * 16, at_vs = ring_at + R::kVScale + q * 16;
-  // run j, which lies in slot sl; EDGE: some of its tokens are not seen, or it has no record
-  auto work_on = [&](int j, auto edge) {
-    constexpr bool EDGE = decltype(edge)::value;
-    const uint32_t run = sl * RB;
-    const int n_tok = len - run0 - kTile * j;  // tokens from the run's first on
-    const bool none = bad >> sl & 1;
-    // scores of tokens 8 x + g of the run for row HL q + h
-    float sc[HL][4];
+        for (int k = 0; k < BLK; ++k) {
+          uint32_t kw[2][WPB];
+          __half2 ks[2], kt[2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      float e[2][4];  // sums of their own for every other product
+          for (int r = 0; r < 2; ++r) {
+            const int t = 16 * mt + 8 * r;
+            const uint32_t p = at_k + run + (k * (kRun * R::kWide / 2) + t * (R::kWide / 2));
+            if constexpr (WPB == 4) load16(p, kw[r]);
+            else load8(p, kw[r]);
+            ks[r] = __half2half2(load_half(at_ks + run + 2 * (t * R::kGroups + 4 * k)));
+            kt[r] = minus24(ks[r]);
+          }
 #pragma unroll
-      for (int k = 0; k < BLK; ++k) {
-        uint32_t kw[2][WPB];
-        __half2 ks[2], kt[2];
+          for (int w = 0; w < WPB; ++w) {
+            uint32_t x[2][4];
+            unit_values(kw[0][w], ks[0], kt[0], s.base, x[0]);
+            unit_values(kw[1][w], ks[1], kt[1], s.base, x[1]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int t = 16 * mt + 8 * r;
-          const uint32_t p = at_k + run + (k * (kRun * R::kWide / 2) + t * (R::kWide / 2));
-          if constexpr (WPB == 4) load16(p, kw[r]);
-          else load8(p, kw[r]);
-          ks[r] = __half2half2(load_half(at_ks + run + 2 * (t * R::kGroups + 4 * k)));
-          kt[r] = minus24(ks[r]);
-        }
-#pragma unroll
-        for (int w = 0; w < WPB; ++w) {
-          uint32_t x[2][4];
-          unit_values(kw[0][w], ks[0], kt[0], s.base, x[0]);
-          unit_values(kw[1][w], ks[1], kt[1], s.base, x[1]);
-#pragma unroll
-          for (int p = NQ - 1; p >= 0; --p) {  // (the lo parts first, while the sums are small)
-            const uint32_t (&f)[4] = qb[p][k * WPB + w];
-            if (k == 0 && w == 0 && p == NQ - 1) {
-              mma_f16_new(e[0], x[0][0], x[1][0], x[0][1], x[1][1], f[0], f[1]);
-              mma_f16_new(e[1], x[0][2], x[1][2], x[0][3], x[1][3], f[2], f[3]);
-            } else {
-              mma_f16(e[0], x[0][0], x[1][0], x[0][1], x[1][1], f[0], f[1]);
-              mma_f16(e[1], x[0][2], x[1][2], x[0][3], x[1][3], f[2], f[3]);
+            for (int p = NQ - 1; p >= 0; --p) {  // (the lo parts first, while the sums are small)
+              const uint32_t (&f)[4] = qb[p][k * WPB + w];
+              if (k == 0 && w == 0 && p == NQ - 1) {
+                mma_f16_new(e[0], x[0][0], x[1][0], x[0][1], x[1][1], f[0], f[1]);
+                mma_f16_new(e[1], x[0][2], x[1][2], x[0][3], x[1][3], f[2], f[3]);
+              } else {
+                mma_f16(e[0], x[0][0], x[1][0], x[0][1], x[1][1], f[0], f[1]);
+                mma_f16(e[1], x[0][2], x[1][2], x[0][3], x[1][3], f[2], f[3]);
+              }
             }
           }
         }
+#pragma unroll
+        for (int h = 0; h < HL; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            sc[h][2 * mt + r] = (WIDE ? e[0][2 * r + h] + e[1][2 * r + h]
+                                      : (e[0][2 * r] + e[1][2 * r]) + (e[0][2 * r + 1] + e[1][2 * r + 1])) * c1[h];
       }
+      if constexpr (EDGE) {
 #pragma unroll
-      for (int h = 0; h < HL; ++h)
+        for (int h = 0; h < HL; ++h)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          sc[h][2 * mt + r] = (WIDE ? e[0][2 * r + h] + e[1][2 * r + h]
-                                    : (e[0][2 * r] + e[1][2 * r]) + (e[0][2 * r + 1] + e[1][2 * r + 1])) * c1[h];
-    }
-    if constexpr (EDGE) {
+          for (int x = 0; x < 4; ++x) {
+            if (none) sc[h][x] = NAN;
+            if (8 * x + g >= (CHUNK ? seen[h] - run0 - kTile * j : n_tok)) sc[h][x] = -INFINITY;
+          }
+      }
+      float alpha[HL], p[HL][4];
 #pragma unroll
-      for (int h = 0; h < HL; ++h)
+      for (int h = 0; h < HL; ++h) {
+        float m = fmaxf(fmaxf(sc[h][0], sc[h][1]), fmaxf(sc[h][2], sc[h][3]));
+        m = fmaxf(m, shfl_xor(m, 4));
+        m = fmaxf(m, shfl_xor(m, 8));
+        m = fmaxf(m, shfl_xor(m, 16));
+        m = fmaxf(m - kHead, M[h]);
+        alpha[h] = fast_ex2(M[h] - m);
+        M[h] = m;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) p[h][x] = fast_ex2(sc[h][x] - m);
+        float sum = (p[h][0] + p[h][1]) + (p[h][2] + p[h][3]);
+        l[h] = fmaf(l[h], alpha[h], sum);
+        if (s.tile_ml) {  // the run's part of its tile's weight
+          sum += shfl_xor(sum, 4);
+          sum += shfl_xor(sum, 8);
+          sum += shfl_xor(sum, 16);
+          if (g == 0)
+            s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + j) * kRuns + warp) * 8 + HL * q + h] =
+                make_float2(m, sum);
+        }
+      }
+      // B fragments of the probabilities, by tokens 8 x .. 8 x + 7
+      uint32_t pb[HL][4];
+      if constexpr (WIDE) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          if (none) sc[h][x] = NAN;
-          if (8 * x + g >= (CHUNK ? seen[h] - run0 - kTile * j : n_tok)) sc[h][x] = -INFINITY;
+          uint32_t hi, lo;
+          split_pair(p[0][x], p[1][x], hi, lo);
+          pb[0][x] = transpose8(hi);
+          pb[1][x] = transpose8(lo);
         }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          uint32_t hi, lo;
+          split_pair(p[0][x], p[0][x + 1], hi, lo);
+          pb[0][x] = transpose8(__byte_perm(hi, lo, 0x5410));
+          pb[0][x + 1] = transpose8(__byte_perm(hi, lo, 0x7632));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[4], vs[4];
+        load_transposed(at_v + run + c * 512, v);
+        load16(at_vs + run + c * 64, vs);
+        if constexpr (EDGE) {  // what lies behind the last token counts as zeros, whatever it is
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int t = 8 * x + 2 * q;
+            vs[x] &= none || t >= n_tok ? 0u : t + 1 < n_tok ? 0xFFFFFFFFu : 0x0000FFFFu;
+          }
+        }
+        uint32_t x[4][4];  // [8 tokens][channel]
+#pragma unroll
+        for (int t = 0; t < 4; ++t) unit_values(v[t], as_half2(vs[t]), minus24(as_half2(vs[t])), s.base, x[t]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // channels 32 c + 4 g + 2 i and the next, in rows g and g + 8
+          float d[4];
+#pragma unroll
+          for (int h = HL - 1; h >= 0; --h) {  // (WIDE: the lo parts, then the hi parts)
+            if (h == HL - 1) mma_f16_new(d, x[0][2 * i], x[0][2 * i + 1], x[1][2 * i], x[1][2 * i + 1], pb[h][0], pb[h][1]);
+            else mma_f16(d, x[0][2 * i], x[0][2 * i + 1], x[1][2 * i], x[1][2 * i + 1], pb[h][0], pb[h][1]);
+            mma_f16(d, x[2][2 * i], x[2][2 * i + 1], x[3][2 * i], x[3][2 * i + 1], pb[h][2], pb[h][3]);
+          }
+          float (&y)[2][HL] = o[2 * c + i];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int h = 0; h < HL; ++h)
+              y[r][h] = fmaf(y[r][h], alpha[h], WIDE ? d[2 * r + h] : d[2 * r] + d[2 * r + 1]);
+        }
+      }
+    };
+    // tokens that every row sees
+    const int whole = CHUNK ? s.pos0 + 8 * b / a.G + 1 : len;
+#pragma unroll 1
+    for (int j = 0; j < nr; ++j) {
+      ok &= mbar_wait8(bar + sl, use, a.err);
+      if ((bad >> sl & 1) || whole - run0 - kTile * j < kRun) work_on(j, std::true_type());
+      else work_on(j, std::false_type());
+      __syncwarp();  // the slot is used up
+      const int ahead = j + STG;
+      if ((ahead & 31) == 0 && ahead < nr) source = address(ahead + lane);
+      request(ahead, sl);
+      sl = next_slot(sl);
+      if (sl == 0) use ^= 1;
     }
-    float alpha[HL], p[HL][4];
+    if (!ok) {  // a copy whose wait ran out still writes to this CTA's memory: each is given as long again
+      *flag = 1;
+      for (int i = 0; i < STG; ++i) mbar_wait8(bar + i, i < sl ? use : use ^ 1, nullptr);
+    }
+    if (s.tile_ml && g == 0)  // runs of the last tile that hold nothing
+      for (int j = nr; j < nt; ++j)
+#pragma unroll
+        for (int h = 0; h < HL; ++h)
+          s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + j) * kRuns + warp) * 8 + HL * q + h] =
+              make_float2(kNone, 0.f);
+    // the four warps meet: each leaves its rows in its own ring
+    float* mine = reinterpret_cast<float*>(ring);
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    __syncwarp();
 #pragma unroll
     for (int h = 0; h < HL; ++h) {
-      float m = fmaxf(fmaxf(sc[h][0], sc[h][1]), fmaxf(sc[h][2], sc[h][3]));
-      m = fmaxf(m, shfl_xor(m, 4));
-      m = fmaxf(m, shfl_xor(m, 8));
-      m = fmaxf(m, shfl_xor(m, 16));
-      m = fmaxf(m - kHead, M[h]);
-      alpha[h] = fast_ex2(M[h] - m);
-      M[h] = m;
+      l[h] += shfl_xor(l[h], 4);
+      l[h] += shfl_xor(l[h], 8);
+      l[h] += shfl_xor(l[h], 16);
+      if (g == 0) ml[warp * 8 + HL * q + h] = make_float2(nr > 0 ? M[h] : -INFINITY, l[h]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) p[h][x] = fast_ex2(sc[h][x] - m);
-      float sum = (p[h][0] + p[h][1]) + (p[h][2] + p[h][3]);
-      l[h] = fmaf(l[h], alpha[h], sum);
-      if (s.tile_ml) {  // the run's part of its tile's weight
-        sum += shfl_xor(sum, 4);
-        sum += shfl_xor(sum, 8);
-        sum += shfl_xor(sum, 16);
-        if (g == 0)
-          s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + j) * kRuns + warp) * 8 + HL * q + h] =
-              make_float2(m, sum);
-      }
+      for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<float2*>(mine + (HL * q + h) * C::OS + 32 * (i / 2) + 4 * g + 2 * (i % 2)) =
+            make_float2(o[i][0][h], o[i][1][h]);
     }
-    // B fragments of the probabilities, by tokens 8 x .. 8 x + 7
-    uint32_t pb[HL][4];
-    if constexpr (WIDE) {
+    __syncthreads();
+    const bool lost = *flag != 0;
+    const int64_t slot = blockIdx.x + (int64_t)b * a.Hkv + kvh;
+    for (int i = tid; i < C::ROWS * (D / 4); i += 128) {
+      const int r = i / (D / 4), c = 4 * (i % (D / 4));
+      if (!row4<CHUNK>(s, b, kvh, r).valid) continue;
+      float2 v[C::NW];
+      float m = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t hi, lo;
-        split_pair(p[0][x], p[1][x], hi, lo);
-        pb[0][x] = transpose8(hi);
-        pb[1][x] = transpose8(lo);
+      for (int w = 0; w < C::NW; ++w) {
+        v[w] = ml[w * 8 + r];
+        m = fmaxf(m, v[w].x);
       }
-    } else {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int x = 0; x < 4; x += 2) {
-        uint32_t hi, lo;
-        split_pair(p[0][x], p[0][x + 1], hi, lo);
-        pb[0][x] = transpose8(__byte_perm(hi, lo, 0x5410));
-        pb[0][x + 1] = transpose8(__byte_perm(hi, lo, 0x7632));
+      for (int w = 0; w < C::NW; ++w) {
+        const float f = v[w].x == -INFINITY ? 0.f : fast_ex2(v[w].x - m);
+        const float4 x = *reinterpret_cast<const float4*>(smem + w * STG * RB + (r * C::OS + c) * 4);
+        sum = fmaf(f, v[w].y, sum);
+        y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y); y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
       }
+      *reinterpret_cast<float4*>(s.acc + (slot * C::ROWS + r) * D + c) = y;
+      if (c == 0) s.ml[slot * C::ROWS + r] = lost ? make_float2(0.f, NAN) : make_float2(m, sum);
     }
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t v[4], vs[4];
-      load_transposed(at_v + run + c * 512, v);
-      load16(at_vs + run + c * 64, vs);
-      if constexpr (EDGE) {  // what lies behind the last token counts as zeros, whatever it is
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int t = 8 * x + 2 * q;
-          vs[x] &= none || t >= n_tok ? 0u : t + 1 < n_tok ? 0xFFFFFFFFu : 0x0000FFFFu;
-        }
-      }
-      uint32_t x[4][4];  // [8 tokens][channel]
-#pragma unroll
-      for (int t = 0; t < 4; ++t) unit_values(v[t], as_half2(vs[t]), minus24(as_half2(vs[t])), s.base, x[t]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {  // channels 32 c + 4 g + 2 i and the next, in rows g and g + 8
-        float d[4];
-#pragma unroll
-        for (int h = HL - 1; h >= 0; --h) {  // (WIDE: the lo parts, then the hi parts)
-          if (h == HL - 1) mma_f16_new(d, x[0][2 * i], x[0][2 * i + 1], x[1][2 * i], x[1][2 * i + 1], pb[h][0], pb[h][1]);
-          else mma_f16(d, x[0][2 * i], x[0][2 * i + 1], x[1][2 * i], x[1][2 * i + 1], pb[h][0], pb[h][1]);
-          mma_f16(d, x[2][2 * i], x[2][2 * i + 1], x[3][2 * i], x[3][2 * i + 1], pb[h][2], pb[h][3]);
-        }
-        float (&y)[2][HL] = o[2 * c + i];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int h = 0; h < HL; ++h)
-            y[r][h] = fmaf(y[r][h], alpha[h], WIDE ? d[2 * r + h] : d[2 * r] + d[2 * r + 1]);
-      }
+    now += nt;
+    if (now >= end) break;
+    // the next segment that holds tiles; the rings go back to the copies
+    tile0 = 0;
+    if (++kvh == a.Hkv) {
+      kvh = 0;
+      do ++b;
+      while (tiles4<CHUNK>(s, b) == 0);
     }
-  };
-  // tokens that every row sees
-  const int whole = CHUNK ? s.pos0 + 8 * b / a.G + 1 : len;
-#pragma unroll 1
-  for (int j = 0; j < nr; ++j) {
-    ok &= mbar_wait8(bar + sl, use, a.err);
-    if ((bad >> sl & 1) || whole - run0 - kTile * j < kRun) work_on(j, std::true_type());
-    else work_on(j, std::false_type());
-    __syncwarp();  // the slot is used up
-    const int ahead = j + STG;
-    if ((ahead & 31) == 0 && ahead < nr) source = address(ahead + lane);
-    request(ahead, sl);
-    sl = next_slot(sl);
-    if (sl == 0) use ^= 1;
-  }
-  if (!ok) {  // a copy whose wait ran out still writes to this CTA's memory: each is given as long again
-    *flag = 1;
-    for (int i = 0; i < STG; ++i) mbar_wait8(bar + i, i < sl ? use : use ^ 1, nullptr);
-  }
-  if (s.tile_ml && g == 0)  // runs of the last tile that hold nothing
-    for (int j = nr; j < nt; ++j)
-#pragma unroll
-      for (int h = 0; h < HL; ++h)
-        s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + j) * kRuns + warp) * 8 + HL * q + h] =
-            make_float2(kNone, 0.f);
-  // the four warps meet: each leaves its rows in its own ring
-  float* mine = reinterpret_cast<float*>(ring);
-  float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-  __syncwarp();
-#pragma unroll
-  for (int h = 0; h < HL; ++h) {
-    l[h] += shfl_xor(l[h], 4);
-    l[h] += shfl_xor(l[h], 8);
-    l[h] += shfl_xor(l[h], 16);
-    if (g == 0) ml[warp * 8 + HL * q + h] = make_float2(nr > 0 ? M[h] : -INFINITY, l[h]);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-      *reinterpret_cast<float2*>(mine + (HL * q + h) * C::OS + 32 * (i / 2) + 4 * g + 2 * (i % 2)) =
-          make_float2(o[i][0][h], o[i][1][h]);
-  }
-  __syncthreads();
-  const bool lost = *flag != 0;
-  const int64_t slot = blockIdx.x + (int64_t)b * a.Hkv + kvh;
-  for (int i = tid; i < C::ROWS * (D / 4); i += 128) {
-    const int r = i / (D / 4), c = 4 * (i % (D / 4));
-    if (!row4<CHUNK>(s, b, kvh, r).valid) continue;
-    float2 v[C::NW];
-    float m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < C::NW; ++w) {
-      v[w] = ml[w * 8 + r];
-      m = fmaxf(m, v[w].x);
-    }
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < C::NW; ++w) {
-      const float f = v[w].x == -INFINITY ? 0.f : fast_ex2(v[w].x - m);
-      const float4 x = *reinterpret_cast<const float4*>(smem + w * STG * RB + (r * C::OS + c) * 4);
-      sum = fmaf(f, v[w].y, sum);
-      y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y); y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
-    }
-    *reinterpret_cast<float4*>(s.acc + (slot * C::ROWS + r) * D + c) = y;
-    if (c == 0) s.ml[slot * C::ROWS + r] = lost ? make_float2(0.f, NAN) : make_float2(m, sum);
-  }
-  now += nt;
-  if (now >= end) break;
-  // the next segment that holds tiles; the rings go back to the copies
-  tile0 = 0;
-  if (++kvh == a.Hkv) {
-    kvh = 0;
-    do ++b;
-    while (tiles4<CHUNK>(s, b) == 0);
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncthreads();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
   }
 }
 
