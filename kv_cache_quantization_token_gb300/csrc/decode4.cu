@@ -41,10 +41,11 @@ namespace {
 constexpr float kNone = -3.0e38f;  // reference exponent before the first run
 constexpr float kHead = 14.f;      // probabilities reach 2^14: lo parts stay normal fp16 numbers
 
-template <int D_, bool WIDE>
+// TW: tiles that a CTA's warps take side by side; more than one in the kernel that does a segment by itself.
+template <int D_, bool WIDE, int TW = 1>
 struct C4 {
   static constexpr int D = D_;
-  static constexpr int NW = kRuns;             // warps, one per run of a tile
+  static constexpr int NW = kRuns * TW;        // warps, one per run of a tile
   static constexpr int HL = WIDE ? 2 : 1;      // rows (heads) whose scores a lane holds
   static constexpr int ROWS = 4 * HL;
   // Runs of a warp under way or in use: two keep some 70 KB per SM in flight, and more were no faster (four sequences of
@@ -52,7 +53,7 @@ struct C4 {
   static constexpr int STG = 2;
   // CTAs resident per SM: what registers allow without spilling, or a little fewer (two of six-head groups at head_dim
   // 64: 17.6 us with four, 18.2 with three; 120 us of batched decode at head_dim 256 with three, 126 with two).
-  static constexpr int CTAS = D == 64 ? 4 : D == 128 ? (WIDE ? 3 : 4) : WIDE ? 2 : 3;
+  static constexpr int CTAS = TW > 1 ? 1 : D == 64 ? 4 : D == 128 ? (WIDE ? 3 : 4) : WIDE ? 2 : 3;
   static constexpr int RB = Run4<D>::kBytes;
   static constexpr int OS = D + 8;             // floats of a row where the warps meet
   static constexpr int OFF_ML = NW * STG * RB; // float2 [NW][8]: (m, l)
@@ -207,10 +208,12 @@ __device__ __forceinline__ Before4 before4(const Split4Args& s, int want, At at,
   return Before4{total, scratch[0], scratch[1]};
 }
 
-// NQ: parts of a query in WIDE products, 1 for 16-bit ones.
-template <int D, bool WIDE, int NQ, bool CHUNK>
-__global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Split4Args s) {
-  using C = C4<D, WIDE>;
+// NQ: parts of a query in WIDE products, 1 for 16-bit ones. TW > 1: a CTA does segment (KV head blockIdx.x, blockIdx.y)
+// by itself and writes its output.
+template <int D, bool WIDE, int NQ, bool CHUNK, int TW>
+__global__ void __launch_bounds__(32 * C4<D, WIDE, TW>::NW, C4<D, WIDE, TW>::CTAS) split4_kernel(const Split4Args s) {
+  using C = C4<D, WIDE, TW>;
+  constexpr bool ALONE = TW > 1;
   using R = Run4<D>;
   constexpr int STG = C::STG, RB = C::RB, HL = C::HL;
   constexpr int BLK = D / R::kWide;        // blocks of K units
@@ -218,6 +221,7 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
   extern __shared__ __align__(128) unsigned char smem[];
   const Decode4Args& a = s.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int part = warp % kRuns;  // the run of a tile that is this warp's
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * STG;
   volatile int* flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLG);
   unsigned char* ring = smem + warp * STG * RB;
@@ -230,7 +234,12 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
   pdl_trigger();
   // this CTA's share, and the segment and tile that it begins with
   int now, end, b, kvh = 0, tile0 = 0;
-  {
+  if constexpr (ALONE) {
+    b = blockIdx.y;
+    kvh = blockIdx.x;
+    now = 0;
+    end = tiles4<CHUNK>(s, b);
+  } else {
     auto begin_in = [&](int t) {  // (with no share: nowhere)
       const Shares4 x(t * a.Hkv, s.ctas, s.few);
       return (int)blockIdx.x < x.n ? x.begin(blockIdx.x) / a.Hkv : -1;
@@ -253,8 +262,10 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
       tile0 = in - kvh * n;
     }
   }
-  if (now >= end) return;
-  if (!CHUNK && a.B > 1) {  // the scratch words go back to the copies
+  if (!ALONE && now >= end) return;  // (a segment of no tokens passes through)
+  if (ALONE) {
+    __syncthreads();  // (the flag)
+  } else if (!CHUNK && a.B > 1) {  // the scratch words go back to the copies
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
   }
@@ -268,15 +279,19 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
     const int nt = min(tiles4<CHUNK>(s, b) - first, end - now);
     const int stop = first + nt;
     const int64_t* table = a.tile_table + ((CHUNK ? 0 : (int64_t)b * a.Hkv) + kvh) * a.max_tiles + first;
-    // Runs of 32 tiles, one address per lane, NULL for one that does not lie in the pool.
+    // This warp's tiles are first + tw, and every TW-th after it. Runs of 32 of them, one address per lane, NULL for one that
+    // does not lie in the pool.
+    const int tw = warp / kRuns;
     auto address = [&](int j) -> const uint8_t* {
-      if (first + j >= stop) return nullptr;
-      const int64_t off = table[j];
-      return (off & 15) || off < 0 || off > a.tiles_bytes - R::kRecord ? nullptr : a.tiles + off + warp * RB;
+      if (first + tw + j * TW >= stop) return nullptr;
+      const int64_t off = table[tw + j * TW];
+      return (off & 15) || off < 0 || off > a.tiles_bytes - R::kRecord ? nullptr : a.tiles + off + part * RB;
     };
     const uint8_t* source = address(lane);
-    const int run0 = kTile * first + kRun * warp;  // first token of this warp
-    const int nr = min(nt, max((len - run0 + kTile - 1) / kTile, 0));  // runs of this warp that hold tokens
+    constexpr int kStep = kTile * TW;                            // tokens from one of this warp's runs to the next
+    const int run0 = kTile * (first + tw) + kRun * part;         // first token of this warp
+    // runs of this warp that hold tokens
+    const int nr = max((int)((min((int64_t)len, (int64_t)kTile * stop) - run0 + kStep - 1) / kStep), 0);
     __syncwarp();
     auto request = [&](int j, int sl) {
       if (j >= nr) return;
@@ -362,7 +377,7 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
     auto work_on = [&](int j, auto edge) {
       constexpr bool EDGE = decltype(edge)::value;
       const uint32_t run = sl * RB;
-      const int n_tok = len - run0 - kTile * j;  // tokens from the run's first on
+      const int n_tok = len - run0 - kStep * j;  // tokens from the run's first on
       const bool none = bad >> sl & 1;
       // scores of tokens 8 x + g of the run for row HL q + h
       float sc[HL][4];
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             if (none) sc[h][x] = NAN;
-            if (8 * x + g >= (CHUNK ? seen[h] - run0 - kTile * j : n_tok)) sc[h][x] = -INFINITY;
+            if (8 * x + g >= (CHUNK ? seen[h] - run0 - kStep * j : n_tok)) sc[h][x] = -INFINITY;
           }
       }
       float alpha[HL], p[HL][4];
@@ -435,7 +450,7 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
           sum += shfl_xor(sum, 8);
           sum += shfl_xor(sum, 16);
           if (g == 0)
-            s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + j) * kRuns + warp) * 8 + HL * q + h] =
+            s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + tw + j * TW) * kRuns + part) * 8 + HL * q + h] =
                 make_float2(m, sum);
         }
       }
@@ -496,7 +511,7 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
 #pragma unroll 1
     for (int j = 0; j < nr; ++j) {
       ok &= mbar_wait8(bar + sl, use, a.err);
-      if ((bad >> sl & 1) || whole - run0 - kTile * j < kRun) work_on(j, std::true_type());
+      if ((bad >> sl & 1) || whole - run0 - kStep * j < kRun) work_on(j, std::true_type());
       else work_on(j, std::false_type());
       __syncwarp();  // the slot is used up
       const int ahead = j + STG;
@@ -510,12 +525,12 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
       for (int i = 0; i < STG; ++i) mbar_wait8(bar + i, i < sl ? use : use ^ 1, nullptr);
     }
     if (s.tile_ml && g == 0)  // runs of the last tile that hold nothing
-      for (int j = nr; j < nt; ++j)
+      for (int j = nr; tw + j * TW < nt; ++j)
 #pragma unroll
         for (int h = 0; h < HL; ++h)
-          s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + j) * kRuns + warp) * 8 + HL * q + h] =
+          s.tile_ml[((((int64_t)b * a.Hkv + kvh) * a.max_tiles + first + tw + j * TW) * kRuns + part) * 8 + HL * q + h] =
               make_float2(kNone, 0.f);
-    // the four warps meet: each leaves its rows in its own ring
+    // the warps meet: each leaves its rows in its own ring
     float* mine = reinterpret_cast<float*>(ring);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     __syncwarp();
@@ -532,10 +547,15 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
     }
     __syncthreads();
     const bool lost = *flag != 0;
+    if (ALONE && lost) {
+      if (tid < 8) ml[tid].y = NAN;
+      __syncthreads();
+    }
     const int64_t slot = blockIdx.x + (int64_t)b * a.Hkv + kvh;
-    for (int i = tid; i < C::ROWS * (D / 4); i += 128) {
+    for (int i = tid; i < C::ROWS * (D / 4); i += 32 * C::NW) {
       const int r = i / (D / 4), c = 4 * (i % (D / 4));
-      if (!row4<CHUNK>(s, b, kvh, r).valid) continue;
+      const Row4 me = row4<CHUNK>(s, b, kvh, r);
+      if (!me.valid) continue;
       float2 v[C::NW];
       float m = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -551,8 +571,21 @@ __global__ void __launch_bounds__(128, C4<D, WIDE>::CTAS) split4_kernel(const Sp
         sum = fmaf(f, v[w].y, sum);
         y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y); y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
       }
+      if constexpr (ALONE) {
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        io_st4(a.out, a.io, me.index * D + c, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+        continue;
+      }
       *reinterpret_cast<float4*>(s.acc + (slot * C::ROWS + r) * D + c) = y;
       if (c == 0) s.ml[slot * C::ROWS + r] = lost ? make_float2(0.f, NAN) : make_float2(m, sum);
+    }
+    if constexpr (ALONE) {
+      if (a.mass_out) {  // (the tiles' parts lie behind the barrier too)
+        const int64_t at = ((int64_t)b * a.Hkv + kvh) * a.max_tiles;
+        join_masses<kRuns, 8>(ml, 1, C::NW, s.tile_ml + at * kRuns * 8, a.G, 0, nt, a.max_tiles,
+                              a.mass_in ? a.mass_in + at : nullptr, a.mass_out + at);
+      }
+      break;
     }
     now += nt;
     if (now >= end) break;
@@ -599,35 +632,61 @@ __global__ void __launch_bounds__(256) merge4_kernel(const Split4Args s, int mas
   join_items<D, ROWS>(s.ml + slot + r, s.acc + (slot + r) * D, pieces, a.out, a.io, (int64_t)blockIdx.y * a.Hq + blockIdx.x);
 }
 
-template <int D, bool WIDE, int NQ, bool CHUNK>
-cudaError_t launch_d4(const Decode4Plan& p, Split4Args& s, void* ws, cudaStream_t st) {
-  using C = C4<D, WIDE>;
-  const Decode4Args& a = s.a;
-  static bool configured[64] = {};
+template <class Kernel>
+cudaError_t allow_shared(Kernel* kernel, int bytes, bool (&configured)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(split4_kernel<D, WIDE, NQ, CHUNK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured[dev] = true;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) configured[dev] = true;
   }
+  return e;
+}
+
+// Tiles that a CTA takes side by side when it does a segment by itself: 16 warps, or 8 that need more registers. One launch and
+// no partial results, so short tables are read by it: of kAloneChannels tiles x channels at most, whatever the number of
+// segments, and up to 4 TW tiles where there are two segments to five SMs. Both ways, in us (joined pieces / by itself), bf16 queries:
+//   D 64, G 4     1 segment: 2 tiles 5.1 / 3.7, 6 5.2 / 5.1, 8 5.4 / 5.6;   64: 4 7.3 / 4.6, 16 9.8 / 8.0
+//   D 128, G 4    1 segment: 2 6.0 / 4.9, 3 5.9 / 5.2, 4 5.7 / 5.9;         64: 4 8.0 / 5.9, 16 12.1 / 11.6
+//   D 128, G 8    1 segment: 1 6.3 / 4.1, 3 6.1 / 5.5, 4 6.1 / 6.1;         64: 4 10.6 / 6.0, 8 12.1 / 8.7
+//   D 256, G 4    1 segment: 1 7.5 / 5.4, 2 7.5 / 5.9, 3 7.2 / 7.5;         64: 4 10.2 / 7.8, 8 11.5 / 11.3
+constexpr int kAloneChannels = 384;
+template <int D, bool WIDE>
+constexpr int kSideBySide = D == 64 || (D == 128 && !WIDE) ? 4 : 2;  // (16 warps, or 8 that need the registers)
+
+template <int D, bool WIDE, int NQ, bool CHUNK>
+cudaError_t launch_d4(const Decode4Plan& p, Split4Args& s, void* ws, cudaStream_t st) {
+  const Decode4Args& a = s.a;
   unsigned char* w = static_cast<unsigned char*>(ws);
+  s.base = kUnitBase;
+  s.tile_ml = a.mass_out ? reinterpret_cast<float2*>(w + p.off_tile) : nullptr;
+  constexpr int TW = kSideBySide<D, WIDE>;
+  const int tiles = CHUNK ? s.n_tiles : a.max_tiles;
+  const int64_t blocks = CHUNK ? ((int64_t)a.B * a.G + 7) / 8 : a.B;  // of sequences, or of eight rows
+  if ((int64_t)tiles * D <= kAloneChannels || (tiles <= 4 * TW && 5 * blocks * a.Hkv >= 2 * sm_count())) {
+    using C = C4<D, WIDE, TW>;
+    static bool configured[64] = {};
+    cudaError_t e = allow_shared(split4_kernel<D, WIDE, NQ, CHUNK, TW>, C::SMEM, configured);
+    if (e != cudaSuccess) return e;
+    LaunchCfg L(dim3(a.Hkv, (unsigned)blocks), dim3(32 * C::NW), C::SMEM, st, a.flags);
+    return cudaLaunchKernelEx(&L.cfg, split4_kernel<D, WIDE, NQ, CHUNK, TW>, s);
+  }
+  using C = C4<D, WIDE>;
   s.ml = reinterpret_cast<float2*>(w);
   s.acc = reinterpret_cast<float*>(w + p.off_acc);
-  s.tile_ml = a.mass_out ? reinterpret_cast<float2*>(w + p.off_tile) : nullptr;
   s.ctas = p.ctas;
   s.few = 2 * sm_count();
-  s.base = kUnitBase;
-  if (p.ctas > 0) {
-    LaunchCfg L(dim3(p.ctas), dim3(128), C::SMEM, st, a.flags);
-    e = cudaLaunchKernelEx(&L.cfg, split4_kernel<D, WIDE, NQ, CHUNK>, s);
-    if (e != cudaSuccess) return e;
-  }
+  static bool configured[64] = {};
+  cudaError_t e = allow_shared(split4_kernel<D, WIDE, NQ, CHUNK, 1>, C::SMEM, configured);
+  if (e != cudaSuccess) return e;
+  LaunchCfg L(dim3(p.ctas), dim3(128), C::SMEM, st, a.flags);
+  e = cudaLaunchKernelEx(&L.cfg, split4_kernel<D, WIDE, NQ, CHUNK, 1>, s);
+  if (e != cudaSuccess) return e;
   const int mass_blocks = a.mass_out ? (a.max_tiles + 255) / 256 : 0;
   // the merge waits for the split kernel on the device, whatever the caller's flags
-  LaunchCfg L(dim3(a.Hq + a.Hkv * mass_blocks, a.B), dim3(256), 0, st, a.flags | KVARN_LAUNCH_PDL);
-  return cudaLaunchKernelEx(&L.cfg, merge4_kernel<D, C::ROWS, CHUNK>, s, mass_blocks);
+  LaunchCfg M(dim3(a.Hq + a.Hkv * mass_blocks, a.B), dim3(256), 0, st, a.flags | KVARN_LAUNCH_PDL);
+  return cudaLaunchKernelEx(&M.cfg, merge4_kernel<D, C::ROWS, CHUNK>, s, mass_blocks);
 }
 
 template <int D, bool CHUNK>

@@ -72,7 +72,10 @@ def put_token(rec, D, t, kc, ks, vc, vs):
 
 class Cache4:
     """A batch of 4-bit caches built here, byte by byte, in a shuffled pool whose unwritten bytes are `fill`; k[b], v[b]
-    are the values, [Hkv][tokens][D] in 64 bits (NaN for poison)."""
+    are the values, [Hkv][tokens][D] in 64 bits (NaN for poison). Its table has `beyond` columns behind the tiles, each
+    an offset that must not be followed."""
+
+    beyond = 0
 
     def __init__(self, seed, lens, Hkv, D, max_tiles=None, fill=0xFF, change=None, spare=0):
         rng = np.random.default_rng(seed)
@@ -106,6 +109,8 @@ class Cache4:
             self.v.append(vb)
         dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
         self.pool = pool
+        self.max_tiles += self.beyond
+        table = np.concatenate([table, np.full((self.B, Hkv, self.beyond), -16)], 2)
         self.tiles, self.table = dev(pool.reshape(-1)), dev(table)
         self.lens = torch.tensor(list(lens), dtype=torch.int32, device=DEV)
 

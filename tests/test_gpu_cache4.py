@@ -251,6 +251,13 @@ def _check_decode(c, q, out, scale=None, mass=None, mass_in=None, bound_extra=0.
                 assert (np.abs(got - base - w) <= 2.0 ** -12 * w + 2.0 ** -23 * (np.abs(base) + w) + 1e-30).all()
 
 
+@pytest.fixture(params=[0, 40])
+def tables(request, monkeypatch):
+    """Short tables, which a block reads by itself, and long ones, whose tiles are shared out."""
+    monkeypatch.setattr(Cache4, "beyond", request.param)
+
+
+@pytest.mark.usefixtures("tables")
 @pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_decode_matches_the_formula(D, io):
@@ -259,6 +266,7 @@ def test_decode_matches_the_formula(D, io):
     _check_decode(c, q, c.decode(q))
 
 
+@pytest.mark.usefixtures("tables")
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("G", [1, 2, 3, 5, 6, 7, 8])
 def test_decode_head_groups(G, D):
@@ -267,6 +275,7 @@ def test_decode_head_groups(G, D):
     _check_decode(c, q, c.decode(q))
 
 
+@pytest.mark.usefixtures("tables")
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_decode_lengths(D):
     """Around every end of a run and a tile; tokens behind the last hold every byte 0xFF, or 0x7C: NaN and infinite
@@ -314,16 +323,17 @@ def _shared(seed, D, H, lens, distinct=5):
     return c, table, _dev(lens, torch.int32), rows_of
 
 
+@pytest.mark.parametrize("longest", [6000, 1000])
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("D,G", [(64, 2), (64, 7), (128, 4), (128, 8), (256, 3), (256, 5)])
-def test_decode_of_ragged_batches(D, G, io):
+def test_decode_of_ragged_batches(D, G, io, longest):
     """More tiles than CTAs: shares that begin and end inside sequences, that span several, and sequences of no
-    tokens between them; weights of all tiles."""
+    tokens between them (or a table short enough for a block per sequence and KV head); weights of all tiles."""
     H = 3
     rng = np.random.default_rng(D + G)
     lens = [int(n) for n in rng.integers(0, 900, 60)]
     lens[0] = lens[7] = lens[8] = lens[31] = lens[-1] = 0
-    lens[5], lens[20] = 6000, 128
+    lens[5], lens[20] = longest, 128
     c, table, ln, rows_of = _shared(D, D, H, lens)
     q = _query(G, (len(lens), H * G, D), io)
     m = torch.zeros(table.shape, device=DEV)
@@ -352,10 +362,11 @@ def test_decode_of_ragged_batches(D, G, io):
     assert bool((out7.view(60, 7, -1)[:, 1:] == 0).all())
 
 
+@pytest.mark.parametrize("n", [600, 2200])  # a block for each row group and head, and tiles shared out
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_prefill_of_few_rows_over_many_segments(D):
+def test_prefill_of_few_rows_over_many_segments(D, n):
     """A chunk on the decode kernels with more tiles than CTAs: shares that span row groups and heads."""
-    H, G, C, n = 8, 4, 31, 600
+    H, G, C = 8, 4, 31
     c, table, _, rows_of = _shared(D + 5, D, H, [n])
     for io in ("f32", "bf16"):
         q = _query(D, (C, H * G, D), io)
@@ -368,13 +379,14 @@ def test_prefill_of_few_rows_over_many_segments(D):
                   p @ np.abs(v))
 
 
-@pytest.mark.parametrize("D,G", [(64, 3), (128, 8), (256, 4)])
+@pytest.mark.usefixtures("tables")
+@pytest.mark.parametrize("D,G", [(64, 3), (64, 8), (128, 4), (128, 8), (256, 4)])
 def test_decode_weights_accumulate(D, G):
     c = Cache4(20 + D, [450, 0, 128, 33], 2, D, max_tiles=6)
     q = _query(5, (4, 2 * G, D), "f32")
-    m = torch.full((4, 2, 6), float("nan"), device=DEV)
+    m = torch.full((4, 2, c.max_tiles), float("nan"), device=DEV)
     _check_decode(c, q, c.decode(q, mass_out=m), mass=m)
-    base = torch.rand(4, 2, 6, device=DEV) * 3
+    base = torch.rand(4, 2, c.max_tiles, device=DEV) * 3
     m2 = base.clone()
     out = c.decode(q, mass_in=m2, mass_out=m2)
     _check_decode(c, q, out, mass=m2, mass_in=base)
@@ -384,8 +396,9 @@ def test_decode_weights_accumulate(D, G):
     assert torch.equal(m2[1], base[1])
 
 
-def test_decode_counts_past_their_table_are_clamped():
-    c = Cache4(30, [256, 40], 2, 128)
+@pytest.mark.parametrize("tokens", [256, 2560])
+def test_decode_counts_past_their_table_are_clamped(tokens):
+    c = Cache4(30, [tokens, 40], 2, 128)
     q = _query(5, (2, 4, 128), "f32")
     want = c.decode(q)
     c.lens = _dev([2 ** 31 - 1, 40], torch.int32)
@@ -395,6 +408,7 @@ def test_decode_counts_past_their_table_are_clamped():
     assert bool((out[0] == 0).all()) and torch.equal(out[1], want[1])
 
 
+@pytest.mark.usefixtures("tables")
 def test_decode_scales_of_either_sign_and_zero():
     c = Cache4(31, [200], 1, 64)
     q = _query(5, (1, 4, 64), "f32")
@@ -402,6 +416,7 @@ def test_decode_scales_of_either_sign_and_zero():
         _check_decode(c, q, c.decode(q, softmax_scale=scale), scale)
 
 
+@pytest.mark.usefixtures("tables")
 def test_decode_with_far_apart_values():
     """Value rows from the smallest scale to the largest magnitude, under keys that favour the small ones."""
     def change(b, h, k, v):
@@ -414,6 +429,7 @@ def test_decode_with_far_apart_values():
         _check_decode(c, q, c.decode(q))
 
 
+@pytest.mark.usefixtures("tables")
 def test_decode_poison_and_bad_queries():
     def change(b, h, k, v):
         if (b, h) == (1, 0):
@@ -433,10 +449,13 @@ def test_decode_poison_and_bad_queries():
         assert bool(out[bad].isnan().all()) and torch.equal(out[~bad], want[~bad])
 
 
-def test_decode_bad_offsets_poison_their_head_only():
-    c = Cache4(34, [900, 300], 2, 128)
-    q = _query(8, (2, 4, 128), "bf16")
-    m = torch.zeros(2, 2, c.max_tiles, device=DEV)
+@pytest.mark.usefixtures("tables")
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 2), (256, 2)])
+def test_decode_bad_offsets_poison_their_head_only(D, G):
+    many = 1 if Cache4.beyond else 40  # (sequences enough that a block reads eight tiles by itself)
+    c = Cache4(34, [900, 300] + [1] * many, 2, D)
+    q = _query(8, (2 + many, 2 * G, D), "bf16")
+    m = torch.zeros(2 + many, 2, c.max_tiles, device=DEV)
     want = c.decode(q, mass_out=m)
     for off in (-16, 8, c.tiles.numel() - c.lay.record_bytes + 16, 1 << 62):
         t = c.table.clone()
@@ -445,17 +464,18 @@ def test_decode_bad_offsets_poison_their_head_only():
         m2 = torch.zeros_like(m)
         out = kvarn.decode_attention4(q, c.tiles, t, c.lens, c.lay, mass_out=m2)
         assert kvarn.device_error() == kvarn.DEVERR_RECORD
-        assert bool(out[0, 2:].isnan().all()) and torch.equal(out[0, :2], want[0, :2]) and torch.equal(out[1], want[1])
-        assert bool(m2[0, 1].isnan().all()) and torch.equal(m2[0, 0], m[0, 0]) and torch.equal(m2[1], m[1])
+        assert bool(out[0, G:].isnan().all()) and torch.equal(out[0, :G], want[0, :G]) and torch.equal(out[1:], want[1:])
+        assert bool(m2[0, 1, :8].isnan().all()) and torch.equal(m2[0, 0], m[0, 0]) and torch.equal(m2[1:], m[1:])
 
 
+@pytest.mark.usefixtures("tables")
 def test_decode_launch_modes_and_graphs_are_bit_identical():
     """Two graphs of different sizes that share a workspace, replayed in turn after a step has moved the cache on."""
     c = Cache4(35, [400, 90, 1], 2, 128, max_tiles=4)
     q = _query(9, (3, 8, 128), "bf16")
     want = c.decode(q)
     assert torch.equal(c.decode(q, flags=kvarn.LAUNCH_PDL), want)
-    ws = torch.empty(kvarn.decode4_workspace_bytes(3, 8, 2, 128, 4), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(kvarn.decode4_workspace_bytes(3, 8, 2, 128, c.max_tiles), dtype=torch.uint8, device=DEV)
     out, few = torch.empty_like(q), torch.empty_like(q[:1])
     row = _query(10, (3, 1, 2, 128), "bf16")
     torch.cuda.synchronize()
