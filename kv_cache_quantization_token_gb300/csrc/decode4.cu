@@ -601,16 +601,17 @@ __global__ void __launch_bounds__(32 * C4<D, WIDE, TW>::NW, C4<D, WIDE, TW>::CTA
   }
 }
 
-// Joins the pieces of query head blockIdx.x of row block blockIdx.y (a sequence, or a position of a CHUNK), or adds up the
-// weights of 256 tiles of a KV head.
-template <int D, int ROWS, bool CHUNK>
+// Joins the pieces of a segment's rows (EACH: those of query head blockIdx.x of row block blockIdx.y, a sequence or a position
+// of a CHUNK; else all of KV head blockIdx.x), or adds up the weights of 256 tiles of a KV head.
+template <int D, int ROWS, bool CHUNK, bool EACH>
 __global__ void __launch_bounds__(256) merge4_kernel(const Split4Args s, int mass_blocks) {
   const Decode4Args& a = s.a;
   __shared__ int scratch[10];
-  const bool mass = (int)blockIdx.x >= a.Hq;
-  const int kvh = mass ? ((int)blockIdx.x - a.Hq) / mass_blocks : (int)blockIdx.x / a.G;
-  const int64_t n = CHUNK ? (int64_t)blockIdx.y * a.G + blockIdx.x % a.G : 0;  // row among a CHUNK's of this KV head
-  const int b = CHUNK ? (int)(n / 8) : blockIdx.y;
+  const int joins = EACH ? a.Hq : a.Hkv;
+  const bool mass = (int)blockIdx.x >= joins;
+  const int kvh = mass ? ((int)blockIdx.x - joins) / mass_blocks : EACH ? (int)blockIdx.x / a.G : (int)blockIdx.x;
+  const int64_t n = EACH && CHUNK ? (int64_t)blockIdx.y * a.G + blockIdx.x % a.G : 0;  // row among a CHUNK's of this KV head
+  const int b = EACH && CHUNK ? (int)(n / 8) : blockIdx.y;
   pdl_trigger();
   // (the lengths are not the split kernel's: they have been there since before its first CTA let this kernel start)
   Before4 at;
@@ -624,12 +625,22 @@ __global__ void __launch_bounds__(256) merge4_kernel(const Split4Args s, int mas
   if (mass) {
     const int64_t first = ((int64_t)b * a.Hkv + kvh) * a.max_tiles;
     join_masses<kRuns, ROWS>(s.ml + slot, 1, pieces, s.tile_ml + first * kRuns * 8, a.G,
-                             ((int)blockIdx.x - a.Hq) % mass_blocks, tiles, a.max_tiles,
+                             ((int)blockIdx.x - joins) % mass_blocks, tiles, a.max_tiles,
                              a.mass_in ? a.mass_in + first : nullptr, a.mass_out + first);
-    return;
+  } else if constexpr (EACH) {
+    const int r = CHUNK ? (int)(n % 8) : (int)blockIdx.x % a.G;
+    join_items<D, ROWS>(s.ml + slot + r, s.acc + (slot + r) * D, pieces, a.out, a.io, (int64_t)blockIdx.y * a.Hq + blockIdx.x);
+  } else if (pieces <= 32) {  // (more where most sequences are empty)
+    const int r = threadIdx.x / 32;
+    const Row4 me = row4<CHUNK>(s, b, kvh, r);
+    if (r < ROWS && me.valid) join_few<D, ROWS>(s.ml + slot + r, s.acc + (slot + r) * D, pieces, a.out, a.io, me.index);
+  } else {
+    for (int r = 0; r < ROWS; ++r) {
+      const Row4 me = row4<CHUNK>(s, b, kvh, r);
+      if (me.valid) join_items<D, ROWS>(s.ml + slot + r, s.acc + (slot + r) * D, pieces, a.out, a.io, me.index);
+      __syncthreads();
+    }
   }
-  const int r = CHUNK ? (int)(n % 8) : (int)blockIdx.x % a.G;
-  join_items<D, ROWS>(s.ml + slot + r, s.acc + (slot + r) * D, pieces, a.out, a.io, (int64_t)blockIdx.y * a.Hq + blockIdx.x);
 }
 
 template <class Kernel>
@@ -685,8 +696,16 @@ cudaError_t launch_d4(const Decode4Plan& p, Split4Args& s, void* ws, cudaStream_
   if (e != cudaSuccess) return e;
   const int mass_blocks = a.mass_out ? (a.max_tiles + 255) / 256 : 0;
   // the merge waits for the split kernel on the device, whatever the caller's flags
-  LaunchCfg M(dim3(a.Hq + a.Hkv * mass_blocks, a.B), dim3(256), 0, st, a.flags | KVARN_LAUNCH_PDL);
-  return cudaLaunchKernelEx(&M.cfg, merge4_kernel<D, C::ROWS, CHUNK>, s, mass_blocks);
+  // A CTA per row joins many pieces fastest; more rows than two for each SM have few pieces, and a warp does one, eight times
+  // fewer CTAs finding their places. (A row / a warp each, us: D 128, 8 heads each, 32 tiles: 24 segments 12.0 / 13.1, 40 15.6 /
+  // 14.4, 128 30.5 / 24.6, 512 100.3 / 76.4; D 64, 4 heads: 64 10.9 / 11.1, 128 17.0 / 14.9, 512 52.3 / 41.8.)
+  const bool each = (int64_t)a.B * a.Hq <= 2 * sm_count();
+  auto merge = [&](auto* kernel, int joins, int64_t rows) {
+    LaunchCfg M(dim3(joins + a.Hkv * mass_blocks, (unsigned)rows), dim3(256), 0, st, a.flags | KVARN_LAUNCH_PDL);
+    return cudaLaunchKernelEx(&M.cfg, kernel, s, mass_blocks);
+  };
+  return each ? merge(merge4_kernel<D, C::ROWS, CHUNK, true>, a.Hq, a.B)
+              : merge(merge4_kernel<D, C::ROWS, CHUNK, false>, a.Hkv, blocks);
 }
 
 template <int D, bool CHUNK>

@@ -70,6 +70,53 @@ __device__ __forceinline__ void join_items(const float2* ml, const float* acc, i
   }
 }
 
+// The same by one warp, for 32 items at most.
+template <int D, int STRIDE>
+__device__ __forceinline__ void join_few(const float2* ml, const float* acc, int items, void* out, int io, int64_t row) {
+  constexpr int N = D < 128 ? 1 : D / 128, PARTS = D < 128 ? 128 / D : 1;  // four channels N times, every PARTS-th item
+  const int lane = threadIdx.x & 31, pt = lane % PARTS, col = 4 * (lane / PARTS);
+  const float2 v = lane < items ? ml[lane * STRIDE] : make_float2(-INFINITY, 0.f);
+  float M = v.x;
+  for (int m = 16; m; m >>= 1) M = fmaxf(M, shfl_xor(M, m));
+  const float w = v.y != 0.f ? fast_ex2(v.x - M) : 0.f;
+  float L = w * v.y;
+  for (int m = 16; m; m >>= 1) L += shfl_xor(L, m);
+  float4 y[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) y[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < items; i0 += 4 * PARTS) {
+    float4 x[4][N];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (const int i = i0 + k * PARTS + pt; i < items)
+          x[k][n] = *reinterpret_cast<const float4*>(acc + (int64_t)i * STRIDE * D + 128 * n + col);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * PARTS + pt;
+      const float f = __shfl_sync(0xffffffffu, w, i & 31);
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (i < items && f != 0.f) {
+          y[n].x = fmaf(f, x[k][n].x, y[n].x); y[n].y = fmaf(f, x[k][n].y, y[n].y);
+          y[n].z = fmaf(f, x[k][n].z, y[n].z); y[n].w = fmaf(f, x[k][n].w, y[n].w);
+        }
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int m = 1; m < PARTS; m <<= 1) {
+      y[n].x += shfl_xor(y[n].x, m); y[n].y += shfl_xor(y[n].y, m);
+      y[n].z += shfl_xor(y[n].z, m); y[n].w += shfl_xor(y[n].w, m);
+    }
+    if (pt == 0)
+      io_st4(out, io, row * D + 128 * n + col, make_float4(y[n].x * inv, y[n].y * inv, y[n].z * inv, y[n].w * inv));
+  }
+}
+
 // Weights of 256 tiles (from 256 * block on) of one KV head: ml of item i of its query head g at g * head + i * STRIDE,
 // tile_ml [tiles][PARTS][8] (maximum, sum) of each tile's parts and heads; n tiles hold tokens, the others keep mass_in.
 template <int PARTS, int STRIDE = 1>

@@ -309,6 +309,24 @@ def test_decode_of_long_sequences():
     assert bool((out[:3] == 0).all()) and bool((out[4:] == 0).all())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode_of_one_long_sequence_among_empty_ones(D):
+    """A warp per row is planned for the pieces, of which the one sequence has more than a warp takes."""
+    c, table, ln, rows_of = _shared(D, D, 3, [0] * 17 + [6000] + [0] * 22)
+    q = _query(D, (40, 9, D), "f32")
+    m = torch.zeros(table.shape, device=DEV)
+    out = kvarn.decode_attention4(q, c.tiles, table, ln, c.lay, mass_out=m)
+    for h in range(3):
+        k, v = rows_of(17, h, 6000)
+        want, p, bound = attend(q[17, 3 * h:3 * h + 3].double().cpu().numpy(), k, v, D ** -0.5, [6000] * 3, np.ones(6000),
+                                2.0 ** -39)
+        check(out[17, 3 * h:3 * h + 3], want, bound, q.dtype)
+        w = np.append(p.sum(0), np.zeros(47 * T - 6000)).reshape(-1, T).sum(1)
+        assert (np.abs(m[17, h].double().cpu().numpy() - w) <= 2.0 ** -12 * w).all()
+    keep = torch.arange(40, device=DEV) != 17
+    assert bool((out[keep] == 0).all()) and bool((m[keep] == 0).all())
+
+
 def _shared(seed, D, H, lens, distinct=5):
     """Ragged sequences whose tables name the same few tiles in any order: (pool's cache, table, lens, K and V rows by
     (b, h))."""
