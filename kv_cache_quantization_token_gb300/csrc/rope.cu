@@ -3,26 +3,29 @@
 //
 //   y = x / sqrt(mean(x^2) + eps) * w;   (a, b) -> (a cos - b sin, a sin + b cos);   y H / sqrt(D)
 //
-// A warp takes a token, or, of few tokens, a part of one's heads. D / 16 of its threads hold a row (token, head), sixteen
-// channels each, as two chunks of eight that are partners in the rotation, so that a pair never leaves its thread and a
-// thread's eight angles, which all heads of the token share, stay in its registers; the sum of squares and the
-// transform's far butterflies meet by shuffles. The warps need nothing of one another.
+// D / 16 threads of a warp hold a row (token, head), sixteen channels each, as two chunks of eight that are partners in the
+// rotation, so that a pair never leaves its thread and a thread's eight angles, which all heads of the token share, stay in
+// its registers; the sum of squares and the transform's far butterflies meet by shuffles. The launch's warps share out all
+// items (rows of a warp) in order, as equally as whole items
+// allow, and stay; they need nothing of one another.
 //
 // An angle is position * frequency in units of 2^-64 of a turn: a 64-bit integer product drops whole turns
 // exactly, whatever the position, and costs three multiply-adds where an fp64 product and its reduction
 // would take GB300's slow fp64 units. The quarter turn nearest to it is taken off before it is rounded to fp32.
 //
-// What bounds it: instructions beside memory. 8,192 tokens of 32 + 8 heads of 128, bf16, packed (168 MB): 38.2 us, 4.4
-// TB/s (65% of the copy rate; the same kernel without norm and rotation 29). A CTA with the angles of several tokens in
-// shared memory took 47 to 58, with more than half of its instructions in addresses, starts and the exchange of partners;
-// sixteen channels to a thread instead of eight 38.2 instead of 41.
+// What bounds it: instructions beside memory. 8,192 tokens of 32 + 8 heads of 128, bf16, packed (168 MB): 31.5 us, 5.3
+// TB/s (78% of the copy rate). A warp per token that comes and goes took 37.4, and 38.2 with the frequencies read from the
+// launch's arguments, which are served one index at a time (1,337 tokens with transform: 6.4, 7.1, 8.4); twenty warps of 96
+// registers instead of sixteen of 128 33.5, two items under way instead of three 33.1; angles of a CTA's tokens in shared
+// memory 47 to 58.
 #include "cache4.cuh"
 
 namespace kvarn {
 namespace {
 
-constexpr int kWarps = 4;  // of a CTA
-constexpr int kAhead = 2;  // items of a warp under way
+constexpr int kWarps = 8;  // of a CTA
+constexpr int kCtas = 2;   // of an SM
+constexpr int kAhead = 3;  // items of a warp under way
 
 // Two chunks of eight consecutive elements of a row of type IO.
 template <int IO>
@@ -62,11 +65,13 @@ __device__ __forceinline__ float2 turned_by(int64_t position, uint64_t turn) {
 }
 
 template <int D, int IO, bool HALVES>
-__global__ void __launch_bounds__(kWarps * 32, 5) norm_rotate_kernel(const RopeArgs a, const __grid_constant__ kvarn_rotary_t rot,
-                                                                  int parts) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const RopeArgs a, const __grid_constant__ kvarn_rotary_t rot) {
   constexpr int L = D / 16, ROWS = 32 / L;  // threads of a row, rows of a warp
   constexpr int SIZE = IO == KVARN_IO_F32 ? 4 : 2;
   __shared__ __align__(16) float exchange[kWarps][512];
+  __shared__ uint64_t turn_s[128];  // (the launch's arguments, at 32 indexes at once, would be read one by one)
+  __shared__ int axis_s[128];
+  __shared__ __align__(16) float weight_s[2][D];  // of q, of k: the first halves of all chunks, then the second ones
   const int lane = threadIdx.x & 31, l = lane % L;
   float* mine = exchange[threadIdx.x / 32];
   const int R = rot.rotary_dim, far = R / 16;  // chunks between partners
@@ -79,58 +84,79 @@ __global__ void __launch_bounds__(kWarps * 32, 5) norm_rotate_kernel(const RopeA
     c0 = bits ? 2 * (l & ~(far - 1)) + (l & (far - 1)) : turned ? l : l + far;
     c1 = c0 + (bits || turned ? far : L - far);
   }
+  for (int i = threadIdx.x; i < R / 2; i += 32 * kWarps) {
+    turn_s[i] = rot.turn[i];
+    axis_s[i] = rot.axis[i];
+  }
   pdl_trigger();
   pdl_wait();
-  // this warp's token and its part of the token's items, each ROWS heads of q or of k
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  int64_t t = unit;
-  int part = 0;
-  if (parts > 1) {
-    t = unit / parts;
-    part = (int)(unit - t * parts);
-  }
-  if (t >= a.n_tokens) return;
+  // Items: ROWS heads of q or of k of a token. This warp's share of all tokens' items in order: `left` of them.
   const int nq = (a.Hq + ROWS - 1) / ROWS, n = nq + (a.Hkv + ROWS - 1) / ROWS;
-  int first = 0, last = n;
-  if (parts > 1) {
-    first = n * part / parts;
-    last = n * (part + 1) / parts;
-  }
-  // Rows are requested kAhead items before they are worked on, the first ones before the angles are formed; the places of
-  // the next item to load and to store go from q to k.
-  const int row = lane / L, by = ROWS * SIZE * D;  // (a token's heads take less than 2^31 bytes)
-  auto place = [&](const void* q, int64_t q_stride, const void* k, int64_t k_stride, int w) {
-    return w < nq ? static_cast<const char*>(q) + t * q_stride * SIZE + (w * ROWS + row) * (SIZE * D)
-                  : static_cast<const char*>(k) + t * k_stride * SIZE + ((w - nq) * ROWS + row) * (SIZE * D);
+  const int64_t items = a.n_tokens * n, warps = (int64_t)gridDim.x * kWarps, me = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  const int64_t begin = items * me / warps;
+  int left = (int)(items * (me + 1) / warps - begin);
+  const int row = lane / L;
+  // Where the next item lies: heads head .. of the heads of q or k of token t, row `row` of them at p.
+  struct Cursor {
+    char* p;
+    int64_t t;
+    int head, heads;
+    bool k;
   };
-  auto there = [&](int w) { return w < nq ? w * ROWS + row < a.Hq : (w - nq) * ROWS + row < a.Hkv; };
-  const char* src = place(a.q, a.q_stride, a.k, a.k_stride, first);
-  char* dst = const_cast<char*>(place(a.q_out, a.qo_stride, a.k_out, a.ko_stride, first));
-  int next = first;
+  auto enter = [&](Cursor& c, const void* q, int64_t q_stride, const void* k, int64_t k_stride) {
+    c.heads = c.k ? a.Hkv : a.Hq;
+    c.p = const_cast<char*>(static_cast<const char*>(c.k ? k : q)) + c.t * (c.k ? k_stride : q_stride) * SIZE +
+          (int64_t)(c.head + row) * (SIZE * D);
+  };
+  auto step = [&](Cursor& c, const void* q, int64_t q_stride, const void* k, int64_t k_stride) {  // true: to another lot of heads
+    c.p += ROWS * SIZE * D;
+    c.head += ROWS;
+    if (c.head < c.heads) return false;
+    c.head = 0;
+    if (c.k || a.Hkv == 0) ++c.t;
+    c.k = !c.k && a.Hkv > 0;
+    enter(c, q, q_stride, k, k_stride);
+    return true;
+  };
+  Cursor in;
+  in.t = begin / n;
+  in.head = (int)(begin - in.t * n);
+  in.k = in.head >= nq;
+  in.head = (in.k ? in.head - nq : in.head) * ROWS;
+  Cursor to = in;
+  enter(in, a.q, a.q_stride, a.k, a.k_stride);
+  enter(to, a.q_out, a.qo_stride, a.k_out, a.ko_stride);
+  // Rows are requested kAhead items before they are worked on, the first ones before the angles are formed. (Rows of an item that
+  // are not there hold what they held.)
+  int to_load = left;
   auto load = [&](Chunks<IO>& v) {
-    if (next == nq) src = place(a.q, a.q_stride, a.k, a.k_stride, nq);
-    if (next < last && there(next)) v.load(src, c0, c1);
-    else v.clear();
-    src += by;
-    ++next;
+    if (to_load <= 0) return;
+    --to_load;
+    if (in.head + row < in.heads) v.load(in.p, c0, c1);
+    step(in, a.q, a.q_stride, a.k, a.k_stride);
   };
   Chunks<IO> v[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(v[i]);
-  float wt[2][8];
-  float2 (&w2)[8] = *reinterpret_cast<float2(*)[8]>(wt);
-  auto weigh = [&](const void* weight) {
-    if (!weight) return;
-    Chunks<IO> wc;
-    wc.load(weight, c0, c1);
-    wc.get(wt);
-  };
-  weigh(first < nq ? a.q_weight : a.k_weight);
+  for (int i = 0; i < kAhead; ++i) {
+    v[i].clear();
+    load(v[i]);
+  }
+  for (int i = threadIdx.x; i < 2 * (D / 8); i += 32 * kWarps)
+    if (const void* w = i < D / 8 ? a.q_weight : a.k_weight) {
+      Eight<IO> e;
+      float x[8];
+      e.load(w, 8 * (i % (D / 8)));
+      e.get(x);
+      for (int j = 0; j < 8; ++j) weight_s[i / (D / 8)][j / 4 * (D / 2) + 4 * (i % (D / 8)) + j % 4] = x[j];
+    }
+  __syncthreads();
+  if (left == 0) return;
   // angles of this thread's eight pairs, formed by pairs across the warp
   float2 cs[4], sn[4];
-  if (R > 0) {
+  auto angles = [&]() {
+    if (R == 0) return;
     for (int i = lane; i < R / 2; i += 32) {
-      const float2 x = turned_by(a.positions[rot.axis[i] * a.n_tokens + t], rot.turn[i]);
+      const float2 x = turned_by(a.positions[axis_s[i] * a.n_tokens + to.t], turn_s[i]);
       mine[i] = x.x;
       mine[128 + i] = x.y;
     }
@@ -145,17 +171,11 @@ __global__ void __launch_bounds__(kWarps * 32, 5) norm_rotate_kernel(const RopeA
       }
     }
     __syncwarp();
-  }
-  int w = first;
+  };
+  angles();
   do {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (w >= last) break;
-        if (w == nq) {
-          dst = const_cast<char*>(place(a.q_out, a.qo_stride, a.k_out, a.ko_stride, nq));
-          weigh(a.k_weight);
-        }
-        const bool weighed = w < nq ? a.q_weight != nullptr : a.k_weight != nullptr;
         float y[2][8];
         float2 (&y2)[8] = *reinterpret_cast<float2(*)[8]>(y);
         v[i].get(y);
@@ -170,16 +190,22 @@ __global__ void __launch_bounds__(kWarps * 32, 5) norm_rotate_kernel(const RopeA
           const float f = rsqrtf(sum * (1.f / D) + a.eps);
 #pragma unroll
           for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
-          if (weighed) {
+          if (to.k ? a.k_weight != nullptr : a.q_weight != nullptr) {
+            const float* wt = weight_s[to.k];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], w2[e]);
+            for (int e = 0; e < 8; e += 2) {
+              const float4 x = *reinterpret_cast<const float4*>(wt + e / 2 % 2 * (D / 2) + 4 * (e < 4 ? c0 : c1));
+              y2[e] = __fmul2_rn(y2[e], make_float2(x.x, x.y));
+              y2[e + 1] = __fmul2_rn(y2[e + 1], make_float2(x.z, x.w));
+            }
           }
         }
         if (turned) {
           if constexpr (HALVES) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 u = y2[e], x = y2[e + 4], m = __fmul2_rn(x, sn[e]);
+              const float2 u = y2[e], x = y2[e + 4];
+              const float2 m = __fmul2_rn(x, sn[e]);
               y2[e] = __ffma2_rn(u, cs[e], make_float2(-m.x, -m.y));
               y2[e + 4] = __ffma2_rn(u, sn[e], __fmul2_rn(x, cs[e]));
             }
@@ -231,24 +257,21 @@ __global__ void __launch_bounds__(kWarps * 32, 5) norm_rotate_kernel(const RopeA
 #pragma unroll
           for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
         }
-        if (there(w)) Chunks<IO>::store(dst, d0, d1, y);
-        dst += by;
-        ++w;
+        if (to.head + row < to.heads) Chunks<IO>::store(to.p, d0, d1, y);
+        if (--left == 0) break;
+        if (step(to, a.q_out, a.qo_stride, a.k_out, a.ko_stride) && !to.k) angles();
       }
-  } while (w < last);
+  } while (left > 0);
 }
 
 template <int D>
 cudaError_t launch_rope(const RopeArgs& a, const kvarn_rotary_t& rot, cudaStream_t st) {
   constexpr int ROWS = 32 / (D / 16);
-  // a token's heads are divided among warps as long as there are warps without work
   const int64_t n = (a.Hq + ROWS - 1) / ROWS + (a.Hkv + ROWS - 1) / ROWS;
-  const int64_t slots = 16 * (int64_t)sm_count();
-  int64_t parts = a.n_tokens < slots ? (slots + a.n_tokens - 1) / a.n_tokens : 1;
-  if (parts > n) parts = n;
-  LaunchCfg L(dim3((unsigned)((a.n_tokens * parts + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, a.flags);
+  const int64_t resident = kCtas * (int64_t)sm_count(), ctas = (a.n_tokens * n + kWarps - 1) / kWarps;
+  LaunchCfg L(dim3((unsigned)(ctas < resident ? ctas : resident)), dim3(kWarps * 32), 0, st, a.flags);
   const bool halves = rot.rotary_dim > 0 && rot.pairing == KVARN_PAIRS_HALVES;
-  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&L.cfg, kernel, a, rot, (int)parts); };
+  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&L.cfg, kernel, a, rot); };
   switch (a.io) {
     case KVARN_IO_F32: return halves ? go(norm_rotate_kernel<D, 0, true>) : go(norm_rotate_kernel<D, 0, false>);
     case KVARN_IO_F16: return halves ? go(norm_rotate_kernel<D, 1, true>) : go(norm_rotate_kernel<D, 1, false>);

@@ -96,6 +96,23 @@ def test_numbers_of_tokens(T):
                37 * some[None], freq, [0] * (D // 2), False, True)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(1, 0), (5, 3), (17, 1)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_warps_that_take_many_tokens(D, Hq, Hkv):
+    """Shares that begin in the middle of a token, end in another and span whole ones: each token as if alone."""
+    T = 12345
+    q, k = _rows(9, (T, Hq, D), "bf16"), _rows(10, (T, Hkv, D), "bf16") if Hkv else None
+    qw, kw = _rows(2, (D,), "bf16"), _rows(3, (D,), "bf16") if Hkv else None
+    pos = torch.arange(T, device=DEV) * 3
+    plan = kvarn.rotary(D // 2)
+    call = lambda i: kvarn.norm_rotate(q[i], None if k is None else k[i], pos[i], plan, q_weight=qw, k_weight=kw, eps=1e-6)
+    got = call(slice(None))
+    for lo in range(0, T, 1000):
+        part = call(slice(lo, min(lo + 1000, T)))
+        for x, y in zip(got, part):
+            assert y is None or torch.equal(x[lo:lo + 1000], y)
+
+
 def test_parts_alone():
     """A norm without weights or rotation, a transform alone (rotate_query's, to rounding), nothing at all."""
     q, k = _rows(9, (6, 3, 128), "f32"), _rows(10, (6, 2, 128), "f32")
