@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = tid & 127, half = (tid >> 7) & 1;
   const int kvh = blockIdx.y, share = blockIdx.z;
-  const int ppc = 128 / a.G, i0 = blockIdx.x * ppc;
+  // The last rows first where they see much more than the first: 8,192 positions from 0 on, 32 / 8 heads of 128, 437 us
+  // instead of 449, 2,048 64 instead of 69 (but 512 over 60k 344 instead of 337).
+  const int ppc = 128 / a.G, i0 = (int)(3LL * a.C > a.pos0 ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * ppc;
   const int my_g = row / ppc, my_i = i0 + row % ppc;
   const bool my_valid = my_i < a.C && my_g < a.G;
   const int64_t my_pos = a.pos0 + my_i;
@@ -619,6 +621,32 @@ __global__ void __launch_bounds__(256) join_kernel(const Att8Args s) {
   io_st4(a.out, a.io, r * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
+// Key shares of `ctas` CTAs that each see `blocks` blocks: as many as fill the SMs once. What is more than half of them
+// or more, but no whole number of rounds, is shared where the rounds then cost less (WHOLE: never): a CTA takes as long to begin and
+// end as 32 blocks, the join as 16 and 8 per share, and kRounds rounds bound the partial results. (head_dim 128, bf16, 160
+// CTAs, us without / with shares: 63 blocks 63 / 73, 235 173 / 158, 938 623 / 476; 320 CTAs, 938 blocks 904 / 806. At
+// head_dim 64 158 / 133, 256 310 / 282, fp32 310 / 254 with 235 blocks.)
+constexpr int kRounds = 5, kShareFrom = 128;  // (no gain with so few blocks)
+template <bool WHOLE>
+int key_shares(int64_t ctas, int64_t blocks) {
+  const int64_t sms = sm_count();
+  int64_t shares = ctas > 0 ? sms / ctas : 1;
+  const int64_t most = blocks / 4;  // two pairs of blocks per share at least
+  if (shares > most) shares = most;
+  if (shares > 64) shares = 64;
+  if (shares < 1) shares = 1;
+  if (WHOLE || 2 * ctas <= sms || blocks <= kShareFrom) return (int)shares;
+  double least = 0;
+  for (int64_t n = 1; n * ctas <= kRounds * sms || n == 1; ++n) {
+    const double cost = (double)((n * ctas + sms - 1) / sms) * ((double)blocks / n + 32) + (n > 1 ? 16 + 8 * n : 0);
+    if (n == 1 || cost < least) {
+      least = cost;
+      shares = n;
+    }
+  }
+  return (int)shares;
+}
+
 // Workspace of a call over n_tblk tiles and win_vis window rows, with or without scales.
 Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D, bool fp32, bool scaled) {
   Plan8 p;
@@ -628,11 +656,7 @@ Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D, bool fp32, b
   p.head_imgs = 2LL * (p.n_tsub + p.n_wsub);
   p.row_blocks = (int)(((int64_t)C + ppc - 1) / ppc);
   const int64_t ctas = (int64_t)p.row_blocks * Hkv;
-  int64_t shares = ctas > 0 ? sm_count() / ctas : 1;
-  const int64_t most = (p.n_tsub + p.n_wsub) / 4;  // two pairs of blocks per share at least
-  if (shares > most) shares = most;
-  if (shares > 64) shares = 64;
-  p.shares = shares < 1 ? 1 : (int)shares;
+  p.shares = scaled ? key_shares<true>(ctas, p.n_tsub + p.n_wsub) : key_shares<false>(ctas, p.n_tsub);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   p.off_scale = up((size_t)Hkv * p.head_imgs * KB * D * 2);
   p.off_ml = p.off_scale + (scaled ? up((size_t)Hkv * (p.n_tsub + p.n_wsub) * 64) : 0);

@@ -169,10 +169,11 @@ size_t prefill4_ws_bytes(int C, int n_tiles, int Hq, int Hkv, int D) {
   const size_t few = up((size_t)entries * sizeof(float2)) + up((size_t)entries * D * sizeof(float));
   if (groups * Hkv <= 6 * heads) return few;  // (few_rows holds for every smaller call)
   // Images: those of this call, and the results of key shares, of which there are only as many as fill the SMs
-  // once (128 rows to a CTA), and O's emptied sums, of a CTA's rows each.
+  // once, or kRounds times (128 rows to a CTA), and O's emptied sums, of a CTA's rows each.
   const Plan8 p = plan8(C, n_tiles, 0, Hq, Hkv, D, true, false);
   const int64_t ctas = (int64_t)p.row_blocks * Hkv;
-  const size_t rows = 128 * (size_t)sms, sums = 128 * (size_t)(ctas > sms ? ctas : sms);
+  const int64_t shared = 2 * ctas > sms && p.n_tsub > kShareFrom ? kRounds * sms : sms;
+  const size_t rows = 128 * (size_t)shared, sums = 128 * (size_t)(ctas > shared ? ctas : shared);
   const size_t images = p.off_ml + up(rows * sizeof(float2)) + up(rows * D * sizeof(float)) + up(sums * D * sizeof(float));
   return few > images ? few : images;
 }

@@ -647,6 +647,23 @@ def test_prefill_of_many_blocks(Hkv, C, n, io):
         _check_prefill(c, q, n - C, c.prefill(q, n - C))
 
 
+@pytest.mark.parametrize("D,io", [(64, "f32"), (128, "bf16"), (256, "f32")])
+def test_prefill_of_more_blocks_than_one_round(D, io):
+    """More blocks of rows than SMs over a long context: keys in shares that take several rounds. Rows of the first and
+    the last blocks."""
+    H, G, C, n = 8, 8, 330, 11000
+    c, table, _, rows_of = _shared(D + 9, D, H, [n])
+    q = _query(D, (C, H * G, D), io)
+    out = kvarn.prefill_attention4(q, n - C, c.tiles, table[0], c.lay)
+    at = [0, 1, 15, 16, 200, 319, 320, 329]
+    for h in (0, 3, 7):
+        k, v = rows_of(0, h, n)
+        qn = q[at, h * G:(h + 1) * G].double().cpu().numpy().reshape(-1, D)
+        want, p, bound = attend(qn, k, v, D ** -0.5, np.repeat(n - C + 1 + np.array(at), G), np.ones(n), 2.0 ** -33)
+        check(out[at, h * G:(h + 1) * G].reshape(-1, D), want, bound, q.dtype, 0.0 if io == "f32" else 2.0 ** -11,
+              p @ np.abs(v))
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_prefill_of_long_fp32_contexts(D):
     """O is emptied into rounded sums every so many blocks: several times, under growing scores."""
