@@ -483,6 +483,10 @@ def _fit(device, *checks):
 
 def _io(t, name):
     """A contiguous CUDA tensor of a query/output type: its KVARN_IO_* code and device index."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous():
+        io = IO_TYPES.get(t.dtype)
+        if io is not None:
+            return io, t.get_device()
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype not in IO_TYPES:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     _dev(t, name, getattr(t, "dtype", None))
@@ -696,18 +700,18 @@ def layout4(head_dim: int) -> Layout4:
 def _rows_of(t, name, dims, dtype=None, device=None):
     """A CUDA tensor [..., heads, D] of `dims` (3 or 4) dimensions whose heads lie side by side and whose
     rows (all but the last two axes) are a constant stride apart, as a slice of a packed
-    product's result: its stride in elements."""
+    product's result: its stride in elements, and its shape."""
     if (isinstance(t, torch.Tensor) and t.is_cuda and (t.dtype in IO_TYPES if dtype is None else t.dtype is dtype)
             and (device is None or t.get_device() == device)):
         shape = t.shape  # (the usual strides, without more ado)
         if len(shape) == dims:
             if t.is_contiguous():
-                return shape[-1] * shape[-2]
+                return shape[-1] * shape[-2], shape
             if dims == 3:
                 row, head, one = t.stride()
                 if one == 1 and head == shape[2] and shape[0] > 1:
-                    return row
-    return _rows_checked(t, name, dims, dtype, device)
+                    return row, shape
+    return _rows_checked(t, name, dims, dtype, device), t.shape
 
 
 def _rows_checked(t, name, dims, dtype, device):
@@ -757,15 +761,15 @@ def _counts4(counts, B, device):
 
 def _rows4(k, v, tiles, tile_table, first, lay, counts, names, what):
     """What write_rows4 and read_rows4 check alike: the strides, sizes and pointers of a call."""
-    k_stride = _rows_of(k, names[0], 4)
-    device = k.get_device()
-    v_stride = _rows_of(v, names[1], 4, k.dtype, device)
+    k_stride, shape = _rows_of(k, names[0], 4)
+    device, dtype = k.get_device(), k.dtype
+    v_stride, v_shape = _rows_of(v, names[1], 4, dtype, device)
     _fit(device, ("tiles", tiles, torch.uint8), ("tile_table", tile_table, torch.int64), (names[2], first, torch.int32))
-    shape, table = k.shape, tile_table.shape
+    table = tile_table.shape
     B, T, Hkv, D = shape
-    if v.shape != shape or len(table) != 3 or table[0] != B or table[1] != Hkv or first.numel() != B:
+    if v_shape != shape or len(table) != 3 or table[0] != B or table[1] != Hkv or first.numel() != B:
         raise ValueError(f"{what}: inconsistent shapes")
-    return device, k_stride, v_stride, _counts4(counts, B, device), (IO_TYPES[k.dtype], B, T, Hkv, D, table[2],
+    return device, k_stride, v_stride, _counts4(counts, B, device), (IO_TYPES[dtype], B, T, Hkv, D, table[2],
                                                                      _layout4_for(lay, D, what))
 
 
@@ -908,21 +912,20 @@ def norm_rotate(q, k, positions, rot, q_weight=None, k_weight=None, eps=None, ha
     Walsh-Hadamard transform. q [T][Hq][D] and k [T][Hkv][D] (or None) fp32, fp16 or bf16, heads contiguous and
     tokens a constant stride apart; positions int64 [T], or [axes][T]. Outputs are new tensors, or q_out and
     k_out (q and k themselves: in place). Returns (q_out, k_out)."""
-    q_stride = _rows_of(q, "q", 3)
-    device, dtype, shape = q.get_device(), q.dtype, q.shape
+    q_stride, shape = _rows_of(q, "q", 3)
+    device, dtype = q.get_device(), q.dtype
     T, Hq, D = shape
     if q_out is None:
         q_out = _result_rows(q, stream)
-    qo_stride = _rows_of(q_out, "q_out", 3, dtype, device)
-    good = q_out.shape == shape
+    qo_stride, o_shape = _rows_of(q_out, "q_out", 3, dtype, device)
+    good = o_shape == shape
     if k is not None:
-        k_stride = _rows_of(k, "k", 3, dtype, device)
+        k_stride, shape = _rows_of(k, "k", 3, dtype, device)
         if k_out is None:
             k_out = _result_rows(k, stream)
-        ko_stride = _rows_of(k_out, "k_out", 3, dtype, device)
-        shape = k.shape
+        ko_stride, o_shape = _rows_of(k_out, "k_out", 3, dtype, device)
         Hkv, k_in, k_to = shape[1], k.data_ptr(), k_out.data_ptr()
-        good = good and shape[0] == T and shape[2] == D and k_out.shape == shape
+        good = good and shape[0] == T and shape[2] == D and o_shape == shape
     else:
         if k_out is not None or k_weight is not None:
             raise ValueError("norm_rotate: k_out or k_weight without k")
@@ -933,26 +936,29 @@ def norm_rotate(q, k, positions, rot, q_weight=None, k_weight=None, eps=None, ha
     if rot is not None:
         _fit(device, ("positions", positions, torch.int64))
         axes = positions.shape
-        if axes[-1:] != (T,) or positions.numel() != rot.n_axes * T:
+        if not axes or axes[-1] != T or positions.numel() != rot.n_axes * T:
             raise ValueError("positions must be [T], or [axes][T] with the plan's axes")
         at, plan = positions.data_ptr(), ctypes.byref(rot)
-    weights = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            weights.append(None)
-            continue
-        _fit(device, (name, w, dtype))
-        if w.numel() != D:
-            raise ValueError(f"{name} must have head_dim elements")
-        if eps is None:
-            raise ValueError(f"{name} without a norm (eps)")
-        weights.append(w.data_ptr())
+    q_scale = k_scale = None
+    if q_weight is not None:
+        q_scale = _weight_ptr(q_weight, "q_weight", device, dtype, D, eps)
+    if k_weight is not None:
+        k_scale = _weight_ptr(k_weight, "k_weight", device, dtype, D, eps)
     if eps is not None and not eps >= 0:
         raise ValueError("eps must not be negative")
     _call(device, "kvarn_norm_rotate", stream, q.data_ptr(), q_stride, k_in, k_stride, IO_TYPES[dtype], T, Hq, Hkv, D,
-          weights[0], weights[1], -1.0 if eps is None else float(eps), at, plan, int(bool(hadamard)), q_out.data_ptr(),
+          q_scale, k_scale, -1.0 if eps is None else float(eps), at, plan, int(bool(hadamard)), q_out.data_ptr(),
           qo_stride, k_to, ko_stride, int(flags))
     return q_out, k_out
+
+
+def _weight_ptr(w, name, device, dtype, D, eps):
+    _fit(device, (name, w, dtype))
+    if w.numel() != D:
+        raise ValueError(f"{name} must have head_dim elements")
+    if eps is None:
+        raise ValueError(f"{name} without a norm (eps)")
+    return w.data_ptr()
 
 
 def _result_rows(like, stream):
