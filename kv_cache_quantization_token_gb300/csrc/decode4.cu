@@ -8,6 +8,8 @@
 //                  the workspace, in the slot CTA + segment.
 //   merge kernel   joins the pieces of a head, found by the same arithmetic, and, on request, adds up tiles' weights.
 //
+// Short tables need neither: a CTA takes a segment by itself, several tiles side by side, and writes its rows and weights.
+//
 // The warps need no exchange while they run because a run's scores and values both stay in one warp: the codes
 // become fp16 numbers in registers, exactly (unit_values), as the A operand of mma.sync m16n8k16, for the scores
 // (16 tokens x 16 channels) and, read transposed, for the values (16 channels x 16 tokens). Queries and
@@ -22,7 +24,7 @@
 // What bounds it: HBM in batches (32 ragged sequences of up to 32k tokens, head_dim 256, 755 MB in 120 us: 6.3 TB/s, 92%
 // of the measured copy rate), instructions otherwise: 2.4 per code at head_dim 128, of which 1.4 unpack it (four
 // sequences of 64k tokens, 302 MB in 58.3 us, 5.2 TB/s, at 2.6 instructions per cycle of 4; head_dim 64 3.9 TB/s in 38.7
-// us; groups of eight heads 3.7 TB/s). Short calls are a chain of latencies: length, table, copy, exchange, merge (3 tiles
+// us; groups of eight heads 3.7 TB/s). Short calls are a chain of latencies: length, table, copy, exchange, merge (4 tiles
 // 5.5 us; 16k tokens 10.2 against 2.8 of bytes). On the way from 172.7 us for the batch: run-time mask base (142),
 // shares by actual lengths instead of items of a fixed span (127), the merge's arithmetic ahead of its wait and typed
 // query loads (120). Not kept: two runs to a step (fewer exchanges, but fewer warps: 81 us against 74 at the time),
