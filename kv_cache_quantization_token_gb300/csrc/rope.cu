@@ -13,10 +13,10 @@
 // exactly, whatever the position, and costs three multiply-adds where an fp64 product and its reduction
 // would take GB300's slow fp64 units. The quarter turn nearest to it is taken off before it is rounded to fp32.
 //
-// What bounds it: instructions beside memory. 8,192 tokens of 32 + 8 heads of 128, bf16, packed (168 MB): 31.5 us, 5.3
-// TB/s (78% of the copy rate). A warp per token that comes and goes took 37.4, and 38.2 with the frequencies read from the
-// launch's arguments, which are served one index at a time (1,337 tokens with transform: 6.4, 7.1, 8.4); twenty warps of 96
-// registers instead of sixteen of 128 33.5, two items under way instead of three 33.1; angles of a CTA's tokens in shared
+// What bounds it: instructions beside memory. 8,192 tokens of 32 + 8 heads of 128, bf16, packed (168 MB): 30.8 us, 5.4
+// TB/s (80% of the copy rate). A warp per token that comes and goes took 37.4, and 38.2 with the frequencies read from the
+// launch's arguments, which are served one index at a time (1,337 tokens with transform: 6.3, 7.1, 8.4); twenty warps of 96
+// registers instead of sixteen of 128 33.5, two items under way instead of three 32.1; angles of a CTA's tokens in shared
 // memory 47 to 58.
 #include "cache4.cuh"
 
@@ -35,17 +35,17 @@ struct Chunks {
     for (auto& e : c)
       for (auto& x : e.w) x = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void load(const void* p, int c0, int c1) {
-    c[0].load(p, 8 * c0);
-    c[1].load(p, 8 * c1);
+  __device__ __forceinline__ void load(const char* p, int apart) {
+    c[0].load(p, 0);
+    c[1].load(p + apart, 0);
   }
   __device__ __forceinline__ void get(float (&x)[2][8]) const {
     c[0].get(x[0]);
     c[1].get(x[1]);
   }
-  __device__ __forceinline__ static void store(void* p, int c0, int c1, const float (&x)[2][8]) {
-    Eight<IO>::store(p, 8 * c0, x[0]);
-    Eight<IO>::store(p, 8 * c1, x[1]);
+  __device__ __forceinline__ static void store(char* p, int apart, const float (&x)[2][8]) {
+    Eight<IO>::store(p, 0, x[0]);
+    Eight<IO>::store(p + apart, 0, x[1]);
   }
 };
 
@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
   const int64_t items = a.n_tokens * n, warps = (int64_t)gridDim.x * kWarps, me = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
   const int64_t begin = items * me / warps;
   int left = (int)(items * (me + 1) / warps - begin);
-  const int row = lane / L;
-  // Where the next item lies: heads head .. of the heads of q or k of token t, row `row` of them at p.
+  const int row = lane / L, apart = 8 * SIZE * (c1 - c0);
+  // Where the next item lies: heads head .. of the heads of q or k of token t, this thread's first chunk at p.
   struct Cursor {
     char* p;
     int64_t t;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
   auto enter = [&](Cursor& c, const void* q, int64_t q_stride, const void* k, int64_t k_stride) {
     c.heads = c.k ? a.Hkv : a.Hq;
     c.p = const_cast<char*>(static_cast<const char*>(c.k ? k : q)) + c.t * (c.k ? k_stride : q_stride) * SIZE +
-          (int64_t)(c.head + row) * (SIZE * D);
+          (int64_t)(c.head + row) * (SIZE * D) + 8 * SIZE * c0;
   };
   auto step = [&](Cursor& c, const void* q, int64_t q_stride, const void* k, int64_t k_stride) {  // true: to another lot of heads
     c.p += ROWS * SIZE * D;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
   auto load = [&](Chunks<IO>& v) {
     if (to_load <= 0) return;
     --to_load;
-    if (in.head + row < in.heads) v.load(in.p, c0, c1);
+    if (in.head + row < in.heads) v.load(in.p, apart);
     step(in, a.q, a.q_stride, a.k, a.k_stride);
   };
   Chunks<IO> v[kAhead];
@@ -172,7 +172,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
     }
     __syncwarp();
   };
+  const float* wt = nullptr;
+  bool weighed = false;
+  auto weigh = [&]() {
+    wt = weight_s[to.k] + 4 * c0;
+    weighed = to.k ? a.k_weight != nullptr : a.q_weight != nullptr;
+  };
   angles();
+  weigh();
   do {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
@@ -190,11 +197,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
           const float f = rsqrtf(sum * (1.f / D) + a.eps);
 #pragma unroll
           for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
-          if (to.k ? a.k_weight != nullptr : a.q_weight != nullptr) {
-            const float* wt = weight_s[to.k];
+          if (weighed) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-              const float4 x = *reinterpret_cast<const float4*>(wt + e / 2 % 2 * (D / 2) + 4 * (e < 4 ? c0 : c1));
+              const float4 x = *reinterpret_cast<const float4*>(wt + e / 2 % 2 * (D / 2) + (e < 4 ? 0 : apart / (2 * SIZE)));
               y2[e] = __fmul2_rn(y2[e], make_float2(x.x, x.y));
               y2[e + 1] = __fmul2_rn(y2[e + 1], make_float2(x.z, x.w));
             }
@@ -218,7 +224,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
             }
           }
         }
-        int d0 = c0, d1 = c1;
+        char* p = to.p;
+        int then = apart;
         if (a.hadamard) {
           if (!bits) {  // to chunks in order, through shared memory
             float* of = mine + (lane - l) * 16;
@@ -228,8 +235,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
               *reinterpret_cast<float4*>(of + 8 * c1 + e) = make_float4(y[1][e], y[1][e + 1], y[1][e + 2], y[1][e + 3]);
             }
             __syncwarp();
-            d0 = 2 * l;
-            d1 = 2 * l + 1;
+            p += 8 * SIZE * (2 * l - c0);
+            then = 8 * SIZE;
 #pragma unroll
             for (int e = 0; e < 16; ++e) y[e / 8][e % 8] = of[16 * l + e];
             __syncwarp();
@@ -257,9 +264,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
 #pragma unroll
           for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
         }
-        if (to.head + row < to.heads) Chunks<IO>::store(to.p, d0, d1, y);
+        if (to.head + row < to.heads) Chunks<IO>::store(p, then, y);
         if (--left == 0) break;
-        if (step(to, a.q_out, a.qo_stride, a.k_out, a.ko_stride) && !to.k) angles();
+        if (step(to, a.q_out, a.qo_stride, a.k_out, a.ko_stride)) {
+          if (!to.k) angles();
+          weigh();
+        }
       }
   } while (left > 0);
 }
