@@ -94,7 +94,7 @@ __device__ __forceinline__ unsigned group_max(unsigned m) {  // over the two thr
 // Row t and head h of sequence blockIdx.y, of the threads that hold it, and where its token lies.
 struct Place {
   int64_t row;      // b * T + t
-  int h;
+  int t, h;
   bool there;       // a row to be moved
   bool inside;      // its token has a place in the table
   bool good;        // the table's record lies inside the pool
@@ -103,24 +103,27 @@ struct Place {
 };
 
 template <int D>
-__device__ __forceinline__ Place place_of(const Rows4Args& a) {
+__device__ __forceinline__ Place row_of(const Rows4Args& a) {
   constexpr int L = D / 16;
   Place p{};
-  const int b = blockIdx.y, i = blockIdx.x * (256 / L) + threadIdx.x / L, t = i / a.Hkv;
-  p.h = i - t * a.Hkv;
-  p.row = (int64_t)b * a.T + t;
-  p.there = t < a.T && !(a.counts && t >= a.counts[b]);
-  if (!p.there) return p;
-  const int first = a.first[b];
-  const int64_t tok = (int64_t)first + t;
+  const int b = blockIdx.y, i = blockIdx.x * (256 / L) + threadIdx.x / L;
+  p.t = i / a.Hkv;
+  p.h = i - p.t * a.Hkv;
+  p.row = (int64_t)b * a.T + p.t;
+  p.there = p.t < a.T && !(a.counts && p.t >= a.counts[b]);
+  return p;
+}
+template <int D>
+__device__ __forceinline__ void find(const Rows4Args& a, int first, Place& p) {  // of a row that is there
+  const int b = blockIdx.y;
+  const int64_t tok = (int64_t)first + p.t;
   p.inside = first >= 0 && tok < (int64_t)kTile * a.max_tiles;
-  if (!p.inside) return p;
+  if (!p.inside) return;
   const int tile = (int)(tok / kTile);
   const int64_t off = a.tile_table[((int64_t)b * a.Hkv + p.h) * a.max_tiles + tile];
   p.good = !(off & 15) && off >= 0 && off <= a.tiles_bytes - Run4<D>::kRecord;
   p.r = (int)tok % kRun;
   p.off = off + (int)tok % kTile / kRun * Run4<D>::kBytes;
-  return p;
 }
 
 template <int D, int IO>
@@ -130,20 +133,22 @@ __global__ void __launch_bounds__(256) write4_kernel(const Rows4Args a) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, c = 16 * (threadIdx.x % L);
-  const Place p = place_of<D>(a);
-  if (p.there && c == 0) {
-    if (!p.inside) report(a.err, KVARN_DEVERR_WINDOW);
-    else if (!p.good) report(a.err, KVARN_DEVERR_RECORD);
-  }
-  const bool move = p.there && p.inside && p.good;
+  const int first = a.first[blockIdx.y];
+  Place p = row_of<D>(a);
   Eight<IO> ek[2]{}, ev[2]{};
-  if (move) {
+  if (p.there) {  // (requested before the row's place is known)
     const int64_t at_k = p.row * a.k_stride + (int64_t)p.h * D + c, at_v = p.row * a.v_stride + (int64_t)p.h * D + c;
     ek[0].load(a.k, at_k);
     ek[1].load(a.k, at_k + 8);
     ev[0].load(a.v, at_v);
     ev[1].load(a.v, at_v + 8);
+    find<D>(a, first, p);
+    if (c == 0) {
+      if (!p.inside) report(a.err, KVARN_DEVERR_WINDOW);
+      else if (!p.good) report(a.err, KVARN_DEVERR_RECORD);
+    }
   }
+  const bool move = p.there && p.inside && p.good;
   const unsigned mk = group_max(max(largest<IO>(ek[0]), largest<IO>(ek[1])));
   const unsigned mv = group_max(max(largest<IO>(ev[0]), largest<IO>(ev[1])));
   const unsigned bad = __ballot_sync(0xffffffffu, max(mk, mv) > __float_as_uint(KVARN_MAX4));
@@ -177,8 +182,10 @@ __global__ void __launch_bounds__(256) read4_kernel(const Rows4Args a, uint32_t 
   pdl_wait();
   // eight channels of the row's lower half and eight of its upper, so that a warp's stores cover whole sectors
   const int c0 = 8 * (threadIdx.x % L);
-  const Place p = place_of<D>(a);
+  const int first = a.first[blockIdx.y];
+  Place p = row_of<D>(a);
   if (!p.there) return;
+  find<D>(a, first, p);
   if (c0 == 0) {
     if (!p.inside) report(a.err, KVARN_DEVERR_WINDOW);
     else if (!p.good) report(a.err, KVARN_DEVERR_RECORD);
