@@ -621,11 +621,11 @@ __global__ void __launch_bounds__(256) join_kernel(const Att8Args s) {
   io_st4(a.out, a.io, r * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
-// Key shares of `ctas` CTAs that each see `blocks` blocks: as many as fill the SMs once. What is more than half of them
-// or more, but no whole number of rounds, is shared where the rounds then cost less (WHOLE: never): a CTA takes as long to begin and
-// end as 32 blocks, the join as 16 and 8 per share, and kRounds rounds bound the partial results. (head_dim 128, bf16, 160
-// CTAs, us without / with shares: 63 blocks 63 / 73, 235 173 / 158, 938 623 / 476; 320 CTAs, 938 blocks 904 / 806. At
-// head_dim 64 158 / 133, 256 310 / 282, fp32 310 / 254 with 235 blocks.)
+// Key shares of `ctas` CTAs that each see `blocks` blocks: as many as fill the SMs once. Where CTAs already fill more than
+// half of them, in rounds that need not be whole, keys are shared if the rounds then cost less (WHOLE: never): a CTA takes
+// as long to begin and end as 32 blocks, the join as 16 and 8 per share; kRounds rounds bound the partial results.
+// (head_dim 128, bf16, 160 CTAs, us without / with shares: 63 blocks 63 / 73, 235 173 / 158, 938 623 / 464; 320 CTAs, 938
+// blocks 904 / 805. At head_dim 64 158 / 136, 256 310 / 282, fp32 310 / 263 with 235 blocks.)
 constexpr int kRounds = 5, kShareFrom = 128;  // (no gain with so few blocks)
 template <bool WHOLE>
 int key_shares(int64_t ctas, int64_t blocks) {

@@ -182,95 +182,95 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rotate_kernel(const R
   weigh();
   do {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        float y[2][8];
-        float2 (&y2)[8] = *reinterpret_cast<float2(*)[8]>(y);
-        v[i].get(y);
-        load(v[i]);
-        if (a.eps >= 0.f) {
-          float2 ss = __fmul2_rn(y2[0], y2[0]);
+    for (int i = 0; i < kAhead; ++i) {
+      float y[2][8];
+      float2 (&y2)[8] = *reinterpret_cast<float2(*)[8]>(y);
+      v[i].get(y);
+      load(v[i]);
+      if (a.eps >= 0.f) {
+        float2 ss = __fmul2_rn(y2[0], y2[0]);
 #pragma unroll
-          for (int e = 1; e < 8; ++e) ss = __ffma2_rn(y2[e], y2[e], ss);
-          float sum = ss.x + ss.y;
+        for (int e = 1; e < 8; ++e) ss = __ffma2_rn(y2[e], y2[e], ss);
+        float sum = ss.x + ss.y;
 #pragma unroll
-          for (int m = L / 2; m; m >>= 1) sum += shfl_xor(sum, m);
-          const float f = rsqrtf(sum * (1.f / D) + a.eps);
+        for (int m = L / 2; m; m >>= 1) sum += shfl_xor(sum, m);
+        const float f = rsqrtf(sum * (1.f / D) + a.eps);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
-          if (weighed) {
+        for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
+        if (weighed) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float4 x = *reinterpret_cast<const float4*>(wt + e / 2 % 2 * (D / 2) + (e < 4 ? 0 : apart / (2 * SIZE)));
-              y2[e] = __fmul2_rn(y2[e], make_float2(x.x, x.y));
-              y2[e + 1] = __fmul2_rn(y2[e + 1], make_float2(x.z, x.w));
-            }
+          for (int e = 0; e < 8; e += 2) {
+            const float4 x = *reinterpret_cast<const float4*>(wt + e / 2 % 2 * (D / 2) + (e < 4 ? 0 : apart / (2 * SIZE)));
+            y2[e] = __fmul2_rn(y2[e], make_float2(x.x, x.y));
+            y2[e + 1] = __fmul2_rn(y2[e + 1], make_float2(x.z, x.w));
           }
-        }
-        if (turned) {
-          if constexpr (HALVES) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 u = y2[e], x = y2[e + 4];
-              const float2 m = __fmul2_rn(x, sn[e]);
-              y2[e] = __ffma2_rn(u, cs[e], make_float2(-m.x, -m.y));
-              y2[e + 4] = __ffma2_rn(u, sn[e], __fmul2_rn(x, cs[e]));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float ce = e & 1 ? cs[e / 2].y : cs[e / 2].x, se = e & 1 ? sn[e / 2].y : sn[e / 2].x;
-              const float2 u = y2[e];
-              y2[e] = make_float2(fmaf(u.x, ce, -u.y * se), fmaf(u.x, se, u.y * ce));
-            }
-          }
-        }
-        char* p = to.p;
-        int then = apart;
-        if (a.hadamard) {
-          if (!bits) {  // to chunks in order, through shared memory
-            float* of = mine + (lane - l) * 16;
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              *reinterpret_cast<float4*>(of + 8 * c0 + e) = make_float4(y[0][e], y[0][e + 1], y[0][e + 2], y[0][e + 3]);
-              *reinterpret_cast<float4*>(of + 8 * c1 + e) = make_float4(y[1][e], y[1][e + 1], y[1][e + 2], y[1][e + 3]);
-            }
-            __syncwarp();
-            p += 8 * SIZE * (2 * l - c0);
-            then = 8 * SIZE;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e / 8][e % 8] = of[16 * l + e];
-            __syncwarp();
-          }
-          // within a pair of elements, then pairs at a time
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y2[e] = make_float2(y2[e].x + y2[e].y, y2[e].x - y2[e].y);
-#pragma unroll
-          for (int m = 1; m < 8; m <<= 1)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (!(e & m)) {
-                const float2 u = y2[e], x = y2[e | m];
-                y2[e] = __fadd2_rn(u, x);
-                y2[e | m] = __ffma2_rn(x, make_float2(-1.f, -1.f), u);
-              }
-#pragma unroll
-          for (int m = 1; m < L; m <<= 1) {
-            const float sign = l & m ? -1.f : 1.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              y2[e] = __ffma2_rn(make_float2(sign, sign), y2[e], make_float2(shfl_xor(y2[e].x, m), shfl_xor(y2[e].y, m)));
-          }
-          const float f = rsqrtf((float)D);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
-        }
-        if (to.head + row < to.heads) Chunks<IO>::store(p, then, y);
-        if (--left == 0) break;
-        if (step(to, a.q_out, a.qo_stride, a.k_out, a.ko_stride)) {
-          if (!to.k) angles();
-          weigh();
         }
       }
+      if (turned) {
+        if constexpr (HALVES) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 u = y2[e], x = y2[e + 4];
+            const float2 m = __fmul2_rn(x, sn[e]);
+            y2[e] = __ffma2_rn(u, cs[e], make_float2(-m.x, -m.y));
+            y2[e + 4] = __ffma2_rn(u, sn[e], __fmul2_rn(x, cs[e]));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float ce = e & 1 ? cs[e / 2].y : cs[e / 2].x, se = e & 1 ? sn[e / 2].y : sn[e / 2].x;
+            const float2 u = y2[e];
+            y2[e] = make_float2(fmaf(u.x, ce, -u.y * se), fmaf(u.x, se, u.y * ce));
+          }
+        }
+      }
+      char* p = to.p;
+      int then = apart;
+      if (a.hadamard) {
+        if (!bits) {  // to chunks in order, through shared memory
+          float* of = mine + (lane - l) * 16;
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4*>(of + 8 * c0 + e) = make_float4(y[0][e], y[0][e + 1], y[0][e + 2], y[0][e + 3]);
+            *reinterpret_cast<float4*>(of + 8 * c1 + e) = make_float4(y[1][e], y[1][e + 1], y[1][e + 2], y[1][e + 3]);
+          }
+          __syncwarp();
+          p += 8 * SIZE * (2 * l - c0);
+          then = 8 * SIZE;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e / 8][e % 8] = of[16 * l + e];
+          __syncwarp();
+        }
+        // within a pair of elements, then pairs at a time
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y2[e] = make_float2(y2[e].x + y2[e].y, y2[e].x - y2[e].y);
+#pragma unroll
+        for (int m = 1; m < 8; m <<= 1)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!(e & m)) {
+              const float2 u = y2[e], x = y2[e | m];
+              y2[e] = __fadd2_rn(u, x);
+              y2[e | m] = __ffma2_rn(x, make_float2(-1.f, -1.f), u);
+            }
+#pragma unroll
+        for (int m = 1; m < L; m <<= 1) {
+          const float sign = l & m ? -1.f : 1.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y2[e] = __ffma2_rn(make_float2(sign, sign), y2[e], make_float2(shfl_xor(y2[e].x, m), shfl_xor(y2[e].y, m)));
+        }
+        const float f = rsqrtf((float)D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y2[e] = __fmul2_rn(y2[e], make_float2(f, f));
+      }
+      if (to.head + row < to.heads) Chunks<IO>::store(p, then, y);
+      if (--left == 0) break;
+      if (step(to, a.q_out, a.qo_stride, a.k_out, a.ko_stride)) {
+        if (!to.k) angles();
+        weigh();
+      }
+    }
   } while (left > 0);
 }
 

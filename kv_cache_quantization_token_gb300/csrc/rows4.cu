@@ -8,9 +8,10 @@
 //
 // What bounds it: instructions and the latency of row, length and table one after another. 7,100 tokens of 8 heads of 128,
 // bf16 (37 MB in and out): writing 9.5 us, reading back 7.8, against 5.5 at the copy rate; a token of each of 32 sequences
-// both ways 4.0, 4.7 with rows requested once their places are known (two or four rows to a thread gained nothing). Sixteen channels of K and of V
-// to a thread instead of eight brought writing from 13.7 to 9.3 (finding a row's place costs as much as coding eight
-// channels). Reading takes two runs of eight channels to a thread, so that a warp's stores cover whole sectors (9.8 -> 8.1).
+// both ways 4.0 (4.7 with rows requested once their places are known). Sixteen channels of K and of V to a thread instead
+// of eight brought writing from 13.7 to 9.3 (finding a row's place costs as much as coding eight channels); two or four
+// rows to a thread gained nothing. Reading takes two runs of eight channels to a thread, so that a warp's stores cover
+// whole sectors (9.8 -> 8.1).
 #include "cache4.cuh"
 
 namespace kvarn {
