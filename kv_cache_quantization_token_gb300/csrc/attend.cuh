@@ -14,7 +14,9 @@
 
 #include <math.h>
 
-#include "cache8.cuh"
+#include <type_traits>
+
+#include "cache4.cuh"
 #include "tcgen05.cuh"
 
 namespace kvarn {
@@ -111,6 +113,7 @@ __device__ __forceinline__ void st_sector(void* p, const uint32_t (&h)[8]) {
 }
 
 // ---------------------------------------------------------------------------
+// NP: parts of queries and weights, 2 for fp32 calls and 1 for those of 16-bit types.
 template <int D, int NP, bool SC>
 __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const Att8Args s) {
   using P = PC8<D, NP>;
@@ -186,40 +189,77 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
     for (int t = 0; t < min(n_blk, R); t += P::LP) copy(t);
   }
 
-  // query rows into TMEM: scaled by a power of two, fp16 (hi and lo); two threads per row
-  if (tid < 256) {
+  // Query rows into TMEM: scaled by a power of two, fp16 (hi and lo); two threads per row. Rows lie apart, so that every load
+  // of a warp meets 32 lines, and what counts is how few there are: 16 bytes each, kept in registers where they fit. (4,096
+  // positions from the start, 32 / 8 heads of 128, bf16: 202 us with eight bytes, twice, and results stored likewise, 169 so.)
+  auto query_rows = [&](auto io) {
+    constexpr int IO = decltype(io)::value, N = D / 16;  // eights of channels of half a row
+    constexpr bool KEEP = N * (IO == KVARN_IO_F32 ? 8 : 4) <= 64;
     const int64_t at = ((int64_t)my_i * a.Hq + hq) * D + half * (D / 2);
+    Eight<IO> e[KEEP ? N : 4]{};
     float m = 0.f;
-    if (my_valid)
-#pragma unroll 8
-      for (int c = 0; c < D / 2; c += 4) {
-        const float4 v = io_ld4(a.q, a.io, at + c);
-        m = fmaxf(fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+    auto largest = [&](const Eight<IO>& e) {
+      float x[8];
+      e.get(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    };
+    if constexpr (KEEP) {
+      if (my_valid)
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i].load(a.q, at + 8 * i);
+#pragma unroll
+      for (int i = 0; i < N; ++i) largest(e[i]);
+    } else if (my_valid) {
+#pragma unroll 1
+      for (int i = 0; i < N; i += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k].load(a.q, at + 8 * (i + k));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) largest(e[k]);
       }
+    }
     xm[half * 128 + row].x = m;
     take_over<64>(kBarPair + (warp & 3));
     const float mq = fmaxf(m, xm[(half ^ 1) * 128 + row].x), up = pow2_to(mq, 10);
     if (half == 0) xm[row].y = fabsf(a.scale) * pow2_inverse(up);
     // (maxima are taken before the positive scales; a row with an infinity becomes NaN)
     const float p2 = mq == INFINITY ? NAN : copysignf(up, a.scale);
-#pragma unroll 1
-    for (int c0 = 0; c0 < D / 2; c0 += 32) {
+    auto put = [&](int c0, const Eight<IO>* e) {  // 32 channels
       uint32_t hw[16], lw[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float4 v = my_valid ? io_ld4(a.q, a.io, at + c0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
-        split_pair(v.x * p2, v.y * p2, hw[2 * e], lw[2 * e]);
-        split_pair(v.z * p2, v.w * p2, hw[2 * e + 1], lw[2 * e + 1]);
+      for (int k = 0; k < 4; ++k) {
+        float x[8];
+        e[k].get(x);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) split_pair(x[i] * p2, x[i + 1] * p2, hw[4 * k + i / 2], lw[4 * k + i / 2]);
       }
       tmem_st16(tmem + lb + P::T_QH + half * (D / 4) + c0 / 2, hw);
       if constexpr (NP == 2 && !P::QL_SMEM) tmem_st16(tmem + lb + P::T_QL + half * (D / 4) + c0 / 2, lw);
       if constexpr (P::QL_SMEM) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(sm + sw_off(row, half * (D / 2) + c0 + 8 * e, 128)) =
-              make_uint4(lw[4 * e], lw[4 * e + 1], lw[4 * e + 2], lw[4 * e + 3]);
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(sm + sw_off(row, half * (D / 2) + c0 + 8 * k, 128)) =
+              make_uint4(lw[4 * k], lw[4 * k + 1], lw[4 * k + 2], lw[4 * k + 3]);
+      }
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int c0 = 0; c0 < D / 2; c0 += 32) put(c0, e + c0 / 8);
+    } else {
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 2; c0 += 32) {
+        if (my_valid)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k].load(a.q, at + c0 + 8 * k);
+        put(c0, e);
       }
     }
+  };
+  if (tid < 256) {
+    if constexpr (NP == 2) query_rows(std::integral_constant<int, KVARN_IO_F32>());
+    else if (a.io == KVARN_IO_F16) query_rows(std::integral_constant<int, KVARN_IO_F16>());
+    else query_rows(std::integral_constant<int, KVARN_IO_BF16>());
     tmem_wait_st();
     if constexpr (P::QL_SMEM) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -579,11 +619,20 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
           }
         }
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 o = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
-          const int c = half * (D / 2) + c0 + i;
-          if (s.p.shares == 1) io_st4(a.out, a.io, orow * D + c, o);
-          else *reinterpret_cast<float4*>(s.acc + out_row * D + c) = o;
+        for (int i = 0; i < 32; ++i) v[i] *= f;
+        const int c = half * (D / 2) + c0;
+        // (as few stores as there can be: each of a warp's meets 32 lines)
+        if (s.p.shares > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) st_sector(s.acc + out_row * D + c + i, *reinterpret_cast<uint32_t(*)[8]>(v + i));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            const float(&x)[8] = *reinterpret_cast<float(*)[8]>(v + i);
+            if constexpr (NP == 2) Eight<KVARN_IO_F32>::store(a.out, orow * D + c + i, x);
+            else if (a.io == KVARN_IO_F16) Eight<KVARN_IO_F16>::store(a.out, orow * D + c + i, x);
+            else Eight<KVARN_IO_BF16>::store(a.out, orow * D + c + i, x);
+          }
         }
       }
     }
