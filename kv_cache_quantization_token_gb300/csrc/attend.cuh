@@ -160,6 +160,17 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
   auto sub_of = [&](int j) { const int v = b0 + j; return !SC || v < vis_t ? v : s.p.n_tsub + (v - vis_t); };
   const uint8_t* head = a.ws + (int64_t)kvh * s.p.head_imgs * P::IMG;
 
+  // Query rows are requested before all else. They lie apart, so that every load of a warp meets 32 lines, and what counts
+  // is how few there are: 16 bytes each, kept in registers where they fit. (4,096 positions from the start, 32 / 8 heads of
+  // 128, bf16: 202 us with eight bytes, twice, and results stored likewise, 169 so.)
+  constexpr int N = D / 16;  // eights of channels of half a row
+  constexpr bool KEEP = N * 4 * NP <= 64;
+  using Raw = Eight<NP == 2 ? KVARN_IO_F32 : KVARN_IO_F16>;  // (or bf16, which is as wide)
+  Raw raw[KEEP ? N : 4]{};
+  const int64_t q_at = ((int64_t)my_i * a.Hq + hq) * D + half * (D / 2);
+  if (KEEP && tid < 256 && my_valid)
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i].load(a.q, q_at + 8 * i);
   if (tid == 0) {
     for (int i = 0; i < 4 * R; ++i) mbar_init_n(bar_fk + i, 1);
     mbar_init_n(bar_o, 2);
@@ -189,34 +200,31 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
     for (int t = 0; t < min(n_blk, R); t += P::LP) copy(t);
   }
 
-  // Query rows into TMEM: scaled by a power of two, fp16 (hi and lo); two threads per row. Rows lie apart, so that every load
-  // of a warp meets 32 lines, and what counts is how few there are: 16 bytes each, kept in registers where they fit. (4,096
-  // positions from the start, 32 / 8 heads of 128, bf16: 202 us with eight bytes, twice, and results stored likewise, 169 so.)
+  // query rows into TMEM: scaled by a power of two, fp16 (hi and lo); two threads per row
   auto query_rows = [&](auto io) {
-    constexpr int IO = decltype(io)::value, N = D / 16;  // eights of channels of half a row
-    constexpr bool KEEP = N * (IO == KVARN_IO_F32 ? 8 : 4) <= 64;
-    const int64_t at = ((int64_t)my_i * a.Hq + hq) * D + half * (D / 2);
-    Eight<IO> e[KEEP ? N : 4]{};
-    float m = 0.f;
-    auto largest = [&](const Eight<IO>& e) {
-      float x[8];
+    auto get = [&](const Raw& r, float (&x)[8]) {
+      Eight<decltype(io)::value> e;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) e.w[i] = r.w[i];
       e.get(x);
+    };
+    float m = 0.f;
+    auto largest = [&](const Raw& r) {
+      float x[8];
+      get(r, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
     };
     if constexpr (KEEP) {
-      if (my_valid)
 #pragma unroll
-        for (int i = 0; i < N; ++i) e[i].load(a.q, at + 8 * i);
-#pragma unroll
-      for (int i = 0; i < N; ++i) largest(e[i]);
+      for (int i = 0; i < N; ++i) largest(raw[i]);
     } else if (my_valid) {
 #pragma unroll 1
       for (int i = 0; i < N; i += 4) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k].load(a.q, at + 8 * (i + k));
+        for (int k = 0; k < 4; ++k) raw[k].load(a.q, q_at + 8 * (i + k));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) largest(e[k]);
+        for (int k = 0; k < 4; ++k) largest(raw[k]);
       }
     }
     xm[half * 128 + row].x = m;
@@ -225,12 +233,12 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
     if (half == 0) xm[row].y = fabsf(a.scale) * pow2_inverse(up);
     // (maxima are taken before the positive scales; a row with an infinity becomes NaN)
     const float p2 = mq == INFINITY ? NAN : copysignf(up, a.scale);
-    auto put = [&](int c0, const Eight<IO>* e) {  // 32 channels
+    auto put = [&](int c0, const Raw* r) {  // 32 channels
       uint32_t hw[16], lw[16];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float x[8];
-        e[k].get(x);
+        get(r[k], x);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) split_pair(x[i] * p2, x[i + 1] * p2, hw[4 * k + i / 2], lw[4 * k + i / 2]);
       }
@@ -245,14 +253,14 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
     };
     if constexpr (KEEP) {
 #pragma unroll
-      for (int c0 = 0; c0 < D / 2; c0 += 32) put(c0, e + c0 / 8);
+      for (int c0 = 0; c0 < D / 2; c0 += 32) put(c0, raw + c0 / 8);
     } else {
 #pragma unroll 1
       for (int c0 = 0; c0 < D / 2; c0 += 32) {
         if (my_valid)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) e[k].load(a.q, at + c0 + 8 * k);
-        put(c0, e);
+          for (int k = 0; k < 4; ++k) raw[k].load(a.q, q_at + c0 + 8 * k);
+        put(c0, raw);
       }
     }
   };
