@@ -29,7 +29,7 @@
 // memory (the A operand), so shared memory feeds B operands only; at head_dim 256 the lo part of the query lives in
 // shared memory.
 //
-// What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 121 us, 1,056 TFLOP/s, 56%
+// What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 117 us, 1,095 TFLOP/s, 57%
 // of the measured bf16 rate; images 17 us of it): the softmax warps. A 64-key block costs the tensor pipe 512
 // cycles and each of four softmax warps 475 instructions (by counters, the other warps' share in them), of which the
 // SM issues 2.6 per cycle. Some 190 are the scores' own (an exponential each, and half a three-way maximum, packed
