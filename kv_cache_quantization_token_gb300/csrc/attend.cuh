@@ -113,8 +113,14 @@ __device__ __forceinline__ void st_sector(void* p, const uint32_t (&h)[8]) {
 }
 
 // ---------------------------------------------------------------------------
-// NP: parts of queries and weights, 2 for fp32 calls and 1 for those of 16-bit types.
-template <int D, int NP, bool SC>
+// NP: parts of queries and weights, 2 for fp32 calls and 1 for those of 16-bit types. (One fp16 number for a weight: 2^-11 of it
+// at most, where half a step of a bf16 output is 2^-9 and of an fp16 output 2^-12 to 2^-11. Two, as with fp32, take 172 us
+// instead of 105 for 512 positions over 15k, 32 / 8 heads of 128.)
+// RS: the sum of weights is of the rounded ones that the product meets, so that they add up to one and of equal values the very
+// value comes out; otherwise it is of those before rounding. For fp16, whose output's step the difference reaches: that chunk is
+// off by 2.24e-4 against 64 bits instead of 2.51e-4 (301 positions over 4.6k at head_dim 64 2.57e-4 and 2.69e-4), and takes 111.3 us
+// instead of 105.0. A step of bf16 is eight times as wide (1.634e-3 instead of 1.638e-3): its calls keep the 6%.
+template <int D, int NP, bool SC, bool RS>
 __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const Att8Args s) {
   using P = PC8<D, NP>;
   constexpr int KB = P::KB, KW = P::KW, R = P::R, NGB = P::NGB, NG = P::NG;
@@ -513,12 +519,16 @@ __global__ void __launch_bounds__(PC8<D, NP>::THREADS, 1) attend_kernel(const At
         for (int e = 0; e < 8; ++e) {
           const float2 x = __ffma2_rn(make_float2(sv[16 * g + 2 * e], sv[16 * g + 2 * e + 1]), k2, c2);
           const float2 w = make_float2(fast_ex2(x.x), fast_ex2(x.y));
-          ls2 = __fadd2_rn(ls2, w);
+          if constexpr (!RS) ls2 = __fadd2_rn(ls2, w);
           if constexpr (NP == 2) {
             split_pair(w.x, w.y, hw[8 * g + e], lw[8 * g + e]);
           } else {
             const __half2 h = __floats2half2_rn(w.x, w.y);
             hw[8 * g + e] = *reinterpret_cast<const uint32_t*>(&h);
+            if constexpr (RS) {  // (sums of mixed types: converting back first 113.7 us instead of 111.7)
+              asm("add.rn.f32.f16 %0, %1, %0;" : "+f"(ls2.x) : "h"(__half_as_ushort(__low2half(h))));
+              asm("add.rn.f32.f16 %0, %1, %0;" : "+f"(ls2.y) : "h"(__half_as_ushort(__high2half(h))));
+            }
           }
         }
         l_part = fmaf(ls2.x + ls2.y, SC ? fast_ex2(-le - kHead) : pow2_inverse(256.f), l_part);  // (2^-kHead)
@@ -726,7 +736,7 @@ Plan8 plan8(int C, int n_tblk, int win_vis, int Hq, int Hkv, int D, bool fp32, b
 }
 
 // The attention kernel behind the grid that makes the images, and the join.
-template <int D, int NP, bool SC>
+template <int D, int NP, bool SC, bool RS>
 cudaError_t launch_attend(const Att8Args& s, cudaStream_t st) {
   using P = PC8<D, NP>;
   static bool configured[64] = {};
@@ -734,12 +744,12 @@ cudaError_t launch_attend(const Att8Args& s, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(attend_kernel<D, NP, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+    e = cudaFuncSetAttribute(attend_kernel<D, NP, SC, RS>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   LaunchCfg L(dim3(s.p.row_blocks, s.a.Hkv, s.p.shares), dim3(P::THREADS), P::SMEM, st, KVARN_LAUNCH_PDL);
-  e = cudaLaunchKernelEx(&L.cfg, attend_kernel<D, NP, SC>, s);
+  e = cudaLaunchKernelEx(&L.cfg, attend_kernel<D, NP, SC, RS>, s);
   if (e != cudaSuccess || s.p.shares == 1) return e;
   const int64_t rows = (int64_t)s.a.C * s.a.Hq;
   LaunchCfg J(dim3((unsigned)((rows + 1024 / D - 1) / (1024 / D))), dim3(256), 0, st, KVARN_LAUNCH_PDL);

@@ -135,11 +135,20 @@ __global__ void __launch_bounds__(256) image4_kernel(const Att8Args s, uint32_t 
   }
 }
 
-template <int D, int NP>
+template <int D, int NP, bool RS>
 cudaError_t launch_p4(const Att8Args& s, cudaStream_t st) {
   image4_kernel<D><<<dim3(s.p.n_tsub / PC8<D, 1>::SUB, s.a.Hkv), 256, 0, st>>>(s, kUnitBase);
   const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_attend<D, NP, false>(s, st);
+  return e != cudaSuccess ? e : launch_attend<D, NP, false, RS>(s, st);
+}
+
+template <int D>
+cudaError_t launch_p4d(const Att8Args& s, cudaStream_t st) {
+  switch (s.a.io) {
+    case KVARN_IO_F32: return launch_p4<D, 2, false>(s, st);
+    case KVARN_IO_F16: return launch_p4<D, 1, true>(s, st);
+    default: return launch_p4<D, 1, false>(s, st);
+  }
 }
 
 // Chunks of few score rows per KV head go to the decode kernels, which need no images but go over the cache once for
@@ -188,11 +197,10 @@ cudaError_t launch_prefill4(const Prefill4Args& a, cudaStream_t st) {
   s.ml = reinterpret_cast<float2*>(a.ws + s.p.off_ml);
   s.acc = reinterpret_cast<float*>(a.ws + s.p.off_acc);
   s.sum = reinterpret_cast<float4*>(a.ws + s.p.off_sum);
-  const bool two = a.io == KVARN_IO_F32;
   switch (a.D) {
-    case 64: return two ? launch_p4<64, 2>(s, st) : launch_p4<64, 1>(s, st);
-    case 128: return two ? launch_p4<128, 2>(s, st) : launch_p4<128, 1>(s, st);
-    default: return two ? launch_p4<256, 2>(s, st) : launch_p4<256, 1>(s, st);
+    case 64: return launch_p4d<64>(s, st);
+    case 128: return launch_p4d<128>(s, st);
+    default: return launch_p4d<256>(s, st);
   }
 }
 

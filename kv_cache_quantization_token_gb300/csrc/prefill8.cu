@@ -187,7 +187,7 @@ cudaError_t launch_p8(const Att8Args& s, cudaStream_t st) {
   const int blocks = s.p.n_tsub / P::SUB + 2 * s.p.n_wsub * (P::KW / kGrp);
   image8_kernel<D, F><<<dim3(blocks, s.a.Hkv), 256, 0, st>>>(s);
   const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_attend<D, NP, true>(s, st);
+  return e != cudaSuccess ? e : launch_attend<D, NP, true, false>(s, st);
 }
 
 template <int D>

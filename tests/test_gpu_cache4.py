@@ -765,6 +765,25 @@ def test_prefill_of_one_position_agrees_with_decode_and_replays():
             assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("C", [9, 70, 200])  # on the decode kernels, on the images in key shares, and without
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill_of_equal_values_gives_them(D, C):
+    """Weights add up to one as the products see them: with the same V row at every token each output is that row. All
+    else is below (n / 16 + 2) 2^-23 + 2^-20 of it (the products' sums, which are cut off, and the sum of weights), 7e-6 here, and
+    half a step of an fp16 number is 2^-12 of it at least: the very row comes out."""
+    n, H, G = 700, 2, 4
+    s = _Store(1, H, D, 6)
+    k = torch.randn(1, n, H, D, generator=torch.Generator().manual_seed(D)).to(DEV)
+    v = _query(D + 1, (1, 1, H, D), "f32").expand(1, n, H, D).contiguous()
+    s.write(k, v, [0])
+    k, v = torch.zeros_like(k), torch.zeros_like(v)
+    s.read(k, v, [0])
+    for scale in (D ** -0.5, 0.3, 1.0):  # many weights to a row, or a few large ones
+        q = _query(C, (C, H * G, D), "f16")
+        out = kvarn.prefill_attention4(q, n - C, s.tiles, s.table[0], s.lay, softmax_scale=scale)
+        assert torch.equal(out.float(), v[0, 0].repeat_interleave(G, 0).expand(C, H * G, D))
+
+
 # ---------------------------------------------------------------- sizes
 
 @pytest.mark.parametrize("D", [64, 256])
