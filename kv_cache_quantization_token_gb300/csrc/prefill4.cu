@@ -152,31 +152,34 @@ cudaError_t launch_p4d(const Att8Args& s, cudaStream_t st) {
 }
 
 // Chunks of few score rows per KV head go to the decode kernels, which need no images but go over the cache once for
-// every eight rows ("group"): some 4 ns of all SMs per group and tile-head, where the images and their kernels take 6
-// groups' worth per tile-head, with fewer than 8 KV heads no less than with 8, and some 4 us more. At head_dim 128, 8 KV
-// heads, bf16 (us, decode kernels against images): 8 groups over 64 tiles 26 / 26, 12 33 / 28; 6 over 128 tiles 33 / 33, 8
-// 41 / 33; 2 KV heads, 24 groups over 128 tiles 33 / 34, 32 41 / 34; head_dim 64, 8 over 64 tiles 18 / 19, 256 40 / 39. Over
-// 774 sizes (1 to 8 KV heads, 1 to 48 groups, 4 to 128 tiles, both kinds of type) the choice costs 0.3% on the mean, 26%
-// at worst.
+// every eight rows ("group"): some 4.3 ns of all SMs per group and tile of a head (head_dim 128; 2.7 at 64, 7.8 at 256). The images
+// with their kernels cost four groups' worth per tile of a head, 24 more per tile, however many heads there are (up to 192
+// tiles: a fit), and some 4 us. At head_dim 128, bf16 (us, decode kernels against images):
+//   8 KV heads   16 tiles: 6 groups 12.9 / 12.8, 12 15.2 / 13.8;   64: 6 22.3 / 24.1, 8 25.6 / 23.8;   128: 6 33.3 / 31.1;
+//                512: 4 73 / 105, 6 106 / 106, 8 137 / 105;   1,024: 4 137 / 198, 8 263 / 198
+//   2            64 tiles: 24 22.2 / 23.4, 32 25.7 / 24.2;   128: 16 24.8 / 34.3, 24 33.1 / 27.8;   512: 8 41.0 / 45.7, 24 106 / 44
+//   1            128 tiles: 32 24.9 / 33.1, 48 33.3 / 30.4;   512: 16 40.9 / 39.3, 48 106 / 40;   1,024: 8 41 / 50, 32 135 / 53
+// Over 2,212 sizes (1 to 16 KV heads, 1 to 64 groups, 4 to 1,024 tiles, each head_dim, fp32 at 128) the choice costs 0.6% on the mean,
+// 36% at worst.
 constexpr int64_t kFewGroups = 64, kFewWork = 800;
 int64_t row_groups(int C, int G) { return ((int64_t)C * G + 7) / 8; }
-int64_t few_heads(int Hkv) { return Hkv > 8 ? Hkv : 8; }
 bool few_rows(int C, int G, int Hkv, int n_tiles) {
   const int64_t groups = row_groups(C, G);
-  return groups <= kFewGroups && (groups * Hkv - 6 * few_heads(Hkv)) * n_tiles <= kFewWork;
+  return groups <= kFewGroups && (groups - 4) * Hkv * n_tiles <= kFewWork + 24 * (n_tiles < 192 ? n_tiles : 192);
 }
 
 }  // namespace
 
 // At least what every call of at most C positions over at most n_tiles tiles needs, whichever kernels serve it.
 size_t prefill4_ws_bytes(int C, int n_tiles, int Hq, int Hkv, int D) {
-  const int64_t heads = few_heads(Hkv), sms = sm_count();
+  const int64_t sms = sm_count();
   const int64_t groups = row_groups(C, Hq / Hkv), work = (groups < kFewGroups ? groups : kFewGroups) * Hkv;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   // Decode kernels: eight rows for each of a call's pieces, at most a CTA's share each and one more per segment.
   const int64_t entries = 8 * (4 * sms + work);  // (four CTAs per SM at most)
   const size_t few = up((size_t)entries * sizeof(float2)) + up((size_t)entries * D * sizeof(float));
-  if (groups * Hkv <= 6 * heads) return few;  // (few_rows holds for every smaller call)
+  // (then of every smaller call too: fewer groups only help, and what the tiles' sides differ by is convex in their number)
+  if (few_rows(C, Hq / Hkv, Hkv, n_tiles)) return few;
   // Images: those of this call, and the results of key shares, of which there are only as many as fill the SMs
   // once, or kRounds times (128 rows to a CTA), and O's emptied sums, of a CTA's rows each.
   const Plan8 p = plan8(C, n_tiles, 0, Hq, Hkv, D, true, false);

@@ -765,6 +765,22 @@ def test_prefill_of_one_position_agrees_with_decode_and_replays():
             assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,H,C,n", [(64, 2, 48, 16000), (128, 1, 96, 20001), (256, 4, 40, 24700)])
+def test_prefill_of_few_rows_over_long_tables(D, H, C, n, io):
+    """On the images from some length on, in as many key shares as there can be."""
+    G = 4
+    c, table, _, rows_of = _shared(D + 11, D, H, [n])
+    q = _query(D, (C, H * G, D), io)
+    out = kvarn.prefill_attention4(q, n - C, c.tiles, table[0], c.lay)
+    at = [0, 1, C // 2, C - 1]
+    for h in range(H):
+        k, v = rows_of(0, h, n)
+        qn = q[at, h * G:(h + 1) * G].double().cpu().numpy().reshape(-1, D)
+        want, p, bound = attend(qn, k, v, D ** -0.5, np.repeat(n - C + 1 + np.array(at), G), np.ones(n), 2.0 ** -33)
+        check(out[at, h * G:(h + 1) * G].reshape(-1, D), want, bound, q.dtype, 0.0 if io == "f32" else 2.0 ** -11, p @ np.abs(v))
+
+
 @pytest.mark.parametrize("C", [9, 70, 200])  # on the decode kernels, on the images in key shares, and without
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_prefill_of_equal_values_gives_them(D, C):
