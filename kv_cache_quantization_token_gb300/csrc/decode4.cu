@@ -658,12 +658,17 @@ cudaError_t allow_shared(Kernel* kernel, int bytes, bool (&configured)[64]) {
 }
 
 // Tiles that a CTA takes side by side when it does a segment by itself: 16 warps, or 8 that need more registers. One launch and
-// no partial results, so short tables are read by it: of kAloneChannels tiles x channels at most, whatever the number of
-// segments, and up to 4 TW tiles where there are two segments to five SMs. Both ways, in us (joined pieces / by itself), bf16 queries:
-//   D 64, G 4     1 segment: 2 tiles 5.1 / 3.7, 6 5.2 / 5.1, 8 5.4 / 5.6;   64: 4 7.3 / 4.6, 16 9.8 / 8.0
-//   D 128, G 4    1 segment: 2 6.0 / 4.9, 3 5.9 / 5.2, 4 5.7 / 5.9;         64: 4 8.0 / 5.9, 16 12.1 / 11.6
-//   D 128, G 8    1 segment: 1 6.3 / 4.1, 3 6.1 / 5.5, 4 6.1 / 6.1;         64: 4 10.6 / 6.0, 8 12.1 / 8.7
-//   D 256, G 4    1 segment: 1 7.5 / 5.4, 2 7.5 / 5.9, 3 7.2 / 7.5;         64: 4 10.2 / 7.8, 8 11.5 / 11.3
+// no partial results, so short tables are read by it: of kAloneChannels tiles x channels at most, or of up to 4 TW tiles where
+// there are two segments to five SMs. An SM holds one such CTA, and nothing covers the ends and beginnings of CTAs one after another: in
+// a second round tables are of 2 TW tiles at most, and more segments than two rounds of them are shared out like long tables. Both
+// ways, in us (joined pieces / by itself), bf16 queries, full tables:
+//   D 64, G 4     8 segments: 2 tiles 5.4 / 3.9, 6 5.5 / 5.4, 8 5.5 / 6.0;   64: 4 7.2 / 5.0, 16 9.8 / 8.4
+//                 304: 4 11.1 / 8.6, 8 11.3 / 11.0, 16 15.8 / 15.9;   512: 4 13.3 / 15.2;   2,048: 1 26.0 / 36.5, 6 47.8 / 68.0
+//   D 128, G 4    8: 2 6.0 / 5.0, 3 5.9 / 5.4, 4 5.9 / 6.0;   64: 4 8.0 / 6.2, 16 12.3 / 11.6
+//                 304: 4 13.9 / 11.3, 8 14.8 / 15.4, 16 22.2 / 23.3;   512: 4 16.9 / 20.5;   2,048: 1 30.0 / 48.6, 6 65.9 / 93.2
+//   D 128, G 8    8: 1 6.1 / 4.5, 3 6.2 / 6.0, 4 6.2 / 6.4;   64: 4 8.0 / 6.6, 8 10.1 / 9.3;   304: 4 14.8 / 12.1;   2,048: 3 54.6 / 74.6
+//   D 256, G 4    8: 1 7.5 / 5.7, 2 7.5 / 6.2, 3 7.3 / 7.7;   64: 4 10.1 / 8.1, 8 11.6 / 11.7;   304: 4 20.0 / 15.6;   2,048: 4 92.9 / 102.6
+// Over 960 sizes (8 to 2,048 segments, 1 to 16 tiles, full and ragged) the choice costs 1.2% on the mean, 35% at worst.
 constexpr int kAloneChannels = 384;
 template <int D, bool WIDE>
 constexpr int kSideBySide = D == 64 || (D == 128 && !WIDE) ? 4 : 2;  // (16 warps, or 8 that need the registers)
@@ -677,7 +682,10 @@ cudaError_t launch_d4(const Decode4Plan& p, Split4Args& s, void* ws, cudaStream_
   constexpr int TW = kSideBySide<D, WIDE>;
   const int tiles = CHUNK ? s.n_tiles : a.max_tiles;
   const int64_t blocks = CHUNK ? ((int64_t)a.B * a.G + 7) / 8 : a.B;  // of sequences, or of eight rows
-  if ((int64_t)tiles * D <= kAloneChannels || (tiles <= 4 * TW && 5 * blocks * a.Hkv >= 2 * sm_count())) {
+  const int64_t segments = blocks * a.Hkv, sms = sm_count();
+  // (tables of no tiles, which would make no shares, among them)
+  if (segments <= sms ? (int64_t)tiles * D <= kAloneChannels || (tiles <= 4 * TW && 5 * segments >= 2 * sms)
+                      : tiles == 0 || (segments <= 2 * sms && tiles <= 2 * TW)) {
     using C = C4<D, WIDE, TW>;
     static bool configured[64] = {};
     cudaError_t e = allow_shared(split4_kernel<D, WIDE, NQ, CHUNK, TW>, C::SMEM, configured);

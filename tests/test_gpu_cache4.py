@@ -380,6 +380,32 @@ def test_decode_of_ragged_batches(D, G, io, longest):
     assert bool((out7.view(60, 7, -1)[:, 1:] == 0).all())
 
 
+@pytest.mark.parametrize("G", [4, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,H,n", [(400, 3, 0), (400, 3, 1), (100, 3, 4), (1, 200, 5), (80, 2, 3), (300, 4, 2)])
+def test_decode_of_many_short_tables(B, H, n, D, G):
+    """Segments in one round of CTAs, two and more; with no tile at all, and lengths from none to full tables."""
+    lens = [(37 * b + 633) % (T * n + 1) for b in range(B)]
+    c, table, dlens, rows_of = _shared(D + G, D, H, lens)
+    table = table[:, :, :n].contiguous()
+    if n and table.shape[2] < n:
+        table = torch.nn.functional.pad(table, (0, n - table.shape[2]))
+    q = _query(B, (B, H * G, D), "bf16")
+    mass = torch.empty(B, H, n, device=DEV)
+    out = kvarn.decode_attention4(q, c.tiles, table, dlens, c.lay, mass_out=mass)
+    assert torch.equal(out, kvarn.decode_attention4(q, c.tiles, table, dlens, c.lay))
+    assert bool((mass.sum(-1) - G * (dlens > 0).float()[:, None]).abs().max() < 1e-4 * G)
+    assert bool((out[dlens == 0] == 0).all())
+    for b in (0, 1, 2, B // 3, B // 2, B - 1):
+        if b >= B or lens[b] == 0:
+            continue
+        for h in (0, H - 1):
+            k, v = rows_of(b, h, lens[b])
+            want, p, bound = attend(q[b, h * G:(h + 1) * G].double().cpu().numpy(), k, v, D ** -0.5, [lens[b]] * G,
+                                    np.ones(lens[b]), 2.0 ** -39)
+            check(out[b, h * G:(h + 1) * G], want, bound, q.dtype)
+
+
 @pytest.mark.parametrize("n", [600, 2200])  # a block for each row group and head, and tiles shared out
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_prefill_of_few_rows_over_many_segments(D, n):
