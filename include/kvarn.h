@@ -774,8 +774,9 @@ int kvarn_read_rows4(const uint8_t* tiles, int64_t tiles_bytes, const int64_t* t
  * or an infinity in a query makes its row NaN. Precision: KVARN_IO_F32 keeps 22 bits of queries and
  * weights; the cached values are exact. Deterministic; grids depend only on the sizes, so the
  * call can be captured. launch_flags: 0 or KVARN_LAUNCH_PDL.
- *   ws : at least kvarn_decode4_workspace_bytes() bytes, 256-byte aligned, no
- *        initialisation. Calls sharing ws must not overlap.
+ *   ws : at least kvarn_decode4_workspace_bytes() bytes, of which a call without mass_out needs
+ *        256 B Hkv max_tiles less; 256-byte aligned, no initialisation. Calls sharing ws must not
+ *        overlap.
  */
 int kvarn_decode4_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int max_tiles, size_t* bytes);
 int kvarn_decode_attention4(const void* q, int io_type, const uint8_t* tiles, int64_t tiles_bytes,

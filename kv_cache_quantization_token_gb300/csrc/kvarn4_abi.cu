@@ -183,8 +183,9 @@ int kvarn_decode_attention4(const void* q, int io_type, const uint8_t* tiles, in
   if (max_tiles > 0 && (!tiles || !tile_table)) return KVARN_ERR_NULL;
   kvarn::Decode4Plan p;
   kvarn::decode4_plan(B, Hq, Hkv, head_dim, max_tiles, &p);
-  if (p.ws_bytes > 0 && !ws) return KVARN_ERR_NULL;
-  if (ws_bytes < p.ws_bytes) return KVARN_ERR_WORKSPACE;
+  const size_t need = mass_out ? p.ws_bytes : p.off_tile;  // (the tiles' weights are the workspace's last part)
+  if (need > 0 && !ws) return KVARN_ERR_NULL;
+  if (ws_bytes < need) return KVARN_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(tiles, 16) || !aligned(ws, 256) || !aligned(tile_table, 8) ||
       !aligned(lens, 4) || !aligned(mass_in, 4) || !aligned(mass_out, 4))
     return KVARN_ERR_ALIGN;

@@ -793,11 +793,12 @@ def read_rows4(tiles, tile_table, first, k_out, v_out, lay: Layout4, counts=None
           n, k_out.data_ptr(), ks, v_out.data_ptr(), vs, *sizes, int(flags))
 
 
-def decode4_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles) -> int:
+def decode4_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles, weights=True) -> int:
+    """Bytes that decode_attention4 needs, with mass_out or (weights False) without."""
     n = ctypes.c_size_t()
     _check("kvarn_decode4_workspace_bytes",
            _L().kvarn_decode4_workspace_bytes(B, Hq, Hkv, head_dim, max_tiles, ctypes.byref(n)))
-    return n.value
+    return n.value if weights else n.value - 256 * B * Hkv * max_tiles
 
 
 def decode_attention4(q, tiles, tile_table, lens, lay: Layout4, softmax_scale=None, mass_in=None,
@@ -821,7 +822,7 @@ def decode_attention4(q, tiles, tile_table, lens, lay: Layout4, softmax_scale=No
                 raise ValueError(f"{name} must have tile_table's shape")
     if ws is None:
         with torch.cuda.device(device):  # the split of the work depends on the device
-            need = decode4_workspace_bytes(B, Hq, Hkv, D, max_tiles)
+            need = decode4_workspace_bytes(B, Hq, Hkv, D, max_tiles, weights=mass_out is not None)
         ws = _scratch(need, q.device, stream)
     if out is None:
         out = _result(q, stream)

@@ -105,6 +105,20 @@ def test_decode_refusals(lib):
     assert n.value >= 2 * 32 * (128 * 4 + 8) + 2 * 8 * 8 * 4 * 64
 
 
+def test_decode_workspaces_with_and_without_weights(lib):
+    for B, Hq, Hkv, D, mt in ((1, 32, 8, 128, 8), (3, 6, 2, 64, 100), (256, 8, 8, 256, 1024)):
+        L = kvarn.layout4(D)
+        both = kvarn.decode4_workspace_bytes(B, Hq, Hkv, D, mt)
+        plain = kvarn.decode4_workspace_bytes(B, Hq, Hkv, D, mt, weights=False)
+        assert 0 < plain < both and plain % 256 == 0 and both - plain == 256 * B * Hkv * mt
+        sizes = dict(B=B, Hq=Hq, Hkv=Hkv, D=D, mt=mt, lay=ctypes.byref(L))
+        assert _decode(lib, **sizes, wsb=plain - 256) == -5
+        assert _decode(lib, **sizes, wsb=plain, mo=P) == -5 and _decode(lib, **sizes, wsb=both - 1, mo=P) == -5
+        # enough of it: what is refused next is the workspace's alignment
+        assert _decode(lib, **sizes, wsb=plain, ws=ctypes.c_void_p((1 << 20) + 128)) == -2
+        assert _decode(lib, **sizes, wsb=both, mo=P, ws=ctypes.c_void_p((1 << 20) + 128)) == -2
+
+
 def _prefill(lib, **kw):
     L = kvarn.layout4(128)
     a = dict(q=P, io=0, C=16, pos0=100, tiles=P, size=1 << 30, table=P, stride=2, Hq=32, Hkv=8, D=128, scale=f32(0.1),

@@ -440,6 +440,20 @@ def test_decode_weights_accumulate(D, G):
     assert torch.equal(m2[1], base[1])
 
 
+@pytest.mark.parametrize("n", [300, 3000])
+def test_decode_without_weights_needs_no_room_for_them(n):
+    c = Cache4(27, [n, 7], 2, 64)
+    q = _query(28, (2, 8, 64), "bf16")
+    need = kvarn.decode4_workspace_bytes(2, 8, 2, 64, c.max_tiles, weights=False)
+    room = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+    out = c.decode(q, ws=room[:need])
+    assert torch.equal(out, c.decode(q)) and torch.equal(out, c.decode(q, mass_out=torch.zeros(2, 2, c.max_tiles, device=DEV)))
+    assert bool((room[need:] == 0xA5).all())
+    _check_decode(c, q, out)
+    with pytest.raises(kvarn.KvarnError):
+        c.decode(q, ws=room[:need], mass_out=torch.zeros(2, 2, c.max_tiles, device=DEV))
+
+
 @pytest.mark.parametrize("tokens", [256, 2560])
 def test_decode_counts_past_their_table_are_clamped(tokens):
     c = Cache4(30, [tokens, 40], 2, 128)
