@@ -678,8 +678,8 @@ int kvarn_evict_tiles(const int64_t* tile_table, const float* tile_mass, const i
  * The 4-bit cache. The pages have no counterpart: 128-token tiles per KV head and
  * byte-offset tile tables as above, but rows are quantised as they are written, token
  * by token, so there is no staging window and nothing to promote: a decode step is
- * kvarn_norm_rotate, kvarn_write_rows4, kvarn_decode_attention4. Records hold 4.5
- * bits per value. kvarn_evict_tiles works on its tables.
+ * kvarn_norm_rotate, kvarn_write_rows4, kvarn_window_advance (the lengths, on the device) and
+ * kvarn_decode_attention4. Records hold 4.5 bits per value. kvarn_evict_tiles works on its tables.
  *
  * A value is code * scale, with one scale for each group of 32 consecutive channels of a
  * token of a head, K and V on their own:
@@ -795,10 +795,11 @@ int kvarn_decode_attention4(const void* q, int io_type, const uint8_t* tiles, in
  *                  tiles of a head, 2^25 - 1 of all (KVARN_ERR_BAD_ARG).
  * A row that sees a poisoned token or a record outside the pool (KVARN_DEVERR_RECORD), or has
  * a NaN or an infinity in its query, is NaN; rows before it are not touched by it. With 16-bit types
- * chunks of many rows round the softmax weights to fp16, as kvarn_prefill_attention8 does.
+ * chunks of many rows round the softmax weights to fp16, as kvarn_prefill_attention8 does; with
+ * KVARN_IO_F16 their sum is of the rounded ones, so that equal values give that very value.
  *   ws : at least kvarn_prefill4_workspace_bytes() bytes for these sizes or larger ones
  *        (n_tiles >= ceil((pos0 + C) / 128)), 256-byte aligned, no initialisation. Calls
- *        sharing ws must not overlap.
+ *        sharing ws must not overlap. The query counts what KVARN_IO_F32 needs, whatever the type.
  */
 int kvarn_prefill4_workspace_bytes(int C, int n_tiles, int Hq, int Hkv, int head_dim, size_t* bytes);
 int kvarn_prefill_attention4(const void* q_chunk, int io_type, int C, int64_t pos0,
@@ -842,8 +843,8 @@ int kvarn_rotary(int rotary_dim, int pairing, const double* inv_freq, const uint
  * Per row (token, head): y = x; with eps >= 0, y = x / sqrt(mean(x^2) + eps) * weight (the sum
  * of squares and all that follows in fp32, rounded once at the end); then the rotation of
  * `rotary` (host pointer; NULL: none); then, with hadamard, y H / sqrt(D) (H as in
- * kvarn_rotate_query: scores of transformed queries and keys are the same, and 4-bit keys
- * lose less).
+ * kvarn_rotate_query: scores of transformed queries and keys are the same, and keys with a few
+ * channels much larger than the others lose less in 4 bits; others no more and no less).
  *   q, k         : io_type [n_tokens][Hq][D] and [n_tokens][Hkv][D]; tokens q_stride (k_stride)
  *                  elements apart, at least Hq * D (Hkv * D). Pointers and strides are multiples
  *                  of 16 bytes. Hkv = 0: queries alone (k, k_out NULL). Any number of heads.

@@ -152,7 +152,7 @@ __device__ __forceinline__ int tiles4(const Split4Args& s, int b) {
 // Shares of `total` tiles, at most one per resident CTA; the first `more` of them hold base + 1 tiles, the others base,
 // so that none is empty and a segment's pieces lie in slots side by side. A share costs a CTA as much as two tiles
 // besides (query, exchange, partial result), so there are three tiles to one, where that leaves `few` (two CTAs per
-// SM): one sequence of 16k tokens takes 10.7 us, with a share per CTA 11.6, with four tiles to a share 11.9; 4k
+// SM): one sequence of 16k tokens took 10.7 us so (10.2 now), with a share per CTA 11.6, with four tiles to a share 11.9; 4k
 // 6.5 with one tile, 7.0 with two. (All counts are below 2^31: 64-bit divisions would take a microsecond of a
 // short call.)
 struct Shares4 {

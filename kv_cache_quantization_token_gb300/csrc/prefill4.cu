@@ -9,9 +9,9 @@
 // Precision is that of the 8-bit cache: fp32 queries and weights are fp16 pairs, 16-bit ones one fp16 number.
 // Chunks of few rows run on the decode kernels instead (few_rows() below).
 //
-// What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 109 us, 1,167 TFLOP/s, 61% of the measured
-// bf16 rate): the products, on the 128 of 152 SMs that have a CTA (tensor pipe 80% busy there), and 13 us of images
-// before them. Without scales in the softmax it takes 4 us less than over the 8-bit cache.
+// What bounds it (512 positions, 32 / 8 heads of 128 over 15,500 tokens, bf16: 104.5 us, 1,224 TFLOP/s, 64% of the measured
+// bf16 rate; fp16 111): the products, on the 128 of 152 SMs that have a CTA (tensor pipe 80% busy there), and 13 us of images
+// before them. Over the 8-bit cache, with scales in the softmax, it takes 117.
 //
 // A poisoned token has NaN in its K image and zeros in its V image, as in its record; tokens behind the last
 // position that the chunk sees count as zeros in V, whatever their bytes, and are hidden in the scores.

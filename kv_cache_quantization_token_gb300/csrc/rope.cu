@@ -16,7 +16,7 @@
 // What bounds it: instructions beside memory. 8,192 tokens of 32 + 8 heads of 128, bf16, packed (168 MB): 30.8 us, 5.4
 // TB/s (80% of the copy rate). A warp per token that comes and goes took 37.4, and 38.2 with the frequencies read from the
 // launch's arguments, which are served one index at a time (1,337 tokens with transform: 6.3, 7.1, 8.4); twenty warps of 96
-// registers instead of sixteen of 128 33.5, two items under way instead of three 32.1; angles of a CTA's tokens in shared
+// registers instead of sixteen of 128 36.4, two items under way instead of three 32.3, four 30.6; angles of a CTA's tokens in shared
 // memory 47 to 58.
 #include "cache4.cuh"
 
